@@ -13,6 +13,8 @@
 #include <string>
 #include <vector>
 
+#include <hip/hip_runtime.h>
+
 #include "pq_internal.h"
 
 namespace pq {
@@ -30,6 +32,24 @@ int set_error(int code, const char* fmt, ...) {
 }
 
 void clear_error() { g_last_error.clear(); }
+
+int launch_status(const char* what) {
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return set_error(PQ_ERR_DEVICE, "%s: launch failed: %s", what, hipGetErrorString(e));
+  return PQ_OK;
+}
+
+int cu_count() {
+  static int cached[64] = {0};
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+  if (cached[dev] == 0) {
+    int n = 0;
+    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) n = 256;
+    cached[dev] = n;
+  }
+  return cached[dev];
+}
 
 int check_partitions(int P, int pb1, int pb2, int N) {
   if (P < 1 || P > PQ_MAX_PARTITIONS)

@@ -14,6 +14,12 @@ void clear_error();
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// PQ_OK, or PQ_ERR_DEVICE with the message of the launch that just failed.
+int launch_status(const char* what);
+
+// Compute units of the current device (cached per device).
+int cu_count();
+
 // Validates (P, pb1, pb2) against N. Returns PQ_OK or an error code (message set).
 int check_partitions(int P, int pb1, int pb2, int N);
 

@@ -724,12 +724,6 @@ __global__ void recip_kernel(const float* __restrict__ x, float* __restrict__ y,
   if (i < n) y[i] = recip_rn(x[i]);
 }
 
-static int launch_status(const char* what) {
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return set_error(PQ_ERR_DEVICE, "%s: launch failed: %s", what, hipGetErrorString(e));
-  return PQ_OK;
-}
-
 // ws_d (kWs): the prefill GEMM's workspace, laid out as pq_gemm_workspace_bytes sizes it.
 template <bool kI8, bool kWs = false>
 static int rotate_quant_launch(const char* what, const uint16_t* x_d, int64_t ldx, int M, int K, int P,
