@@ -50,6 +50,9 @@ enum pq_status {
   PQ_ERR_DEVICE = -7     /* the HIP runtime reported an error at launch */
 };
 
+/* Element types of the entry points that take several. */
+enum pq_type { PQ_F16 = 0, PQ_BF16 = 1, PQ_F32 = 2 };
+
 /* ABI version of the loaded library (PQ_ABI_VERSION it was built with). */
 int pq_abi_version(void);
 
@@ -315,6 +318,32 @@ int pq_add_rms_rotate_quant(const uint16_t* x_d, int64_t ldx, const uint16_t* re
                             const uint16_t* w_d, float eps, int gemma, int M, int K, int P,
                             const void* rec_d, const uint16_t* cs_d, uint16_t* res_out_d, int64_t ldo,
                             uint16_t* hs_d, uint8_t* a_d, float* asg_d, float* rs_d, pq_stream_t stream);
+
+/*
+ * The norms before and after a block with its gate and the residual scale (device), one launch: what
+ * lies between a block's last projection and the next block's first prologue. Per token row, in
+ * binary32 with one rounding where h and hs are stored:
+ *   n  = x * rstd(x) * w_post'                        (w_post_d NULL: n = x)
+ *   h  = res_scale * res + scale * a(gate) * n        the new residual stream, type of res
+ *   hs = h * rstd(h) * w_pre'                         from h as stored (w_pre_d NULL: not written)
+ * with rstd(v) = 1 / sqrt(mean_k(v^2) + eps), w' = 1 + w (gemma != 0) or w, a = identity, sigmoid or tanh.
+ * Rows whose squares overflow binary32 get rstd 0, as in any binary32 norm; NaN stays in its row.
+ *
+ * x_d        f16 or bf16 [M, ldx] (x_type), the block's output (pq_gemm's bf16 y, say).
+ * res_d      f16, bf16 or f32 [M, ldr] (res_type); res_out_d the same type [M, ldo]: res_d itself with
+ *            ldo == ldr (in place), or rows that overlap no input.
+ * w_post_d, w_pre_d   [K], of hs's type. hs_d  f16 or bf16 [M, ldh] (out_type).
+ * gate_d     of x's type, or NULL: gate_cols == K: [M, ldg] rows, or one row for every token with
+ *            ldg == 0; gate_cols == 1: one value per token, ldg elements apart.
+ * K % 8 == 0, K <= 32768; rows start on 16-byte lines (pointers 16-byte aligned, strides whole 16-byte
+ * steps and >= K); a gate of one value per token needs the alignment of its element only.
+ * Errors: PQ_ERR_SHAPE (also for an output that overlaps an input or the other output), PQ_ERR_NULL, PQ_ERR_ALIGN.
+ */
+enum pq_gate_act { PQ_GATE_NONE = 0, PQ_GATE_SIGMOID = 1, PQ_GATE_TANH = 2 };
+int pq_block_norms(const void* x_d, int64_t ldx, int x_type, const void* res_d, int64_t ldr, int res_type,
+                   const void* w_post_d, const void* gate_d, int64_t ldg, int gate_cols, int gate_act,
+                   const void* w_pre_d, float eps, float scale, float res_scale, int gemma, int M, int K,
+                   void* res_out_d, int64_t ldo, void* hs_d, int64_t ldh, int out_type, pq_stream_t stream);
 
 /*
  * Verification hooks: run the exact device arithmetic the prologue uses on plain arrays, so

@@ -11,6 +11,8 @@ Calls (same names as the C entry points, without the ``pq_`` prefix):
 * ``pack_weights(qweight, qzeros, scales)``  device; AWQ tensors -> (wpk, sz)
 * ``rotate_quant(x, rec, cs)``               device; -> (A, ASG, RS)
 * ``gemm(A, ASG, RS, wpk, sz, N, pb1, pb2)`` device; -> y bf16
+* ``block_norms(x, residual, ...)``           device; -> (new residual, normalised row): the norms before
+  and after a block with its gate and residual scale
 * ``e4m3_encode(q)``, ``recip_f32(x)``       device verification hooks
 """
 import ctypes
@@ -60,6 +62,8 @@ SIGNATURES = {
     "pq_gemm5": (_I, [_P, _P, _P, _I, _I, _I, _P, _P, _I, _I, _I, _P, _I64, _P, _SZ, _P]),
     "pq_add_rms_rotate_quant": (_I, [_P, _I64, _P, _I64, _P, ctypes.c_float, _I, _I, _I, _I, _P, _P, _P, _I64,
                                      _P, _P, _P, _P, _P]),
+    "pq_block_norms": (_I, [_P, _I64, _I, _P, _I64, _I, _P, _P, _I64, _I, _I, _P, ctypes.c_float, ctypes.c_float,
+                            ctypes.c_float, _I, _I, _I, _P, _I64, _P, _I64, _I, _P]),
     "pq_e4m3_encode": (_I, [_P, _P, _I64, _P]),
     "pq_recip_f32": (_I, [_P, _P, _I64, _P]),
     "pq_bf16_round": (_I, [_P, _P, _I64, _P]),
@@ -129,6 +133,23 @@ def _validate(specs, rows=()):
     ValueError), then that each is a CUDA tensor on the first one's device (TypeError), so a
     shape mismatch is reported the same way whatever the devices."""
     import torch
+    # the usual call passes everything: one cheap look at each tensor, and the ordered checks below
+    # only to name what is wrong
+    dev = None
+    for t, name, dtype, shape in specs:
+        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous() and
+                (t.shape == shape if isinstance(shape, tuple) else t.numel() >= shape) and
+                (dev is None or t.device == dev)):
+            break
+        dev = t.device
+    else:
+        for t, name, dtype, shape in rows:
+            if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.shape == shape and
+                    t.stride(1) == 1 and (dev is None or t.device == dev)):
+                break
+            dev = t.device
+        else:
+            return
     for t, name, dtype, shape in list(specs) + list(rows):
         if not isinstance(t, torch.Tensor) or t.dtype != dtype:
             raise TypeError(f"{name}: expected a tensor of {dtype}")
@@ -179,6 +200,50 @@ def _prologue_specs(x, rec, cs, K):
         raise ValueError("rec: a [8, K/2, 8] record set serves one partition only")
     cs_shape = (P, K) if cs.dim() == 2 else (K,)
     return P, [(rec, "rec", torch.uint8, rec_shape), (cs, "cs", torch.float16, cs_shape)]
+
+
+def _addr(t):
+    """Address of an optional tensor, as ctypes takes it."""
+    return None if t is None else t.data_ptr()
+
+
+def _pitch(t):
+    """Row stride of a [M, K] tensor in elements; that of a single row is of no consequence."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _new(shape, dtype, device, stream):
+    """An output or workspace of a call on ``stream``: from that stream's own memory, so that it is not
+    handed out again before the stream has passed the call."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _launch(fn, device, stream, *args):
+    """Calls the C entry point ``fn`` on the tensors' device, queued on ``stream`` or that device's current one."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"stream: on {stream.device}, the tensors are on {device}")
+    if torch.cuda.current_device() == device.index:
+        rc = getattr(lib(), fn)(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = getattr(lib(), fn)(*args, stream.cuda_stream)
+    if rc != PQ_OK:
+        _check(fn, rc)
+
+
+def _type_code(dtype, name, allowed):
+    """The pq_type of a torch dtype among ``allowed`` (names of torch dtypes)."""
+    code = {"torch.float16": 0, "torch.bfloat16": 1, "torch.float32": 2}.get(str(dtype))
+    if code is None or str(dtype)[6:] not in allowed:
+        raise TypeError(f"{name}: expected a tensor of {' or '.join(allowed)}, got {dtype}")
+    return code
 
 
 # ------------------------------------------------------------------------------------------
@@ -457,6 +522,65 @@ def gemm_tok(A, AS, RS, wpk, sz, N, pb1=NO_BOUNDARY, pb2=NO_BOUNDARY, out=None, 
     import torch
     return _gemm_common("pq_gemm_tok", A, AS, RS, wpk, sz, N, pb1, pb2, out, workspace, stream,
                         a_dtype=torch.uint8, tok=True)
+
+
+GATE_ACTS = {"none": 0, "sigmoid": 1, "tanh": 2}
+
+
+def block_norms(x, residual, w_post=None, gate=None, w_pre=None, eps=1e-6, scale=1.0, res_scale=1.0, gate_act="none",
+                gemma=False, residual_out=None, out=None, stream=None):
+    """The norms before and after a block, its gate and the residual scale in one launch:
+    ``n = rmsnorm(x, w_post)`` (``x`` without ``w_post``), ``h = res_scale * residual + scale * a(gate) * n``,
+    ``hs = rmsnorm(h, w_pre)`` from the stored ``h`` -> (h, hs), hs None without ``w_pre``.
+
+    x f16 or bf16 [M, K]; residual f16, bf16 or f32 [M, K]; w_post, w_pre [K] of hs's type (f16 or bf16);
+    gate of x's type: [K] (one row for every token), [M, K], or [M, 1] (one value per token); gate_act "none",
+    "sigmoid" or "tanh". gemma: the norms multiply by 1 + w. residual_out may be ``residual`` itself (in place).
+    K a multiple of 8 up to 32768; rows of 2-D tensors start on 16-byte lines."""
+    import torch
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x: expected a [M, K] tensor")
+    if not isinstance(residual, torch.Tensor):
+        raise TypeError("residual: expected a tensor")
+    M, K = x.shape
+    xt = _type_code(x.dtype, "x", ("float16", "bfloat16"))
+    rt = _type_code(residual.dtype, "residual", ("float16", "bfloat16", "float32"))
+    act = GATE_ACTS.get(gate_act)
+    if act is None:
+        raise ValueError(f"gate_act: {gate_act!r}, expected one of {', '.join(GATE_ACTS)}")
+    specs, rows = [], [(x, "x", x.dtype, (M, K)), (residual, "residual", residual.dtype, (M, K))]
+    wt = next((w.dtype for w in (w_pre, w_post) if isinstance(w, torch.Tensor)), torch.float16)
+    ot = _type_code(wt, "w_pre" if w_pre is not None else "w_post", ("float16", "bfloat16"))
+    for w, name in ((w_post, "w_post"), (w_pre, "w_pre")):
+        if w is not None:
+            specs.append((w, name, wt, (K,)))
+    ldg, gcols = 0, K
+    if gate is not None:
+        if isinstance(gate, torch.Tensor) and gate.dim() == 1:
+            specs.append((gate, "gate", x.dtype, (K,)))
+        else:
+            gcols = 1 if isinstance(gate, torch.Tensor) and gate.dim() == 2 and gate.shape[1] == 1 else K
+            if gcols == 1:
+                gate = gate.as_strided((M, 1), (gate.stride(0), 1)) if gate.shape[0] == M else gate
+            rows.append((gate, "gate", x.dtype, (M, gcols)))
+    if residual_out is not None:
+        rows.append((residual_out, "residual_out", residual.dtype, (M, K)))
+    if out is not None:
+        if w_pre is None:
+            raise ValueError("out: nothing is written there without w_pre")
+        rows.append((out, "out", wt, (M, K)))
+    _validate(specs, rows=rows)
+    if gate is not None and gate.dim() == 2:
+        ldg = _pitch(gate)
+    if residual_out is None:
+        residual_out = _new((M, K), residual.dtype, x.device, stream)
+    if out is None and w_pre is not None:
+        out = _new((M, K), wt, x.device, stream)
+    _launch("pq_block_norms", x.device, stream,
+            x.data_ptr(), _pitch(x), xt, residual.data_ptr(), _pitch(residual), rt, _addr(w_post), _addr(gate), ldg, gcols,
+            act, _addr(w_pre), float(eps), float(scale), float(res_scale), 1 if gemma else 0, M, K,
+            residual_out.data_ptr(), _pitch(residual_out), _addr(out), _pitch(out) if out is not None else K, ot)
+    return residual_out, out
 
 
 def e4m3_encode(q, stream=None):

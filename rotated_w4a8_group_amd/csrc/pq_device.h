@@ -24,6 +24,12 @@ __device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(pq_f32x2{lo, hi}, pq_bf16x2));
 }
 
+// Two floats rounded to nearest even f16, packed the same way.
+typedef _Float16 pq_f16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t f16x2_rn(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(pq_f32x2{lo, hi}, pq_f16x2));
+}
+
 __device__ __forceinline__ float bf16_to_f32(uint32_t h) { return __builtin_bit_cast(float, (h & 0xFFFFu) << 16); }
 
 // The prefill GEMM's zero-point operand, activation side: K' = 3G values per row,
