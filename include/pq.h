@@ -148,6 +148,17 @@ int pq_rotate_quant(const uint16_t* x_d, int64_t ldx, int M, int K, int P, const
                     pq_stream_t stream);
 
 /*
+ * The rotation alone (device): pq_rotate_quant's channel scale and 8 layers (the same binary32
+ * arithmetic), the result rounded once (to nearest even) to the type of x instead of quantised - the
+ * 16-bit rows that products with weights of the rotated space take (pq_matvec).
+ *
+ * x_d   f16 or bf16 (x_type) [M, ldx], as in pq_rotate_quant; rec_d, cs_d as there (cs f16 always).
+ * y_d   out, type of x, [P, M, K], 16-byte aligned, not overlapping x (PQ_ERR_SHAPE).
+ */
+int pq_rotate(const uint16_t* x_d, int64_t ldx, int x_type, int M, int K, int P, const void* rec_d,
+              const uint16_t* cs_d, uint16_t* y_d, pq_stream_t stream);
+
+/*
  * W4A8 group GEMM (device): for column n in partition p(n) = [n >= pb1] + [n >= pb2],
  *   y[m, n] = bf16_rne( sum_g asg_p[m,g] * ( sc[g,n] * sum_{k in g} D(A_p[m,k]) * (c[k,n] - 8)
  *                                            - fl16(sc[g,n]*(zp[g,n]-8)) * rs_p[m,g] ) )
@@ -171,6 +182,23 @@ size_t pq_gemm_workspace_bytes(int M, int N, int K);
 int pq_gemm(const uint8_t* a_d, const float* asg_d, const float* rs_d, int M, int K, int P,
             const void* wpk_d, const uint16_t* sz_d, int N, int pb1, int pb2, uint16_t* y_d,
             int64_t ldy, void* ws_d, size_t ws_bytes, pq_stream_t stream);
+
+/*
+ * Products of few 16-bit rows with the packed weights (device): for column n in partition p(n),
+ *   y[m, n] = fl( sum_g ( sc[g,n] * sum_{k in g} x_p[m,k] (c[k,n] - 8)
+ *                         - fl16(sc[g,n]*(zp[g,n]-8)) * sum_{k in g} x_p[m,k] ) )
+ * pq_gemm's weights (the same wpk_d and sz_d) with activations that are not quantised; sums in binary32, one
+ * rounding to the type of y. A row of x with an infinity or a NaN gives NaN in its whole row of y.
+ *
+ * x_d     f16 or bf16 (x_type) [P, M, ldx] (first K columns of a row used; partition p starts at row
+ *         p * M), 16-byte aligned, ldx a multiple of 8, K <= ldx <= 2^26. For weights of the rotated
+ *         space: pq_rotate's y.
+ * y_d     out, f16 or bf16 (y_type) [M, ldy], ldy even and >= N, 4-byte aligned.
+ * 0 <= M <= 16, K % 128 == 0, N % 16 == 0; P, pb1, pb2 as for pq_gemm. No workspace.
+ */
+int pq_matvec(const uint16_t* x_d, int64_t ldx, int x_type, int M, int K, int P, const void* wpk_d,
+              const uint16_t* sz_d, int N, int pb1, int pb2, uint16_t* y_d, int64_t ldy, int y_type,
+              pq_stream_t stream);
 
 /*
  * The prologue and the GEMM sharing the GEMM's workspace, so that nothing runs between them

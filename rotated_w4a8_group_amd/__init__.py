@@ -10,7 +10,9 @@ Calls (same names as the C entry points, without the ``pq_`` prefix):
 * ``build_records(pairs, theta)``            host; numpy int16 [8, K], f16 [8, K/2]
 * ``pack_weights(qweight, qzeros, scales)``  device; AWQ tensors -> (wpk, sz)
 * ``rotate_quant(x, rec, cs)``               device; -> (A, ASG, RS)
+* ``rotate(x, rec, cs)``                     device; -> rotated rows of x's type, not quantised
 * ``gemm(A, ASG, RS, wpk, sz, N, pb1, pb2)`` device; -> y bf16
+* ``matvec(x, wpk, sz, N, pb1, pb2)``        device; 16-bit rows (at most 16) -> y of their type
 * ``block_norms(x, residual, ...)``           device; -> (new residual, normalised row): the norms before
   and after a block with its gate and residual scale
 * ``e4m3_encode(q)``, ``recip_f32(x)``       device verification hooks
@@ -46,8 +48,10 @@ SIGNATURES = {
     "pq_packed_weight_bytes": (_SZ, [_I, _I]),
     "pq_pack_weights": (_I, [_P, _P, _P, _I, _I, _P, _P, _P]),
     "pq_rotate_quant": (_I, [_P, _I64, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
+    "pq_rotate": (_I, [_P, _I64, _I, _I, _I, _I, _P, _P, _P, _P]),
     "pq_gemm_workspace_bytes": (_SZ, [_I, _I, _I]),
     "pq_gemm": (_I, [_P, _P, _P, _I, _I, _I, _P, _P, _I, _I, _I, _P, _I64, _P, _SZ, _P]),
+    "pq_matvec": (_I, [_P, _I64, _I, _I, _I, _I, _P, _P, _I, _I, _I, _P, _I64, _I, _P]),
     "pq_rotate_quant_for_gemm": (_I, [_P, _I64, _I, _I, _I, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "pq_gemm_prepared": (_I, [_P, _P, _P, _I, _I, _I, _P, _P, _I, _I, _I, _P, _I64, _P, _SZ, _P]),
     "pq_gemm_noalloc_max_scratch_bytes": (_SZ, []),
@@ -370,6 +374,24 @@ def rotate_quant_for_gemm(x, rec, cs, workspace, out=None, stream=None):
                                 workspace=workspace)
 
 
+def rotate(x, rec, cs, out=None, stream=None):
+    """The rotation alone: x f16 or bf16 [M, K] (row stride may exceed K), rec uint8 [P, 8, K/2, 8] (or [8, K/2, 8]),
+    cs f16 [P, K] (or [K]) -> y [P, M, K] of x's type, ``rotate_quant``'s rotated rows before their quantisation."""
+    import torch
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x: expected a [M, K] tensor")
+    M, K = x.shape
+    xt = _type_code(x.dtype, "x", ("float16", "bfloat16"))
+    P, specs = _prologue_specs(x, rec, cs, K)
+    if out is not None:
+        specs.append((out, "out", x.dtype, (P, M, K)))
+    _validate(specs, rows=[(x, "x", x.dtype, (M, K))])
+    if out is None:
+        out = _new((P, M, K), x.dtype, x.device, stream)
+    _launch("pq_rotate", x.device, stream, x.data_ptr(), _pitch(x), xt, M, K, P, rec.data_ptr(), cs.data_ptr(), out.data_ptr())
+    return out
+
+
 def gemm_workspace_bytes(M, N, K):
     return int(lib().pq_gemm_workspace_bytes(M, N, K))
 
@@ -416,6 +438,45 @@ def gemm(A, ASG, RS, wpk, sz, N, pb1=NO_BOUNDARY, pb2=NO_BOUNDARY, out=None, wor
     -> y bf16 [M, N] (or into ``out``, a bf16 [M, ldy >= N] view with unit column stride)."""
     import torch
     return _gemm_common("pq_gemm", A, ASG, RS, wpk, sz, N, pb1, pb2, out, workspace, stream, a_dtype=torch.uint8)
+
+
+def matvec(x, wpk, sz, N, pb1=NO_BOUNDARY, pb2=NO_BOUNDARY, out=None, dtype=None, stream=None):
+    """Products of few 16-bit rows with the packed weights of ``gemm``: x f16 or bf16 [P, M, K] (or [M, K] for one
+    partition; row stride may exceed K), M <= 16 -> y [M, N] of ``dtype`` (f16 or bf16; x's type by default), or into
+    ``out``, a [M, ldy >= N] view with unit column stride."""
+    import torch
+    if not isinstance(x, torch.Tensor) or x.dim() not in (2, 3):
+        raise ValueError("x: expected a [P, M, K] or [M, K] tensor")
+    xt = _type_code(x.dtype, "x", ("float16", "bfloat16"))
+    P, M, K = (1, *x.shape) if x.dim() == 2 else x.shape
+    if K == 0 or K % GROUP:
+        raise ValueError(f"x: K={K} must be a positive multiple of {GROUP}")
+    if M > 16:
+        raise ValueError(f"x: M={M} rows, at most 16 (gemm takes more, quantised)")
+    need = lib().pq_packed_weight_bytes(K, N)
+    if need == 0:
+        raise ValueError(f"N={N}: not a shape the library packs (N % 16 == 0 needed)")
+    specs = [(wpk, "wpk", torch.uint8, (need,)), (sz, "sz", torch.float16, (K // GROUP, N, 2))]
+    rows = []
+    if x.dim() == 3:
+        specs.append((x, "x", x.dtype, (P, M, K)))
+        ldx = K
+    else:
+        rows.append((x, "x", x.dtype, (M, K)))
+        ldx = _pitch(x)
+    if out is not None:
+        if not isinstance(out, torch.Tensor) or out.dim() != 2 or out.shape[0] != M or out.shape[1] < N:
+            raise ValueError(f"out: expected a f16 or bf16 [{M}, >= {N}] tensor")
+        if dtype is not None and out.dtype != dtype:
+            raise TypeError(f"out: {out.dtype}, dtype says {dtype}")
+        rows.append((out, "out", out.dtype, (M, out.shape[1])))
+    yt = _type_code(out.dtype if out is not None else dtype or x.dtype, "out", ("float16", "bfloat16"))
+    _validate(specs, rows=rows)
+    if out is None:
+        out = _new((M, N), dtype or x.dtype, x.device, stream)
+    _launch("pq_matvec", x.device, stream, x.data_ptr(), ldx, xt, M, K, P, wpk.data_ptr(), sz.data_ptr(), N, pb1, pb2,
+            out.data_ptr(), _pitch(out), yt)
+    return out
 
 
 def gemm_prepared(A, ASG, RS, wpk, sz, N, pb1=NO_BOUNDARY, pb2=NO_BOUNDARY, out=None, workspace=None, stream=None):

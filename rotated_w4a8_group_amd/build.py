@@ -28,6 +28,7 @@ SOURCES = [
     ("pq_prologue.hip", ["-ffp-contract=off"]),
     ("pq_norms.hip", []),
     # matrix-core results land in VGPRs (the fold reads them there; no AGPR copies)
+    ("pq_matvec.hip", ["-mllvm", "-amdgpu-mfma-vgpr-form"]),
     ("pq_gemm.hip", ["-mllvm", "-amdgpu-mfma-vgpr-form"]),
 ]
 

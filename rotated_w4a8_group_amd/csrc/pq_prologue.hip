@@ -444,6 +444,111 @@ __global__ __launch_bounds__(256) void rotate_quant_kernel(
 }
 
 // ---------------------------------------------------------------------------------------
+// The rotation alone (pq_rotate): the prologue's channel scale and layers, its result rounded once to
+// the type of x instead of quantised, for consumers that take 16-bit rows in the weights' rotated space.
+// Same units, loads and LDS images as rotate_quant_kernel; a lane ends with 8 neighbouring channels of
+// a token and stores them as 16 bytes. kBf16: x and y are bf16 (x * cs is exact in binary32 either
+// way: 8 x 11 or 11 x 11 significand bits).
+template <bool kVec16, bool kBf16>
+__global__ __launch_bounds__(256) void rotate_kernel(
+    const uint16_t* __restrict__ x, int64_t ldx, int M, int K, int P, const uint2* __restrict__ rec,
+    const uint16_t* __restrict__ cs, uint16_t* __restrict__ y, int tok, int chunks) {
+  __shared__ __align__(16) uint8_t sbuf[kProWaves][kProQuads * kProQuadBytes];
+
+  const int G = K >> 7;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int nb = gridDim.x, q8 = nb >> 3, b = blockIdx.x;
+  const int bx = b < 8 * q8 ? (b & 7) * q8 + (b >> 3) : b;
+  const int unit = bx * kProWaves + wave;
+  if (unit >= chunks * G * P) return;
+  const int g = unit % G;
+  const int chunk = (unit / G) % chunks;
+  const int p = unit / (G * chunks);
+  const int m0 = chunk * tok;
+  const int m_end = min(M, m0 + tok);
+  const int lane = threadIdx.x & 63;
+  const int t = lane >> 4, c = lane & 15;
+  const int half = K >> 1;
+
+  uint8_t* const buf = sbuf[wave];
+  uint8_t* const slot = buf + (9 * c) * 16 + 4 * t;
+  const uint16_t* const xg = x + g * 128 + 8 * c;
+  auto load_step = [&](int mb, uint4 (&dst)[kProQuads]) {
+#pragma unroll
+    for (int q = 0; q < kProQuads; ++q) {
+      const int m = min(mb + 4 * q + t, m_end - 1);   // clamped: always a valid row
+      dst[q] = load_x8<kVec16>(xg + static_cast<size_t>(m) * ldx);
+    }
+  };
+  uint4 xa[kProQuads], xb[kProQuads];
+  load_step(m0, xa);
+
+  RotRec R;
+  {
+    uint2 q[PQ_LAYERS];
+#pragma unroll
+    for (int r = 0; r < PQ_LAYERS; ++r) q[r] = rec[(static_cast<size_t>(p) * PQ_LAYERS + r) * half + g * 64 + lane];
+    rot_decode(q, R);
+  }
+  const uint32_t* csp = reinterpret_cast<const uint32_t*>(cs + static_cast<size_t>(p) * K + g * 128 + 8 * c);
+  float csf[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = csp[i];
+    csf[2 * i] = half_lo(w);
+    csf[2 * i + 1] = half_hi(w);
+  }
+  uint16_t* const yg = y + static_cast<size_t>(p) * M * K + g * 128 + 8 * c;
+
+  auto run_step = [&](int mb, const uint4 (&xs)[kProQuads]) {
+#pragma unroll
+    for (int q = 0; q < kProQuads; ++q) {
+      const uint32_t xw[4] = {xs[q].x, xs[q].y, xs[q].z, xs[q].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        if constexpr (kBf16) {
+          lo = bf16_to_f32(xw[i]) * csf[2 * i];
+          hi = __builtin_bit_cast(float, xw[i] & 0xFFFF0000u) * csf[2 * i + 1];
+        } else {
+          lo = mul_hf<false>(xw[i], csf[2 * i]);
+          hi = mul_hf<true>(xw[i], csf[2 * i + 1]);
+        }
+        *reinterpret_cast<float*>(slot + q * kProQuadBytes + (2 * i) * 16) = lo;
+        *reinterpret_cast<float*>(slot + q * kProQuadBytes + (2 * i + 1) * 16) = hi;
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+    rot_layers<kProQuads, kProQuadBytes>(buf, R);
+    float v[kProQuads][8];
+#pragma unroll
+    for (int q = 0; q < kProQuads; ++q)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[q][j] = *reinterpret_cast<const float*>(slot + q * kProQuadBytes + j * 16);
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int q = 0; q < kProQuads; ++q) {
+      const int m = mb + 4 * q + t;
+      if (m < m_end) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = kBf16 ? bf16x2_rn(v[q][2 * i], v[q][2 * i + 1]) : f16x2_rn(v[q][2 * i], v[q][2 * i + 1]);
+        *reinterpret_cast<uint4*>(yg + static_cast<size_t>(m) * K) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  };
+  for (int mb = m0;; mb += 2 * kProStep) {
+    load_step(mb + kProStep, xb);
+    run_step(mb, xa);
+    if (mb + kProStep >= m_end) break;
+    load_step(mb + 2 * kProStep, xa);
+    run_step(mb + kProStep, xb);
+    if (mb + 2 * kProStep >= m_end) break;
+  }
+}
+
+// ---------------------------------------------------------------------------------------
 // Per-token variant: one e4m3 scale per (partition, token) = the largest of the token's group
 // scales ("Numbers", the per-token prefill bullet; section "2026-09-08: MXFP4-PARO prod decode",
 // item 1). The scale needs every group of the row before any code is written, so a 16-wave
@@ -724,6 +829,19 @@ __global__ void recip_kernel(const float* __restrict__ x, float* __restrict__ y,
   if (i < n) y[i] = recip_rn(x[i]);
 }
 
+// Wave units of the per-group kernels: tokens per unit (a multiple of the 8-token step, as few as
+// keep the unit count near kProUnits: short units for small M, at most 256 tokens), token chunks and
+// workgroups. False where the units pass the kernels' 32-bit numbering.
+static bool prologue_units(int M, int G, int P, int* tok, int* chunks, int64_t* blocks) {
+  const int64_t rows = static_cast<int64_t>(G) * P;
+  const int64_t want = (static_cast<int64_t>(M) * rows + kProUnits - 1) / kProUnits;
+  *tok = static_cast<int>(std::min<int64_t>(256, std::max<int64_t>(kProStep, (want + kProStep - 1) / kProStep * kProStep)));
+  const int64_t n = (static_cast<int64_t>(M) + *tok - 1) / *tok;
+  *chunks = static_cast<int>(n);
+  *blocks = (n * rows + kProWaves - 1) / kProWaves;
+  return n * rows <= 0x7FFFFFFF;
+}
+
 // ws_d (kWs): the prefill GEMM's workspace, laid out as pq_gemm_workspace_bytes sizes it.
 template <bool kI8, bool kWs = false>
 static int rotate_quant_launch(const char* what, const uint16_t* x_d, int64_t ldx, int M, int K, int P,
@@ -738,15 +856,9 @@ static int rotate_quant_launch(const char* what, const uint16_t* x_d, int64_t ld
   if (!aligned(x_d, 4) || !aligned(rec_d, 8) || !aligned(cs_d, 4) || !aligned(a_d, 16) || !aligned(asg_d, 4) || !aligned(rs_d, 4))
     return set_error(PQ_ERR_ALIGN, "%s: misaligned pointer", what);
   const int G = K / PQ_GROUP;
-  // tokens per wave unit: a multiple of the 8-token step, as few as keep the unit count near
-  // kProUnits (short units for small M, at most 256 tokens)
-  const int64_t rows = static_cast<int64_t>(G) * P;
-  const int64_t want = (static_cast<int64_t>(M) * rows + kProUnits - 1) / kProUnits;
-  const int tok = static_cast<int>(std::min<int64_t>(256, std::max<int64_t>(kProStep, (want + kProStep - 1) / kProStep * kProStep)));
-  const int64_t chunks = (M + tok - 1) / tok;
-  const int64_t units = chunks * rows;
-  const int64_t blocks = (units + kProWaves - 1) / kProWaves;
-  if (units > 0x7FFFFFFF) return set_error(PQ_ERR_SHAPE, "%s: problem too large", what);
+  int tok, chunks;
+  int64_t blocks;
+  if (!prologue_units(M, G, P, &tok, &chunks, &blocks)) return set_error(PQ_ERR_SHAPE, "%s: problem too large", what);
   const bool vec16 = aligned(x_d, 16) && (ldx % 8) == 0;
   uint16_t* zpa = nullptr;
   float* asgt = nullptr;
@@ -757,8 +869,7 @@ static int rotate_quant_launch(const char* what, const uint16_t* x_d, int64_t ld
   auto kern = vec16 ? rotate_quant_kernel<true, kI8, kWs> : rotate_quant_kernel<false, kI8, kWs>;
   hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
                      reinterpret_cast<hipStream_t>(stream), x_d, ldx, M, K, P,
-                     static_cast<const uint2*>(rec_d), cs_d, a_d, asg_d, rs_d, tok,
-                     static_cast<int>(chunks), zpa, asgt);
+                     static_cast<const uint2*>(rec_d), cs_d, a_d, asg_d, rs_d, tok, chunks, zpa, asgt);
   return launch_status(what);
 }
 
@@ -771,6 +882,35 @@ int pq_rotate_quant(const uint16_t* x_d, int64_t ldx, int M, int K, int P, const
                     pq_stream_t stream) {
   pq::clear_error();
   return pq::rotate_quant_launch<false>("pq_rotate_quant", x_d, ldx, M, K, P, rec_d, cs_d, a_d, asg_d, rs_d, stream);
+}
+
+int pq_rotate(const uint16_t* x_d, int64_t ldx, int x_type, int M, int K, int P, const void* rec_d,
+              const uint16_t* cs_d, uint16_t* y_d, pq_stream_t stream) {
+  using namespace pq;
+  clear_error();
+  const char* what = "pq_rotate";
+  if (M < 0) return set_error(PQ_ERR_SHAPE, "%s: M=%d < 0", what, M);
+  if (K <= 0 || K % PQ_GROUP || K > (1 << 24)) return set_error(PQ_ERR_SHAPE, "%s: K=%d must be a positive multiple of 128", what, K);
+  if (x_type != PQ_F16 && x_type != PQ_BF16) return set_error(PQ_ERR_SHAPE, "%s: x_type=%d must be f16 or bf16", what, x_type);
+  if (P < 1 || P > PQ_MAX_PARTITIONS) return set_error(PQ_ERR_PARTITION, "%s: P=%d must be in 1..3", what, P);
+  if (ldx < K || (ldx & 1)) return set_error(PQ_ERR_SHAPE, "%s: ldx=%lld must be even and >= K=%d", what, static_cast<long long>(ldx), K);
+  if (M == 0) return PQ_OK;
+  if (!x_d || !rec_d || !cs_d || !y_d) return set_error(PQ_ERR_NULL, "%s: NULL pointer", what);
+  if (!aligned(x_d, 4) || !aligned(rec_d, 8) || !aligned(cs_d, 4) || !aligned(y_d, 16))
+    return set_error(PQ_ERR_ALIGN, "%s: misaligned pointer", what);
+  const uintptr_t x0 = reinterpret_cast<uintptr_t>(x_d), y0 = reinterpret_cast<uintptr_t>(y_d);
+  const uintptr_t x1 = x0 + 2 * (static_cast<uintptr_t>(M - 1) * static_cast<uintptr_t>(ldx) + static_cast<uintptr_t>(K));
+  const uintptr_t y1 = y0 + 2 * static_cast<uintptr_t>(P) * static_cast<uintptr_t>(M) * static_cast<uintptr_t>(K);
+  if (x0 < y1 && y0 < x1) return set_error(PQ_ERR_SHAPE, "%s: y overlaps x", what);
+  int tok, chunks;
+  int64_t blocks;
+  if (!prologue_units(M, K / PQ_GROUP, P, &tok, &chunks, &blocks)) return set_error(PQ_ERR_SHAPE, "%s: problem too large", what);
+  const bool vec16 = aligned(x_d, 16) && (ldx % 8) == 0;
+  auto kern = x_type == PQ_BF16 ? (vec16 ? rotate_kernel<true, true> : rotate_kernel<false, true>)
+                                : (vec16 ? rotate_kernel<true, false> : rotate_kernel<false, false>);
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, reinterpret_cast<hipStream_t>(stream),
+                     x_d, ldx, M, K, P, static_cast<const uint2*>(rec_d), cs_d, y_d, tok, chunks);
+  return launch_status(what);
 }
 
 int pq_rotate_quant_for_gemm(const uint16_t* x_d, int64_t ldx, int M, int K, int P, const void* rec_d,
