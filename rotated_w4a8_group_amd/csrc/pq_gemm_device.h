@@ -13,6 +13,32 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
+__device__ __forceinline__ v4f mfma_fp8(const v8i& a, const v8i& b) {
+  const v4f zero = {0.f, 0.f, 0.f, 0.f};
+  // format 0 = OCP e4m3 for both operands; scale operands 0 select the unscaled instruction
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 0, 0, 0, 0, 0, 0);
+}
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+
+// Integer-code product of one 128-group: two 16x16x64 int8 matrix-core steps over the same
+// 32-byte fragments as the fp8 step (each step pairs the same byte positions of A and B, so the
+// two halves together cover every k of the group once); exact in int32, returned as float.
+__device__ __forceinline__ v4f mfma_i8(const v8i& a, const v8i& b) {
+  v4i c = {0, 0, 0, 0};
+  c = __builtin_amdgcn_mfma_i32_16x16x64_i8(v4i{a[0], a[1], a[2], a[3]}, v4i{b[0], b[1], b[2], b[3]}, c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_i32_16x16x64_i8(v4i{a[4], a[5], a[6], a[7]}, v4i{b[4], b[5], b[6], b[7]}, c, 0, 0, 0);
+  return v4f{static_cast<float>(c[0]), static_cast<float>(c[1]), static_cast<float>(c[2]), static_cast<float>(c[3])};
+}
+
+// The group product for either activation code domain: e4m3 codes times the raw weight codes as
+// e4m3 values c * 2^-9, or int8 codes times the raw codes as integers.
+template <bool kI8>
+__device__ __forceinline__ v4f group_product(const v8i& a, const v8i& b) {
+  if constexpr (kI8) return mfma_i8(a, b);
+  else return mfma_fp8(a, b);
+}
+
 __device__ __forceinline__ v8i unpack_codes(const u32x4& w) {
   v8i b;
   b[0] = static_cast<int>(w.x & 0x0F0F0F0Fu);
@@ -24,6 +50,38 @@ __device__ __forceinline__ v8i unpack_codes(const u32x4& w) {
   b[6] = static_cast<int>(w.w & 0x0F0F0F0Fu);
   b[7] = static_cast<int>((w.w >> 4) & 0x0F0F0F0Fu);
   return b;
+}
+
+// int5 weights: the codes' fifth bits ride in a plane beside the nibble image, and the matrix
+// core takes c - 16 as the e4m3 value (c - 16) * 2^-9, exact for every code. With the fifth bit
+// set that is the low nibble's own byte (as in the int4 path); without it the value is negative
+// with magnitude 16 - l, whose e4m3 byte is 0x80 | (16 - l) = 0x90 - l (16 * 2^-9 = 2^-5 is the
+// byte 0x10). Bit 8b + j of a lane's plane word belongs to byte b of operand dword j; v_perm
+// takes each byte from the nibble value (selector 4 + b) or its negative (selector b).
+template <int J>
+__device__ __forceinline__ int w5_dword(uint32_t L, uint32_t H) {
+  const uint32_t hb = (J >= 2 ? (H >> (J - 2)) : (H << (2 - J))) & 0x04040404u;
+  return static_cast<int>(__builtin_amdgcn_perm(L, 0x90909090u - L, 0x03020100u | hb));
+}
+
+__device__ __forceinline__ v8i unpack_codes5(const u32x4& w, uint32_t H) {
+  v8i b;
+  b[0] = w5_dword<0>(w.x & 0x0F0F0F0Fu, H);
+  b[1] = w5_dword<1>((w.x >> 4) & 0x0F0F0F0Fu, H);
+  b[2] = w5_dword<2>(w.y & 0x0F0F0F0Fu, H);
+  b[3] = w5_dword<3>((w.y >> 4) & 0x0F0F0F0Fu, H);
+  b[4] = w5_dword<4>(w.z & 0x0F0F0F0Fu, H);
+  b[5] = w5_dword<5>((w.z >> 4) & 0x0F0F0F0Fu, H);
+  b[6] = w5_dword<6>(w.w & 0x0F0F0F0Fu, H);
+  b[7] = w5_dword<7>((w.w >> 4) & 0x0F0F0F0Fu, H);
+  return b;
+}
+
+// The weight operand of one fragment: int4 nibbles, or nibbles plus the fifth-bit word.
+template <bool kW5>
+__device__ __forceinline__ v8i weight_operand(const u32x4& w, uint32_t H) {
+  if constexpr (kW5) return unpack_codes5(w, H);
+  else return unpack_codes(w);
 }
 
 // {512*sc, zero-point factor} from one SZ word (sc in the low half, zsc in the high half). The
