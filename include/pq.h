@@ -224,6 +224,26 @@ int pq_gemm_prepared(const uint8_t* a_d, const float* asg_d, const float* rs_d, 
                      int64_t ldy, void* ws_d, size_t ws_bytes, pq_stream_t stream);
 
 /*
+ * The gated feed-forward pair in one launch (device): the products with the gate and up columns of a merged
+ * projection, the activation and the product. With g and u pq_gemm's sums before their rounding to bf16,
+ *   h[m, f] = fl( act(g[m, f]) * u[m, f] ),  g from column f, u from column F + f,  0 <= f < F,
+ * act = silu (g sigmoid(g)) or gelu in its tanh form; one rounding, to the type of h. The f16 h is what the
+ * prologue of the next projection takes.
+ *
+ * a_d, asg_d, rs_d   as for pq_gemm: P = 1, the two projections share one rotation, or P = 2, partition 0 the
+ *                    gate's and partition 1 the up projection's (PQ_ERR_PARTITION otherwise).
+ * wpk_d, sz_d        from pq_pack_weights for N = 2 F columns, gate columns first. F % 16 == 0.
+ * act                enum pq_act.
+ * h_d                out f16 or bf16 (h_type) [M, ldh], ldh even and >= F, 4-byte aligned.
+ * ws_d, ws_bytes     as for pq_gemm at N = 2 F (none at M <= 16); prepared != 0: ws_d holds what
+ *                    pq_rotate_quant_for_gemm wrote for these a_d, asg_d and rs_d, as for pq_gemm_prepared.
+ */
+enum pq_act { PQ_ACT_SILU = 0, PQ_ACT_GELU = 1 };
+int pq_gemm_glu(const uint8_t* a_d, const float* asg_d, const float* rs_d, int M, int K, int P, const void* wpk_d,
+                const uint16_t* sz_d, int F, int act, uint16_t* h_d, int64_t ldh, int h_type, void* ws_d,
+                size_t ws_bytes, int prepared, pq_stream_t stream);
+
+/*
  * pq_gemm without a workspace, for callers that cannot allocate device memory (code under HIP graph
  * capture, tight serving loops, harnesses that forbid hipMalloc). Same arguments, arithmetic,
  * kernels and results as pq_gemm, minus ws_d/ws_bytes: at M > 16 the zero-point operand and the

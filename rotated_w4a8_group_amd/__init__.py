@@ -12,6 +12,7 @@ Calls (same names as the C entry points, without the ``pq_`` prefix):
 * ``rotate_quant(x, rec, cs)``               device; -> (A, ASG, RS)
 * ``rotate(x, rec, cs)``                     device; -> rotated rows of x's type, not quantised
 * ``gemm(A, ASG, RS, wpk, sz, N, pb1, pb2)`` device; -> y bf16
+* ``gemm_glu(A, ASG, RS, wpk, sz, F)``       device; gate | up projection -> act(gate) * up, f16 or bf16
 * ``matvec(x, wpk, sz, N, pb1, pb2)``        device; 16-bit rows (at most 16) -> y of their type
 * ``block_norms(x, residual, ...)``           device; -> (new residual, normalised row): the norms before
   and after a block with its gate and residual scale
@@ -54,6 +55,7 @@ SIGNATURES = {
     "pq_matvec": (_I, [_P, _I64, _I, _I, _I, _I, _P, _P, _I, _I, _I, _P, _I64, _I, _P]),
     "pq_rotate_quant_for_gemm": (_I, [_P, _I64, _I, _I, _I, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "pq_gemm_prepared": (_I, [_P, _P, _P, _I, _I, _I, _P, _P, _I, _I, _I, _P, _I64, _P, _SZ, _P]),
+    "pq_gemm_glu": (_I, [_P, _P, _P, _I, _I, _I, _P, _P, _I, _I, _P, _I64, _I, _P, _SZ, _I, _P]),
     "pq_gemm_noalloc_max_scratch_bytes": (_SZ, []),
     "pq_gemm_noalloc": (_I, [_P, _P, _P, _I, _I, _I, _P, _P, _I, _I, _I, _P, _I64, _P]),
     "pq_rotate_quant_tok": (_I, [_P, _I64, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
@@ -485,6 +487,56 @@ def gemm_prepared(A, ASG, RS, wpk, sz, N, pb1=NO_BOUNDARY, pb2=NO_BOUNDARY, out=
     import torch
     return _gemm_common("pq_gemm_prepared", A, ASG, RS, wpk, sz, N, pb1, pb2, out, workspace, stream,
                         a_dtype=torch.uint8, prepared=True)
+
+
+GLU_ACTS = {"silu": 0, "gelu": 1}
+
+
+def gemm_glu(A, ASG, RS, wpk, sz, F, act="silu", out=None, dtype=None, workspace=None, prepared=False, stream=None):
+    """The gated feed-forward pair in one launch: ``h = act(g) * u`` of ``gemm``'s merged gate | up projection (wpk, sz
+    from pack_weights of N = 2 F columns, gate first), g and u not rounded in between. A u8 [P, M, K], ASG/RS f32
+    [P, M, G] with P = 1 (one rotation for both) or 2 (the gate's, the up projection's) -> h [M, F] of ``dtype`` (f16 by
+    default, what the next prologue takes, or bf16), or into ``out``, a [M, ldh >= F] view with unit column stride.
+    act "silu" or "gelu" (tanh form). workspace: gemm_workspace_bytes(M, 2 F, K) bytes; prepared: it holds
+    what ``rotate_quant_for_gemm`` wrote for these A, ASG and RS."""
+    import torch
+    if not isinstance(A, torch.Tensor) or A.dim() != 3:
+        raise ValueError("A: expected a [P, M, K] tensor")
+    P, M, K = A.shape
+    if K == 0 or K % GROUP:
+        raise ValueError(f"A: K={K} must be a positive multiple of {GROUP}")
+    G = K // GROUP
+    code = GLU_ACTS.get(act)
+    if code is None:
+        raise ValueError(f"act: {act!r}, expected one of {', '.join(GLU_ACTS)}")
+    L = lib()
+    need = L.pq_packed_weight_bytes(K, 2 * F) if F % 16 == 0 else 0
+    if need == 0:
+        raise ValueError(f"F={F}: must be a positive multiple of 16")
+    specs = [(A, "A", torch.uint8, (P, M, K)), (ASG, "ASG", torch.float32, (P, M, G)), (RS, "RS", torch.float32, (P, M, G)),
+             (wpk, "wpk", torch.uint8, (need,)), (sz, "sz", torch.float16, (G, 2 * F, 2))]
+    ws_bytes = L.pq_gemm_workspace_bytes(M, 2 * F, K)
+    if workspace is not None:
+        specs.append((workspace, "workspace", torch.uint8, ws_bytes))
+    elif prepared and ws_bytes:
+        raise ValueError("workspace: with prepared, the call reads the workspace rotate_quant_for_gemm filled")
+    rows = []
+    if out is not None:
+        if not isinstance(out, torch.Tensor) or out.dim() != 2 or out.shape[0] != M or out.shape[1] < F:
+            raise ValueError(f"out: expected a f16 or bf16 [{M}, >= {F}] tensor")
+        if dtype is not None and out.dtype != dtype:
+            raise TypeError(f"out: {out.dtype}, dtype says {dtype}")
+        rows.append((out, "out", out.dtype, (M, out.shape[1])))
+    ht = _type_code(out.dtype if out is not None else dtype or torch.float16, "out", ("float16", "bfloat16"))
+    _validate(specs, rows=rows)
+    if out is None:
+        out = _new((M, F), dtype or torch.float16, A.device, stream)
+    if workspace is None and ws_bytes:
+        workspace = _new((ws_bytes,), torch.uint8, A.device, stream)
+    _launch("pq_gemm_glu", A.device, stream, A.data_ptr(), ASG.data_ptr(), RS.data_ptr(), M, K, P, wpk.data_ptr(),
+            sz.data_ptr(), F, code, out.data_ptr(), _pitch(out), ht, _addr(workspace),
+            workspace.numel() if workspace is not None else 0, 1 if prepared else 0)
+    return out
 
 
 def gemm_noalloc(A, ASG, RS, wpk, sz, N, pb1=NO_BOUNDARY, pb2=NO_BOUNDARY, out=None, stream=None):

@@ -29,6 +29,7 @@ SOURCES = [
     ("pq_norms.hip", []),
     # matrix-core results land in VGPRs (the fold reads them there; no AGPR copies)
     ("pq_matvec.hip", ["-mllvm", "-amdgpu-mfma-vgpr-form"]),
+    ("pq_glu.hip", ["-mllvm", "-amdgpu-mfma-vgpr-form"]),
     ("pq_gemm.hip", ["-mllvm", "-amdgpu-mfma-vgpr-form"]),
 ]
 
@@ -43,7 +44,7 @@ def hipcc() -> str:
 def build(verbose: bool = False) -> str:
     cc = hipcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
-    objs = []
+    objs, jobs = [], []
     for src, extra in SOURCES:
         obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
         lang = ["-x", "hip"]
@@ -51,8 +52,11 @@ def build(verbose: bool = False) -> str:
                                                        os.path.join(CSRC, src), "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
-        subprocess.run(cmd, check=True)
+        jobs.append((cmd, subprocess.Popen(cmd)))
         objs.append(obj)
+    failed = [cmd for cmd, job in jobs if job.wait() != 0]   # waits for every one
+    if failed:
+        raise subprocess.CalledProcessError(1, failed[0])
     tmp = OUT + ".tmp"
     cmd = [cc, "-shared", "-fPIC", f"--offload-arch={ARCH}"] + objs + ["-o", tmp]
     if verbose:

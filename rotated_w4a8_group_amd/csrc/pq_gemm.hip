@@ -209,6 +209,13 @@ __global__ void zpe_act_kernel(const float* __restrict__ ASG, const float* __res
   zpa[idx] = u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
 }
 
+void zero_point_operands(const float* asg, const float* rs, int M, int G, int P, void* ws, int ws_parts, void* stream) {
+  const int64_t zt = static_cast<int64_t>(P) * ((M + 15) / 16) * zpe_chunks(G) * 64;
+  float* asgt = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + zpe_act_bytes(M, G, ws_parts));
+  hipLaunchKernelGGL(zpe_act_kernel<false>, dim3(static_cast<unsigned>((zt + 255) / 256)), dim3(256), 0,
+                     static_cast<hipStream_t>(stream), asg, rs, M, G, P, static_cast<u32x4*>(ws), asgt);
+}
+
 // Per-token scales broadcast to every group, [P][M][G], for the decode kernel.
 __global__ void tok_expand_kernel(const float* __restrict__ AS, int PM, int G, float* __restrict__ asg) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;

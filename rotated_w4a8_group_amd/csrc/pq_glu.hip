@@ -1,0 +1,298 @@
+// The gated feed-forward pair (pq_gemm_glu): h = act(x Wg) * (x Wu) in one launch, for the merged
+// projection gate | up that pq_pack_weights lays out (N = 2 F columns), from the prologue's e4m3 codes.
+// The products, the fold and the zero point are the GEMM's (pq_gemm.hip); what is new is that one
+// workgroup takes the gate and the up columns of the same outputs, so that both sums meet in binary32
+// registers and neither projection is written to memory, read back or rounded in between. The weights
+// need no layout of their own: a column strip is addressed where it lies.
+//
+// M <= 16: the weight stream bounds it. One 8-wave workgroup per CU takes a contiguous range of output
+// columns (an even number, so that every CU streams the same bytes to within 2 of about 34 columns) and
+// both projections' tiles of that range; the waves split the groups and stream them through private LDS
+// rings, as the decode GEMM does.
+// M > 16: the prefill tile with its column strips alternating gate and up (pq_prefill.h); the matrix
+// cores and the fold bound it, as they do the GEMM.
+#include "pq_device.h"
+#include "pq_gemm_device.h"
+#include "pq_internal.h"
+#include "pq_prefill.h"
+
+namespace pq {
+
+// ---------------------------------------------------------------------------------------
+// M <= 16
+constexpr int kGdWaves = 8;
+constexpr int kGdRingBytes = 20480;                  // per wave
+constexpr int kGdLds = kGdWaves * kGdRingBytes;
+
+// NT tiles of each projection, MA activation rows held (8 when M <= 8, else 16) of PA partitions
+template <int NT, int MA, int PA>
+struct GluSlot {
+  static constexpr int kOffA = 2 * NT * 1024;                   // [PA][MA rows][128 B]
+  static constexpr int kOffSz = kOffA + PA * MA * 128;          // [gate, up][16 NT] words
+  static constexpr int kOffSc = kOffSz + 2 * NT * 64;           // [PA][16 asg, 16 rs]
+  static constexpr int kBytes = kOffSc + PA * 128;
+  static constexpr int kDepth = kGdRingBytes / kBytes > 8 ? 8 : kGdRingBytes / kBytes;
+  static constexpr int kLoads = 2 * NT + PA * (MA / 8) + 2 + 2 * PA;
+  static_assert(kDepth >= 2 && (kDepth - 1) * kLoads <= 63, "ring");
+};
+
+// The most tiles of a projection that a range may touch for its slot to fit the ring twice, and the most
+// columns that touch no more wherever an even start lies.
+constexpr int glu_max_tiles(int MA, int PA) { return MA * PA == 8 ? 4 : MA * PA == 16 ? 3 : 2; }
+constexpr int glu_max_columns(int MA, int PA) { return 16 * (glu_max_tiles(MA, PA) - 1) + 2; }
+
+template <int NT, int MR, int MA, int PA>
+__device__ __forceinline__ void glu_decode_body(
+    const uint8_t* __restrict__ A, const float* __restrict__ ASG, const float* __restrict__ RS, int M, int K,
+    const u32x4* __restrict__ wpk, const uint32_t* __restrict__ sz, int F, int c0, int c1, int act,
+    uint16_t* __restrict__ h, int64_t ldh, bool out_bf16, uint8_t* smem) {
+  using S = GluSlot<NT, MA, PA>;
+  constexpr int D = S::kDepth;
+  const int G = K >> 7;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 15, kq = lane >> 4;
+  const int tfirst = c0 >> 4, n0 = 16 * tfirst;
+  const int g0 = (G * wave) / kGdWaves, g1 = (G * (wave + 1)) / kGdWaves;
+
+  // Sources as in the decode GEMM: a scalar base per group and a fixed lane offset; lanes of columns
+  // outside [c0, c1) load no codes (every tile keeps at least 2 columns, so every load is issued).
+  const uint8_t* wbase = reinterpret_cast<const uint8_t*>(wpk) + static_cast<size_t>(tfirst) * G * 1024;
+  const size_t up = static_cast<size_t>(F / 16) * G * 1024;     // from a gate tile to its up tile
+  bool won[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int n = n0 + 16 * t + col;
+    won[t] = n >= c0 && n < c1;
+  }
+  const int ar0 = min(lane >> 3, M - 1), ar1 = min((lane >> 3) + 8, M - 1);
+  const uint32_t aoff0 = static_cast<uint32_t>(ar0 * K + 16 * (lane & 7));
+  const uint32_t aoff1 = static_cast<uint32_t>(ar1 * K + 16 * (lane & 7));
+  const size_t MG = static_cast<size_t>(M) * G;
+  const int srow = lane & 15;
+  const bool as_on = lane < 16 && srow < M, rs_on = lane >= 16 && lane < 32 && srow < M;
+  const uint32_t soff = static_cast<uint32_t>(4 * (srow < M ? srow : 0) * G);
+
+  uint8_t* ringp = smem + wave * kGdRingBytes;
+  const uint32_t ring = lds_addr(ringp);
+  auto issue = [&](int g, int slot) {
+    const uint32_t sb = ring + slot * S::kBytes;
+    const uint8_t* wg = wbase + static_cast<size_t>(g) * 1024;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+      if (won[t]) {
+        lds_dma16_s(wg + static_cast<size_t>(t) * G * 1024, 16 * lane, sb + t * 1024);
+        lds_dma16_s(wg + up + static_cast<size_t>(t) * G * 1024, 16 * lane, sb + (NT + t) * 1024);
+      }
+    const uint32_t* zg = sz + static_cast<size_t>(g) * 2 * F + n0;
+    if (lane < 16 * NT) {
+      lds_dma4_s(zg, 4 * lane, sb + S::kOffSz);
+      lds_dma4_s(zg + F, 4 * lane, sb + S::kOffSz + NT * 64);
+    }
+#pragma unroll
+    for (int p = 0; p < PA; ++p) {
+      const uint8_t* ag = A + static_cast<size_t>(p) * M * K + 128 * static_cast<size_t>(g);
+      lds_dma16_s(ag, aoff0, sb + S::kOffA + p * MA * 128);
+      if constexpr (MA == 16) lds_dma16_s(ag, aoff1, sb + S::kOffA + p * MA * 128 + 1024);
+      if (as_on) lds_dma4_s(ASG + p * MG + g, soff, sb + S::kOffSc + p * 128);
+      if (rs_on) lds_dma4_s(RS + p * MG + g, soff, sb + S::kOffSc + p * 128);
+    }
+  };
+  const int ng = g1 - g0;
+  for (int i = 0; i < D - 1 && i < ng; ++i) issue(g0 + i, i);
+
+  v4f acc[2][NT];
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[s][t] = v4f{0.f, 0.f, 0.f, 0.f};
+  const int arow = (lane & 15) & (MA - 1);
+  int slot = 0;
+  for (int g = g0; g < g1; ++g) {
+    if (g + D - 1 < g1) {
+      issue(g + D - 1, slot == 0 ? D - 1 : slot - 1);
+      wait_vm<(D - 1) * S::kLoads>();   // group g has landed; D - 1 groups remain in flight
+    } else {
+      wait_vm<0>();
+    }
+    const uint8_t* sp = ringp + slot * S::kBytes;
+    v8i av[PA];
+    v4f as[PA], rs[PA];
+#pragma unroll
+    for (int p = 0; p < PA; ++p) {
+      const uint8_t* ap = sp + S::kOffA + p * MA * 128 + arow * 128 + 32 * kq;
+      const u32x4 a0 = *reinterpret_cast<const u32x4*>(ap);
+      const u32x4 a1 = *reinterpret_cast<const u32x4*>(ap + 16);
+      av[p] = v8i{(int)a0.x, (int)a0.y, (int)a0.z, (int)a0.w, (int)a1.x, (int)a1.y, (int)a1.z, (int)a1.w};
+      as[p] = *reinterpret_cast<const v4f*>(sp + S::kOffSc + p * 128 + 16 * kq);
+      rs[p] = *reinterpret_cast<const v4f*>(sp + S::kOffSc + p * 128 + 64 + 16 * kq);
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int p = PA == 1 ? 0 : s;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const u32x4 bw = *reinterpret_cast<const u32x4*>(sp + (s * NT + t) * 1024 + 16 * lane);
+        const float2 f = sz_factors<false>(*reinterpret_cast<const uint32_t*>(sp + S::kOffSz + s * NT * 64 + 4 * (16 * t + col)));
+        const v4f T = mfma_fp8(av[p], unpack_codes(bw));
+#pragma unroll
+        for (int i = 0; i < MR; ++i) acc[s][t][i] += as[p][i] * (f.x * T[i] - f.y * rs[p][i]);
+      }
+    }
+    slot = slot + 1 == D ? 0 : slot + 1;
+  }
+
+  __syncthreads();   // every ring has drained: the reduction reuses that LDS
+  constexpr int W = 16 * NT;
+  float* sred = reinterpret_cast<float*>(smem);   // [waves][16 rows][gate, up][16 NT]
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < MR; ++i) sred[((wave * 16 + 4 * kq + i) * 2 + s) * W + 16 * t + col] = acc[s][t][i];
+  __syncthreads();
+  const int half = (c1 - c0) >> 1, pairs = M * half;   // c0, c1 and ldh even: 4-byte stores
+  for (int idx = tid; idx < pairs; idx += 64 * kGdWaves) {
+    const int m = idx / half, c = c0 - n0 + 2 * (idx % half);
+    float v[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+    for (int w = 0; w < kGdWaves; ++w)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        v[s][0] += sred[((w * 16 + m) * 2 + s) * W + c];
+        v[s][1] += sred[((w * 16 + m) * 2 + s) * W + c + 1];
+      }
+    const float h0 = glu_value(v[0][0], v[1][0], act), h1 = glu_value(v[0][1], v[1][1], act);
+    *reinterpret_cast<uint32_t*>(h + static_cast<size_t>(m) * ldh + n0 + c) = out_bf16 ? bf16x2_rn(h0, h1) : f16x2_rn(h0, h1);
+  }
+}
+
+// F / 2 column pairs dealt out evenly over gridDim.x ranges; consecutive ranges go to one XCD, so that a line
+// shared by neighbours is fetched once into its L2.
+template <int MR, int MA, int PA>
+__global__ __launch_bounds__(64 * kGdWaves, 1) void glu_decode_kernel(
+    const uint8_t* __restrict__ A, const float* __restrict__ ASG, const float* __restrict__ RS, int M, int K,
+    const u32x4* __restrict__ wpk, const uint32_t* __restrict__ sz, int F, int act, uint16_t* __restrict__ h, int64_t ldh,
+    int out_bf16) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kGdLds];
+  const int b = blockIdx.x, W = gridDim.x;
+  const int r = W % 8 == 0 ? (b % 8) * (W / 8) + b / 8 : b;
+  const int base = (F / 2) / W, extra = (F / 2) % W;
+  const int c0 = 2 * (r * base + min(r, extra)), c1 = c0 + 2 * (base + (r < extra));
+  const int nt = ((c1 - 1) >> 4) - (c0 >> 4) + 1;
+  constexpr int kMax = glu_max_tiles(MA, PA);
+  if (nt == 1) glu_decode_body<1, MR, MA, PA>(A, ASG, RS, M, K, wpk, sz, F, c0, c1, act, h, ldh, out_bf16 != 0, smem);
+  else if (nt == 2) glu_decode_body<2, MR, MA, PA>(A, ASG, RS, M, K, wpk, sz, F, c0, c1, act, h, ldh, out_bf16 != 0, smem);
+  if constexpr (kMax >= 3)
+    if (nt == 3) glu_decode_body<3, MR, MA, PA>(A, ASG, RS, M, K, wpk, sz, F, c0, c1, act, h, ldh, out_bf16 != 0, smem);
+  if constexpr (kMax >= 4)
+    if (nt == 4) glu_decode_body<4, MR, MA, PA>(A, ASG, RS, M, K, wpk, sz, F, c0, c1, act, h, ldh, out_bf16 != 0, smem);
+}
+
+// ---------------------------------------------------------------------------------------
+// M > 16
+template <int PA>
+__global__ __launch_bounds__(512, 1) void glu_prefill_kernel(
+    const uint8_t* __restrict__ A, const float* __restrict__ ASGT, int M, int K, const u32x4* __restrict__ wpk,
+    const u32x4* __restrict__ zpe, const u32x4* __restrict__ zpa, const float* __restrict__ s9img, int F, int act,
+    uint16_t* __restrict__ h, int64_t ldh, int out_bf16, PrefillMap map, bool vec16) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kPfLds];
+  const int b = blockIdx.x;
+  const int bm = PA == 1 ? 256 : 128;
+  const bool piece = b >= map.full;
+  const int big = piece ? map.full + (b - map.full) / map.split : b;
+  const int r = piece ? (b - map.full) % map.split : 0;
+  const int t = xcd_tile(big, map.ntiles);
+  int trow, tcol;
+  tile_rc(t, map.tiles_m, map.tiles_n, trow, tcol);
+  int m0 = trow * bm, n0 = tcol * 256;   // n0: gate and up columns together, twice the output column
+  const int split = piece ? map.split : 1;
+  if (split == 2) m0 += (bm / 2) * r;
+  else if (split == 4) { m0 += 128 * (r & 1); n0 += 128 * (r >> 1); }
+  else if (split == 8) { m0 += 64 * (r & 3); n0 += 128 * (r >> 2); }
+  if (m0 >= M || n0 >= 2 * F) return;   // a piece wholly past the matrix
+#define PQ_GLU_TILE(TM, TN)                                                                                          \
+  prefill_tile<TM, TN, 2, 4, false, false, false, kPfStages, PA>(A, ASGT, M, K, wpk, nullptr, zpe, zpa, s9img, 2 * F, 0, m0, \
+                                                                 n0, h, ldh, vec16, smem, act, out_bf16 != 0)
+  if constexpr (PA == 1) {
+    if (split == 1) PQ_GLU_TILE(256, 256);
+    else if (split == 2) PQ_GLU_TILE(128, 256);
+    else if (split == 4) PQ_GLU_TILE(128, 128);
+    else PQ_GLU_TILE(64, 128);
+  } else {
+    if (split == 1) PQ_GLU_TILE(128, 256);
+    else PQ_GLU_TILE(64, 256);
+  }
+#undef PQ_GLU_TILE
+}
+
+}  // namespace pq
+
+extern "C" {
+
+int pq_gemm_glu(const uint8_t* a_d, const float* asg_d, const float* rs_d, int M, int K, int P, const void* wpk_d,
+                const uint16_t* sz_d, int F, int act, uint16_t* h_d, int64_t ldh, int h_type, void* ws_d,
+                size_t ws_bytes, int prepared, pq_stream_t stream) {
+  using namespace pq;
+  clear_error();
+  const char* what = "pq_gemm_glu";
+  if (M < 0) return set_error(PQ_ERR_SHAPE, "%s: M=%d < 0", what, M);
+  if (K <= 0 || K % PQ_GROUP || K > (1 << 24)) return set_error(PQ_ERR_SHAPE, "%s: K=%d must be a positive multiple of 128", what, K);
+  if (F <= 0 || F % 16 || F > (1 << 23)) return set_error(PQ_ERR_SHAPE, "%s: F=%d must be a positive multiple of 16", what, F);
+  if (ldh < F || (ldh & 1)) return set_error(PQ_ERR_SHAPE, "%s: ldh=%lld must be even and >= F=%d", what, static_cast<long long>(ldh), F);
+  if (act != PQ_ACT_SILU && act != PQ_ACT_GELU) return set_error(PQ_ERR_SHAPE, "%s: act=%d", what, act);
+  if (h_type != PQ_F16 && h_type != PQ_BF16) return set_error(PQ_ERR_SHAPE, "%s: h_type=%d must be f16 or bf16", what, h_type);
+  if (P != 1 && P != 2) return set_error(PQ_ERR_PARTITION, "%s: P=%d must be 1 or 2 (the gate's rotation and the up projection's)", what, P);
+  const size_t need = pq_gemm_workspace_bytes(M, 2 * F, K);
+  if (ws_bytes < need) return set_error(PQ_ERR_WORKSPACE, "%s: workspace too small", what);
+  if (M == 0) return PQ_OK;
+  if (!a_d || !asg_d || !rs_d || !wpk_d || !sz_d || !h_d) return set_error(PQ_ERR_NULL, "%s: NULL pointer", what);
+  if (need && !ws_d) return set_error(PQ_ERR_NULL, "%s: NULL workspace", what);
+  if (!aligned(a_d, 16) || !aligned(asg_d, 4) || !aligned(rs_d, 4) || !aligned(wpk_d, 16) || !aligned(sz_d, 4) ||
+      !aligned(h_d, 4) || !aligned(ws_d, 16))
+    return set_error(PQ_ERR_ALIGN, "%s: misaligned pointer", what);
+  // lane offsets into a partition's codes and scales are 32-bit
+  if (static_cast<int64_t>(M) * K > 0x7FFFFFFF) return set_error(PQ_ERR_SHAPE, "%s: M * K too large for one call (split the rows)", what);
+  const int G = K / PQ_GROUP, cus = cu_count();
+  const u32x4* wpk = static_cast<const u32x4*>(wpk_d);
+  const size_t N = 2 * static_cast<size_t>(F);
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const int out_bf16 = h_type == PQ_BF16;
+  if (M <= 16) {
+    const int MA = M <= 8 ? 8 : 16, most = glu_max_columns(MA, P);
+    // the fewest whole rounds of one range per CU whose ranges are short enough
+    const int64_t rounds = (static_cast<int64_t>(F) + static_cast<int64_t>(cus) * most - 1) / (static_cast<int64_t>(cus) * most);
+    const int64_t ranges = std::min<int64_t>(F / 2, rounds * cus);
+#define PQ_GLU_DECODE(MR, MA, PA)                                                                                     \
+  hipLaunchKernelGGL((glu_decode_kernel<MR, MA, PA>), dim3(static_cast<unsigned>(ranges)), dim3(64 * kGdWaves), 0, s, a_d, \
+                     asg_d, rs_d, M, K, wpk, reinterpret_cast<const uint32_t*>(sz_d), F, act, h_d, ldh, out_bf16)
+    if (P == 1) {
+      if (M == 1) PQ_GLU_DECODE(1, 8, 1);
+      else if (M <= 8) PQ_GLU_DECODE(4, 8, 1);
+      else PQ_GLU_DECODE(4, 16, 1);
+    } else {
+      if (M == 1) PQ_GLU_DECODE(1, 8, 2);
+      else if (M <= 8) PQ_GLU_DECODE(4, 8, 2);
+      else PQ_GLU_DECODE(4, 16, 2);
+    }
+#undef PQ_GLU_DECODE
+    return launch_status(what);
+  }
+  if (static_cast<int64_t>((M + 127) / 128) * ((2 * F + 127) / 128) * 8 > 0x7FFFFFFF)
+    return set_error(PQ_ERR_SHAPE, "%s: problem too large", what);
+  const PrefillMap map = prefill_map(M, 2 * F, P == 1 ? kPfWide : kPfPair, cus);
+  const int64_t grid = static_cast<int64_t>(map.full) + static_cast<int64_t>(map.ntiles - map.full) * map.split;
+  const uint8_t* wb = static_cast<const uint8_t*>(wpk_d);
+  const u32x4* zpe = reinterpret_cast<const u32x4*>(wb + static_cast<size_t>(K) * N / 2);
+  const float* s9img = reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(zpe) + (N / 16) * zpe_chunks(G) * 1024);
+  if (!prepared) zero_point_operands(asg_d, rs_d, M, G, P, ws_d, PQ_MAX_PARTITIONS, s);
+  const float* asgt = reinterpret_cast<const float*>(static_cast<const uint8_t*>(ws_d) + zpe_act_bytes(M, G, PQ_MAX_PARTITIONS));
+  const bool vec16 = aligned(h_d, 16) && ldh % 8 == 0;
+  auto kern = P == 1 ? glu_prefill_kernel<1> : glu_prefill_kernel<2>;
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(grid)), dim3(64 * kPfWaves), 0, s, a_d, asgt, M, K, wpk, zpe,
+                     static_cast<const u32x4*>(ws_d), s9img, F, act, h_d, ldh, out_bf16, map, vec16);
+  return launch_status(what);
+}
+
+}  // extern "C"

@@ -28,4 +28,7 @@ int check_partitions(int P, int pb1, int pb2, int N);
 size_t zpe_act_bytes(int M, int G, int P);
 size_t asgt_bytes(int M, int G, int P);
 
+// Fills the prefill GEMM's workspace from ASG and RS (P partitions, laid out for ws_parts).
+void zero_point_operands(const float* asg, const float* rs, int M, int G, int P, void* ws, int ws_parts, void* stream);
+
 }  // namespace pq

@@ -3,6 +3,7 @@
 
 #include "pq_device.h"
 #include "pq_gemm_device.h"
+#include "pq_internal.h"
 
 namespace pq {
 
@@ -31,24 +32,45 @@ constexpr int kPfStages = 3;
 constexpr int kPfWaves = 8;
 constexpr int kPfLds = kPfStages * 51200;   // the 256x256 ring (the largest)
 
-template <int TM, int TN, int WM, int WN, bool kTok = false, bool kW5 = false, int S = kPfStages>
+// kGlu: 0 for a plain product. 1 or 2: the gated pair of pq_gemm_glu with that many partitions. The
+// weights are then gate | up, N = 2 F columns; the tile's TN columns are TN/2 of each, interleaved by
+// 16-column strips (even strips gate, odd strips up, pf_strip), so that a lane holds the gate and up
+// values of the same output in neighbouring fragments and the epilogue writes act(gate) * up. With two
+// partitions the stage holds both partitions' activation rows and scales.
+template <int TM, int TN, int WM, int WN, bool kTok = false, bool kW5 = false, int S = kPfStages, int kGlu = 0>
 struct PfTile {
+  static constexpr int PA = kGlu == 2 ? 2 : 1;                 // activation partitions in a stage
   static constexpr int MF = TM / WM / 16, NF = TN / WN / 16;   // fragments per wave
   static constexpr int kOffA = 0;                              // [TM rows][8 chunks][16 B], chunks swizzled
-  static constexpr int kOffB = TM * 128;                       // [TN/16 tiles][64 lanes][16 B]
+  static constexpr int kOffB = PA * TM * 128;                       // [TN/16 tiles][64 lanes][16 B]
   static constexpr int kOffAsg = kOffB + TN * 64;              // [TM] f32
-  static constexpr int kOffS9 = kOffAsg + TM * 4;              // [TN] f32 column factors 512 sc
+  static constexpr int kOffS9 = kOffAsg + PA * TM * 4;              // [TN] f32 column factors 512 sc
   static constexpr int kOffH = kOffS9 + TN * 4;                // int5: [TN/16 tiles][64 lanes] u32
   static constexpr int kStage = (kOffH + (kW5 ? TN * 16 : 0) + 255) / 256 * 256;
-  static constexpr int nA = TM / 8, nB = TN / 16, nAs = kTok ? 0 : TM / 64, nS9 = TN / 64;
+  static constexpr int nA = PA * TM / 8, nB = TN / 16, nAs = kTok ? 0 : PA * TM / 64, nS9 = TN / 64;
   static constexpr int nH = kW5 ? TN / 16 : 0;
   static constexpr int nD = nA + nB + nAs + nS9 + nH;          // direct loads per group
   static constexpr int kPerWave = (nD + 3) / 4;                 // loads per wave of the issuing half
-  static constexpr int kOutStride = TN + 8;                    // bf16 per staged output row
+  static constexpr int kOutCols = kGlu ? TN / 2 : TN;
+  static constexpr int kOutStride = kOutCols + 8;              // 16-bit values per staged output row
   static_assert(WM * WN == kPfWaves && MF >= 1 && NF >= 1 && TM % 64 == 0 && TN % 64 == 0, "tile");
   static_assert(S >= 2 && S * kStage <= kPfLds && TM * kOutStride * 2 <= kPfLds, "LDS");
   static_assert(kPerWave <= 31, "vmcnt");
 };
+
+// The 16-column strip of the weights that strip j of a gated tile reads, h0 its first output column: past
+// F the last one, whose results are never stored.
+__device__ __forceinline__ int pf_strip(int h0, int j, int F) {
+  return min(h0 / 16 + (j >> 1), F / 16 - 1) + (j & 1 ? F / 16 : 0);
+}
+
+// act(g) * u for silu and gelu (tanh form): both are g * sigmoid(t), t = g or 2 sqrt(2/pi) (g + 0.044715 g^3).
+// exp and the reciprocal by the hardware's instructions (1 ulp each; the product t log2(e) rounds by
+// |t| 2^-24, 2^-18 at the t where sigmoid leaves binary32): far below the 16-bit rounding of the result.
+__device__ __forceinline__ float glu_value(float g, float u, int act) {
+  const float t = act == PQ_ACT_GELU ? g * __builtin_fmaf(0.0713548162726f * g, g, 1.59576912161f) : g;
+  return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504089f * t)) * u;
+}
 
 template <int N>
 __device__ __forceinline__ void wait_vm_lgkm_barrier() {
@@ -111,13 +133,15 @@ __device__ __forceinline__ void tile_rc(int t, int tiles_m, int tiles_n, int& ro
   }
 }
 
-template <int TM, int TN, int WM, int WN, bool kTok, bool kI8, bool kW5, int S = kPfStages>
+template <int TM, int TN, int WM, int WN, bool kTok, bool kI8, bool kW5, int S = kPfStages, int kGlu = 0>
 __device__ __forceinline__ void prefill_tile(
     const uint8_t* __restrict__ A, const float* __restrict__ ASGT, int M, int K,
     const u32x4* __restrict__ wpk, const uint32_t* __restrict__ hi, const u32x4* __restrict__ zpe,
     const u32x4* __restrict__ zpa, const float* __restrict__ s9img, int N, int p, int m0, int n0,
-    uint16_t* __restrict__ y, int64_t ldy, bool vec16, uint8_t* smem) {
-  using TL = PfTile<TM, TN, WM, WN, kTok, kW5, S>;
+    uint16_t* __restrict__ y, int64_t ldy, bool vec16, uint8_t* smem, int act = 0, bool out_bf16 = true) {
+  using TL = PfTile<TM, TN, WM, WN, kTok, kW5, S, kGlu>;
+  constexpr int PA = TL::PA;
+  const int F = N / 2, h0 = n0 / 2;   // gated pair: N = 2 F, the tile's first output column
   static_assert(S == 2 || S == 3, "the wait counts below cover rings of 2 and 3 stages");
   constexpr int D = S - 1;   // groups loaded ahead
   constexpr int MF = TL::MF, NF = TL::NF, PW = TL::kPerWave;
@@ -147,26 +171,27 @@ __device__ __forceinline__ void prefill_tile(
   for (int i = 0; i < PW; ++i) {
     const int d = ((wave & 3) + 4 * i) % TL::nD;
     if (d < TL::nA) {
-      const int r = 8 * d + (lane >> 3);                 // tile row; lane%8 = chunk slot
+      const int r = 8 * (PA == 1 ? d : d % (TM / 8)) + (lane >> 3);   // tile row; lane%8 = chunk slot
       const int row = min(m0 + r, M - 1);
-      sbase[i] = Ap;
+      sbase[i] = PA == 1 || d < TM / 8 ? Ap : Ap + static_cast<size_t>(M) * K;
       voff[i] = static_cast<uint32_t>(row * K + 16 * ((lane & 7) ^ (r & 7) ^ ((r >> 3) & 1)));
       step[i] = 128; dst[i] = TL::kOffA + d * 1024; wide[i] = true;
     } else if (d < TL::nA + TL::nB) {
       const int j = d - TL::nA;
-      const int tt = min(n0 / 16 + j, last_tile);
+      const int tt = kGlu ? pf_strip(h0, j, F) : min(n0 / 16 + j, last_tile);
       sbase[i] = reinterpret_cast<const uint8_t*>(wpk) + static_cast<size_t>(tt) * G * 1024;
       voff[i] = 16 * lane;
       step[i] = 1024; dst[i] = TL::kOffB + j * 1024; wide[i] = true;
     } else if (d < TL::nA + TL::nB + TL::nAs) {
       const int j = d - TL::nA - TL::nB;
-      sbase[i] = reinterpret_cast<const uint8_t*>(asgp);
-      voff[i] = static_cast<uint32_t>(min(m0 + 64 * j + lane, M - 1) * 4);
+      sbase[i] = reinterpret_cast<const uint8_t*>(PA == 1 || j < TM / 64 ? asgp : asgp + static_cast<size_t>(G) * M);
+      voff[i] = static_cast<uint32_t>(min(m0 + 64 * (PA == 1 ? j : j % (TM / 64)) + lane, M - 1) * 4);
       step[i] = static_cast<size_t>(M) * 4; dst[i] = TL::kOffAsg + j * 256; wide[i] = false;
     } else if (d < TL::nA + TL::nB + TL::nAs + TL::nS9) {
       const int j = d - TL::nA - TL::nB - TL::nAs;
       sbase[i] = reinterpret_cast<const uint8_t*>(s9img);
-      voff[i] = static_cast<uint32_t>(min(n0 + 64 * j + lane, N - 1) * 4);
+      voff[i] = kGlu ? static_cast<uint32_t>((16 * pf_strip(h0, 4 * j + (lane >> 4), F) + (lane & 15)) * 4)
+                     : static_cast<uint32_t>(min(n0 + 64 * j + lane, N - 1) * 4);
       step[i] = static_cast<size_t>(N) * 4; dst[i] = TL::kOffS9 + j * 256; wide[i] = false;
     } else {
       const int j = d - TL::nA - TL::nB - TL::nAs - TL::nS9;   // int5 fifth-bit words of tile j
@@ -189,7 +214,7 @@ __device__ __forceinline__ void prefill_tile(
   // TM/16 activation-side and TN/16 weight-side fragments, 1 KiB each, go to a stage at
   // f * 1024 (f = fragment) like one more group; this half's share: fragments (wave % 4) + 4 i.
   // The source of each is computed on the scalar unit when it is issued.
-  constexpr int NZ = TM / 16 + TN / 16, PWZ = (NZ + 3) / 4;
+  constexpr int ZA = PA * TM / 16, NZ = ZA + TN / 16, PWZ = (NZ + 3) / 4;
   static_assert(PWZ <= PW && NZ * 1024 <= TL::kStage, "zero-point chunks ride the group ring");
   const int KC = zpe_chunks(G), MT = (M + 15) / 16;
   auto zissue = [&](int stage, int c) {
@@ -198,9 +223,10 @@ __device__ __forceinline__ void prefill_tile(
     for (int i = 0; i < PWZ; ++i) {
       const int f = (wave & 3) + 4 * i;
       if (f < NZ) {
-        const uint8_t* src = (f < TM / 16)
-            ? reinterpret_cast<const uint8_t*>(zpa) + ((static_cast<size_t>(p) * MT + min(m0 / 16 + f, MT - 1)) * KC + c) * 1024
-            : reinterpret_cast<const uint8_t*>(zpe) + (static_cast<size_t>(min(n0 / 16 + f - TM / 16, last_tile)) * KC + c) * 1024;
+        const int fa = PA == 1 ? f : f % (TM / 16), fp = PA == 1 ? p : f / (TM / 16);
+        const uint8_t* src = (f < ZA)
+            ? reinterpret_cast<const uint8_t*>(zpa) + ((static_cast<size_t>(fp) * MT + min(m0 / 16 + fa, MT - 1)) * KC + c) * 1024
+            : reinterpret_cast<const uint8_t*>(zpe) + (static_cast<size_t>(kGlu ? pf_strip(h0, f - ZA, F) : min(n0 / 16 + f - ZA, last_tile)) * KC + c) * 1024;
         lds_dma16_s(src, 16 * lane, st + f * 1024);
       }
     }
@@ -254,34 +280,44 @@ __device__ __forceinline__ void prefill_tile(
     // fragment lane l: row l%16 of the 16-row block, k chunks 2(l/16) and 2(l/16)+1, swizzled
     const int arow = lane & 15, ac0 = 2 * (lane >> 4), asw = (arow & 7) ^ (arow >> 3);
     const int aoff0 = arow * 128 + 16 * (ac0 ^ asw), aoff1 = arow * 128 + 16 * ((ac0 + 1) ^ asw);
-    auto load_a = [&](int mf, v8i& a, float& as) {
-      const uint8_t* ap = st + TL::kOffA + (wm * MF + mf) * 2048;
+    auto load_a = [&](int mf, v8i& a, float& as, int pa) {
+      const uint8_t* ap = st + TL::kOffA + (wm * MF + mf + pa * (TM / 16)) * 2048;
       const u32x4 a0 = *reinterpret_cast<const u32x4*>(ap + aoff0);
       const u32x4 a1 = *reinterpret_cast<const u32x4*>(ap + aoff1);
       a = v8i{(int)a0.x, (int)a0.y, (int)a0.z, (int)a0.w, (int)a1.x, (int)a1.y, (int)a1.z, (int)a1.w};
-      if constexpr (!kTok) as = *reinterpret_cast<const float*>(st + TL::kOffAsg + (wm * MF * 16 + 16 * mf + arow) * 4);
+      if constexpr (!kTok) as = *reinterpret_cast<const float*>(st + TL::kOffAsg + (wm * MF * 16 + 16 * mf + arow + pa * TM) * 4);
     };
     // Row fragment mf's products are interleaved one for one with the folds of fragment mf-1
     // (acc += f T, f = asg * 512 sc: 8 VALU per product), so the matrix core and the vector ALU
     // work side by side; fragment mf+1's operands are read from LDS while mf computes, and the
     // weight codes are unpacked beside fragment 0's products.
     v4f Tb[2][NF];
-    v8i a[2];
-    float asb[2] = {0.f, 0.f};
-    load_a(0, a[0], asb[0]);
+    v8i a[2][PA];
+    float asb[2][PA];
+#pragma unroll
+    for (int pa = 0; pa < PA; ++pa) {
+      asb[0][pa] = asb[1][pa] = 0.f;
+      load_a(0, a[0][pa], asb[0][pa], pa);
+    }
 #pragma unroll
     for (int mf = 0; mf <= MF; ++mf) {
       // fragment mf-1's row scale is taken before the prefetch reuses its slot
       const int pm = mf - 1;
-      float as = 0.f;
-      if constexpr (!kTok) as = kI8 ? asb[pm & 1] * 0x1p-9f : asb[pm & 1];   // integer products carry no 2^-9
-      if (mf + 1 < MF) load_a(mf + 1, a[(mf + 1) & 1], asb[(mf + 1) & 1]);
+      float asp[PA];
+#pragma unroll
+      for (int pa = 0; pa < PA; ++pa) {
+        asp[pa] = 0.f;
+        if constexpr (!kTok) asp[pa] = kI8 ? asb[pm & 1][pa] * 0x1p-9f : asb[pm & 1][pa];   // integer products carry no 2^-9
+        if (mf + 1 < MF) load_a(mf + 1, a[(mf + 1) & 1][pa], asb[(mf + 1) & 1][pa], pa);
+      }
 #pragma unroll
       for (int nf = 0; nf < NF; ++nf) {
         if (mf == 0) bf[nf] = weight_operand<kW5>(braw[nf], hw[nf]);
-        if (mf < MF) Tb[mf & 1][nf] = group_product<kI8>(bf[nf], a[mf & 1]);
+        const int pa = PA == 1 ? 0 : nf & 1;   // gated pair of two partitions: odd strips are the up projection
+        if (mf < MF) Tb[mf & 1][nf] = group_product<kI8>(bf[nf], a[mf & 1][pa]);
         if (mf > 0) {
           const v4f& T = Tb[pm & 1][nf];
+          const float as = asp[pa];
           if constexpr (kTok) {
             // per-token scales: the row scale is applied once in the epilogue
             acc[pm][nf][0] = __builtin_fmaf(s9[nf].x, T[0], acc[pm][nf][0]);
@@ -311,14 +347,16 @@ __device__ __forceinline__ void prefill_tile(
     u32x4 zb[NF];
 #pragma unroll
     for (int nf = 0; nf < NF; ++nf)
-      zb[nf] = *reinterpret_cast<const u32x4*>(st + (TM / 16 + wn * NF + nf) * 1024 + lane * 16);
+      zb[nf] = *reinterpret_cast<const u32x4*>(st + (ZA + wn * NF + nf) * 1024 + lane * 16);
 #pragma unroll
     for (int mf = 0; mf < MF; ++mf) {
-      const u32x4 za = *reinterpret_cast<const u32x4*>(st + (wm * MF + mf) * 1024 + lane * 16);
+      u32x4 za[PA];
+#pragma unroll
+      for (int pa = 0; pa < PA; ++pa) za[pa] = *reinterpret_cast<const u32x4*>(st + (wm * MF + mf + pa * (TM / 16)) * 1024 + lane * 16);
 #pragma unroll
       for (int nf = 0; nf < NF; ++nf)
         acc[mf][nf] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, zb[nf]),
-                                                               __builtin_bit_cast(bf16x8, za), acc[mf][nf], 0, 0, 0);
+                                                               __builtin_bit_cast(bf16x8, za[PA == 1 ? 0 : nf & 1]), acc[mf][nf], 0, 0, 0);
     }
   }
 
@@ -331,6 +369,17 @@ __device__ __forceinline__ void prefill_tile(
   for (int mf = 0; mf < MF; ++mf) {
     float a = 1.0f;
     if constexpr (kTok) a = ASGT[static_cast<size_t>(p) * M + min(m0 + wm * MF * 16 + 16 * mf + (lane & 15), M - 1)];
+    if constexpr (kGlu != 0) {
+#pragma unroll
+      for (int nf = 0; nf < NF; nf += 2) {
+        float h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = glu_value(acc[mf][nf][i], acc[mf][nf + 1][i], act);
+        *reinterpret_cast<uint2*>(ot + (wm * MF * 16 + 16 * mf + (lane & 15)) * TL::kOutStride + wn * NF * 8 + 8 * nf + 4 * kq) =
+            out_bf16 ? make_uint2(bf16x2_rn(h[0], h[1]), bf16x2_rn(h[2], h[3])) : make_uint2(f16x2_rn(h[0], h[1]), f16x2_rn(h[2], h[3]));
+      }
+      continue;
+    }
 #pragma unroll
     for (int nf = 0; nf < NF; ++nf) {
       v4f v = acc[mf][nf];
@@ -340,13 +389,14 @@ __device__ __forceinline__ void prefill_tile(
     }
   }
   __syncthreads();
-  store_tile_rows<TM, TN, TL::kOutStride>(ot, y, ldy, m0, n0, M, N, vec16);
+  store_tile_rows<TM, TL::kOutCols, TL::kOutStride>(ot, y, ldy, m0, kGlu ? h0 : n0, M, kGlu ? F : N, vec16);
 }
 
 // Tile shapes of the prefill grid: 256x256 (pieces 128x256, 128x128, 64x128), or 128x128 (pieces
 // 64x128) when a partition boundary is not on a 256-column line. int5 whole 256x256 tiles run a
 // ring of two stages: the fifth-bit planes make a stage 54 KiB, and three do not fit in LDS.
-enum PfShape : int { kPfWide = 0, kPfNarrow = 1 };
+// The gated pair of two partitions: 128x256 tiles, whose stage holds two sets of activation rows (pieces 64x256).
+enum PfShape : int { kPfWide = 0, kPfNarrow = 1, kPfPair = 2 };
 struct PrefillMap {
   int tiles_m;   // whole tiles per tile column
   int tiles_n;   // whole tiles per tile row
@@ -369,7 +419,7 @@ inline PrefillMap prefill_map(int M, int N, int shape, int cus) {
   m.full = static_cast<int>(full);
   m.split = 1;
   if (rem > 0) {
-    static const int cands[2][3] = {{8, 4, 2}, {2, 0, 0}};
+    static const int cands[3][3] = {{8, 4, 2}, {2, 0, 0}, {2, 0, 0}};
     for (int i = 0; i < 3 && cands[shape][i]; ++i)
       if (rem * cands[shape][i] <= cus) { m.split = cands[shape][i]; break; }
   }
