@@ -141,19 +141,23 @@ def _validate(specs, rows=()):
     import torch
     # the usual call passes everything: one cheap look at each tensor, and the ordered checks below
     # only to name what is wrong
-    dev = None
+    dev, tensor = None, torch.Tensor
     for t, name, dtype, shape in specs:
-        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous() and
-                (t.shape == shape if isinstance(shape, tuple) else t.numel() >= shape) and
-                (dev is None or t.device == dev)):
+        if not (isinstance(t, tensor) and t.dtype is dtype and t.is_contiguous() and
+                (t.numel() >= shape if type(shape) is int else t.shape == shape)):
             break
-        dev = t.device
+        d = t.get_device()
+        if d < 0 or (dev is not None and d != dev):
+            break
+        dev = d
     else:
         for t, name, dtype, shape in rows:
-            if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.shape == shape and
-                    t.stride(1) == 1 and (dev is None or t.device == dev)):
+            if not (isinstance(t, tensor) and t.dtype is dtype and t.shape == shape and t.stride(1) == 1):
                 break
-            dev = t.device
+            d = t.get_device()
+            if d < 0 or (dev is not None and d != dev):
+                break
+            dev = d
         else:
             return
     for t, name, dtype, shape in list(specs) + list(rows):
@@ -231,24 +235,33 @@ def _new(shape, dtype, device, stream):
 def _launch(fn, device, stream, *args):
     """Calls the C entry point ``fn`` on the tensors' device, queued on ``stream`` or that device's current one."""
     import torch
+    f = getattr(_lib or lib(), fn)
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        handle = torch._C._cuda_getCurrentRawStream(device.index)   # current_stream(device).cuda_stream, without the object
     elif stream.device != device:
         raise ValueError(f"stream: on {stream.device}, the tensors are on {device}")
-    if torch.cuda.current_device() == device.index:
-        rc = getattr(lib(), fn)(*args, stream.cuda_stream)
+    else:
+        handle = stream.cuda_stream
+    if torch._C._cuda_getDevice() == device.index:
+        rc = f(*args, handle)
     else:
         with torch.cuda.device(device):
-            rc = getattr(lib(), fn)(*args, stream.cuda_stream)
+            rc = f(*args, handle)
     if rc != PQ_OK:
         _check(fn, rc)
 
 
-def _type_code(dtype, name, allowed):
-    """The pq_type of a torch dtype among ``allowed`` (names of torch dtypes)."""
-    code = {"torch.float16": 0, "torch.bfloat16": 1, "torch.float32": 2}.get(str(dtype))
-    if code is None or str(dtype)[6:] not in allowed:
-        raise TypeError(f"{name}: expected a tensor of {' or '.join(allowed)}, got {dtype}")
+_codes = {}
+
+
+def _type_code(dtype, name, allowed=2):
+    """The pq_type of a torch dtype: f16, bf16, and f32 where ``allowed`` is 3."""
+    if not _codes:
+        import torch
+        _codes.update({torch.float16: 0, torch.bfloat16: 1, torch.float32: 2})
+    code = _codes.get(dtype, 3)
+    if code >= allowed:
+        raise TypeError(f"{name}: expected a tensor of float16{', bfloat16 or float32' if allowed == 3 else ' or bfloat16'}, got {dtype}")
     return code
 
 
@@ -383,7 +396,7 @@ def rotate(x, rec, cs, out=None, stream=None):
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x: expected a [M, K] tensor")
     M, K = x.shape
-    xt = _type_code(x.dtype, "x", ("float16", "bfloat16"))
+    xt = _type_code(x.dtype, "x")
     P, specs = _prologue_specs(x, rec, cs, K)
     if out is not None:
         specs.append((out, "out", x.dtype, (P, M, K)))
@@ -449,7 +462,7 @@ def matvec(x, wpk, sz, N, pb1=NO_BOUNDARY, pb2=NO_BOUNDARY, out=None, dtype=None
     import torch
     if not isinstance(x, torch.Tensor) or x.dim() not in (2, 3):
         raise ValueError("x: expected a [P, M, K] or [M, K] tensor")
-    xt = _type_code(x.dtype, "x", ("float16", "bfloat16"))
+    xt = _type_code(x.dtype, "x")
     P, M, K = (1, *x.shape) if x.dim() == 2 else x.shape
     if K == 0 or K % GROUP:
         raise ValueError(f"x: K={K} must be a positive multiple of {GROUP}")
@@ -472,7 +485,7 @@ def matvec(x, wpk, sz, N, pb1=NO_BOUNDARY, pb2=NO_BOUNDARY, out=None, dtype=None
         if dtype is not None and out.dtype != dtype:
             raise TypeError(f"out: {out.dtype}, dtype says {dtype}")
         rows.append((out, "out", out.dtype, (M, out.shape[1])))
-    yt = _type_code(out.dtype if out is not None else dtype or x.dtype, "out", ("float16", "bfloat16"))
+    yt = _type_code(out.dtype if out is not None else dtype or x.dtype, "out")
     _validate(specs, rows=rows)
     if out is None:
         out = _new((M, N), dtype or x.dtype, x.device, stream)
@@ -527,7 +540,7 @@ def gemm_glu(A, ASG, RS, wpk, sz, F, act="silu", out=None, dtype=None, workspace
         if dtype is not None and out.dtype != dtype:
             raise TypeError(f"out: {out.dtype}, dtype says {dtype}")
         rows.append((out, "out", out.dtype, (M, out.shape[1])))
-    ht = _type_code(out.dtype if out is not None else dtype or torch.float16, "out", ("float16", "bfloat16"))
+    ht = _type_code(out.dtype if out is not None else dtype or torch.float16, "out")
     _validate(specs, rows=rows)
     if out is None:
         out = _new((M, F), dtype or torch.float16, A.device, stream)
@@ -656,14 +669,14 @@ def block_norms(x, residual, w_post=None, gate=None, w_pre=None, eps=1e-6, scale
     if not isinstance(residual, torch.Tensor):
         raise TypeError("residual: expected a tensor")
     M, K = x.shape
-    xt = _type_code(x.dtype, "x", ("float16", "bfloat16"))
-    rt = _type_code(residual.dtype, "residual", ("float16", "bfloat16", "float32"))
+    xt = _type_code(x.dtype, "x")
+    rt = _type_code(residual.dtype, "residual", 3)
     act = GATE_ACTS.get(gate_act)
     if act is None:
         raise ValueError(f"gate_act: {gate_act!r}, expected one of {', '.join(GATE_ACTS)}")
     specs, rows = [], [(x, "x", x.dtype, (M, K)), (residual, "residual", residual.dtype, (M, K))]
     wt = next((w.dtype for w in (w_pre, w_post) if isinstance(w, torch.Tensor)), torch.float16)
-    ot = _type_code(wt, "w_pre" if w_pre is not None else "w_post", ("float16", "bfloat16"))
+    ot = _type_code(wt, "w_pre" if w_pre is not None else "w_post")
     for w, name in ((w_post, "w_post"), (w_pre, "w_pre")):
         if w is not None:
             specs.append((w, name, wt, (K,)))
