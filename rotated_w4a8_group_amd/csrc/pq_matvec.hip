@@ -42,7 +42,7 @@ struct MatvecSlot {
   static constexpr int kBytes = kOffSz + (kSzWords * 4 + 15) / 16 * 16;
   static constexpr int kXLoads = (MX + 3) / 4;                  // 4 rows of 256 B per load
   static constexpr int kLoads = NT + kXLoads + kSzLoads;
-  static constexpr int kDepth = kMvRingBytes / kBytes > 4 ? 4 : kMvRingBytes / kBytes;
+  static constexpr int kDepth = kMvRingBytes / kBytes > 2 ? 2 : kMvRingBytes / kBytes;
   static_assert(kDepth >= 2 && (kDepth - 1) * kLoads <= 63, "ring");
 };
 
@@ -141,7 +141,8 @@ __device__ __forceinline__ void matvec_body(
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const u32x4 bw = *reinterpret_cast<const u32x4*>(sp + t * 1024 + 16 * lane);
-      const float2 f = sz_factors<false>(*reinterpret_cast<const uint32_t*>(sp + S::kOffSz + 4 * (16 * t + col)));
+      const uint32_t szw = *reinterpret_cast<const uint32_t*>(sp + S::kOffSz + 4 * (16 * t + col));
+      const float sc = f16_to_f32(szw), zz = __builtin_fmaf(sc, 8.0f, f16_to_f32(szw >> 16));
       const uint32_t w[4] = {bw.x, bw.y, bw.z, bw.w};
       v4f T = zero;
 #pragma unroll
@@ -150,9 +151,8 @@ __device__ __forceinline__ void matvec_body(
         const u32x4 b = {codes16<kBf16, false>(lo), codes16<kBf16, true>(lo), codes16<kBf16, false>(hi), codes16<kBf16, true>(hi)};
         T = mfma16<kBf16>(xa[q], b, T);
       }
-      const float sc = f.x * 0x1p-9f;   // the codes carry no 2^-9 here
 #pragma unroll
-      for (int i = 0; i < MR; ++i) acc[t][i] += sc * T[i] - f.y * rs[i];
+      for (int i = 0; i < MR; ++i) acc[t][i] += sc * T[i] - zz * rs[i];
     }
     slot = slot + 1 == D ? 0 : slot + 1;
   }
