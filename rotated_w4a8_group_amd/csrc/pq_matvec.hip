@@ -6,7 +6,11 @@
 // The weight stream is what bounds it, so the kernel streams as the W4A8 decode kernel does: one
 // 8-wave workgroup per CU on a range of whole 4-column quarters, the waves splitting the groups, each
 // with a private LDS ring that direct global -> LDS loads fill; one group is computed while the
-// next is in flight; partial sums meet in LDS in a fixed order.
+// next is in flight; partial sums meet in LDS in a fixed order. One group ahead is the best depth
+// everywhere: K=5120, N=17408, M=1 takes 11.6 / 10.7 / 11.9 us a launch with none, one and two groups
+// ahead, K=5120, N=8192 6.7 / 6.0 / 6.4 us, K=17408, N=5120 14.7 / 12.2 / 12.3 us (weights in the last
+// level cache; each further group adds about 0.35 us, the time the CU's load path takes to accept it).
+// Two workgroups per CU on half the columns each: 10.9 and 18.1 us for the first and last.
 //
 // A group's codes become 16-bit matrix operands without a table: a nibble is the OCP e4m3 byte of
 // c * 2^-9, and one convert instruction turns two such bytes times 2^9 into two f16 or bf16 values,
@@ -42,8 +46,8 @@ struct MatvecSlot {
   static constexpr int kBytes = kOffSz + (kSzWords * 4 + 15) / 16 * 16;
   static constexpr int kXLoads = (MX + 3) / 4;                  // 4 rows of 256 B per load
   static constexpr int kLoads = NT + kXLoads + kSzLoads;
-  static constexpr int kDepth = kMvRingBytes / kBytes > 2 ? 2 : kMvRingBytes / kBytes;
-  static_assert(kDepth >= 2 && (kDepth - 1) * kLoads <= 63, "ring");
+  static constexpr int kDepth = 2;
+  static_assert(kDepth * kBytes <= kMvRingBytes && (kDepth - 1) * kLoads <= 63, "ring");
 };
 
 // Two codes (e4m3 bytes of c * 2^-9, the low or high half of w) as 16-bit values.
