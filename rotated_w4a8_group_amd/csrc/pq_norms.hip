@@ -8,12 +8,21 @@
 //
 // Both norms need the whole row before any of its elements can be written, so a row stays in
 // registers: one workgroup per row, thread t holding the 8-element chunks t, t + T, ... (NC of them,
-// T threads). The row is read once and written once; the two sums of squares are reduced over the
-// wave by lane permutations and over the waves through LDS, in an order that depends on the shape
-// alone, so results do not change from run to run. Up to 2 chunks per thread every load of the row,
-// weights and gate included, is issued before anything waits; at 4 the norm weights are read where
-// they are used (from L2: every row reads the same ones), which keeps 1024 threads within 128
-// registers each.
+// T threads) of x and res as loaded, then of h as stored. The row is read once and written once; the two sums of
+// squares are reduced over the wave by lane permutations and over the waves through LDS, in an order
+// that depends on the shape alone, so results do not change from run to run.
+//
+// Memory bounds it from about 1000 rows on, the latency of load, two reductions and store below. What
+// that decided, at M=8192, K=5120 (bf16 x, f16 stream; 335 MB) unless said otherwise, in one session:
+//  - x and res as nontemporal loads, h and hs as nontemporal stores: 72.8 us (4.6 TB/s, a large copy's
+//    rate) against 94 with plain loads, 98 with both plain. A f32 stream's loads stay plain (101 against 107 us).
+//  - norm weights and the gate read where they are used, not with the row: 94 against 106 us (registers for
+//    more rows in flight); 3.8 against 4.4 us for one row.
+//  - threads: 1024 up to 512 rows, 512 up to 1024 rows, 256 above, i.e. as many as keep about two
+//    rows' worth of threads on each CU. One row of 5120: 3.8 / 4.3 / 5.1 us with 1024 / 512 / 256; 1024
+//    rows: 11.8 / 8.6 / 9.3; 2048 rows: 21.7 / 19.5 / 15.8.
+//  - one wave per row (no barriers): 81 us, 26.0 against 27.4 at M=16384, K=1024; persistent workgroups
+//    that keep the weights in registers: 127. Neither kept.
 #include <algorithm>
 
 #include "pq_device.h"
@@ -35,16 +44,16 @@ struct NormArgs {
   void* hs;
   int64_t ldx, ldr, ldg, ldo, ldh;
   int M, K;
-  int x_bf16, out_bf16, res_bf16;   // 16-bit types: 0 = f16, 1 = bf16
   int gate_cols;                    // K, or 1 (one value per row)
   int gate_act;
   float eps, scale, res_scale, one; // one: 1 for w' = 1 + w, else 0
 };
 
 // 8 values of a 16-bit type from 16 loaded bytes.
-__device__ __forceinline__ void unpack8(const uint4& q, int bf16, float (&v)[8]) {
+template <bool kBf16>
+__device__ __forceinline__ void unpack8(const uint4& q, float (&v)[8]) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-  if (bf16) {
+  if constexpr (kBf16) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       v[2 * i] = __builtin_bit_cast(float, w[i] << 16);
@@ -60,9 +69,10 @@ __device__ __forceinline__ void unpack8(const uint4& q, int bf16, float (&v)[8])
 }
 
 // 8 values rounded (to nearest even) to a 16-bit type.
-__device__ __forceinline__ uint4 pack8(const float (&v)[8], int bf16) {
+template <bool kBf16>
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
   uint32_t w[4];
-  if (bf16) {
+  if constexpr (kBf16) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = bf16x2_rn(v[2 * i], v[2 * i + 1]);
   } else {
@@ -78,53 +88,62 @@ __device__ __forceinline__ float gate_value(float t, int act) {
   return t;
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+// 16 bytes that nothing reads again before they have left the caches.
+typedef uint32_t norm_u32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ uint4 load_nt(const void* p) {
+  const norm_u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const norm_u32x4*>(p));
+  return make_uint4(v.x, v.y, v.z, v.w);
+}
+__device__ __forceinline__ void store_nt(void* p, const uint4& v) {
+  __builtin_nontemporal_store(norm_u32x4{v.x, v.y, v.z, v.w}, reinterpret_cast<norm_u32x4*>(p));
 }
 
-template <int NC, bool kRes32>
+__device__ __forceinline__ float wave_sum(float v) {
+  v += __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0xB1, 0xF, 0xF, true));    // pairs
+  v += __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x4E, 0xF, 0xF, true));    // quads
+  v += __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x141, 0xF, 0xF, true));   // 8 lanes
+  v += __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x140, 0xF, 0xF, true));   // 16 lanes
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+
+// kX, kO: x and gate, hs and the norm weights are bf16 (else f16); kR: the stream's pq_type.
+template <int NC, bool kX, int kR, bool kO>
 __global__ __launch_bounds__(kNormMaxThreads) void block_norms_kernel(NormArgs a) {
+  constexpr bool kRes32 = kR == PQ_F32;
   __shared__ float red[2][kNormMaxThreads / 64];
   const int tid = threadIdx.x, T = blockDim.x, waves = T >> 6, wave = tid >> 6;
   const int64_t m = blockIdx.x;
   const int chunks = a.K >> 3;
   const uint4 zero = make_uint4(0, 0, 0, 0);
+  auto load = [&](const void* base, int c) {
+    return c < chunks ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + 8 * c) : zero;
+  };
+  auto load_once = [&](const void* base, int c) { return c < chunks ? load_nt(static_cast<const uint16_t*>(base) + 8 * c) : zero; };
 
-  constexpr bool kLate = NC > 2;
-  uint4 xq[NC], rq[NC][kRes32 ? 2 : 1], pq[NC], gq[NC], wq[NC];
+  uint4 xq[NC], rq[NC][kRes32 ? 2 : 1];
   const uint16_t* xr = static_cast<const uint16_t*>(a.x) + m * a.ldx;
   const uint16_t* gr = static_cast<const uint16_t*>(a.gate) + m * a.ldg;
   const bool gate_row = a.gate && a.gate_cols != 1;
-  auto weights = [&](const void* w, int c) {
-    return c < chunks && w ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(w) + 8 * c) : zero;
-  };
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
     const int c = tid + j * T;
-    const bool on = c < chunks;
-    xq[j] = on ? *reinterpret_cast<const uint4*>(xr + 8 * c) : zero;
+    xq[j] = load_once(xr, c);
     if constexpr (kRes32) {
       const uint4* rr = reinterpret_cast<const uint4*>(static_cast<const float*>(a.res) + m * a.ldr + 8 * c);
-      rq[j][0] = on ? rr[0] : zero;
-      rq[j][1] = on ? rr[1] : zero;
+      rq[j][0] = c < chunks ? rr[0] : zero;
+      rq[j][1] = c < chunks ? rr[1] : zero;
     } else {
-      rq[j][0] = on ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.res) + m * a.ldr + 8 * c) : zero;
-    }
-    gq[j] = on && gate_row ? *reinterpret_cast<const uint4*>(gr + 8 * c) : zero;
-    if constexpr (!kLate) {
-      pq[j] = weights(a.w_post, c);
-      wq[j] = weights(a.w_pre, c);
+      rq[j][0] = load_once(static_cast<const uint16_t*>(a.res) + m * a.ldr, c);
     }
   }
   float g1 = 1.0f;
   if (a.gate && !gate_row) {
     const uint32_t b = gr[0];
-    g1 = gate_value(a.x_bf16 ? bf16_to_f32(b) : f16_to_f32(b), a.gate_act);
+    g1 = gate_value(kX ? bf16_to_f32(b) : f16_to_f32(b), a.gate_act);
   }
 
-  // sum over the workgroup, the same value in every thread
+  // sum over the row's threads, the same value in every one
   auto total = [&](float s, float* slot) {
     s = wave_sum(s);
     if ((tid & 63) == 0) slot[wave] = s;
@@ -135,74 +154,117 @@ __global__ __launch_bounds__(kNormMaxThreads) void block_norms_kernel(NormArgs a
   };
   auto rstd = [&](float ss) { return 1.0f / __builtin_sqrtf(ss / static_cast<float>(a.K) + a.eps); };
 
-  float v[NC][8];
-  float ss = 0.0f;
-#pragma unroll
-  for (int j = 0; j < NC; ++j) {
-    unpack8(xq[j], a.x_bf16, v[j]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss += v[j][i] * v[j][i];
-  }
+  float rx = 1.0f;
   if (a.w_post) {
-    const float r = rstd(total(ss, red[0]));
+    float ss = 0.0f;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      float w[8];
-      unpack8(kLate ? weights(a.w_post, tid + j * T) : pq[j], a.out_bf16, w);
+      float v[8];
+      unpack8<kX>(xq[j], v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[j][i] = (v[j][i] * r) * (a.one + w[i]);
+      for (int i = 0; i < 8; ++i) ss += v[i] * v[i];
     }
+    rx = rstd(total(ss, red[0]));
   }
   // h, rounded as it is stored
   float hh = 0.0f;
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
     const int c = tid + j * T;
-    float g[8], r[8];
-    if (gate_row) {
-      unpack8(gq[j], a.x_bf16, g);
+    float v[8], r[8];
+    unpack8<kX>(xq[j], v);
+    if (a.w_post) {
+      float w[8];
+      unpack8<kO>(load(a.w_post, c), w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) g[i] = gate_value(g[i], a.gate_act);
+      for (int i = 0; i < 8; ++i) v[i] = (v[i] * rx) * (a.one + w[i]);
+    }
+    if (gate_row) {
+      float g[8];
+      unpack8<kX>(load(gr, c), g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= gate_value(g[i], a.gate_act);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) g[i] = g1;
+      for (int i = 0; i < 8; ++i) v[i] *= g1;
     }
     if constexpr (kRes32) {
       const uint32_t w[8] = {rq[j][0].x, rq[j][0].y, rq[j][0].z, rq[j][0].w, rq[j][1].x, rq[j][1].y, rq[j][1].z, rq[j][1].w};
 #pragma unroll
       for (int i = 0; i < 8; ++i) r[i] = __builtin_bit_cast(float, w[i]);
     } else {
-      unpack8(rq[j][0], a.res_bf16, r);
+      unpack8<kR == PQ_BF16>(rq[j][0], r);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[j][i] = a.res_scale * r[i] + a.scale * (v[j][i] * g[i]);
+    for (int i = 0; i < 8; ++i) v[i] = a.res_scale * r[i] + a.scale * v[i];
     if constexpr (kRes32) {
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = __builtin_bit_cast(uint32_t, v[i]);
+      rq[j][0] = make_uint4(w[0], w[1], w[2], w[3]);
+      rq[j][1] = make_uint4(w[4], w[5], w[6], w[7]);
       if (c < chunks) {
-        float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.res_out) + m * a.ldo + 8 * c);
-        o[0] = make_float4(v[j][0], v[j][1], v[j][2], v[j][3]);
-        o[1] = make_float4(v[j][4], v[j][5], v[j][6], v[j][7]);
+        float* o = static_cast<float*>(a.res_out) + m * a.ldo + 8 * c;
+        store_nt(o, rq[j][0]);
+        store_nt(o + 4, rq[j][1]);
       }
     } else {
-      const uint4 o = pack8(v[j], a.res_bf16);
-      if (c < chunks) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.res_out) + m * a.ldo + 8 * c) = o;
-      unpack8(o, a.res_bf16, v[j]);
+      rq[j][0] = pack8<kR == PQ_BF16>(v);
+      if (c < chunks) store_nt(static_cast<uint16_t*>(a.res_out) + m * a.ldo + 8 * c, rq[j][0]);
+      unpack8<kR == PQ_BF16>(rq[j][0], v);
     }
     if (c < chunks) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) hh += v[j][i] * v[j][i];
+      for (int i = 0; i < 8; ++i) hh += v[i] * v[i];
     }
   }
   if (!a.w_pre) return;
-  const float r = rstd(total(hh, red[1]));
+  const float rh = rstd(total(hh, red[1]));
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
     const int c = tid + j * T;
-    float w[8];
-    unpack8(kLate ? weights(a.w_pre, c) : wq[j], a.out_bf16, w);
+    float v[8], w[8];
+    if constexpr (kRes32) {
+      const uint32_t q[8] = {rq[j][0].x, rq[j][0].y, rq[j][0].z, rq[j][0].w, rq[j][1].x, rq[j][1].y, rq[j][1].z, rq[j][1].w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[j][i] = (v[j][i] * r) * (a.one + w[i]);
-    if (c < chunks) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.hs) + m * a.ldh + 8 * c) = pack8(v[j], a.out_bf16);
+      for (int i = 0; i < 8; ++i) v[i] = __builtin_bit_cast(float, q[i]);
+    } else {
+      unpack8<kR == PQ_BF16>(rq[j][0], v);
+    }
+    unpack8<kO>(load(a.w_pre, c), w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = (v[i] * rh) * (a.one + w[i]);
+    if (c < chunks) store_nt(static_cast<uint16_t*>(a.hs) + m * a.ldh + 8 * c, pack8<kO>(v));
   }
+}
+
+template <bool kX, int kR, bool kO>
+static void norms_launch(const NormArgs& a, hipStream_t s) {
+  const int chunks = a.K / 8, T = a.M <= 512 ? 1024 : a.M <= 1024 ? 512 : 256;
+  const int nc = std::min(kNormMaxNC, (chunks + T - 1) / T);
+  const int threads = ((chunks + nc - 1) / nc + 63) / 64 * 64;
+#define PQ_NORM_LAUNCH(NC) \
+  hipLaunchKernelGGL((block_norms_kernel<NC, kX, kR, kO>), dim3(static_cast<unsigned>(a.M)), dim3(threads), 0, s, a)
+  if (nc == 1) PQ_NORM_LAUNCH(1);
+  else if (nc == 2) PQ_NORM_LAUNCH(2);
+  else if (nc == 3) PQ_NORM_LAUNCH(3);
+  else PQ_NORM_LAUNCH(4);
+#undef PQ_NORM_LAUNCH
+}
+template <bool kX, int kR>
+static void norms_for_out(const NormArgs& a, int out_type, hipStream_t s) {
+  if (out_type == PQ_BF16) norms_launch<kX, kR, true>(a, s);
+  else norms_launch<kX, kR, false>(a, s);
+}
+template <bool kX>
+static void norms_for_res(const NormArgs& a, int res_type, int out_type, hipStream_t s) {
+  if (res_type == PQ_F32) norms_for_out<kX, PQ_F32>(a, out_type, s);
+  else if (res_type == PQ_BF16) norms_for_out<kX, PQ_BF16>(a, out_type, s);
+  else norms_for_out<kX, PQ_F16>(a, out_type, s);
+}
+static void norms_for_x(const NormArgs& a, int x_type, int res_type, int out_type, hipStream_t s) {
+  if (x_type == PQ_BF16) norms_for_res<true>(a, res_type, out_type, s);
+  else norms_for_res<false>(a, res_type, out_type, s);
 }
 
 // Whether any byte of the M rows of `wa` bytes every `lda` bytes at a is one of b's rows. Exact where
@@ -275,23 +337,9 @@ int pq_block_norms(const void* x_d, int64_t ldx, int x_type, const void* res_d, 
   if (clash) return set_error(PQ_ERR_SHAPE, "%s: an output overlaps an input or the other output", what);
 
   NormArgs a{x_d, res_d, w_post_d, gate_d, w_pre_d, res_out_d, hs_d, ldx, ldr, ldg, ldo, ldh, M, K,
-             x_type == PQ_BF16, out_type == PQ_BF16, res_type == PQ_BF16, gate_cols, gate_act,
-             eps, scale, res_scale, gemma ? 1.0f : 0.0f};
-  const int chunks = K / 8;
-  // threads for about two chunks each, at least one wave, and no more chunks per thread than needed
-  int nc = 1;
-  while (nc < kNormMaxNC && (chunks + nc - 1) / nc > 512) nc *= 2;
-  const int threads = ((chunks + nc - 1) / nc + 63) / 64 * 64;
+             gate_cols, gate_act, eps, scale, res_scale, gemma ? 1.0f : 0.0f};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-#define PQ_NORM_LAUNCH(NC)                                                                              \
-  do {                                                                                                  \
-    auto kern = res_type == PQ_F32 ? block_norms_kernel<NC, true> : block_norms_kernel<NC, false>;      \
-    hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(M)), dim3(threads), 0, s, a);                   \
-  } while (0)
-  if (nc == 1) PQ_NORM_LAUNCH(1);
-  else if (nc == 2) PQ_NORM_LAUNCH(2);
-  else PQ_NORM_LAUNCH(4);
-#undef PQ_NORM_LAUNCH
+  norms_for_x(a, x_type, res_type, out_type, s);
   return launch_status(what);
 }
 
