@@ -127,10 +127,19 @@ __device__ __forceinline__ void lds_dma16_s(const void* sbase, uint32_t voff, ui
 __device__ __forceinline__ void lds_dma4_s(const void* sbase, uint32_t voff, uint32_t lds) {
   asm volatile("s_nop 4\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(sbase), "{m0}"(lds) : "memory");
 }
+// A wave-uniform address in scalar registers, where the compiler computed it on the vector ALU.
+__device__ __forceinline__ const void* scalar_addr(const void* p) {
+  const uint64_t a = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a)), hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a >> 32));
+  return reinterpret_cast<const void*>(static_cast<uint64_t>(hi) << 32 | lo);
+}
 template <int N>
 __device__ __forceinline__ void wait_vm() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
+
+// Every LDS read issued so far has returned: before a direct load is issued into memory that they read.
+__device__ __forceinline__ void wait_lds_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 // ---------------------------------------------------------------------------------------
 // The column ranges of the kernels that give every CU the same share of the weights (decode, below

@@ -9,7 +9,8 @@
 // columns (an even number, so that every CU streams the same bytes to within 2 of about 34 columns) and
 // both projections' tiles of that range; the waves split the groups and stream them through private LDS
 // rings, as the decode GEMM does.
-// M > 16: the prefill tile with its column strips alternating gate and up (pq_prefill.h); the matrix
+// Up to about 128 rows: the same for blocks of rows, both operands streamed.
+// Above: the prefill tile with its column strips alternating gate and up (pq_prefill.h); the matrix
 // cores and the fold bound it, as they do the GEMM.
 #include "pq_device.h"
 #include "pq_gemm_device.h"
@@ -110,6 +111,7 @@ __device__ __forceinline__ void glu_decode_body(
   int slot = 0;
   for (int g = g0; g < g1; ++g) {
     if (g + D - 1 < g1) {
+      wait_lds_reads();   // group g - 1's, from the slot that is filled now
       issue(g + D - 1, slot == 0 ? D - 1 : slot - 1);
       wait_vm<(D - 1) * S::kLoads>();   // group g has landed; D - 1 groups remain in flight
     } else {
@@ -191,7 +193,202 @@ __global__ __launch_bounds__(64 * kGdWaves, 1) void glu_decode_kernel(
 }
 
 // ---------------------------------------------------------------------------------------
-// M > 16
+// From 17 rows on, while the weights or the launch are still most of the work: the same streaming scheme for
+// blocks of 16 MF rows. The 8 waves of a workgroup split the groups; a wave's LDS slot holds one group's tiles of
+// both projections, the block's activation rows (16-byte chunks swizzled as in the prefill tile), SZ words
+// and the rows' scales and sums, so the zero point is folded in the loop and no pass runs before. A wave
+// loads a group, waits for it and computes it: the other wave of its SIMD computes meanwhile. (Four waves
+// with two slots each, which load one group ahead, take 21.9 us where this takes 19.4, at M=64, K=5120,
+// F=8704: a wave is held up while its loads are accepted, and then its SIMD is idle.) The sums meet in LDS in
+// a fixed order.
+constexpr int kGmWaves = 8;
+constexpr int kGmColumns = 50;    // a range's columns at most: 4 tiles from any even start
+
+template <int NT, int MF, int PA>
+struct GluMidSlot {
+  static constexpr int kOffA = 2 * NT * 1024;                   // [PA][16 MF rows][8 chunks of 16 B]
+  static constexpr int kOffSz = kOffA + PA * MF * 2048;         // [gate, up][16 NT] words
+  static constexpr int kOffSc = kOffSz + 2 * NT * 64;           // [PA][16 MF asg, 16 MF rs]
+  static constexpr int kBytes = kOffSc + PA * MF * 128;
+  static constexpr int kRed = 4 * 16 * MF * 2 * 16 * NT * 4;    // the sums of four waves reuse the slots
+  static constexpr int kLds = kGmWaves * kBytes > kRed ? kGmWaves * kBytes : kRed;
+  static_assert(kLds <= 163840, "LDS");
+};
+
+template <int NT, int MF, int PA>
+__device__ __forceinline__ void glu_mid_body(
+    const uint8_t* __restrict__ A, const float* __restrict__ ASG, const float* __restrict__ RS, int M, int K,
+    const u32x4* __restrict__ wpk, const uint32_t* __restrict__ sz, int F, int m0, int c0, int c1, int act,
+    uint16_t* __restrict__ h, int64_t ldh, bool out_bf16, uint8_t* smem) {
+  using S = GluMidSlot<NT, MF, PA>;
+  const int G = K >> 7;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 15, kq = lane >> 4;
+  const int tfirst = c0 >> 4, n0 = 16 * tfirst;
+  const int g0 = (G * wave) / kGmWaves, g1 = (G * (wave + 1)) / kGmWaves;
+
+  const uint8_t* wbase = reinterpret_cast<const uint8_t*>(wpk) + static_cast<size_t>(tfirst) * G * 1024;
+  const size_t up = static_cast<size_t>(F / 16) * G * 1024;
+  bool won[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int n = n0 + 16 * t + col;
+    won[t] = n >= c0 && n < c1;
+  }
+  // lane l of activation load j: row 8 j + l / 8 of the block (rows past M repeat row M - 1)
+  uint32_t aoff[2 * MF];
+#pragma unroll
+  for (int j = 0; j < 2 * MF; ++j) {
+    const int r = 8 * j + (lane >> 3);
+    aoff[j] = static_cast<uint32_t>(min(m0 + r, M - 1) * K + 16 * ((lane & 7) ^ (r & 7) ^ ((r >> 3) & 1)));
+  }
+  const size_t MG = static_cast<size_t>(M) * G;
+  const uint32_t soff = static_cast<uint32_t>(min(m0 + lane, M - 1) * 4 * G);
+
+  const uint8_t* sp = smem + wave * S::kBytes;
+  const uint32_t sb = lds_addr(sp);
+  auto issue = [&](int g) {
+    const uint8_t* wg = wbase + static_cast<size_t>(g) * 1024;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+      if (won[t]) {
+        lds_dma16_s(scalar_addr(wg + static_cast<size_t>(t) * G * 1024), 16 * lane, sb + t * 1024);
+        lds_dma16_s(scalar_addr(wg + up + static_cast<size_t>(t) * G * 1024), 16 * lane, sb + (NT + t) * 1024);
+      }
+    const uint32_t* zg = sz + static_cast<size_t>(g) * 2 * F + n0;
+    if (lane < 16 * NT) {
+      lds_dma4_s(scalar_addr(zg), 4 * lane, sb + S::kOffSz);
+      lds_dma4_s(scalar_addr(zg + F), 4 * lane, sb + S::kOffSz + NT * 64);
+    }
+#pragma unroll
+    for (int p = 0; p < PA; ++p) {
+      const uint8_t* ag = A + static_cast<size_t>(p) * M * K + 128 * static_cast<size_t>(g);
+#pragma unroll
+      for (int j = 0; j < 2 * MF; ++j) lds_dma16_s(scalar_addr(ag), aoff[j], sb + S::kOffA + (p * 2 * MF + j) * 1024);
+      if (lane < 16 * MF) {
+        lds_dma4_s(scalar_addr(ASG + p * MG + g), soff, sb + S::kOffSc + p * MF * 128);
+        lds_dma4_s(scalar_addr(RS + p * MG + g), soff, sb + S::kOffSc + p * MF * 128 + MF * 64);
+      }
+    }
+  };
+  v4f acc[2][NT][MF];
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int f = 0; f < MF; ++f) acc[s][t][f] = v4f{0.f, 0.f, 0.f, 0.f};
+  const int sw = (col & 7) ^ (col >> 3);
+  const int aread0 = col * 128 + 16 * ((2 * kq) ^ sw), aread1 = col * 128 + 16 * ((2 * kq + 1) ^ sw);
+  for (int g = g0; g < g1; ++g) {
+    wait_lds_reads();   // the last group's, from the slot that is filled now
+    issue(g);
+    wait_vm<0>();
+    v8i bw[2][NT];
+    float2 fz[2][NT];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        bw[s][t] = unpack_codes(*reinterpret_cast<const u32x4*>(sp + (s * NT + t) * 1024 + 16 * lane));
+        fz[s][t] = sz_factors<false>(*reinterpret_cast<const uint32_t*>(sp + S::kOffSz + s * NT * 64 + 4 * (16 * t + col)));
+      }
+#pragma unroll
+    for (int p = 0; p < PA; ++p) {
+#pragma unroll
+      for (int f = 0; f < MF; ++f) {
+        const uint8_t* ap = sp + S::kOffA + (p * MF + f) * 2048;
+        const u32x4 a0 = *reinterpret_cast<const u32x4*>(ap + aread0);
+        const u32x4 a1 = *reinterpret_cast<const u32x4*>(ap + aread1);
+        const v8i av = v8i{(int)a0.x, (int)a0.y, (int)a0.z, (int)a0.w, (int)a1.x, (int)a1.y, (int)a1.z, (int)a1.w};
+        const v4f as = *reinterpret_cast<const v4f*>(sp + S::kOffSc + p * MF * 128 + 64 * f + 16 * kq);
+        const v4f rs = *reinterpret_cast<const v4f*>(sp + S::kOffSc + p * MF * 128 + MF * 64 + 64 * f + 16 * kq);
+#pragma unroll
+        for (int s = PA == 1 ? 0 : p; s < (PA == 1 ? 2 : p + 1); ++s)
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const v4f T = mfma_fp8(av, bw[s][t]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[s][t][f][i] += as[i] * (fz[s][t].x * T[i] - fz[s][t].y * rs[i]);
+          }
+      }
+    }
+  }
+
+  __syncthreads();   // every slot is free: the sums reuse that LDS
+  constexpr int W = 16 * NT;
+  float* sred = reinterpret_cast<float*>(smem);
+  // the upper four waves hand their sums to the lower four, which add them in registers
+  if (wave >= 4) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int f = 0; f < MF; ++f)
+          *reinterpret_cast<v4f*>(sred + ((((wave - 4) * 2 + s) * NT + t) * MF + f) * 256 + 4 * lane) = acc[s][t][f];
+  }
+  __syncthreads();
+  if (wave < 4) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int f = 0; f < MF; ++f)
+          acc[s][t][f] += *reinterpret_cast<const v4f*>(sred + (((wave * 2 + s) * NT + t) * MF + f) * 256 + 4 * lane);
+  }
+  __syncthreads();
+  if (wave < 4) {   // [4 waves][16 MF rows][gate, up][16 NT]
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int f = 0; f < MF; ++f)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sred[((wave * 16 * MF + 16 * f + 4 * kq + i) * 2 + s) * W + 16 * t + col] = acc[s][t][f][i];
+  }
+  __syncthreads();
+  const int half = (c1 - c0) >> 1, pairs = min(16 * MF, M - m0) * half;
+  for (int idx = tid; idx < pairs; idx += 64 * kGmWaves) {
+    const int m = idx / half, c = c0 - n0 + 2 * (idx % half);
+    float v[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const float2 q = *reinterpret_cast<const float2*>(sred + ((w * 16 * MF + m) * 2 + s) * W + c);
+        v[s][0] += q.x;
+        v[s][1] += q.y;
+      }
+    const float h0 = glu_value(v[0][0], v[1][0], act), h1 = glu_value(v[0][1], v[1][1], act);
+    *reinterpret_cast<uint32_t*>(h + static_cast<size_t>(m0 + m) * ldh + n0 + c) = out_bf16 ? bf16x2_rn(h0, h1) : f16x2_rn(h0, h1);
+  }
+}
+
+// Workgroup b: row block b / ranges, range b % ranges of the column pairs (consecutive ranges on one XCD).
+template <int MF, int PA>
+__global__ __launch_bounds__(64 * kGmWaves, 1) void glu_mid_kernel(
+    const uint8_t* __restrict__ A, const float* __restrict__ ASG, const float* __restrict__ RS, int M, int K,
+    const u32x4* __restrict__ wpk, const uint32_t* __restrict__ sz, int F, int ranges, int act, uint16_t* __restrict__ h,
+    int64_t ldh, int out_bf16) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[GluMidSlot<4, MF, PA>::kLds];
+  const int b = xcd_tile(blockIdx.x, gridDim.x);
+  // uniform, but the divisions run on the vector ALU: back to scalar registers, which the loads' bases need
+  const int block = __builtin_amdgcn_readfirstlane(b / ranges), r = b - block * ranges, m0 = 16 * MF * block;
+  const int base = __builtin_amdgcn_readfirstlane((F / 2) / ranges), extra = F / 2 - base * ranges;
+  const int c0 = 2 * (r * base + min(r, extra)), c1 = c0 + 2 * (base + (r < extra));
+  const int nt = ((c1 - 1) >> 4) - (c0 >> 4) + 1;
+  if (nt == 1) glu_mid_body<1, MF, PA>(A, ASG, RS, M, K, wpk, sz, F, m0, c0, c1, act, h, ldh, out_bf16 != 0, smem);
+  else if (nt == 2) glu_mid_body<2, MF, PA>(A, ASG, RS, M, K, wpk, sz, F, m0, c0, c1, act, h, ldh, out_bf16 != 0, smem);
+  else if (nt == 3) glu_mid_body<3, MF, PA>(A, ASG, RS, M, K, wpk, sz, F, m0, c0, c1, act, h, ldh, out_bf16 != 0, smem);
+  else glu_mid_body<4, MF, PA>(A, ASG, RS, M, K, wpk, sz, F, m0, c0, c1, act, h, ldh, out_bf16 != 0, smem);
+}
+
+// ---------------------------------------------------------------------------------------
+// Prompts
 template <int PA>
 __global__ __launch_bounds__(512, 1) void glu_prefill_kernel(
     const uint8_t* __restrict__ A, const float* __restrict__ ASGT, int M, int K, const u32x4* __restrict__ wpk,
@@ -279,6 +476,27 @@ int pq_gemm_glu(const uint8_t* a_d, const float* asg_d, const float* rs_d, int M
 #undef PQ_GLU_DECODE
     return launch_status(what);
   }
+  // Row blocks of at most 64 rows (32 with two rotations, whose slots hold two sets of rows), as even as whole
+  // 16-row fragments make them, times the fewest ranges that are short enough, in whole rounds of one workgroup
+  // per CU. Each round costs about the same, so this is the way while there are few: K=5120, F=8704 takes 13.5 to
+  // 14.0 us at M=17..32, 19.4 at 64, 34.8 at 128 (two rounds) and 63 at 256 (four), the tiles below 53 at all
+  // of these; with fewer than 8 groups some waves have none, and two rounds of 2 groups (M=2000, K=256, F=512)
+  // take 10.4 us against 8.6.
+  const int blocks = P == 1 ? (M + 63) / 64 : (M + 31) / 32, MF = (M + 16 * blocks - 1) / (16 * blocks);
+  const int least = (F + kGmColumns - 1) / kGmColumns;
+  const int64_t rounds = (static_cast<int64_t>(blocks) * least + cus - 1) / cus;
+  if (rounds == 1 || (rounds == 2 && G >= kGmWaves)) {
+    const int ranges = static_cast<int>(std::min<int64_t>(F / 2, std::max<int64_t>(least, rounds * cus / blocks)));
+#define PQ_GLU_MID(MF, PA)                                                                                                    \
+  hipLaunchKernelGGL((glu_mid_kernel<MF, PA>), dim3(static_cast<unsigned>(blocks) * ranges), dim3(64 * kGmWaves), 0, s, a_d, asg_d, \
+                     rs_d, M, K, wpk, reinterpret_cast<const uint32_t*>(sz_d), F, ranges, act, h_d, ldh, out_bf16)
+    if (P == 2) PQ_GLU_MID(2, 2);
+    else if (MF == 2) PQ_GLU_MID(2, 1);
+    else if (MF == 3) PQ_GLU_MID(3, 1);
+    else PQ_GLU_MID(4, 1);
+#undef PQ_GLU_MID
+    return launch_status(what);
+  }
   if (static_cast<int64_t>((M + 127) / 128) * ((2 * F + 127) / 128) * 8 > 0x7FFFFFFF)
     return set_error(PQ_ERR_SHAPE, "%s: problem too large", what);
   const PrefillMap map = prefill_map(M, 2 * F, P == 1 ? kPfWide : kPfPair, cus);
@@ -286,9 +504,9 @@ int pq_gemm_glu(const uint8_t* a_d, const float* asg_d, const float* rs_d, int M
   const uint8_t* wb = static_cast<const uint8_t*>(wpk_d);
   const u32x4* zpe = reinterpret_cast<const u32x4*>(wb + static_cast<size_t>(K) * N / 2);
   const float* s9img = reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(zpe) + (N / 16) * zpe_chunks(G) * 1024);
-  if (!prepared) zero_point_operands(asg_d, rs_d, M, G, P, ws_d, PQ_MAX_PARTITIONS, s);
   const float* asgt = reinterpret_cast<const float*>(static_cast<const uint8_t*>(ws_d) + zpe_act_bytes(M, G, PQ_MAX_PARTITIONS));
   const bool vec16 = aligned(h_d, 16) && ldh % 8 == 0;
+  if (!prepared) zero_point_operands(asg_d, rs_d, M, G, P, ws_d, PQ_MAX_PARTITIONS, s);
   auto kern = P == 1 ? glu_prefill_kernel<1> : glu_prefill_kernel<2>;
   hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(grid)), dim3(64 * kPfWaves), 0, s, a_d, asgt, M, K, wpk, zpe,
                      static_cast<const u32x4*>(ws_d), s9img, F, act, h_d, ldh, out_bf16, map, vec16);

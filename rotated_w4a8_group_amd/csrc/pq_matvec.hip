@@ -129,6 +129,7 @@ __device__ __forceinline__ void matvec_body(
   int slot = 0;
   for (int g = g0; g < g1; ++g) {
     if (g + D - 1 < g1) {
+      wait_lds_reads();   // group g - 1's, from the slot that is filled now
       issue(g + D - 1, slot == 0 ? D - 1 : slot - 1);
       wait_vm<(D - 1) * S::kLoads>();   // group g has landed; D - 1 groups remain in flight
     } else {

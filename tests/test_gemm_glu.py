@@ -142,7 +142,9 @@ def test_few_rows(M, K, F, P, act, ht, pad):
 
 @gpu
 @pytest.mark.parametrize("M,K,F,P,act,ht,pad", [
-    (17, 128, 16, 1, "silu", "f16", 0), (17, 256, 48, 2, "gelu", "bf16", 2), (64, 1152, 144, 1, "gelu", "f16", 2), (300, 1024, 1424, 1, "gelu", "bf16", 0),
+    (17, 128, 16, 1, "silu", "f16", 0), (33, 5120, 8704, 1, "silu", "f16", 0), (48, 1280, 8704, 1, "gelu", "bf16", 2), (65, 1152, 8704, 1, "silu", "f16", 0),
+    (128, 5120, 8704, 1, "silu", "bf16", 0), (129, 1024, 8704, 1, "silu", "f16", 0), (31, 640, 8704, 2, "gelu", "bf16", 0), (50, 1152, 8704, 2, "silu", "f16", 2),
+    (2000, 256, 512, 1, "silu", "f16", 0), (600, 512, 1024, 1, "gelu", "f16", 0), (17, 256, 48, 2, "gelu", "bf16", 2), (64, 1152, 144, 1, "gelu", "f16", 2), (300, 1024, 1424, 1, "gelu", "bf16", 0),
     (300, 1024, 1424, 2, "silu", "f16", 0), (129, 384, 2064, 2, "silu", "bf16", 8), (513, 640, 4112, 1, "silu", "f16", 0), (257, 256, 8720, 2, "gelu", "f16", 0),
     (1100, 512, 8704, 1, "silu", "bf16", 0), (2048, 256, 8704, 2, "silu", "f16", 0)])
 def test_many_rows(M, K, F, P, act, ht, pad):
@@ -171,13 +173,15 @@ def test_one_signed_rows(M):
 
 
 @gpu
-@pytest.mark.parametrize("M", [1, 8, 16, 17, 300, 700])
+@pytest.mark.parametrize("M", [1, 8, 16, 17, 300, 700, 3000])
 def test_two_equal_partitions_are_one(M):
+    """The same bits where both forms add the groups in the same order (M = 700 takes different kernels)."""
     pair = Pair(1152, 2064, 660)
     A, S, R = _codes(1, M, 1152, M)
-    one = _run(A, S, R, pair)
-    two = _run(*(t.expand(2, *t.shape[1:]).contiguous() for t in (A, S, R)), pair)
-    assert torch.equal(one, two)
+    both = [t.expand(2, *t.shape[1:]).contiguous() for t in (A, S, R)]
+    one, two = _run(A, S, R, pair), _run(*both, pair)
+    assert M == 700 or torch.equal(one, two)
+    _check(f"equal partitions M={M}", two, *both, pair, "silu")
 
 
 @gpu
