@@ -448,7 +448,12 @@ __global__ __launch_bounds__(256) void rotate_quant_kernel(
 // the type of x instead of quantised, for consumers that take 16-bit rows in the weights' rotated space.
 // Same units, loads and LDS images as rotate_quant_kernel; a lane ends with 8 neighbouring channels of
 // a token and stores them as 16 bytes. kBf16: x and y are bf16 (x * cs is exact in binary32 either
-// way: 8 x 11 or 11 x 11 significand bits).
+// way: 8 x 11 or 11 x 11 significand bits). Bound, like the prologue, by the layers' vector instructions (6 per
+// pair, token and layer, each rounding separately so that the rows are the prologue's): M=8192, K=5120 takes
+// 44 us (3.8 TB/s; those instructions alone 26), M=1021 with three partitions 20.5; one row 3.8, the launch.
+// Stores that stream past the caches: 44 against 48 us. Fewer, longer units, or 5 and 6 waves per SIMD: no faster,
+// or slower (M=2048: 15.4 us with 16384 units, 17.2 with 4096, 18.0 with 6 waves).
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 template <bool kVec16, bool kBf16>
 __global__ __launch_bounds__(256) void rotate_kernel(
     const uint16_t* __restrict__ x, int64_t ldx, int M, int K, int P, const uint2* __restrict__ rec,
@@ -534,7 +539,7 @@ __global__ __launch_bounds__(256) void rotate_kernel(
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           w[i] = kBf16 ? bf16x2_rn(v[q][2 * i], v[q][2 * i + 1]) : f16x2_rn(v[q][2 * i], v[q][2 * i + 1]);
-        *reinterpret_cast<uint4*>(yg + static_cast<size_t>(m) * K) = make_uint4(w[0], w[1], w[2], w[3]);
+        __builtin_nontemporal_store(u32x4{w[0], w[1], w[2], w[3]}, reinterpret_cast<u32x4*>(yg + static_cast<size_t>(m) * K));
       }
     }
   };
