@@ -152,7 +152,7 @@ def _validate(specs, rows=()):
         dev = d
     else:
         for t, name, dtype, shape in rows:
-            if not (isinstance(t, tensor) and t.dtype is dtype and t.shape == shape and t.stride(1) == 1):
+            if not (isinstance(t, tensor) and t.dtype is dtype and t.shape == shape and t.stride()[1] == 1):
                 break
             d = t.get_device()
             if d < 0 or (dev is not None and d != dev):
@@ -217,9 +217,9 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _pitch(t):
+def _pitch(t, M, K):
     """Row stride of a [M, K] tensor in elements; that of a single row is of no consequence."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return t.stride()[0] if M > 1 else K
 
 
 def _new(shape, dtype, device, stream):
@@ -403,7 +403,7 @@ def rotate(x, rec, cs, out=None, stream=None):
     _validate(specs, rows=[(x, "x", x.dtype, (M, K))])
     if out is None:
         out = _new((P, M, K), x.dtype, x.device, stream)
-    _launch("pq_rotate", x.device, stream, x.data_ptr(), _pitch(x), xt, M, K, P, rec.data_ptr(), cs.data_ptr(), out.data_ptr())
+    _launch("pq_rotate", x.device, stream, x.data_ptr(), _pitch(x, M, K), xt, M, K, P, rec.data_ptr(), cs.data_ptr(), out.data_ptr())
     return out
 
 
@@ -478,7 +478,7 @@ def matvec(x, wpk, sz, N, pb1=NO_BOUNDARY, pb2=NO_BOUNDARY, out=None, dtype=None
         ldx = K
     else:
         rows.append((x, "x", x.dtype, (M, K)))
-        ldx = _pitch(x)
+        ldx = _pitch(x, M, K)
     if out is not None:
         if not isinstance(out, torch.Tensor) or out.dim() != 2 or out.shape[0] != M or out.shape[1] < N:
             raise ValueError(f"out: expected a f16 or bf16 [{M}, >= {N}] tensor")
@@ -490,7 +490,7 @@ def matvec(x, wpk, sz, N, pb1=NO_BOUNDARY, pb2=NO_BOUNDARY, out=None, dtype=None
     if out is None:
         out = _new((M, N), dtype or x.dtype, x.device, stream)
     _launch("pq_matvec", x.device, stream, x.data_ptr(), ldx, xt, M, K, P, wpk.data_ptr(), sz.data_ptr(), N, pb1, pb2,
-            out.data_ptr(), _pitch(out), yt)
+            out.data_ptr(), _pitch(out, M, N), yt)
     return out
 
 
@@ -547,7 +547,7 @@ def gemm_glu(A, ASG, RS, wpk, sz, F, act="silu", out=None, dtype=None, workspace
     if workspace is None and ws_bytes:
         workspace = _new((ws_bytes,), torch.uint8, A.device, stream)
     _launch("pq_gemm_glu", A.device, stream, A.data_ptr(), ASG.data_ptr(), RS.data_ptr(), M, K, P, wpk.data_ptr(),
-            sz.data_ptr(), F, code, out.data_ptr(), _pitch(out), ht, _addr(workspace),
+            sz.data_ptr(), F, code, out.data_ptr(), _pitch(out, M, F), ht, _addr(workspace),
             workspace.numel() if workspace is not None else 0, 1 if prepared else 0)
     return out
 
@@ -675,11 +675,12 @@ def block_norms(x, residual, w_post=None, gate=None, w_pre=None, eps=1e-6, scale
     if act is None:
         raise ValueError(f"gate_act: {gate_act!r}, expected one of {', '.join(GATE_ACTS)}")
     specs, rows = [], [(x, "x", x.dtype, (M, K)), (residual, "residual", residual.dtype, (M, K))]
-    wt = next((w.dtype for w in (w_pre, w_post) if isinstance(w, torch.Tensor)), torch.float16)
-    ot = _type_code(wt, "w_pre" if w_pre is not None else "w_post")
-    for w, name in ((w_post, "w_post"), (w_pre, "w_pre")):
-        if w is not None:
-            specs.append((w, name, wt, (K,)))
+    wt = w_pre.dtype if isinstance(w_pre, torch.Tensor) else w_post.dtype if isinstance(w_post, torch.Tensor) else torch.float16
+    ot = _type_code(wt, "w_post" if w_pre is None else "w_pre")
+    if w_post is not None:
+        specs.append((w_post, "w_post", wt, (K,)))
+    if w_pre is not None:
+        specs.append((w_pre, "w_pre", wt, (K,)))
     ldg, gcols = 0, K
     if gate is not None:
         if isinstance(gate, torch.Tensor) and gate.dim() == 1:
@@ -697,15 +698,15 @@ def block_norms(x, residual, w_post=None, gate=None, w_pre=None, eps=1e-6, scale
         rows.append((out, "out", wt, (M, K)))
     _validate(specs, rows=rows)
     if gate is not None and gate.dim() == 2:
-        ldg = _pitch(gate)
+        ldg = _pitch(gate, M, gcols)
     if residual_out is None:
         residual_out = _new((M, K), residual.dtype, x.device, stream)
     if out is None and w_pre is not None:
         out = _new((M, K), wt, x.device, stream)
     _launch("pq_block_norms", x.device, stream,
-            x.data_ptr(), _pitch(x), xt, residual.data_ptr(), _pitch(residual), rt, _addr(w_post), _addr(gate), ldg, gcols,
+            x.data_ptr(), _pitch(x, M, K), xt, residual.data_ptr(), _pitch(residual, M, K), rt, _addr(w_post), _addr(gate), ldg, gcols,
             act, _addr(w_pre), float(eps), float(scale), float(res_scale), 1 if gemma else 0, M, K,
-            residual_out.data_ptr(), _pitch(residual_out), _addr(out), _pitch(out) if out is not None else K, ot)
+            residual_out.data_ptr(), _pitch(residual_out, M, K), _addr(out), K if out is None else _pitch(out, M, K), ot)
     return residual_out, out
 
 
