@@ -194,39 +194,38 @@ __global__ __launch_bounds__(64 * kGdWaves, 1) void glu_decode_kernel(
 
 // ---------------------------------------------------------------------------------------
 // From 17 rows on, while the weights or the launch are still most of the work: the same streaming scheme for
-// blocks of 16 MF rows. The 8 waves of a workgroup split the groups; a wave's LDS slot holds one group's tiles of
+// blocks of 16 MF rows. The W waves of a workgroup split the groups; a wave's LDS slot holds one group's tiles of
 // both projections, the block's activation rows (16-byte chunks swizzled as in the prefill tile), SZ words
 // and the rows' scales and sums, so the zero point is folded in the loop and no pass runs before. A wave
-// loads a group, waits for it and computes it: the other wave of its SIMD computes meanwhile. (Four waves
-// with two slots each, which load one group ahead, take 21.9 us where this takes 19.4, at M=64, K=5120,
+// loads a group, waits for it and computes it: the other waves of its SIMD compute meanwhile. (Four waves
+// with two slots each, which load one group ahead, take 21.9 us where eight with one take 19.4, at M=64, K=5120,
 // F=8704: a wave is held up while its loads are accepted, and then its SIMD is idle.) The sums meet in LDS in
-// a fixed order.
-constexpr int kGmWaves = 8;
+// an order that the shape fixes.
 constexpr int kGmColumns = 50;    // a range's columns at most: 4 tiles from any even start
 
-template <int NT, int MF, int PA>
+template <int NT, int MF, int PA, int W>
 struct GluMidSlot {
   static constexpr int kOffA = 2 * NT * 1024;                   // [PA][16 MF rows][8 chunks of 16 B]
   static constexpr int kOffSz = kOffA + PA * MF * 2048;         // [gate, up][16 NT] words
   static constexpr int kOffSc = kOffSz + 2 * NT * 64;           // [PA][16 MF asg, 16 MF rs]
   static constexpr int kBytes = kOffSc + PA * MF * 128;
-  static constexpr int kRed = 4 * 16 * MF * 2 * 16 * NT * 4;    // the sums of four waves reuse the slots
-  static constexpr int kLds = kGmWaves * kBytes > kRed ? kGmWaves * kBytes : kRed;
+  static constexpr int kRed = (W / 2) * 16 * MF * 2 * 16 * NT * 4;   // the sums of half the waves reuse the slots
+  static constexpr int kLds = W * kBytes > kRed ? W * kBytes : kRed;
   static_assert(kLds <= 163840, "LDS");
 };
 
-template <int NT, int MF, int PA>
+template <int NT, int MF, int PA, int W>
 __device__ __forceinline__ void glu_mid_body(
     const uint8_t* __restrict__ A, const float* __restrict__ ASG, const float* __restrict__ RS, int M, int K,
     const u32x4* __restrict__ wpk, const uint32_t* __restrict__ sz, int F, int m0, int c0, int c1, int act,
     uint16_t* __restrict__ h, int64_t ldh, bool out_bf16, uint8_t* smem) {
-  using S = GluMidSlot<NT, MF, PA>;
+  using S = GluMidSlot<NT, MF, PA, W>;
   const int G = K >> 7;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, kq = lane >> 4;
   const int tfirst = c0 >> 4, n0 = 16 * tfirst;
-  const int g0 = (G * wave) / kGmWaves, g1 = (G * (wave + 1)) / kGmWaves;
+  const int g0 = (G * wave) / W, g1 = (G * (wave + 1)) / W;
 
   const uint8_t* wbase = reinterpret_cast<const uint8_t*>(wpk) + static_cast<size_t>(tfirst) * G * 1024;
   const size_t up = static_cast<size_t>(F / 16) * G * 1024;
@@ -317,20 +316,20 @@ __device__ __forceinline__ void glu_mid_body(
   }
 
   __syncthreads();   // every slot is free: the sums reuse that LDS
-  constexpr int W = 16 * NT;
+  constexpr int C = 16 * NT;
   float* sred = reinterpret_cast<float*>(smem);
-  // the upper four waves hand their sums to the lower four, which add them in registers
-  if (wave >= 4) {
+  // the upper half of the waves hand their sums to the lower half, which add them in registers
+  if (wave >= W / 2) {
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int f = 0; f < MF; ++f)
-          *reinterpret_cast<v4f*>(sred + ((((wave - 4) * 2 + s) * NT + t) * MF + f) * 256 + 4 * lane) = acc[s][t][f];
+          *reinterpret_cast<v4f*>(sred + ((((wave - W / 2) * 2 + s) * NT + t) * MF + f) * 256 + 4 * lane) = acc[s][t][f];
   }
   __syncthreads();
-  if (wave < 4) {
+  if (wave < W / 2) {
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -340,7 +339,7 @@ __device__ __forceinline__ void glu_mid_body(
           acc[s][t][f] += *reinterpret_cast<const v4f*>(sred + (((wave * 2 + s) * NT + t) * MF + f) * 256 + 4 * lane);
   }
   __syncthreads();
-  if (wave < 4) {   // [4 waves][16 MF rows][gate, up][16 NT]
+  if (wave < W / 2) {   // [W / 2 waves][16 MF rows][gate, up][16 NT]
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -348,18 +347,18 @@ __device__ __forceinline__ void glu_mid_body(
 #pragma unroll
         for (int f = 0; f < MF; ++f)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sred[((wave * 16 * MF + 16 * f + 4 * kq + i) * 2 + s) * W + 16 * t + col] = acc[s][t][f][i];
+          for (int i = 0; i < 4; ++i) sred[((wave * 16 * MF + 16 * f + 4 * kq + i) * 2 + s) * C + 16 * t + col] = acc[s][t][f][i];
   }
   __syncthreads();
   const int half = (c1 - c0) >> 1, pairs = min(16 * MF, M - m0) * half;
-  for (int idx = tid; idx < pairs; idx += 64 * kGmWaves) {
+  for (int idx = tid; idx < pairs; idx += 64 * W) {
     const int m = idx / half, c = c0 - n0 + 2 * (idx % half);
     float v[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
-    for (int w = 0; w < 4; ++w)
+    for (int w = 0; w < W / 2; ++w)
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        const float2 q = *reinterpret_cast<const float2*>(sred + ((w * 16 * MF + m) * 2 + s) * W + c);
+        const float2 q = *reinterpret_cast<const float2*>(sred + ((w * 16 * MF + m) * 2 + s) * C + c);
         v[s][0] += q.x;
         v[s][1] += q.y;
       }
@@ -369,22 +368,22 @@ __device__ __forceinline__ void glu_mid_body(
 }
 
 // Workgroup b: row block b / ranges, range b % ranges of the column pairs (consecutive ranges on one XCD).
-template <int MF, int PA>
-__global__ __launch_bounds__(64 * kGmWaves, 1) void glu_mid_kernel(
+template <int MF, int PA, int W>
+__global__ __launch_bounds__(64 * W, 2) void glu_mid_kernel(
     const uint8_t* __restrict__ A, const float* __restrict__ ASG, const float* __restrict__ RS, int M, int K,
     const u32x4* __restrict__ wpk, const uint32_t* __restrict__ sz, int F, int ranges, int act, uint16_t* __restrict__ h,
     int64_t ldh, int out_bf16) {
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[GluMidSlot<4, MF, PA>::kLds];
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   const int b = xcd_tile(blockIdx.x, gridDim.x);
   // uniform, but the divisions run on the vector ALU: back to scalar registers, which the loads' bases need
   const int block = __builtin_amdgcn_readfirstlane(b / ranges), r = b - block * ranges, m0 = 16 * MF * block;
   const int base = __builtin_amdgcn_readfirstlane((F / 2) / ranges), extra = F / 2 - base * ranges;
   const int c0 = 2 * (r * base + min(r, extra)), c1 = c0 + 2 * (base + (r < extra));
   const int nt = ((c1 - 1) >> 4) - (c0 >> 4) + 1;
-  if (nt == 1) glu_mid_body<1, MF, PA>(A, ASG, RS, M, K, wpk, sz, F, m0, c0, c1, act, h, ldh, out_bf16 != 0, smem);
-  else if (nt == 2) glu_mid_body<2, MF, PA>(A, ASG, RS, M, K, wpk, sz, F, m0, c0, c1, act, h, ldh, out_bf16 != 0, smem);
-  else if (nt == 3) glu_mid_body<3, MF, PA>(A, ASG, RS, M, K, wpk, sz, F, m0, c0, c1, act, h, ldh, out_bf16 != 0, smem);
-  else glu_mid_body<4, MF, PA>(A, ASG, RS, M, K, wpk, sz, F, m0, c0, c1, act, h, ldh, out_bf16 != 0, smem);
+  if (nt == 1) glu_mid_body<1, MF, PA, W>(A, ASG, RS, M, K, wpk, sz, F, m0, c0, c1, act, h, ldh, out_bf16 != 0, smem);
+  else if (nt == 2) glu_mid_body<2, MF, PA, W>(A, ASG, RS, M, K, wpk, sz, F, m0, c0, c1, act, h, ldh, out_bf16 != 0, smem);
+  else if (nt == 3) glu_mid_body<3, MF, PA, W>(A, ASG, RS, M, K, wpk, sz, F, m0, c0, c1, act, h, ldh, out_bf16 != 0, smem);
+  else glu_mid_body<4, MF, PA, W>(A, ASG, RS, M, K, wpk, sz, F, m0, c0, c1, act, h, ldh, out_bf16 != 0, smem);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -477,23 +476,33 @@ int pq_gemm_glu(const uint8_t* a_d, const float* asg_d, const float* rs_d, int M
     return launch_status(what);
   }
   // Row blocks of at most 64 rows (32 with two rotations, whose slots hold two sets of rows), as even as whole
-  // 16-row fragments make them, times the fewest ranges that are short enough, in whole rounds of one workgroup
-  // per CU. Each round costs about the same, so this is the way while there are few: K=5120, F=8704 takes 13.5 to
-  // 14.0 us at M=17..32, 19.4 at 64, 34.8 at 128 (two rounds) and 63 at 256 (four), the tiles below 53 at all
-  // of these; with fewer than 8 groups some waves have none, and two rounds of 2 groups (M=2000, K=256, F=512)
-  // take 10.4 us against 8.6.
+  // 16-row fragments make them, times column ranges. Where every CU gets at most one such piece of work they are
+  // cut for one 8-wave workgroup per CU, up to two pieces per CU for two 4-wave workgroups, beyond that the tiles
+  // below take it. K=5120, F=8704: 13.5 to 14.0 us at M=17..32, 19.4 at 64, 31 at 128 (36 as two rounds of 8-wave
+  // workgroups), 58 at 256, where the tiles take 53 at all of these; M=17..64 in 4-wave workgroups 16 to 24.
   const int blocks = P == 1 ? (M + 63) / 64 : (M + 31) / 32, MF = (M + 16 * blocks - 1) / (16 * blocks);
-  const int least = (F + kGmColumns - 1) / kGmColumns;
-  const int64_t rounds = (static_cast<int64_t>(blocks) * least + cus - 1) / cus;
-  if (rounds == 1 || (rounds == 2 && G >= kGmWaves)) {
-    const int ranges = static_cast<int>(std::min<int64_t>(F / 2, std::max<int64_t>(least, rounds * cus / blocks)));
-#define PQ_GLU_MID(MF, PA)                                                                                                    \
-  hipLaunchKernelGGL((glu_mid_kernel<MF, PA>), dim3(static_cast<unsigned>(blocks) * ranges), dim3(64 * kGmWaves), 0, s, a_d, asg_d, \
-                     rs_d, M, K, wpk, reinterpret_cast<const uint32_t*>(sz_d), F, ranges, act, h_d, ldh, out_bf16)
-    if (P == 2) PQ_GLU_MID(2, 2);
-    else if (MF == 2) PQ_GLU_MID(2, 1);
-    else if (MF == 3) PQ_GLU_MID(3, 1);
-    else PQ_GLU_MID(4, 1);
+  const int64_t least = (F + kGmColumns - 1) / kGmColumns, work = blocks * least;
+  if (work <= 2 * static_cast<int64_t>(cus)) {
+    const int slots = work <= cus ? cus : 2 * cus;
+    const int ranges = static_cast<int>(std::min<int64_t>(F / 2, std::max<int64_t>(least, slots / blocks)));
+    const int most = 2 * ((F / 2 + ranges - 1) / ranges), nt = (most + 14 + 15) / 16;   // tiles that a range may touch
+#define PQ_GLU_MID(MF, PA, W)                                                                                                  \
+  do {                                                                                                                         \
+    const int lds = nt == 1 ? GluMidSlot<1, MF, PA, W>::kLds : nt == 2 ? GluMidSlot<2, MF, PA, W>::kLds                        \
+                  : nt == 3 ? GluMidSlot<3, MF, PA, W>::kLds : GluMidSlot<4, MF, PA, W>::kLds;                                  \
+    hipLaunchKernelGGL((glu_mid_kernel<MF, PA, W>), dim3(static_cast<unsigned>(blocks) * ranges), dim3(64 * W), lds, s, a_d,   \
+                       asg_d, rs_d, M, K, wpk, reinterpret_cast<const uint32_t*>(sz_d), F, ranges, act, h_d, ldh, out_bf16);    \
+  } while (0)
+#define PQ_GLU_MID_WAVES(MF, PA)          \
+  do {                                    \
+    if (work <= cus) PQ_GLU_MID(MF, PA, 8); \
+    else PQ_GLU_MID(MF, PA, 4);           \
+  } while (0)
+    if (P == 2) PQ_GLU_MID_WAVES(2, 2);
+    else if (MF == 2) PQ_GLU_MID_WAVES(2, 1);
+    else if (MF == 3) PQ_GLU_MID_WAVES(3, 1);
+    else PQ_GLU_MID_WAVES(4, 1);
+#undef PQ_GLU_MID_WAVES
 #undef PQ_GLU_MID
     return launch_status(what);
   }
