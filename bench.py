@@ -92,7 +92,9 @@ def measure_ceilings(torch, np):
 
 
 TRAFFIC_RECORD = os.path.join(ROOT, "profiles", "gemm_prefill_gate_up_m2048_traffic.json")
-GEMM_SOURCE = os.path.join(ROOT, "rotated_w4a8_group_amd", "csrc", "pq_gemm.hip")
+# what the prefill kernel is made of; profiling.py hashes the same files in this order
+GEMM_SOURCES = [os.path.join(ROOT, "rotated_w4a8_group_amd", "csrc", f)
+                for f in ("pq_gemm.hip", "pq_prefill.h", "pq_gemm_device.h")]
 
 
 def measured_traffic():
@@ -102,7 +104,7 @@ def measured_traffic():
     import hashlib
     try:
         rec = json.load(open(TRAFFIC_RECORD))
-        src = hashlib.sha256(open(GEMM_SOURCE, "rb").read()).hexdigest()
+        src = hashlib.sha256(b"".join(open(f, "rb").read() for f in GEMM_SOURCES)).hexdigest()
     except (OSError, ValueError):
         return None
     if rec.get("source_sha256") != src:

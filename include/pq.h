@@ -193,7 +193,7 @@ int pq_gemm(const uint8_t* a_d, const float* asg_d, const float* rs_d, int M, in
  * x_d     f16 or bf16 (x_type) [P, M, ldx] (first K columns of a row used; partition p starts at row
  *         p * M), 16-byte aligned, ldx a multiple of 8, K <= ldx <= 2^26. For weights of the rotated
  *         space: pq_rotate's y.
- * y_d     out, f16 or bf16 (y_type) [M, ldy], ldy even and >= N, 4-byte aligned.
+ * y_d     out, f16 or bf16 (y_type) [M, ldy], ldy even and >= N, 4-byte aligned; overlaps no input.
  * 0 <= M <= 16, K % 128 == 0, N % 16 == 0; P, pb1, pb2 as for pq_gemm. No workspace.
  */
 int pq_matvec(const uint16_t* x_d, int64_t ldx, int x_type, int M, int K, int P, const void* wpk_d,
@@ -234,9 +234,12 @@ int pq_gemm_prepared(const uint8_t* a_d, const float* asg_d, const float* rs_d, 
  *                    gate's and partition 1 the up projection's (PQ_ERR_PARTITION otherwise).
  * wpk_d, sz_d        from pq_pack_weights for N = 2 F columns, gate columns first. F % 16 == 0.
  * act                enum pq_act.
- * h_d                out f16 or bf16 (h_type) [M, ldh], ldh even and >= F, 4-byte aligned.
+ * h_d                out f16 or bf16 (h_type) [M, ldh], ldh even and >= F, 4-byte aligned; overlaps no input.
  * ws_d, ws_bytes     as for pq_gemm at N = 2 F (none at M <= 16); prepared != 0: ws_d holds what
  *                    pq_rotate_quant_for_gemm wrote for these a_d, asg_d and rs_d, as for pq_gemm_prepared.
+ *                    Small calls do without the workspace's contents; which is the library's choice.
+ * Rows m >= M of h are never written. The order in which the groups are added depends on (M, K, F, P), so the same
+ * call gives the same bits, and a row alone may differ from that row in a batch in the last bits of its sums.
  */
 enum pq_act { PQ_ACT_SILU = 0, PQ_ACT_GELU = 1 };
 int pq_gemm_glu(const uint8_t* a_d, const float* asg_d, const float* rs_d, int M, int K, int P, const void* wpk_d,

@@ -5,7 +5,7 @@ Used to produce the text summaries and the HBM traffic record that are kept with
   python profiling.py summary <results.db> [--title T] [--command C]
       per-kernel dispatch count and average / median / min duration, as Markdown
   python profiling.py traffic --fetch <db> --write <db>
-          --copy-fetch <db> --copy-write <db> --kernels k1,k2 --source <file> --out <json>
+          --copy-fetch <db> --copy-write <db> --kernels k1,k2 --source <file>[,<file>] --out <json>
       FETCH_SIZE / WRITE_SIZE per dispatch of the named kernels, scaled by what the same
       counters read for a plain copy of known size (bench.py --copy-calibration)
 """
@@ -94,7 +94,7 @@ def traffic(fetch_db, write_db, copy_fetch_db, copy_write_db, kernels, source, c
     write_b = sum(statistics.median(v) for v in raw_w.values()) * 1024.0 * write_scale
     rec = {
         "kernels": list(kernels),
-        "source_sha256": hashlib.sha256(open(source, "rb").read()).hexdigest(),
+        "source_sha256": hashlib.sha256(b"".join(open(f, "rb").read() for f in source.split(","))).hexdigest(),
         "fetch_kib_per_dispatch_raw": raw_f,
         "write_kib_per_dispatch_raw": raw_w,
         "copy_kernel": copy_name,

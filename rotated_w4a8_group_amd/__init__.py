@@ -471,7 +471,7 @@ def matvec(x, wpk, sz, N, pb1=NO_BOUNDARY, pb2=NO_BOUNDARY, out=None, dtype=None
     need = lib().pq_packed_weight_bytes(K, N)
     if need == 0:
         raise ValueError(f"N={N}: not a shape the library packs (N % 16 == 0 needed)")
-    specs = [(wpk, "wpk", torch.uint8, (need,)), (sz, "sz", torch.float16, (K // GROUP, N, 2))]
+    specs = [(wpk, "wpk", torch.uint8, need), (sz, "sz", torch.float16, (K // GROUP, N, 2))]
     rows = []
     if x.dim() == 3:
         specs.append((x, "x", x.dtype, (P, M, K)))
@@ -527,7 +527,7 @@ def gemm_glu(A, ASG, RS, wpk, sz, F, act="silu", out=None, dtype=None, workspace
     if need == 0:
         raise ValueError(f"F={F}: must be a positive multiple of 16")
     specs = [(A, "A", torch.uint8, (P, M, K)), (ASG, "ASG", torch.float32, (P, M, G)), (RS, "RS", torch.float32, (P, M, G)),
-             (wpk, "wpk", torch.uint8, (need,)), (sz, "sz", torch.float16, (G, 2 * F, 2))]
+             (wpk, "wpk", torch.uint8, need), (sz, "sz", torch.float16, (G, 2 * F, 2))]
     ws_bytes = L.pq_gemm_workspace_bytes(M, 2 * F, K)
     if workspace is not None:
         specs.append((workspace, "workspace", torch.uint8, ws_bytes))

@@ -238,11 +238,17 @@ __global__ __launch_bounds__(kNormMaxThreads) void block_norms_kernel(NormArgs a
   }
 }
 
+// Chunks per thread and threads per row.
+static void norms_shape(int M, int K, int* nc, int* threads) {
+  const int chunks = K / 8, T = M <= 512 ? 1024 : M <= 1024 ? 512 : 256;
+  *nc = std::min(kNormMaxNC, (chunks + T - 1) / T);
+  *threads = ((chunks + *nc - 1) / *nc + 63) / 64 * 64;
+}
+
 template <bool kX, int kR, bool kO>
 static void norms_launch(const NormArgs& a, hipStream_t s) {
-  const int chunks = a.K / 8, T = a.M <= 512 ? 1024 : a.M <= 1024 ? 512 : 256;
-  const int nc = std::min(kNormMaxNC, (chunks + T - 1) / T);
-  const int threads = ((chunks + nc - 1) / nc + 63) / 64 * 64;
+  int nc, threads;
+  norms_shape(a.M, a.K, &nc, &threads);
 #define PQ_NORM_LAUNCH(NC) \
   hipLaunchKernelGGL((block_norms_kernel<NC, kX, kR, kO>), dim3(static_cast<unsigned>(a.M)), dim3(threads), 0, s, a)
   if (nc == 1) PQ_NORM_LAUNCH(1);
@@ -308,6 +314,10 @@ int pq_block_norms(const void* x_d, int64_t ldx, int x_type, const void* res_d, 
     if (ldg < 0 || (gate_cols == K && (ldg % 8 || (ldg && ldg < K))))
       return set_error(PQ_ERR_SHAPE, "%s: gate row stride %lld", what, static_cast<long long>(ldg));
   }
+  int nc, threads;
+  norms_shape(M, K, &nc, &threads);
+  if (static_cast<int64_t>(M) * threads > 0xFFFFFFFFll)   // the runtime counts a launch's threads in 32 bits
+    return set_error(PQ_ERR_SHAPE, "%s: M=%d rows too many for one call (split the rows)", what, M);
   if (M == 0) return PQ_OK;
   if (!x_d || !res_d || !res_out_d || (w_pre_d && !hs_d)) return set_error(PQ_ERR_NULL, "%s: NULL pointer", what);
   if (!aligned(x_d, 16) || !aligned(res_d, 16) || !aligned(res_out_d, 16) || !aligned(w_post_d, 16) || !aligned(w_pre_d, 16) ||

@@ -50,6 +50,7 @@ def _call(**kw):
     (dict(ro=FAKE + (1 << 20) + 512), -2),                       # the residual shifted by one row
     (dict(ro=FAKE + (1 << 20), ldo=512), -2),                    # the residual with another stride
     (dict(hs=FAKE + (3 << 20) - 512), -2), (dict(gate=FAKE + (4 << 20), ldg=0), -2),
+    (dict(M=2**31 - 1), -2), (dict(M=2**26 + 2**10, K=8, ldx=8, ldr=8, ldo=8, ldh=8, gc=8), -2),
     (dict(M=0), 0), (dict(M=0, x=None, hs=None), 0), (dict(M=0, K=32768, ldx=32768, ldr=32768, ldo=32768, ldh=32768), 0),
 ])
 def test_refusals(kw, code):
