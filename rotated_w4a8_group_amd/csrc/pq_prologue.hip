@@ -467,8 +467,8 @@ __global__ __launch_bounds__(256) void rotate_kernel(
   const int unit = bx * kProWaves + wave;
   if (unit >= chunks * G * P) return;
   const int g = unit % G;
-  const int chunk = (unit / G) % chunks;
-  const int p = unit / (G * chunks);
+  const int p = (unit / G) % P;             // partitions before token chunks: the rows stay in the XCD's L2 for all of them
+  const int chunk = unit / (G * P);
   const int m0 = chunk * tok;
   const int m_end = min(M, m0 + tok);
   const int lane = threadIdx.x & 63;
