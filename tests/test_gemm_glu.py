@@ -116,7 +116,9 @@ def _check(tag, h, A, S, R, pair, act, rows=None):
     ratio = ((got - ref).abs() / bound).max().item()
     rel = ((got - ref).norm() / ref.norm().clamp_min(1e-300)).item()
     print(f"[glu {tag}] worst error/bound {ratio:.3f}, relative {rel:.2e}", flush=True)
-    assert ratio <= 1.0 and rel <= 2e-3, tag
+    # 2e-3 of the norm for v before its rounding; rounding moves each value by at most e |v|, so the norm by at most
+    # e |v| <= e (1 + 2e-3) |ref|. In bf16 (e = 2^-8 = 3.9e-3) that part alone can pass 2e-3 where a few values carry the norm.
+    assert ratio <= 1.0 and rel <= 2e-3 + e * (1 + 2e-3), tag
 
 
 def _run(A, S, R, pair, act="silu", dtype=torch.float16, pad=0, **kw):
@@ -144,7 +146,7 @@ def test_few_rows(M, K, F, P, act, ht, pad):
 @pytest.mark.parametrize("M,K,F,P,act,ht,pad", [
     (17, 128, 16, 1, "silu", "f16", 0), (33, 5120, 8704, 1, "silu", "f16", 0), (48, 1280, 8704, 1, "gelu", "bf16", 2), (65, 1152, 8704, 1, "silu", "f16", 0),
     (128, 5120, 8704, 1, "silu", "bf16", 0), (129, 1024, 8704, 1, "silu", "f16", 0), (31, 640, 8704, 2, "gelu", "bf16", 0), (50, 1152, 8704, 2, "silu", "f16", 2),
-    (2000, 256, 512, 1, "silu", "f16", 0), (600, 512, 1024, 1, "gelu", "f16", 0), (17, 256, 48, 2, "gelu", "bf16", 2), (64, 1152, 144, 1, "gelu", "f16", 2), (300, 1024, 1424, 1, "gelu", "bf16", 0),
+    (1200, 384, 8704, 1, "gelu", "bf16", 2), (700, 640, 8704, 2, "silu", "f16", 2), (2000, 256, 512, 1, "silu", "f16", 0), (600, 512, 1024, 1, "gelu", "f16", 0), (17, 256, 48, 2, "gelu", "bf16", 2), (64, 1152, 144, 1, "gelu", "f16", 2), (300, 1024, 1424, 1, "gelu", "bf16", 0),
     (300, 1024, 1424, 2, "silu", "f16", 0), (129, 384, 2064, 2, "silu", "bf16", 8), (513, 640, 4112, 1, "silu", "f16", 0), (257, 256, 8720, 2, "gelu", "f16", 0),
     (1100, 512, 8704, 1, "silu", "bf16", 0), (2048, 256, 8704, 2, "silu", "f16", 0)])
 def test_many_rows(M, K, F, P, act, ht, pad):
