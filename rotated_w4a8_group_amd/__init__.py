@@ -100,6 +100,31 @@ def lib():
     return _lib
 
 
+_fast = None
+
+
+def _native():
+    """The compiled calls of rotate, matvec, gemm_glu and block_norms (``_binding.so``), which take the usual call - plain
+    tensors that pass every check, on the current device and stream - and answer NotImplemented to any other; False where
+    they are not built for this interpreter and torch: the functions below then do every call, about 3 us slower each."""
+    global _fast
+    if _fast is None:
+        import torch  # noqa: F401  (its libraries first)
+        L = lib()
+        try:
+            from . import _binding as b
+        except ImportError as e:
+            if os.path.exists(os.path.join(_HERE, "_binding.so")):
+                import warnings
+                warnings.warn(f"_binding.so does not load ({e}): calls go through Python")
+            _fast = False
+            return _fast
+        b.bind(_check, *(ctypes.cast(getattr(L, f), _P).value for f in (
+            "pq_rotate", "pq_matvec", "pq_gemm_glu", "pq_block_norms", "pq_packed_weight_bytes", "pq_gemm_workspace_bytes")))
+        _fast = b
+    return _fast
+
+
 def _check(fn, code):
     if code != PQ_OK:
         raise PQError(fn, code, lib().pq_last_error().decode())
@@ -392,6 +417,11 @@ def rotate_quant_for_gemm(x, rec, cs, workspace, out=None, stream=None):
 def rotate(x, rec, cs, out=None, stream=None):
     """The rotation alone: x f16 or bf16 [M, K] (row stride may exceed K), rec uint8 [P, 8, K/2, 8] (or [8, K/2, 8]),
     cs f16 [P, K] (or [K]) -> y [P, M, K] of x's type, ``rotate_quant``'s rotated rows before their quantisation."""
+    f = _native() if _fast is None else _fast
+    if f and stream is None:
+        done = f.rotate(x, rec, cs, out)
+        if done is not NotImplemented:
+            return done
     import torch
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x: expected a [M, K] tensor")
@@ -459,6 +489,11 @@ def matvec(x, wpk, sz, N, pb1=NO_BOUNDARY, pb2=NO_BOUNDARY, out=None, dtype=None
     """Products of few 16-bit rows with the packed weights of ``gemm``: x f16 or bf16 [P, M, K] (or [M, K] for one
     partition; row stride may exceed K), M <= 16 -> y [M, N] of ``dtype`` (f16 or bf16; x's type by default), or into
     ``out``, a [M, ldy >= N] view with unit column stride."""
+    f = _native() if _fast is None else _fast
+    if f and stream is None:
+        done = f.matvec(x, wpk, sz, N, pb1, pb2, out, dtype)
+        if done is not NotImplemented:
+            return done
     import torch
     if not isinstance(x, torch.Tensor) or x.dim() not in (2, 3):
         raise ValueError("x: expected a [P, M, K] or [M, K] tensor")
@@ -512,6 +547,11 @@ def gemm_glu(A, ASG, RS, wpk, sz, F, act="silu", out=None, dtype=None, workspace
     default, what the next prologue takes, or bf16), or into ``out``, a [M, ldh >= F] view with unit column stride.
     act "silu" or "gelu" (tanh form). workspace: gemm_workspace_bytes(M, 2 F, K) bytes; prepared: it holds
     what ``rotate_quant_for_gemm`` wrote for these A, ASG and RS."""
+    f = _native() if _fast is None else _fast
+    if f and stream is None:
+        done = f.gemm_glu(A, ASG, RS, wpk, sz, F, GLU_ACTS.get(act), out, dtype, workspace, prepared)
+        if done is not NotImplemented:
+            return done
     import torch
     if not isinstance(A, torch.Tensor) or A.dim() != 3:
         raise ValueError("A: expected a [P, M, K] tensor")
@@ -663,6 +703,11 @@ def block_norms(x, residual, w_post=None, gate=None, w_pre=None, eps=1e-6, scale
     gate of x's type: [K] (one row for every token), [M, K], or [M, 1] (one value per token); gate_act "none",
     "sigmoid" or "tanh". gemma: the norms multiply by 1 + w. residual_out may be ``residual`` itself (in place).
     K a multiple of 8 up to 32768; rows of 2-D tensors start on 16-byte lines."""
+    f = _native() if _fast is None else _fast
+    if f and stream is None:
+        done = f.block_norms(x, residual, w_post, gate, w_pre, eps, scale, res_scale, GATE_ACTS.get(gate_act), gemma, residual_out, out)
+        if done is not NotImplemented:
+            return done
     import torch
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x: expected a [M, K] tensor")

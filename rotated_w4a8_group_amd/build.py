@@ -1,4 +1,5 @@
-"""Builds the package's HIP library ``libpq.so`` in-tree for gfx950 with hipcc.
+"""Builds the package's HIP library ``libpq.so`` in-tree for gfx950 with hipcc, and the compiled part of the
+Python binding, ``_binding.so``, against the interpreter's and torch's headers.
 
 Usage: ``python -m rotated_w4a8_group_amd.build`` (also called by ``__graft_entry__.build``).
 Every call recompiles. Objects go to ``_build/`` under the repository root.
@@ -13,6 +14,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "libpq.so")
+BINDING = os.path.join(PKG, "_binding.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 ARCH = "gfx950"
 
@@ -41,6 +43,21 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found (ROCm is required to build the library)")
 
 
+def binding_command(out: str) -> list:
+    """Host code only: the device is reached through libpq.so's entry points."""
+    import sysconfig
+
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    dirs = [INCLUDE, inc, os.path.join(inc, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"],
+            os.path.join(os.path.dirname(os.path.dirname(hipcc())), "include")]
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1"]
+    for d in dirs:
+        cmd += ["-isystem" if d.startswith(inc) else "-I", d]
+    return cmd + [os.path.join(CSRC, "pq_binding.cpp"), "-L", os.path.join(os.path.dirname(inc), "lib"),
+                  "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-o", out]
+
+
 def build(verbose: bool = False) -> str:
     cc = hipcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -54,6 +71,11 @@ def build(verbose: bool = False) -> str:
             print(" ".join(cmd), flush=True)
         jobs.append((cmd, subprocess.Popen(cmd)))
         objs.append(obj)
+    btmp = BINDING + ".tmp"
+    cmd = binding_command(btmp)
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    jobs.append((cmd, subprocess.Popen(cmd)))
     failed = [cmd for cmd, job in jobs if job.wait() != 0]   # waits for every one
     if failed:
         raise subprocess.CalledProcessError(1, failed[0])
@@ -63,6 +85,7 @@ def build(verbose: bool = False) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, OUT)
+    os.replace(btmp, BINDING)
     return OUT
 
 
