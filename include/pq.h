@@ -152,7 +152,7 @@ int pq_rotate_quant(const uint16_t* x_d, int64_t ldx, int M, int K, int P, const
  * arithmetic), the result rounded once (to nearest even) to the type of x instead of quantised - the
  * 16-bit rows that products with weights of the rotated space take (pq_matvec).
  *
- * x_d   f16 or bf16 (x_type) [M, ldx], as in pq_rotate_quant; rec_d, cs_d as there (cs f16 always).
+ * x_d   f16 or bf16 (x_type) [M, ldx], as in pq_rotate_quant, ldx at most 2^26; rec_d, cs_d as there (cs f16 always).
  * y_d   out, type of x, [P, M, K], 16-byte aligned, not overlapping x (PQ_ERR_SHAPE).
  */
 int pq_rotate(const uint16_t* x_d, int64_t ldx, int x_type, int M, int K, int P, const void* rec_d,

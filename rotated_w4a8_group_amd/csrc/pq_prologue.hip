@@ -448,41 +448,67 @@ __global__ __launch_bounds__(256) void rotate_quant_kernel(
 // the type of x instead of quantised, for consumers that take 16-bit rows in the weights' rotated space.
 // Same units, loads and LDS images as rotate_quant_kernel; a lane ends with 8 neighbouring channels of
 // a token and stores them as 16 bytes. kBf16: x and y are bf16 (x * cs is exact in binary32 either
-// way: 8 x 11 or 11 x 11 significand bits). Bound, like the prologue, by the layers' vector instructions (6 per
-// pair, token and layer, each rounding separately so that the rows are the prologue's): M=8192, K=5120 takes
-// 44 us (3.8 TB/s; those instructions alone 26), M=1021 with three partitions 20.5; one row 3.8, the launch.
-// Stores that stream past the caches: 44 against 48 us. Fewer, longer units, or 5 and 6 waves per SIMD: no faster,
-// or slower (M=2048: 15.4 us with 16384 units, 17.2 with 4096, 18.0 with 6 waves).
+// way: 8 x 11 or 11 x 11 significand bits). Bound, like the prologue, by the layers: their vector instructions (6 per
+// pair, token and layer, each rounding separately so that the rows are the prologue's) are 96 % of the vector
+// issue of M=1021 with three partitions before the steps below, and the LDS works 76 % of that time beside them.
+// M=8192, K=5120 takes 44 us (3.8 TB/s), M=1021 with three partitions 19.7; one row 3.3, the launch. What brought it there:
+//  - stores that stream past the caches: 44 against 48 us.
+//  - a workgroup of one wave (its LDS begins at 0, nothing to add to a row's address), scalar bases with 32-bit lane
+//    offsets, the unit's numbers by multiplication: 500 vector instructions a unit of 8 tokens against 586, 384 of
+//    them the layers'. One row 3.7 -> 3.3 us, M=300, K=2048, P=2 4.85 -> 4.5, M=1021, P=3 20.5 -> 19.7.
+//  - the exchange between layers by ds_bpermute: 24.4 against 20.6 us; 8-byte LDS writes: 21.4. Neither kept.
+//  - fewer, longer units, or 5 and 6 waves per SIMD: no faster, or slower (M=2048: 15.4 us with 16384 units, 17.2 with
+//    4096, 18.0 with 6 waves).
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-template <bool kVec16, bool kBf16>
-__global__ __launch_bounds__(256) void rotate_kernel(
-    const uint16_t* __restrict__ x, int64_t ldx, int M, int K, int P, const uint2* __restrict__ rec,
-    const uint16_t* __restrict__ cs, uint16_t* __restrict__ y, int tok, int chunks) {
-  __shared__ __align__(16) uint8_t sbuf[kProWaves][kProQuads * kProQuadBytes];
 
-  const int G = K >> 7;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int nb = gridDim.x, q8 = nb >> 3, b = blockIdx.x;
-  const int bx = b < 8 * q8 ? (b & 7) * q8 + (b >> 3) : b;
-  const int unit = bx * kProWaves + wave;
-  if (unit >= chunks * G * P) return;
-  const int g = unit % G;
-  const int p = (unit / G) % P;             // partitions before token chunks: the rows stay in the XCD's L2 for all of them
-  const int chunk = unit / (G * P);
-  const int m0 = chunk * tok;
+// n / d and n % d for n < 2^31 on the scalar unit: the quotient by floor(2^32 / d) is short by at most one.
+struct Divisor {
+  uint32_t d, inv;
+};
+static Divisor divisor(uint32_t d) { return {d, d == 1 ? 0xFFFFFFFFu : static_cast<uint32_t>((uint64_t{1} << 32) / d)}; }
+__device__ __forceinline__ uint32_t divide(uint32_t n, const Divisor& v, uint32_t& rem) {
+  uint32_t q = __umulhi(n, v.inv), r = n - q * v.d;
+  if (r >= v.d) { ++q; r -= v.d; }
+  rem = r;
+  return q;
+}
+
+// A wave-uniform address that the compiler keeps in scalar registers, so that a lane adds its 32-bit offset in
+// the memory instruction (it would rather carry 64-bit lane addresses from one access to the next).
+template <typename T>
+__device__ __forceinline__ T* uniform(T* p) {
+  uint64_t a = reinterpret_cast<uint64_t>(p);
+  asm("" : "+s"(a));
+  return (T*)(__attribute__((address_space(1))) T*)a;
+}
+
+template <bool kVec16, bool kBf16>
+__global__ __launch_bounds__(64) void rotate_kernel(
+    const uint16_t* __restrict__ x, uint32_t ldx, int M, int K, Divisor dG, Divisor dP, const uint2* __restrict__ rec,
+    const uint16_t* __restrict__ cs, uint16_t* __restrict__ y, int tok) {
+  __shared__ __align__(16) uint8_t buf[kProQuads * kProQuadBytes];
+
+  const uint32_t nb = gridDim.x, q8 = nb >> 3, b = blockIdx.x;
+  const uint32_t unit = b < 8 * q8 ? (b & 7) * q8 + (b >> 3) : b;
+  uint32_t g, p;                            // partitions before token chunks: the rows stay in the XCD's L2 for all of them
+  const uint32_t chunk = divide(divide(unit, dG, g), dP, p);
+  const int m0 = static_cast<int>(chunk) * tok;
   const int m_end = min(M, m0 + tok);
-  const int lane = threadIdx.x & 63;
-  const int t = lane >> 4, c = lane & 15;
+  const uint32_t lane = threadIdx.x;
+  const uint32_t t = lane >> 4, c = lane & 15;
   const int half = K >> 1;
 
-  uint8_t* const buf = sbuf[wave];
+  // Rows and columns as a scalar base and a 32-bit lane offset: 3 rows of at most 2^27 bytes. Rows past
+  // the last one repeat it (the offsets grow with the row, so the smaller one is the clamped row's).
   uint8_t* const slot = buf + (9 * c) * 16 + 4 * t;
-  const uint16_t* const xg = x + g * 128 + 8 * c;
+  const uint8_t* const xg = reinterpret_cast<const uint8_t*>(x + g * 128);
+  const uint32_t xoff = t * 2 * ldx + 16 * c;
   auto load_step = [&](int mb, uint4 (&dst)[kProQuads]) {
 #pragma unroll
     for (int q = 0; q < kProQuads; ++q) {
-      const int m = min(mb + 4 * q + t, m_end - 1);   // clamped: always a valid row
-      dst[q] = load_x8<kVec16>(xg + static_cast<size_t>(m) * ldx);
+      const int m = min(mb + 4 * q, m_end - 1), left = min(m_end - 1 - m, 3);
+      const uint32_t off = min(xoff, 2 * ldx * left + 16 * c);
+      dst[q] = load_x8<kVec16>(reinterpret_cast<const uint16_t*>(uniform(xg + static_cast<size_t>(m) * ldx * 2) + off));
     }
   };
   uint4 xa[kProQuads], xb[kProQuads];
@@ -491,19 +517,21 @@ __global__ __launch_bounds__(256) void rotate_kernel(
   RotRec R;
   {
     uint2 q[PQ_LAYERS];
+    const uint2* const rp = rec + static_cast<size_t>(p) * PQ_LAYERS * half + g * 64;
 #pragma unroll
-    for (int r = 0; r < PQ_LAYERS; ++r) q[r] = rec[(static_cast<size_t>(p) * PQ_LAYERS + r) * half + g * 64 + lane];
+    for (int r = 0; r < PQ_LAYERS; ++r) q[r] = uniform(rp + static_cast<size_t>(r) * half)[lane];
     rot_decode(q, R);
   }
-  const uint32_t* csp = reinterpret_cast<const uint32_t*>(cs + static_cast<size_t>(p) * K + g * 128 + 8 * c);
+  const uint32_t* csp = reinterpret_cast<const uint32_t*>(cs + static_cast<size_t>(p) * K + g * 128);
   float csf[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t w = csp[i];
+    const uint32_t w = csp[4 * c + i];
     csf[2 * i] = half_lo(w);
     csf[2 * i + 1] = half_hi(w);
   }
-  uint16_t* const yg = y + static_cast<size_t>(p) * M * K + g * 128 + 8 * c;
+  uint8_t* const yg = reinterpret_cast<uint8_t*>(y + static_cast<size_t>(p) * M * K + g * 128);
+  const uint32_t yoff = t * 2 * K + 16 * c;
 
   auto run_step = [&](int mb, const uint4 (&xs)[kProQuads]) {
 #pragma unroll
@@ -533,23 +561,24 @@ __global__ __launch_bounds__(256) void rotate_kernel(
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int q = 0; q < kProQuads; ++q) {
-      const int m = mb + 4 * q + t;
-      if (m < m_end) {
+      const int m = mb + 4 * q;
+      if (m + static_cast<int>(t) < m_end) {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           w[i] = kBf16 ? bf16x2_rn(v[q][2 * i], v[q][2 * i + 1]) : f16x2_rn(v[q][2 * i], v[q][2 * i + 1]);
-        __builtin_nontemporal_store(u32x4{w[0], w[1], w[2], w[3]}, reinterpret_cast<u32x4*>(yg + static_cast<size_t>(m) * K));
+        __builtin_nontemporal_store(u32x4{w[0], w[1], w[2], w[3]}, reinterpret_cast<u32x4*>(uniform(yg + static_cast<size_t>(m) * K * 2) + yoff));
       }
     }
   };
   for (int mb = m0;; mb += 2 * kProStep) {
-    load_step(mb + kProStep, xb);
+    const bool two = mb + kProStep < m_end, three = mb + 2 * kProStep < m_end;
+    if (two) load_step(mb + kProStep, xb);
     run_step(mb, xa);
-    if (mb + kProStep >= m_end) break;
-    load_step(mb + 2 * kProStep, xa);
+    if (!two) break;
+    if (three) load_step(mb + 2 * kProStep, xa);
     run_step(mb + kProStep, xb);
-    if (mb + 2 * kProStep >= m_end) break;
+    if (!three) break;
   }
 }
 
@@ -898,7 +927,8 @@ int pq_rotate(const uint16_t* x_d, int64_t ldx, int x_type, int M, int K, int P,
   if (K <= 0 || K % PQ_GROUP || K > (1 << 24)) return set_error(PQ_ERR_SHAPE, "%s: K=%d must be a positive multiple of 128", what, K);
   if (x_type != PQ_F16 && x_type != PQ_BF16) return set_error(PQ_ERR_SHAPE, "%s: x_type=%d must be f16 or bf16", what, x_type);
   if (P < 1 || P > PQ_MAX_PARTITIONS) return set_error(PQ_ERR_PARTITION, "%s: P=%d must be in 1..3", what, P);
-  if (ldx < K || (ldx & 1)) return set_error(PQ_ERR_SHAPE, "%s: ldx=%lld must be even and >= K=%d", what, static_cast<long long>(ldx), K);
+  if (ldx < K || (ldx & 1) || ldx > (1 << 26))
+    return set_error(PQ_ERR_SHAPE, "%s: ldx=%lld must be even and in K..2^26", what, static_cast<long long>(ldx));
   if (M == 0) return PQ_OK;
   if (!x_d || !rec_d || !cs_d || !y_d) return set_error(PQ_ERR_NULL, "%s: NULL pointer", what);
   if (!aligned(x_d, 4) || !aligned(rec_d, 8) || !aligned(cs_d, 4) || !aligned(y_d, 16))
@@ -907,14 +937,16 @@ int pq_rotate(const uint16_t* x_d, int64_t ldx, int x_type, int M, int K, int P,
   const uintptr_t x1 = x0 + 2 * (static_cast<uintptr_t>(M - 1) * static_cast<uintptr_t>(ldx) + static_cast<uintptr_t>(K));
   const uintptr_t y1 = y0 + 2 * static_cast<uintptr_t>(P) * static_cast<uintptr_t>(M) * static_cast<uintptr_t>(K);
   if (x0 < y1 && y0 < x1) return set_error(PQ_ERR_SHAPE, "%s: y overlaps x", what);
+  const int G = K / PQ_GROUP;
   int tok, chunks;
   int64_t blocks;
-  if (!prologue_units(M, K / PQ_GROUP, P, &tok, &chunks, &blocks)) return set_error(PQ_ERR_SHAPE, "%s: problem too large", what);
+  if (!prologue_units(M, G, P, &tok, &chunks, &blocks) || static_cast<int64_t>(chunks) * G * P > 0x3FFFFFF)   // a launch's threads: 32 bits
+    return set_error(PQ_ERR_SHAPE, "%s: problem too large", what);
   const bool vec16 = aligned(x_d, 16) && (ldx % 8) == 0;
   auto kern = x_type == PQ_BF16 ? (vec16 ? rotate_kernel<true, true> : rotate_kernel<false, true>)
                                 : (vec16 ? rotate_kernel<true, false> : rotate_kernel<false, false>);
-  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, reinterpret_cast<hipStream_t>(stream),
-                     x_d, ldx, M, K, P, static_cast<const uint2*>(rec_d), cs_d, y_d, tok, chunks);
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(chunks) * G * P), dim3(64), 0, reinterpret_cast<hipStream_t>(stream),
+                     x_d, static_cast<uint32_t>(ldx), M, K, divisor(G), divisor(P), static_cast<const uint2*>(rec_d), cs_d, y_d, tok);
   return launch_status(what);
 }
 

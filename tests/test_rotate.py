@@ -27,7 +27,7 @@ def _call(**kw):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(M=-1), -2), (dict(K=0), -2), (dict(K=100), -2), (dict(xt=2), -2), (dict(xt=-1), -2), (dict(P=0), -4), (dict(P=4), -4),
-    (dict(ldx=254), -2), (dict(ldx=257), -2), (dict(x=None), -1), (dict(rec=None), -1), (dict(cs=None), -1), (dict(y=None), -1),
+    (dict(ldx=254), -2), (dict(ldx=257), -2), (dict(ldx=(1 << 26) + 8), -2), (dict(x=None), -1), (dict(rec=None), -1), (dict(cs=None), -1), (dict(y=None), -1),
     (dict(x=FAKE + 2), -3), (dict(rec=FAKE + 4), -3), (dict(cs=FAKE + 2), -3), (dict(y=FAKE + (1 << 20) + 8), -3),
     (dict(y=FAKE), -2), (dict(y=FAKE + 1024), -2), (dict(x=FAKE + (1 << 20) + 1536, P=1), -2), (dict(x=FAKE + (1 << 20) + 4096, P=3), -2),
     (dict(M=0), 0), (dict(M=0, x=None, y=None), 0)])
