@@ -13,16 +13,18 @@
 // that depends on the shape alone, so results do not change from run to run.
 //
 // Memory bounds it from about 1000 rows on, the latency of load, two reductions and store below. What
-// that decided, at M=8192, K=5120 (bf16 x, f16 stream; 335 MB) unless said otherwise, in one session:
-//  - x and res as nontemporal loads, h and hs as nontemporal stores: 72.8 us (4.6 TB/s, a large copy's
-//    rate) against 94 with plain loads, 98 with both plain. A f32 stream's loads stay plain (101 against 107 us).
-//  - norm weights and the gate read where they are used, not with the row: 94 against 106 us (registers for
-//    more rows in flight); 3.8 against 4.4 us for one row.
-//  - threads: 1024 up to 512 rows, 512 up to 1024 rows, 256 above, i.e. as many as keep about two
-//    rows' worth of threads on each CU. One row of 5120: 3.8 / 4.3 / 5.1 us with 1024 / 512 / 256; 1024
-//    rows: 11.8 / 8.6 / 9.3; 2048 rows: 21.7 / 19.5 / 15.8.
-//  - one wave per row (no barriers): 81 us, 26.0 against 27.4 at M=16384, K=1024; persistent workgroups
-//    that keep the weights in registers: 127. Neither kept.
+// that decided, at M=8192, K=5120 (bf16 x, f16 stream; 335 MB) unless said otherwise:
+//  - every load is one 16-byte instruction that every thread issues (the row's last chunk again past its end): 61.0 us
+//    (5.5 TB/s) against 71.5 with loads under a condition, which the compiler split into four words; one row 3.35 against 3.8.
+//  - x and res as nontemporal loads, h and hs as nontemporal stores: 73 us against 94 with plain loads, 98 with
+//    both plain. A f32 stream's loads stay plain (90 against 92 us, M=4096, K=1000 11.9 against 13.7).
+//  - norm weights and the gate read where they are used, not with the row: no faster earlier (one row 3.35 against
+//    3.45, M=1024 with gate rows and a f32 stream 14.1 against 17.5).
+//  - one chunk per thread up to 512 rows and for K <= 2048, else two, more only past 1024 threads. M=512 6.1 / 6.2
+//    / 6.6 us with 1, 2, 3 chunks, 1024 rows 11.8 / 8.4 / 9.1, 8192 67.0 / 59.9 / 60.8; M=2048, K=17408 54 with 3, 69
+//    with 4; M=9600, K=1024 18.0 / 18.1 / 18.8.
+//  - one wave per row (no barriers): 81 us when this kernel took 73; persistent workgroups that keep the weights in
+//    registers: 127. Neither kept.
 #include <algorithm>
 
 #include "pq_device.h"
@@ -49,9 +51,11 @@ struct NormArgs {
   float eps, scale, res_scale, one; // one: 1 for w' = 1 + w, else 0
 };
 
+typedef uint32_t norm_u32x4 __attribute__((ext_vector_type(4)));
+
 // 8 values of a 16-bit type from 16 loaded bytes.
 template <bool kBf16>
-__device__ __forceinline__ void unpack8(const uint4& q, float (&v)[8]) {
+__device__ __forceinline__ void unpack8(const norm_u32x4& q, float (&v)[8]) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
   if constexpr (kBf16) {
 #pragma unroll
@@ -70,7 +74,7 @@ __device__ __forceinline__ void unpack8(const uint4& q, float (&v)[8]) {
 
 // 8 values rounded (to nearest even) to a 16-bit type.
 template <bool kBf16>
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+__device__ __forceinline__ norm_u32x4 pack8(const float (&v)[8]) {
   uint32_t w[4];
   if constexpr (kBf16) {
 #pragma unroll
@@ -79,7 +83,7 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = f16x2_rn(v[2 * i], v[2 * i + 1]);
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  return norm_u32x4{w[0], w[1], w[2], w[3]};
 }
 
 __device__ __forceinline__ float gate_value(float t, int act) {
@@ -88,15 +92,10 @@ __device__ __forceinline__ float gate_value(float t, int act) {
   return t;
 }
 
-// 16 bytes that nothing reads again before they have left the caches.
-typedef uint32_t norm_u32x4 __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ uint4 load_nt(const void* p) {
-  const norm_u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const norm_u32x4*>(p));
-  return make_uint4(v.x, v.y, v.z, v.w);
-}
-__device__ __forceinline__ void store_nt(void* p, const uint4& v) {
-  __builtin_nontemporal_store(norm_u32x4{v.x, v.y, v.z, v.w}, reinterpret_cast<norm_u32x4*>(p));
-}
+// 16 bytes, and 16 bytes that nothing reads again before they have left the caches.
+__device__ __forceinline__ norm_u32x4 load16(const void* p) { return *reinterpret_cast<const norm_u32x4*>(p); }
+__device__ __forceinline__ norm_u32x4 load_nt(const void* p) { return __builtin_nontemporal_load(reinterpret_cast<const norm_u32x4*>(p)); }
+__device__ __forceinline__ void store_nt(void* p, const norm_u32x4& v) { __builtin_nontemporal_store(v, reinterpret_cast<norm_u32x4*>(p)); }
 
 __device__ __forceinline__ float wave_sum(float v) {
   v += __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0xB1, 0xF, 0xF, true));    // pairs
@@ -111,45 +110,47 @@ __device__ __forceinline__ float wave_sum(float v) {
 template <int NC, bool kX, int kR, bool kO>
 __global__ __launch_bounds__(kNormMaxThreads) void block_norms_kernel(NormArgs a) {
   constexpr bool kRes32 = kR == PQ_F32;
-  __shared__ float red[2][kNormMaxThreads / 64];
-  const int tid = threadIdx.x, T = blockDim.x, waves = T >> 6, wave = tid >> 6;
+  constexpr int kMaxWaves = kNormMaxThreads / 64;
+  __shared__ __attribute__((aligned(16))) float red[2][kMaxWaves];
+  const uint32_t tid = threadIdx.x, T = blockDim.x, waves = T >> 6, wave = tid >> 6;
   const int64_t m = blockIdx.x;
-  const int chunks = a.K >> 3;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  auto load = [&](const void* base, int c) {
-    return c < chunks ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + 8 * c) : zero;
-  };
-  auto load_once = [&](const void* base, int c) { return c < chunks ? load_nt(static_cast<const uint16_t*>(base) + 8 * c) : zero; };
+  const uint32_t chunks = static_cast<uint32_t>(a.K) >> 3;
+  if (tid < 2 * kMaxWaves && tid % kMaxWaves >= waves) red[tid / kMaxWaves][tid % kMaxWaves] = 0.0f;   // waves that are not there add 0
 
-  uint4 xq[NC], rq[NC][kRes32 ? 2 : 1];
+  // Chunk c = tid + j T of a row; a thread past the row's end loads the last chunk again (every load is
+  // issued, without branches), adds nothing to the sums and stores nothing.
+  auto chunk = [&](int j) { return tid + j * T; };
+  auto at = [&](const void* row, int j, uint32_t bytes) { return static_cast<const uint8_t*>(row) + bytes * min(chunk(j), chunks - 1); };
+
+  norm_u32x4 xq[NC], rq[NC][kRes32 ? 2 : 1];
   const uint16_t* xr = static_cast<const uint16_t*>(a.x) + m * a.ldx;
   const uint16_t* gr = static_cast<const uint16_t*>(a.gate) + m * a.ldg;
-  const bool gate_row = a.gate && a.gate_cols != 1;
+  const void* rr = static_cast<const uint8_t*>(a.res) + m * a.ldr * (kRes32 ? 4 : 2);
+  const bool gate_row = a.gate && a.gate_cols != 1, gate_one = a.gate && a.gate_cols == 1;
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
-    const int c = tid + j * T;
-    xq[j] = load_once(xr, c);
+    xq[j] = load_nt(at(xr, j, 16));
     if constexpr (kRes32) {
-      const uint4* rr = reinterpret_cast<const uint4*>(static_cast<const float*>(a.res) + m * a.ldr + 8 * c);
-      rq[j][0] = c < chunks ? rr[0] : zero;
-      rq[j][1] = c < chunks ? rr[1] : zero;
+      rq[j][0] = load16(at(rr, j, 32));
+      rq[j][1] = load16(at(rr, j, 32) + 16);
     } else {
-      rq[j][0] = load_once(static_cast<const uint16_t*>(a.res) + m * a.ldr, c);
+      rq[j][0] = load_nt(at(rr, j, 16));
     }
   }
-  float g1 = 1.0f;
-  if (a.gate && !gate_row) {
-    const uint32_t b = gr[0];
-    g1 = gate_value(kX ? bf16_to_f32(b) : f16_to_f32(b), a.gate_act);
-  }
+  uint32_t g1q = 0;
+  if (gate_one) g1q = gr[0];
 
-  // sum over the row's threads, the same value in every one
+  // sum over the row's threads, the same value in every one: the waves' sums in order
   auto total = [&](float s, float* slot) {
     s = wave_sum(s);
     if ((tid & 63) == 0) slot[wave] = s;
     __syncthreads();
-    float t = slot[0];
-    for (int w = 1; w < waves; ++w) t += slot[w];
+    float t = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kMaxWaves; w += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(slot + w);
+      t = (((t + q.x) + q.y) + q.z) + q.w;
+    }
     return t;
   };
   auto rstd = [&](float ss) { return 1.0f / __builtin_sqrtf(ss / static_cast<float>(a.K) + a.eps); };
@@ -159,29 +160,40 @@ __global__ __launch_bounds__(kNormMaxThreads) void block_norms_kernel(NormArgs a
     float ss = 0.0f;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      float v[8];
+      float v[8], s = ss;
       unpack8<kX>(xq[j], v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss += v[i] * v[i];
+      for (int i = 0; i < 8; ++i) s += v[i] * v[i];
+      ss = chunk(j) < chunks ? s : ss;
     }
     rx = rstd(total(ss, red[0]));
   }
+  norm_u32x4 wq[NC], gq[NC];   // before the stores to res_out, which the compiler lets no load pass
+  if (a.w_post) {
+#pragma unroll
+    for (int j = 0; j < NC; ++j) wq[j] = load16(at(a.w_post, j, 16));
+  }
+  if (gate_row) {
+#pragma unroll
+    for (int j = 0; j < NC; ++j) gq[j] = load16(at(gr, j, 16));
+  }
+  const float g1 = gate_one ? gate_value(kX ? bf16_to_f32(g1q) : f16_to_f32(g1q), a.gate_act) : 1.0f;
   // h, rounded as it is stored
   float hh = 0.0f;
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
-    const int c = tid + j * T;
+    const uint32_t c = chunk(j);
     float v[8], r[8];
     unpack8<kX>(xq[j], v);
     if (a.w_post) {
       float w[8];
-      unpack8<kO>(load(a.w_post, c), w);
+      unpack8<kO>(wq[j], w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = (v[i] * rx) * (a.one + w[i]);
     }
     if (gate_row) {
       float g[8];
-      unpack8<kX>(load(gr, c), g);
+      unpack8<kX>(gq[j], g);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] *= gate_value(g[i], a.gate_act);
     } else {
@@ -201,8 +213,8 @@ __global__ __launch_bounds__(kNormMaxThreads) void block_norms_kernel(NormArgs a
       uint32_t w[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[i] = __builtin_bit_cast(uint32_t, v[i]);
-      rq[j][0] = make_uint4(w[0], w[1], w[2], w[3]);
-      rq[j][1] = make_uint4(w[4], w[5], w[6], w[7]);
+      rq[j][0] = norm_u32x4{w[0], w[1], w[2], w[3]};
+      rq[j][1] = norm_u32x4{w[4], w[5], w[6], w[7]};
       if (c < chunks) {
         float* o = static_cast<float*>(a.res_out) + m * a.ldo + 8 * c;
         store_nt(o, rq[j][0]);
@@ -213,16 +225,18 @@ __global__ __launch_bounds__(kNormMaxThreads) void block_norms_kernel(NormArgs a
       if (c < chunks) store_nt(static_cast<uint16_t*>(a.res_out) + m * a.ldo + 8 * c, rq[j][0]);
       unpack8<kR == PQ_BF16>(rq[j][0], v);
     }
-    if (c < chunks) {
+    float s = hh;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) hh += v[i] * v[i];
-    }
+    for (int i = 0; i < 8; ++i) s += v[i] * v[i];
+    hh = c < chunks ? s : hh;
   }
   if (!a.w_pre) return;
+#pragma unroll
+  for (int j = 0; j < NC; ++j) wq[j] = load16(at(a.w_pre, j, 16));
   const float rh = rstd(total(hh, red[1]));
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
-    const int c = tid + j * T;
+    const uint32_t c = chunk(j);
     float v[8], w[8];
     if constexpr (kRes32) {
       const uint32_t q[8] = {rq[j][0].x, rq[j][0].y, rq[j][0].z, rq[j][0].w, rq[j][1].x, rq[j][1].y, rq[j][1].z, rq[j][1].w};
@@ -231,17 +245,17 @@ __global__ __launch_bounds__(kNormMaxThreads) void block_norms_kernel(NormArgs a
     } else {
       unpack8<kR == PQ_BF16>(rq[j][0], v);
     }
-    unpack8<kO>(load(a.w_pre, c), w);
+    unpack8<kO>(wq[j], w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = (v[i] * rh) * (a.one + w[i]);
     if (c < chunks) store_nt(static_cast<uint16_t*>(a.hs) + m * a.ldh + 8 * c, pack8<kO>(v));
   }
 }
 
-// Chunks per thread and threads per row.
+// Chunks per thread (one, or two for long rows where there are more rows than two a CU) and threads per row.
 static void norms_shape(int M, int K, int* nc, int* threads) {
-  const int chunks = K / 8, T = M <= 512 ? 1024 : M <= 1024 ? 512 : 256;
-  *nc = std::min(kNormMaxNC, (chunks + T - 1) / T);
+  const int chunks = K / 8, least = (chunks + kNormMaxThreads - 1) / kNormMaxThreads;
+  *nc = std::max(least, M > 512 && chunks > 256 ? 2 : 1);
   *threads = ((chunks + *nc - 1) / *nc + 63) / 64 * 64;
 }
 
