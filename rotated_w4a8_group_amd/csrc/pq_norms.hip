@@ -338,7 +338,8 @@ int pq_block_norms(const void* x_d, int64_t ldx, int x_type, const void* res_d, 
       (w_pre_d && !aligned(hs_d, 16)) || !aligned(gate_d, gate_cols == 1 ? 2 : 16))
     return set_error(PQ_ERR_ALIGN, "%s: misaligned pointer", what);
   // Outputs may not overlap inputs or each other, but for the residual updated in place (the same rows:
-  // a thread writes an element after it has read it, and no other thread reads it).
+  // a thread writes an element after it has read it, and what other threads may read of it, past the row's
+  // end of their own, they do not use).
   const int64_t rb = res_type == PQ_F32 ? 4 : 2, kr = rb * K, k2 = 2 * static_cast<int64_t>(K);
   const bool inplace = res_out_d == res_d && ldo == ldr;
   auto clashes = [&](const void* p, int64_t ld, int64_t width, const void* o, int64_t lo, int64_t wo) {
