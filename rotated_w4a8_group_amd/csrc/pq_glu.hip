@@ -210,7 +210,7 @@ struct GluMidSlot {
   static constexpr int kOffSz = kOffA + PA * MF * 2048;         // [gate, up][16 NT] words
   static constexpr int kOffSc = kOffSz + 2 * NT * 64;           // [PA][16 MF asg, 16 MF rs]
   static constexpr int kBytes = kOffSc + PA * MF * 128;
-  static constexpr int kRed = (W / 2) * 16 * MF * 2 * 16 * NT * 4;   // the sums of half the waves reuse the slots
+  static constexpr int kRed = (W / 2) * 16 * MF * (2 * 16 * NT + 4) * 4;   // the sums of half the waves reuse the slots
   static constexpr int kLds = W * kBytes > kRed ? W * kBytes : kRed;
   static_assert(kLds <= 163840, "LDS");
 };
@@ -317,7 +317,7 @@ __device__ __forceinline__ void glu_mid_body(
   }
 
   __syncthreads();   // every slot is free: the sums reuse that LDS
-  constexpr int C = 16 * NT;
+  constexpr int C = 16 * NT, R = 2 * C + 4;   // a row's sums; the 4 extra words put every fourth row a quarter of the banks further
   float* sred = reinterpret_cast<float*>(smem);
   // the upper half of the waves hand their sums to the lower half, which add them in registers
   if (wave >= W / 2) {
@@ -348,7 +348,7 @@ __device__ __forceinline__ void glu_mid_body(
 #pragma unroll
         for (int f = 0; f < MF; ++f)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sred[((wave * 16 * MF + 16 * f + 4 * kq + i) * 2 + s) * C + 16 * t + col] = acc[s][t][f][i];
+          for (int i = 0; i < 4; ++i) sred[(wave * 16 * MF + 16 * f + 4 * kq + i) * R + s * C + 16 * t + col] = acc[s][t][f][i];
   }
   __syncthreads();
   const int half = (c1 - c0) >> 1, pairs = min(16 * MF, M - m0) * half;
@@ -359,7 +359,7 @@ __device__ __forceinline__ void glu_mid_body(
     for (int w = 0; w < W / 2; ++w)
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        const float2 q = *reinterpret_cast<const float2*>(sred + ((w * 16 * MF + m) * 2 + s) * C + c);
+        const float2 q = *reinterpret_cast<const float2*>(sred + (w * 16 * MF + m) * R + s * C + c);
         v[s][0] += q.x;
         v[s][1] += q.y;
       }
@@ -368,18 +368,18 @@ __device__ __forceinline__ void glu_mid_body(
   }
 }
 
-// Workgroup b: row block b / ranges, range b % ranges of the column pairs (consecutive ranges on one XCD).
+// Workgroup b: row block b / ranges, range b % ranges of the columns, dealt out `gran` at a time (consecutive ranges on one XCD).
 template <int MF, int PA, int W>
 __global__ __launch_bounds__(64 * W, 2) void glu_mid_kernel(
     const uint8_t* __restrict__ A, const float* __restrict__ ASG, const float* __restrict__ RS, int M, int K,
-    const u32x4* __restrict__ wpk, const uint32_t* __restrict__ sz, int F, int ranges, int act, uint16_t* __restrict__ h,
+    const u32x4* __restrict__ wpk, const uint32_t* __restrict__ sz, int F, int ranges, int gran, int act, uint16_t* __restrict__ h,
     int64_t ldh, int out_bf16) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   const int b = xcd_tile(blockIdx.x, gridDim.x);
   // uniform, but the divisions run on the vector ALU: back to scalar registers, which the loads' bases need
   const int block = __builtin_amdgcn_readfirstlane(b / ranges), r = b - block * ranges, m0 = 16 * MF * block;
-  const int base = __builtin_amdgcn_readfirstlane((F / 2) / ranges), extra = F / 2 - base * ranges;
-  const int c0 = 2 * (r * base + min(r, extra)), c1 = c0 + 2 * (base + (r < extra));
+  const int units = F / gran, base = __builtin_amdgcn_readfirstlane(units / ranges), extra = units - base * ranges;
+  const int c0 = gran * (r * base + min(r, extra)), c1 = c0 + gran * (base + (r < extra));
   const int nt = ((c1 - 1) >> 4) - (c0 >> 4) + 1;
   if (nt == 1) glu_mid_body<1, MF, PA, W>(A, ASG, RS, M, K, wpk, sz, F, m0, c0, c1, act, h, ldh, out_bf16 != 0, smem);
   else if (nt == 2) glu_mid_body<2, MF, PA, W>(A, ASG, RS, M, K, wpk, sz, F, m0, c0, c1, act, h, ldh, out_bf16 != 0, smem);
@@ -486,13 +486,17 @@ int pq_gemm_glu(const uint8_t* a_d, const float* asg_d, const float* rs_d, int M
   if (work <= 2 * static_cast<int64_t>(cus)) {
     const int slots = work <= cus ? cus : 2 * cus;
     const int ranges = static_cast<int>(std::min<int64_t>(F / 2, std::max<int64_t>(least, slots / blocks)));
-    const int most = 2 * ((F / 2 + ranges - 1) / ranges), nt = (most + 14 + 15) / 16;   // tiles that a range may touch
+    // Columns are dealt out in pairs, so that every CU streams as many, or, from three row blocks on (the weights come
+    // from the L2 then), in whole tiles where that leaves a range fewer tiles to compute and to sum: M=301, K=1024,
+    // F=1424 6.8 against 7.9 us, M=192, K=4096, F=2048 13.6 / 15.5; with fewer blocks no faster, or 4 % slower.
+    const int most = 2 * ((F / 2 + ranges - 1) / ranges), pairs_nt = (most + 14 + 15) / 16;   // tiles that a range may touch
+    const int tiles_nt = (F / 16 + ranges - 1) / ranges, gran = blocks > 2 && tiles_nt < pairs_nt && F / 16 >= ranges ? 16 : 2, nt = gran == 16 ? tiles_nt : pairs_nt;
 #define PQ_GLU_MID(MF, PA, W)                                                                                                  \
   do {                                                                                                                         \
     const int lds = nt == 1 ? GluMidSlot<1, MF, PA, W>::kLds : nt == 2 ? GluMidSlot<2, MF, PA, W>::kLds                        \
                   : nt == 3 ? GluMidSlot<3, MF, PA, W>::kLds : GluMidSlot<4, MF, PA, W>::kLds;                                  \
     hipLaunchKernelGGL((glu_mid_kernel<MF, PA, W>), dim3(static_cast<unsigned>(blocks) * ranges), dim3(64 * W), lds, s, a_d,   \
-                       asg_d, rs_d, M, K, wpk, reinterpret_cast<const uint32_t*>(sz_d), F, ranges, act, h_d, ldh, out_bf16);    \
+                       asg_d, rs_d, M, K, wpk, reinterpret_cast<const uint32_t*>(sz_d), F, ranges, gran, act, h_d, ldh, out_bf16);    \
   } while (0)
 #define PQ_GLU_MID_WAVES(MF, PA)          \
   do {                                    \
