@@ -481,11 +481,14 @@ int pq_gemm_glu(const uint8_t* a_d, const float* asg_d, const float* rs_d, int M
   // 16-row fragments make them, times column ranges. Where every CU gets at most one such piece of work they are
   // cut for one 8-wave workgroup per CU, up to two pieces per CU for two 4-wave workgroups, beyond that the tiles
   // below take it. K=5120, F=8704: 13.5 to 14.0 us at M=17..32, 19.4 at 64, 31 at 128 (36 as two rounds of 8-wave
-  // workgroups), 58 at 256, where the tiles take 53 at all of these; M=17..64 in 4-wave workgroups 16 to 24.
+  // workgroups), 58 at 256, where the tiles take 53 at all of these; M=17..64 in 4-wave workgroups 16 to 24. Four
+  // waves also where there are at most 4 groups, of which half of eight waves would get none: M=512, K=512, F=1024
+  // 5.0 against 6.2 us, M=100, K=512, F=4096 4.9 / 6.0, M=301, K=512, F=1424 6.5 / 6.2; at 5 groups 7.5 / 6.2.
   const int blocks = P == 1 ? (M + 63) / 64 : (M + 31) / 32, MF = (M + 16 * blocks - 1) / (16 * blocks);
   const int64_t least = (F + kGmColumns - 1) / kGmColumns, work = blocks * least;
   if (work <= 2 * static_cast<int64_t>(cus)) {
-    const int slots = work <= cus ? cus : 2 * cus;
+    const bool eight = work <= cus && G > 4;
+    const int slots = eight ? cus : 2 * cus;
     const int ranges = static_cast<int>(std::min<int64_t>(F / 2, std::max<int64_t>(least, slots / blocks)));
     // Columns are dealt out in pairs, so that every CU streams as many, or, from three row blocks on (the weights come
     // from the L2 then), in whole tiles where that leaves a range fewer tiles to compute and to sum: M=301, K=1024,
@@ -501,7 +504,7 @@ int pq_gemm_glu(const uint8_t* a_d, const float* asg_d, const float* rs_d, int M
   } while (0)
 #define PQ_GLU_MID_WAVES(MF, PA)          \
   do {                                    \
-    if (work <= cus) PQ_GLU_MID(MF, PA, 8); \
+    if (eight) PQ_GLU_MID(MF, PA, 8); \
     else PQ_GLU_MID(MF, PA, 4);           \
   } while (0)
     if (P == 2) PQ_GLU_MID_WAVES(2, 2);
