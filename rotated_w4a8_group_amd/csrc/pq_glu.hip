@@ -9,7 +9,8 @@
 // columns (an even number, so that every CU streams the same bytes to within 2 of about 34 columns) and
 // both projections' tiles of that range; the waves split the groups and stream them through private LDS
 // rings, as the decode GEMM does, one group ahead of the one that is computed (as many as the ring holds: K=5120,
-// F=4352 7.9 against 7.4 us at M=1, 9.1 against 8.5 at M=7 with two rotations).
+// F=4352 7.9 against 7.4 us at M=1, 9.1 against 8.5 at M=7 with two rotations; nor do narrow layers, whose slots are
+// small, gain by more: K=10112, F=64 7.25 us with one group ahead, 7.65 with three).
 // Up to about 128 rows: the same for blocks of rows, both operands streamed.
 // Above: the prefill tile with its column strips alternating gate and up (pq_prefill.h); the matrix
 // cores and the fold bound it, as they do the GEMM.
@@ -198,8 +199,8 @@ __global__ __launch_bounds__(64 * kGdWaves, 1) void glu_decode_kernel(
 // From 17 rows on, while the weights or the launch are still most of the work: the same streaming scheme for
 // blocks of 16 MF rows. The W waves of a workgroup split the groups; a wave's LDS slot holds one group's tiles of
 // both projections, the block's activation rows (16-byte chunks swizzled as in the prefill tile), SZ words
-// and the rows' scales and sums, so the zero point is folded in the loop and no pass runs before. A wave
-// loads a group, waits for it and computes it: the other waves of its SIMD compute meanwhile. (Four waves
+// and the rows' scales and sums, so the zero point is folded in the loop and no pass runs before. Where only one
+// slot fits, a wave loads a group, waits for it and computes it: the other waves of its SIMD compute meanwhile. (Four waves
 // with two slots each, which load one group ahead, take 21.9 us where eight with one take 19.4, at M=64, K=5120,
 // F=8704: a wave is held up while its loads are accepted, and then its SIMD is idle.) The sums meet in LDS in
 // an order that the shape fixes.
@@ -212,7 +213,11 @@ struct GluMidSlot {
   static constexpr int kOffSc = kOffSz + 2 * NT * 64;           // [PA][16 MF asg, 16 MF rs]
   static constexpr int kBytes = kOffSc + PA * MF * 128;
   static constexpr int kRed = (W / 2) * 16 * MF * (2 * 16 * NT + 4) * 4;   // the sums of half the waves reuse the slots
-  static constexpr int kLds = W * kBytes > kRed ? W * kBytes : kRed;
+  // Two slots, one group ahead, where they fit: M=17, K=5120, F=2048 6.7 against 7.3 us, M=18, K=7808, F=720 8.6 / 9.2,
+  // M=33, K=10240, F=1024 13.7 / 14.4, M=40, K=5120, F=2048 9.4 / 9.2.
+  static constexpr int kDepth = 2 * W * kBytes <= (W == 8 ? 163840 : 81920) ? 2 : 1;
+  static constexpr int kLoads = 2 * NT + PA * 2 * MF + 2 + 2 * PA;
+  static constexpr int kLds = kDepth * W * kBytes > kRed ? kDepth * W * kBytes : kRed;
   static_assert(kLds <= 163840, "LDS");
 };
 
@@ -247,9 +252,11 @@ __device__ __forceinline__ void glu_mid_body(
   const size_t MG = static_cast<size_t>(M) * G;
   const uint32_t soff = static_cast<uint32_t>(min(m0 + lane, M - 1) * 4 * G);
 
-  const uint8_t* sp = smem + wave * S::kBytes;
-  const uint32_t sb = lds_addr(sp);
-  auto issue = [&](int g) {
+  constexpr int D = S::kDepth;
+  const uint8_t* ringp = smem + wave * D * S::kBytes;
+  const uint32_t ring = lds_addr(ringp);
+  auto issue = [&](int g, int slot) {
+    const uint32_t sb = ring + slot * S::kBytes;
     const uint8_t* wg = wbase + static_cast<size_t>(g) * 1024;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -282,10 +289,22 @@ __device__ __forceinline__ void glu_mid_body(
       for (int f = 0; f < MF; ++f) acc[s][t][f] = v4f{0.f, 0.f, 0.f, 0.f};
   const int sw = (col & 7) ^ (col >> 3);
   const int aread0 = col * 128 + 16 * ((2 * kq) ^ sw), aread1 = col * 128 + 16 * ((2 * kq + 1) ^ sw);
+  if (D == 2 && g0 < g1) issue(g0, 0);
+  int slot = 0;
   for (int g = g0; g < g1; ++g) {
-    wait_lds_reads();   // the last group's, from the slot that is filled now
-    issue(g);
-    wait_vm<0>();
+    if (D == 1) {
+      wait_lds_reads();   // the last group's, from the slot that is filled now
+      issue(g, 0);
+      wait_vm<0>();
+    } else if (g + 1 < g1) {
+      wait_lds_reads();
+      issue(g + 1, slot ^ 1);
+      wait_vm<S::kLoads>();
+    } else {
+      wait_vm<0>();
+    }
+    const uint8_t* sp = ringp + slot * S::kBytes;
+    if (D == 2) slot ^= 1;
     v8i bw[2][NT];
     float2 fz[2][NT];
 #pragma unroll
@@ -367,6 +386,13 @@ __device__ __forceinline__ void glu_mid_body(
     const float h0 = glu_value(v[0][0], v[1][0], act), h1 = glu_value(v[0][1], v[1][1], act);
     *reinterpret_cast<uint32_t*>(h + static_cast<size_t>(m0 + m) * ldh + n0 + c) = out_bf16 ? bf16x2_rn(h0, h1) : f16x2_rn(h0, h1);
   }
+}
+
+// LDS for ranges of at most nt tiles: a range that touches fewer may take more (two slots of less).
+template <int MF, int PA, int W>
+static int glu_mid_lds(int nt) {
+  const int each[4] = {GluMidSlot<1, MF, PA, W>::kLds, GluMidSlot<2, MF, PA, W>::kLds, GluMidSlot<3, MF, PA, W>::kLds, GluMidSlot<4, MF, PA, W>::kLds};
+  return *std::max_element(each, each + nt);
 }
 
 // Workgroup b: row block b / ranges, range b % ranges of the columns, dealt out `gran` at a time (consecutive ranges on one XCD).
@@ -497,8 +523,7 @@ int pq_gemm_glu(const uint8_t* a_d, const float* asg_d, const float* rs_d, int M
     const int tiles_nt = (F / 16 + ranges - 1) / ranges, gran = blocks > 2 && tiles_nt < pairs_nt && F / 16 >= ranges ? 16 : 2, nt = gran == 16 ? tiles_nt : pairs_nt;
 #define PQ_GLU_MID(MF, PA, W)                                                                                                  \
   do {                                                                                                                         \
-    const int lds = nt == 1 ? GluMidSlot<1, MF, PA, W>::kLds : nt == 2 ? GluMidSlot<2, MF, PA, W>::kLds                        \
-                  : nt == 3 ? GluMidSlot<3, MF, PA, W>::kLds : GluMidSlot<4, MF, PA, W>::kLds;                                  \
+    const int lds = glu_mid_lds<MF, PA, W>(nt);                                                                                \
     hipLaunchKernelGGL((glu_mid_kernel<MF, PA, W>), dim3(static_cast<unsigned>(blocks) * ranges), dim3(64 * W), lds, s, a_d,   \
                        asg_d, rs_d, M, K, wpk, reinterpret_cast<const uint32_t*>(sz_d), F, ranges, gran, act, h_d, ldh, out_bf16);    \
   } while (0)
