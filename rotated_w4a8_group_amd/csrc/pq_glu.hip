@@ -504,7 +504,7 @@ int pq_gemm_glu(const uint8_t* a_d, const float* asg_d, const float* rs_d, int M
     const int64_t rounds = (static_cast<int64_t>(F) + static_cast<int64_t>(cus) * most - 1) / (static_cast<int64_t>(cus) * most);
     const int64_t ranges = std::min<int64_t>(F / 2, rounds * cus);
 #define PQ_GLU_DECODE(MR, MA, PA)                                                                                     \
-  hipLaunchKernelGGL((glu_decode_kernel<MR, MA, PA>), dim3(static_cast<unsigned>(ranges)), dim3(64 * kGdWaves), 0, s, a_d, \
+  launch_kernel((glu_decode_kernel<MR, MA, PA>), dim3(static_cast<unsigned>(ranges)), dim3(64 * kGdWaves), 0, s, a_d, \
                      asg_d, rs_d, M, K, wpk, reinterpret_cast<const uint32_t*>(sz_d), F, act, h_d, ldh, out_bf16)
     if (P == 1) {
       if (M == 1) PQ_GLU_DECODE(1, 8, 1);
@@ -539,7 +539,7 @@ int pq_gemm_glu(const uint8_t* a_d, const float* asg_d, const float* rs_d, int M
 #define PQ_GLU_MID(MF, PA, W)                                                                                                  \
   do {                                                                                                                         \
     const int lds = glu_mid_lds<MF, PA, W>(nt);                                                                                \
-    hipLaunchKernelGGL((glu_mid_kernel<MF, PA, W>), dim3(static_cast<unsigned>(blocks) * ranges), dim3(64 * W), lds, s, a_d,   \
+    launch_kernel((glu_mid_kernel<MF, PA, W>), dim3(static_cast<unsigned>(blocks) * ranges), dim3(64 * W), lds, s, a_d,   \
                        asg_d, rs_d, M, K, wpk, reinterpret_cast<const uint32_t*>(sz_d), F, ranges, gran, act, h_d, ldh, out_bf16);    \
   } while (0)
 #define PQ_GLU_MID_WAVES(MF, PA)          \
@@ -571,12 +571,12 @@ int pq_gemm_glu(const uint8_t* a_d, const float* asg_d, const float* rs_d, int M
   const int rows128 = (M + 127) / 128, cols128 = (2 * F + 127) / 128;
   const int64_t small = static_cast<int64_t>(rows128) * cols128;
   if (P == 1 && map.full == 0 && map.split < 4 && 4 * small <= 9 * static_cast<int64_t>(cus)) {
-    hipLaunchKernelGGL(glu_small_tile_kernel, dim3(static_cast<unsigned>(small)), dim3(64 * kPfWaves), 0, s, a_d, asgt, M, K, wpk, zpe,
+    launch_kernel(glu_small_tile_kernel, dim3(static_cast<unsigned>(small)), dim3(64 * kPfWaves), 0, s, a_d, asgt, M, K, wpk, zpe,
                        static_cast<const u32x4*>(ws_d), s9img, F, act, h_d, ldh, out_bf16, rows128, cols128, vec16);
     return launch_status(what);
   }
   auto kern = P == 1 ? glu_prefill_kernel<1> : glu_prefill_kernel<2>;
-  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(grid)), dim3(64 * kPfWaves), 0, s, a_d, asgt, M, K, wpk, zpe,
+  launch_kernel(kern, dim3(static_cast<unsigned>(grid)), dim3(64 * kPfWaves), 0, s, a_d, asgt, M, K, wpk, zpe,
                      static_cast<const u32x4*>(ws_d), s9img, F, act, h_d, ldh, out_bf16, map, vec16);
   return launch_status(what);
 }

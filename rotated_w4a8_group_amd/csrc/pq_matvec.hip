@@ -241,7 +241,7 @@ int pq_matvec(const uint16_t* x_d, int64_t ldx, int x_type, int M, int K, int P,
 #define PQ_MATVEC_LAUNCH(MR, MX)                                                                                  \
   do {                                                                                                            \
     auto kern = x_type == PQ_BF16 ? matvec_kernel<true, MR, MX> : matvec_kernel<false, MR, MX>;                   \
-    hipLaunchKernelGGL(kern, dim3(map.wg0[3]), dim3(64 * kMvWaves), 0, s, x_d, ldx, M, K, wpk, sz, N, map, y_d, ldy, \
+    launch_kernel(kern, dim3(map.wg0[3]), dim3(64 * kMvWaves), 0, s, x_d, ldx, M, K, wpk, sz, N, map, y_d, ldy, \
                        y_type == PQ_BF16 ? 1 : 0);                                                                 \
   } while (0)
   if (M == 1) PQ_MATVEC_LAUNCH(1, 1);

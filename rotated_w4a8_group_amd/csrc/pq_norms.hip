@@ -264,7 +264,7 @@ static void norms_launch(const NormArgs& a, hipStream_t s) {
   int nc, threads;
   norms_shape(a.M, a.K, &nc, &threads);
 #define PQ_NORM_LAUNCH(NC) \
-  hipLaunchKernelGGL((block_norms_kernel<NC, kX, kR, kO>), dim3(static_cast<unsigned>(a.M)), dim3(threads), 0, s, a)
+  launch_kernel((block_norms_kernel<NC, kX, kR, kO>), dim3(static_cast<unsigned>(a.M)), dim3(threads), 0, s, a)
   if (nc == 1) PQ_NORM_LAUNCH(1);
   else if (nc == 2) PQ_NORM_LAUNCH(2);
   else if (nc == 3) PQ_NORM_LAUNCH(3);

@@ -945,7 +945,7 @@ int pq_rotate(const uint16_t* x_d, int64_t ldx, int x_type, int M, int K, int P,
   const bool vec16 = aligned(x_d, 16) && (ldx % 8) == 0;
   auto kern = x_type == PQ_BF16 ? (vec16 ? rotate_kernel<true, true> : rotate_kernel<false, true>)
                                 : (vec16 ? rotate_kernel<true, false> : rotate_kernel<false, false>);
-  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(chunks) * G * P), dim3(64), 0, reinterpret_cast<hipStream_t>(stream),
+  launch_kernel(kern, dim3(static_cast<unsigned>(chunks) * G * P), dim3(64), 0, reinterpret_cast<hipStream_t>(stream),
                      x_d, static_cast<uint32_t>(ldx), M, K, divisor(G), divisor(P), static_cast<const uint2*>(rec_d), cs_d, y_d, tok);
   return launch_status(what);
 }
