@@ -11,7 +11,7 @@
 // rings, as the decode GEMM does, one group ahead of the one that is computed (as many as the ring holds: K=5120,
 // F=4352 7.9 against 7.4 us at M=1, 9.1 against 8.5 at M=7 with two rotations; nor do narrow layers, whose slots are
 // small, gain by more: K=10112, F=64 7.25 us with one group ahead, 7.65 with three).
-// Up to about 128 rows: the same for blocks of rows, both operands streamed.
+// Up to about 128 rows of a wide layer, more of a narrow one: the same for blocks of rows, both operands streamed.
 // Above: the prefill tile with its column strips alternating gate and up (pq_prefill.h); the matrix
 // cores and the fold bound it, as they do the GEMM.
 #include "pq_device.h"
@@ -395,16 +395,18 @@ static int glu_mid_lds(int nt) {
   return *std::max_element(each, each + nt);
 }
 
-// Workgroup b: row block b / ranges, range b % ranges of the columns, dealt out `gran` at a time (consecutive ranges on one XCD).
+// Workgroup b: of row block and column range, one is b / fast, the other (rows_fast: the block) b % fast; `fast` is how many
+// there are of the latter. Consecutive b run on one XCD. The columns are dealt out `gran` at a time.
 template <int MF, int PA, int W>
 __global__ __launch_bounds__(64 * W, 2) void glu_mid_kernel(
     const uint8_t* __restrict__ A, const float* __restrict__ ASG, const float* __restrict__ RS, int M, int K,
-    const u32x4* __restrict__ wpk, const uint32_t* __restrict__ sz, int F, int ranges, int gran, int act, uint16_t* __restrict__ h,
+    const u32x4* __restrict__ wpk, const uint32_t* __restrict__ sz, int F, int ranges, int gran, int fast, int rows_fast, int act, uint16_t* __restrict__ h,
     int64_t ldh, int out_bf16) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   const int b = xcd_tile(blockIdx.x, gridDim.x);
   // uniform, but the divisions run on the vector ALU: back to scalar registers, which the loads' bases need
-  const int block = __builtin_amdgcn_readfirstlane(b / ranges), r = b - block * ranges, m0 = 16 * MF * block;
+  const int q = __builtin_amdgcn_readfirstlane(b / fast), rest = b - q * fast;
+  const int block = rows_fast ? rest : q, r = rows_fast ? q : rest, m0 = 16 * MF * block;
   const int units = F / gran, base = __builtin_amdgcn_readfirstlane(units / ranges), extra = units - base * ranges;
   const int c0 = gran * (r * base + min(r, extra)), c1 = c0 + gran * (base + (r < extra));
   const int nt = ((c1 - 1) >> 4) - (c0 >> 4) + 1;
@@ -412,6 +414,49 @@ __global__ __launch_bounds__(64 * W, 2) void glu_mid_kernel(
   else if (nt == 2) glu_mid_body<2, MF, PA, W>(A, ASG, RS, M, K, wpk, sz, F, m0, c0, c1, act, h, ldh, out_bf16 != 0, smem);
   else if (nt == 3) glu_mid_body<3, MF, PA, W>(A, ASG, RS, M, K, wpk, sz, F, m0, c0, c1, act, h, ldh, out_bf16 != 0, smem);
   else glu_mid_body<4, MF, PA, W>(A, ASG, RS, M, K, wpk, sz, F, m0, c0, c1, act, h, ldh, out_bf16 != 0, smem);
+}
+
+// How the rows and columns are cut: blocks of 16 MF rows times column ranges. It serves while blocks of the most rows a slot
+// holds (64, or 32 with two rotations) times ranges of kGmColumns are at most two per CU; where they are at most one, and K has
+// more than 4 groups (of fewer, half of eight waves would get none), one 8-wave workgroup per CU, else two of 4 waves. Among the
+// block heights the one whose workgroups issue and compute least per group and CU: loads (2 MF P of activations, 2 nt of
+// weights, 2 + 2 P of scales) and 2 nt MF products; two 4-wave workgroups side by side count as 1.6. The tallest blocks throughout
+// were slower wherever F is small: M=297, K=5504, F=208 12.6 against 6.6 us, M=68, K=8448, F=544 15.9 / 10.5, M=32, K=10240,
+// F=1024 12.4 / 8.4; M=18, K=7808, F=720 is one of the few the rule costs something, 8.4 / 9.3.
+// K=5120, F=8704: 13.0 to 13.4 us at M=17..32, 20.4 at 64, 30.6 at 128 (the tiles below take 50 at M=129..256, this kernel 58).
+struct GluMidPlan {
+  int MF, blocks, ranges;
+  int gran, nt;    // columns are dealt out gran at a time; tiles of a projection that a range may touch
+  bool eight;      // one 8-wave workgroup per CU, else two 4-wave workgroups
+  bool rows_fast;  // consecutive workgroups take the blocks of one range, else the ranges of one block
+};
+static bool glu_mid_plan(int M, int F, int P, int G, int cus, GluMidPlan* best) {
+  const int64_t least = (F + kGmColumns - 1) / kGmColumns;
+  const int most_mf = P == 1 ? 4 : 2;
+  if ((M + 16 * most_mf - 1) / (16 * most_mf) * least > 2 * static_cast<int64_t>(cus)) return false;
+  int64_t cost = -1;
+  for (int MF = most_mf; MF >= 1; --MF) {
+    GluMidPlan p{};
+    p.MF = MF;
+    p.blocks = (M + 16 * MF - 1) / (16 * MF);
+    const int64_t work = p.blocks * least;
+    if (work > 2 * static_cast<int64_t>(cus)) break;
+    p.eight = work <= cus && G > 4;
+    p.ranges = static_cast<int>(std::min<int64_t>(F / 2, std::max<int64_t>(least, (p.eight ? cus : 2 * cus) / p.blocks)));
+    const int widest = 2 * ((F / 2 + p.ranges - 1) / p.ranges), pairs_nt = (widest + 14 + 15) / 16, tiles_nt = (F / 16 + p.ranges - 1) / p.ranges;
+    // Columns are dealt out in pairs, so that every CU streams as many, or, from three row blocks on (the weights come
+    // from the L2 then), in whole tiles where that leaves a range fewer tiles to compute and to sum: M=301, K=1024,
+    // F=1424 6.8 against 7.9 us, M=192, K=4096, F=2048 13.6 / 15.5; with fewer blocks no faster, or 4 % slower.
+    p.gran = p.blocks > 2 && tiles_nt < pairs_nt && F / 16 >= p.ranges ? 16 : 2;
+    p.nt = p.gran == 16 ? tiles_nt : pairs_nt;
+    const int64_t per_cu = p.eight ? 10 : 8 * ((static_cast<int64_t>(p.blocks) * p.ranges + cus - 1) / cus);
+    const int64_t c = per_cu * (2 * MF * P + 2 * p.nt + 2 + 2 * P + 2 * p.nt * MF);
+    if (cost < 0 || c <= cost) { cost = c; *best = p; }
+  }
+  // What an XCD's consecutive workgroups share: the weights of a range, or the rows of a block where those are more bytes
+  // (M=90, K=4096, F=4096, two rotations 13.8 against 16.4 us, M=192, K=4096, F=2048 10.6 / 12.4; M=844, K=6912, F=32 7.3 / 6.5).
+  best->rows_fast = F > static_cast<int64_t>(M) * P;
+  return cost >= 0;
 }
 
 // ---------------------------------------------------------------------------------------
@@ -518,38 +563,25 @@ int pq_gemm_glu(const uint8_t* a_d, const float* asg_d, const float* rs_d, int M
 #undef PQ_GLU_DECODE
     return launch_status(what);
   }
-  // Row blocks of at most 64 rows (32 with two rotations, whose slots hold two sets of rows), as even as whole
-  // 16-row fragments make them, times column ranges. Where every CU gets at most one such piece of work they are
-  // cut for one 8-wave workgroup per CU, up to two pieces per CU for two 4-wave workgroups, beyond that the tiles
-  // below take it. K=5120, F=8704: 13.5 to 14.0 us at M=17..32, 19.4 at 64, 31 at 128 (36 as two rounds of 8-wave
-  // workgroups), 58 at 256, where the tiles take 53 at all of these; M=17..64 in 4-wave workgroups 16 to 24. Four
-  // waves also where there are at most 4 groups, of which half of eight waves would get none: M=512, K=512, F=1024
-  // 5.0 against 6.2 us, M=100, K=512, F=4096 4.9 / 6.0, M=301, K=512, F=1424 6.5 / 6.2; at 5 groups 7.5 / 6.2.
-  const int blocks = P == 1 ? (M + 63) / 64 : (M + 31) / 32, MF = (M + 16 * blocks - 1) / (16 * blocks);
-  const int64_t least = (F + kGmColumns - 1) / kGmColumns, work = blocks * least;
-  if (work <= 2 * static_cast<int64_t>(cus)) {
-    const bool eight = work <= cus && G > 4;
-    const int slots = eight ? cus : 2 * cus;
-    const int ranges = static_cast<int>(std::min<int64_t>(F / 2, std::max<int64_t>(least, slots / blocks)));
-    // Columns are dealt out in pairs, so that every CU streams as many, or, from three row blocks on (the weights come
-    // from the L2 then), in whole tiles where that leaves a range fewer tiles to compute and to sum: M=301, K=1024,
-    // F=1424 6.8 against 7.9 us, M=192, K=4096, F=2048 13.6 / 15.5; with fewer blocks no faster, or 4 % slower.
-    const int most = 2 * ((F / 2 + ranges - 1) / ranges), pairs_nt = (most + 14 + 15) / 16;   // tiles that a range may touch
-    const int tiles_nt = (F / 16 + ranges - 1) / ranges, gran = blocks > 2 && tiles_nt < pairs_nt && F / 16 >= ranges ? 16 : 2, nt = gran == 16 ? tiles_nt : pairs_nt;
+  GluMidPlan plan;
+  if (glu_mid_plan(M, F, P, G, cus, &plan)) {
 #define PQ_GLU_MID(MF, PA, W)                                                                                                  \
   do {                                                                                                                         \
-    const int lds = glu_mid_lds<MF, PA, W>(nt);                                                                                \
-    launch_kernel((glu_mid_kernel<MF, PA, W>), dim3(static_cast<unsigned>(blocks) * ranges), dim3(64 * W), lds, s, a_d,   \
-                       asg_d, rs_d, M, K, wpk, reinterpret_cast<const uint32_t*>(sz_d), F, ranges, gran, act, h_d, ldh, out_bf16);    \
+    const int lds = glu_mid_lds<MF, PA, W>(plan.nt);                                                                           \
+    launch_kernel((glu_mid_kernel<MF, PA, W>), dim3(static_cast<unsigned>(plan.blocks) * plan.ranges), dim3(64 * W), lds, s,   \
+                  a_d, asg_d, rs_d, M, K, wpk, reinterpret_cast<const uint32_t*>(sz_d), F, plan.ranges, plan.gran,             \
+                  plan.rows_fast ? plan.blocks : plan.ranges, plan.rows_fast ? 1 : 0, act, h_d, ldh, out_bf16);                \
   } while (0)
 #define PQ_GLU_MID_WAVES(MF, PA)          \
   do {                                    \
-    if (eight) PQ_GLU_MID(MF, PA, 8); \
+    if (plan.eight) PQ_GLU_MID(MF, PA, 8); \
     else PQ_GLU_MID(MF, PA, 4);           \
   } while (0)
-    if (P == 2) PQ_GLU_MID_WAVES(2, 2);
-    else if (MF == 2) PQ_GLU_MID_WAVES(2, 1);
-    else if (MF == 3) PQ_GLU_MID_WAVES(3, 1);
+    if (P == 2 && plan.MF == 1) PQ_GLU_MID_WAVES(1, 2);
+    else if (P == 2) PQ_GLU_MID_WAVES(2, 2);
+    else if (plan.MF == 1) PQ_GLU_MID_WAVES(1, 1);
+    else if (plan.MF == 2) PQ_GLU_MID_WAVES(2, 1);
+    else if (plan.MF == 3) PQ_GLU_MID_WAVES(3, 1);
     else PQ_GLU_MID_WAVES(4, 1);
 #undef PQ_GLU_MID_WAVES
 #undef PQ_GLU_MID
