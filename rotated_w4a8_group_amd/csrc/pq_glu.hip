@@ -497,7 +497,7 @@ __global__ __launch_bounds__(512, 1) void glu_prefill_kernel(
 }
 
 // 128 x 128 tiles (64 output columns), two workgroups per CU, one rotation: for grids of up to about two such tiles per
-// CU, where 256 x 256 tiles would leave many CUs without work (pq_gemm_glu says when).
+// CU, where 256 x 256 tiles would leave many CUs without work, and for very short rows (pq_gemm_glu says when).
 using GluSmallTile = PfTile<128, 128, 2, 4, false, false, kPfStages, 1>;
 __global__ __launch_bounds__(512, 4) void glu_small_tile_kernel(
     const uint8_t* __restrict__ A, const float* __restrict__ ASGT, int M, int K, const u32x4* __restrict__ wpk,
@@ -599,10 +599,12 @@ int pq_gemm_glu(const uint8_t* a_d, const float* asg_d, const float* rs_d, int M
   if (!prepared) zero_point_operands(asg_d, rs_d, M, G, P, ws_d, PQ_MAX_PARTITIONS, s);
   // Less than a round of 256 x 256 tiles, that the map above takes whole or in halves: 128 x 128 tiles, two at a time on a CU, up
   // to 2.25 per CU. K=5120, F=8704: M=256 52.9 against 53.4 us, M=300 51.9 / 81.1, M=384 51.6 / 81, M=512 76.0 / 81.5,
-  // M=768 (3.2 per CU) 96.4 / 82.1; K=2048, F=4096: M=512 19.8 / 20.7.
+  // M=768 (3.2 per CU) 96.4 / 82.1; K=2048, F=4096: M=512 19.8 / 20.7. Also for one or two groups, where a tile is mostly its
+  // beginning and its end, which two workgroups overlap: M=1200, K=256, F=4640 16.9 against 18.8 us, M=2048, K=256, F=8704 32.2 /
+  // 33.4; at eight groups 58.1 / 56.1.
   const int rows128 = (M + 127) / 128, cols128 = (2 * F + 127) / 128;
   const int64_t small = static_cast<int64_t>(rows128) * cols128;
-  if (P == 1 && map.full == 0 && map.split < 4 && 4 * small <= 9 * static_cast<int64_t>(cus)) {
+  if (P == 1 && (G <= 2 || (map.full == 0 && map.split < 4 && 4 * small <= 9 * static_cast<int64_t>(cus)))) {
     launch_kernel(glu_small_tile_kernel, dim3(static_cast<unsigned>(small)), dim3(64 * kPfWaves), 0, s, a_d, asgt, M, K, wpk, zpe,
                        static_cast<const u32x4*>(ws_d), s9img, F, act, h_d, ldh, out_bf16, rows128, cols128, vec16);
     return launch_status(what);

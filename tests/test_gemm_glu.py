@@ -157,6 +157,7 @@ def test_few_rows(M, K, F, P, act, ht, pad):
     (297, 1408, 208, 1, "silu", "f16", 0), (68, 2176, 544, 1, "gelu", "bf16", 2), (844, 768, 32, 1, "silu", "bf16", 0), (33, 1152, 1024, 2, "silu", "f16", 0),
     (18, 1024, 720, 1, "gelu", "f16", 0), (735, 384, 944, 1, "silu", "bf16", 2), (50, 640, 8704, 1, "gelu", "bf16", 0), (1000, 256, 512, 1, "silu", "f16", 0),
     (350, 1024, 352, 1, "gelu", "f16", 0), (19, 5120, 16, 1, "silu", "f16", 0), (4000, 128, 16, 1, "gelu", "bf16", 0), (75, 1664, 128, 2, "gelu", "f16", 2),
+    (1300, 256, 4640, 1, "silu", "f16", 0), (1500, 128, 4112, 1, "gelu", "bf16", 2),
     (1200, 384, 8704, 1, "gelu", "bf16", 2), (700, 640, 8704, 2, "silu", "f16", 2), (2000, 256, 512, 1, "silu", "f16", 0), (600, 512, 1024, 1, "gelu", "f16", 0), (17, 256, 48, 2, "gelu", "bf16", 2), (64, 1152, 144, 1, "gelu", "f16", 2), (300, 1024, 1424, 1, "gelu", "bf16", 0),
     (300, 1024, 1424, 2, "silu", "f16", 0), (129, 384, 2064, 2, "silu", "bf16", 8), (513, 640, 4112, 1, "silu", "f16", 0), (257, 256, 8720, 2, "gelu", "f16", 0),
     (1100, 512, 8704, 1, "silu", "bf16", 0), (2048, 256, 8704, 2, "silu", "f16", 0)])
