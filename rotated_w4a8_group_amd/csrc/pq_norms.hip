@@ -86,8 +86,11 @@ __device__ __forceinline__ norm_u32x4 pack8(const float (&v)[8]) {
   return norm_u32x4{w[0], w[1], w[2], w[3]};
 }
 
+// The sigmoid by the hardware's exp2 and reciprocal (1 ulp each): relative error at most (5 + 2 |t|) 2^-24, the exponent's
+// two roundings counting |t| each; +-infinity gives 1 and 0, NaN stays. expf and a division made 8192 rows of 5120 with a
+// channel gate 68.4 us, this 61.5; one row with its own gates 4.5, this 3.8.
 __device__ __forceinline__ float gate_value(float t, int act) {
-  if (act == PQ_GATE_SIGMOID) return 1.0f / (1.0f + expf(-t));
+  if (act == PQ_GATE_SIGMOID) return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504089f * t));
   if (act == PQ_GATE_TANH) return tanhf(t);
   return t;
 }

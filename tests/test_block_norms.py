@@ -5,10 +5,12 @@
 Tolerance, with u = 2^-24 and e = eps/2 of the stored type. The sum of K squares has at most 32
 terms per thread, 6 wave and 15 workgroup additions, so its relative error is at most 55 u; rstd halves it
 and adds the mean's division, the eps, the square root and the division (4 u): 32 u. Products with x, w' (one
-rounding for 1 + w), the gate and the scale: 6 u; the gate's own function at most 8 u (expf and
-tanhf within 2 ulp, a sum and a division). So |n-part| <= 48 u relative, the residual's product 1 u, their sum 1 u:
+rounding for 1 + w), the gate and the scale: 6 u; the gate's own function at most 8 u (tanhf within 2 ulp; the
+sigmoid's exp2, sum and reciprocal 1 ulp each) and, for the sigmoid, 2 |t| u more: its exponent -t log2(e) is a rounded product
+with a rounded constant, and a relative u of the exponent is |t| u of exp(-t). So |n-part| <= (48 + 2 |t|) u relative, the
+residual's product 1 u, their sum 1 u:
 
-    |h - h_ref|   <= e |h_ref|  + 1.01 (50 u |scale a n| + 3 u |res_scale res|) + tiny
+    |h - h_ref|   <= e |h_ref|  + 1.01 ((50 + 2 |t|) u |scale a n| + 3 u |res_scale res|) + tiny      (2 |t|: sigmoid gates)
     |hs - hs_ref| <= e |hs_ref| + 1.01 * 48 u |hs_ref| + tiny          (hs_ref from the kernel's own stored h)
 
 tiny: half the smallest subnormal of the stored type (f32: the smallest normal, as intermediates may flush)."""
@@ -93,12 +95,14 @@ def _act(t, act):
 
 
 def _reference(x, res, w_post, gate, eps, scale, res_scale, gate_act, gemma):
-    """(h_ref in 64 bits, |scale a n|, |res_scale res|)"""
+    """(h_ref in 64 bits, (1 + 2 |t| / 50) |scale a n|, |res_scale res|)"""
     n = _norm(x, w_post, eps, gemma) if w_post is not None else x.double()
+    more = 1.0
     if gate is not None:
         n = n * _act(gate, gate_act)
+        more = 1 + gate.double().abs() / 25 if gate_act == "sigmoid" else 1.0
     n, r = np.float32(scale).item() * n, np.float32(res_scale).item() * res.double()
-    return n + r, n.abs(), r.abs()
+    return n + r, n.abs() * more, r.abs()
 
 
 def _check(tag, got, ref_parts, w_pre, eps, gemma):
@@ -231,3 +235,23 @@ def test_empty_and_streams_and_graph():
         eager = pq.block_norms(x, res, wp, gt, wn)
         torch.cuda.synchronize()
         assert torch.equal(stream_h, eager[0]) and torch.equal(out, eager[1]), r
+
+
+@gpu
+@pytest.mark.parametrize("xt", [torch.float16, torch.bfloat16])
+def test_gate_extremes(xt):
+    """Gates at and past the ends of the functions, infinite and NaN: one value per element, per token and per channel."""
+    vals = torch.tensor([0.0, -0.0, 1e-6, -1e-6, 4.0, -4.0, 20.0, -20.0, 80.0, -80.0, 88.0, -88.0, 200.0, -200.0, 6e4, -6e4], device="cuda").to(xt)
+    K = 256
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn((16, K), generator=g, device="cuda").to(xt)
+    res = torch.randn((16, K), generator=g, device="cuda")
+    for act in ("sigmoid", "tanh"):
+        for gate in (vals[:, None].expand(16, K).contiguous(), vals[:, None].contiguous(), vals.repeat(16)):
+            got = pq.block_norms(x, res, gate=gate, gate_act=act)
+            _check(f"extremes {act} {tuple(gate.shape)}", got, _reference(x, res, None, gate, 1e-6, 1.0, 1.0, act, False), None, 1e-6, False)
+        gate = torch.zeros((16, K), dtype=xt, device="cuda")
+        gate[0], gate[1], gate[2, 7] = float("inf"), float("-inf"), float("nan")
+        h, _ = pq.block_norms(x, res, gate=gate, gate_act=act)
+        assert torch.equal(h[0], res[0] + x[0].float()) and torch.equal(h[1], res[1] if act == "sigmoid" else res[1] - x[1].float())
+        assert torch.isnan(h).sum() == 1 and torch.isnan(h[2, 7])
