@@ -5,13 +5,14 @@
 // registers and neither projection is written to memory, read back or rounded in between. The weights
 // need no layout of their own: a column strip is addressed where it lies.
 //
-// M <= 16: the weight stream bounds it. One 8-wave workgroup per CU takes a contiguous range of output
-// columns (an even number, so that every CU streams the same bytes to within 2 of about 34 columns) and
-// both projections' tiles of that range; the waves split the groups and stream them through private LDS
+// M <= 16, layers of at most one such range per CU: the weight stream bounds it. One 8-wave workgroup per CU takes a
+// contiguous range of output columns (an even number, so that every CU streams the same bytes to within 2 of about 34
+// columns) and both projections' tiles of that range; the waves split the groups and stream them through private LDS
 // rings, as the decode GEMM does, one group ahead of the one that is computed (as many as the ring holds: K=5120,
 // F=4352 7.9 against 7.4 us at M=1, 9.1 against 8.5 at M=7 with two rotations; nor do narrow layers, whose slots are
 // small, gain by more: K=10112, F=64 7.25 us with one group ahead, 7.65 with three).
-// Up to about 128 rows of a wide layer, more of a narrow one: the same for blocks of rows, both operands streamed.
+// Up to about 128 rows of a wide layer, more of a narrow one, and M <= 16 of a wider one: the same for blocks of rows, both operands
+// streamed.
 // Above: the prefill tile with its column strips alternating gate and up (pq_prefill.h); the matrix
 // cores and the fold bound it, as they do the GEMM.
 #include "pq_device.h"
@@ -543,10 +544,15 @@ int pq_gemm_glu(const uint8_t* a_d, const float* asg_d, const float* rs_d, int M
   const size_t N = 2 * static_cast<size_t>(F);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const int out_bf16 = h_type == PQ_BF16;
-  if (M <= 16) {
-    const int MA = M <= 8 ? 8 : 16, most = glu_max_columns(MA, P);
-    // the fewest whole rounds of one range per CU whose ranges are short enough
-    const int64_t rounds = (static_cast<int64_t>(F) + static_cast<int64_t>(cus) * most - 1) / (static_cast<int64_t>(cus) * most);
+  GluMidPlan plan;
+  const bool mid = glu_mid_plan(M, F, P, G, cus, &plan);
+  const int MA = M <= 8 ? 8 : 16, most = glu_max_columns(MA, P);
+  // the fewest whole rounds of one range per CU whose ranges are short enough
+  const int64_t rounds = (static_cast<int64_t>(F) + static_cast<int64_t>(cus) * most - 1) / (static_cast<int64_t>(cus) * most);
+  // Layers too wide for one round go to the row blocks, whose ranges are longer, while those fit: K=5120: M=9, F=9216 13.1 us here,
+  // 11.5 there, M=16, F=8704 with two rotations 17.2 / 13.6; M=12, K=2048, F=19984 14.8 / 11.1. One round: M=16, F=8704 11.7 in
+  // either, M=8, F=1424 6.7 here, 7.4 there.
+  if (M <= 16 && (rounds == 1 || !mid)) {
     const int64_t ranges = std::min<int64_t>(F / 2, rounds * cus);
 #define PQ_GLU_DECODE(MR, MA, PA)                                                                                     \
   launch_kernel((glu_decode_kernel<MR, MA, PA>), dim3(static_cast<unsigned>(ranges)), dim3(64 * kGdWaves), 0, s, a_d, \
@@ -563,8 +569,7 @@ int pq_gemm_glu(const uint8_t* a_d, const float* asg_d, const float* rs_d, int M
 #undef PQ_GLU_DECODE
     return launch_status(what);
   }
-  GluMidPlan plan;
-  if (glu_mid_plan(M, F, P, G, cus, &plan)) {
+  if (mid) {
 #define PQ_GLU_MID(MF, PA, W)                                                                                                  \
   do {                                                                                                                         \
     const int lds = glu_mid_lds<MF, PA, W>(plan.nt);                                                                           \

@@ -139,7 +139,8 @@ def _run(A, S, R, pair, act="silu", dtype=torch.float16, pad=0, **kw):
 @pytest.mark.parametrize("M,K,F,P,act,ht,pad", [
     (1, 128, 16, 1, "silu", "f16", 0), (1, 5120, 8704, 1, "silu", "f16", 0), (2, 384, 48, 2, "gelu", "bf16", 2), (8, 5120, 8704, 1, "gelu", "bf16", 0),
     (8, 1152, 8704, 2, "silu", "f16", 8), (9, 640, 8704, 1, "silu", "bf16", 0), (16, 1152, 8704, 2, "gelu", "f16", 2), (16, 256, 13008, 1, "silu", "f16", 0),
-    (3, 256, 20496, 1, "gelu", "f16", 0), (5, 128, 20496, 2, "silu", "bf16", 0), (1, 17408, 5120, 1, "silu", "f16", 0)])
+    (3, 256, 20496, 1, "gelu", "f16", 0), (5, 128, 20496, 2, "silu", "bf16", 0), (2, 128, 25616, 1, "gelu", "f16", 0), (12, 128, 26000, 2, "silu", "f16", 0), (9, 256, 9216, 1, "silu", "bf16", 2),
+    (16, 640, 8704, 2, "gelu", "f16", 0), (1, 256, 16384, 2, "silu", "f16", 0), (1, 17408, 5120, 1, "silu", "f16", 0)])
 def test_few_rows(M, K, F, P, act, ht, pad):
     print(f"[glu] M={M} K={K} F={F} P={P} {act} {ht}", flush=True)
     pair = Pair(K, F, 600 + M)
