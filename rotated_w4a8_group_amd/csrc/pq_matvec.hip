@@ -33,9 +33,13 @@ constexpr int kMvWaves = 8;
 constexpr int kMvRingBytes = 20480;                  // per wave: the rings fill the LDS
 constexpr int kMvLds = kMvWaves * kMvRingBytes;
 
-// Rows of x held in a ring slot, and the longest range whose slots fit the ring twice: up to 8 rows
-// 20 quarters (6 tiles at most), above that 17 (5 tiles at any 4-column start).
-constexpr int mv_max_quarters(int M) { return M <= 8 ? 20 : 17; }
+// Rows of x held in a ring slot, the most tiles that a range may touch (whose slots fit the ring twice, or, above 8 rows, 5
+// tiles twice and 6 to 8 once) and the longest range that touches no more wherever it starts. Wide layers so take one round
+// where 20 quarters (17 above 8 rows) took a second of the few ranges left over: M=1, K=5120, N=20496 16.6 -> 12.5 us, M=16,
+// N=18432 20.0 -> 12.4, M=6, K=256, three partitions of 22336 columns 7.1 -> 4.5.
+constexpr int mv_rows(int M) { return M == 1 ? 1 : M <= 4 ? 4 : M <= 8 ? 8 : 16; }
+constexpr int mv_max_tiles(int MX) { return MX == 1 ? 9 : MX == 4 ? 8 : MX == 8 ? 7 : 8; }
+constexpr int mv_max_quarters(int M) { return 4 * mv_max_tiles(mv_rows(M)) - 3; }
 
 template <int NT, int MX>
 struct MatvecSlot {
@@ -46,7 +50,7 @@ struct MatvecSlot {
   static constexpr int kBytes = kOffSz + (kSzWords * 4 + 15) / 16 * 16;
   static constexpr int kXLoads = (MX + 3) / 4;                  // 4 rows of 256 B per load
   static constexpr int kLoads = NT + kXLoads + kSzLoads;
-  static constexpr int kDepth = 2;
+  static constexpr int kDepth = 2 * kBytes <= kMvRingBytes ? 2 : 1;
   static_assert(kDepth * kBytes <= kMvRingBytes && (kDepth - 1) * kLoads <= 63, "ring");
 };
 
@@ -201,12 +205,15 @@ __global__ __launch_bounds__(64 * kMvWaves, 1) void matvec_kernel(
   const uint16_t* xp = x + static_cast<size_t>(q) * M * ldx;
 #define PQ_MATVEC_CASE(n) \
   case n: matvec_body<n, MR, MX, kBf16>(xp, ldx, M, K, wpk, sz, N, c0, c1, y, ldy, out_bf16 != 0, smem); break;
+  constexpr int most = mv_max_tiles(MX);
   switch (nt) {
     PQ_MATVEC_CASE(1) PQ_MATVEC_CASE(2) PQ_MATVEC_CASE(3) PQ_MATVEC_CASE(4) PQ_MATVEC_CASE(5)
-    default:
-      if constexpr (MX <= 8) matvec_body<6, MR, MX, kBf16>(xp, ldx, M, K, wpk, sz, N, c0, c1, y, ldy, out_bf16 != 0, smem);
-      break;
+    default: break;
   }
+#define PQ_MATVEC_WIDE(n) \
+  if constexpr (most >= n) { if (nt == n) matvec_body<n, MR, MX, kBf16>(xp, ldx, M, K, wpk, sz, N, c0, c1, y, ldy, out_bf16 != 0, smem); }
+  PQ_MATVEC_WIDE(6) PQ_MATVEC_WIDE(7) PQ_MATVEC_WIDE(8) PQ_MATVEC_WIDE(9)
+#undef PQ_MATVEC_WIDE
 #undef PQ_MATVEC_CASE
 }
 
@@ -234,7 +241,16 @@ int pq_matvec(const uint16_t* x_d, int64_t ldx, int x_type, int M, int K, int P,
   if (!aligned(x_d, 16) || !aligned(wpk_d, 16) || !aligned(sz_d, 4) || !aligned(y_d, 4))
     return set_error(PQ_ERR_ALIGN, "%s: misaligned pointer", what);
   DecodeMap map;
-  decode_map(N, pb1, pb2, cu_count(), mv_max_quarters(M), &map);
+  // As few rounds of one range per CU as the longest ranges allow, all of about the same length; a partition rounds its number
+  // of ranges up, so somewhat longer ones are tried before another round is taken (M=12, N=24576 19.9 -> 15.5 us in two).
+  const int maxq = mv_max_quarters(M), cus = cu_count();
+  for (int slots = cus, done = 0; !done; slots += cus) {
+    if (static_cast<int64_t>(slots) * maxq < N / 4) continue;
+    for (int want = slots; want > std::max(0, slots - 8) && !done; --want) {
+      decode_map(N, pb1, pb2, want, maxq, &map);
+      done = map.wg0[3] <= slots;
+    }
+  }
   const u32x4* wpk = static_cast<const u32x4*>(wpk_d);
   const uint32_t* sz = reinterpret_cast<const uint32_t*>(sz_d);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);

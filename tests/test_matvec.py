@@ -118,7 +118,9 @@ def test_every_row_count(K, N):
 
 @gpu
 @pytest.mark.parametrize("M,K,N,xt", [(1, 5120, 17408, "f16"), (8, 5120, 17408, "bf16"), (16, 5120, 17408, "f16"), (1, 17408, 5120, "bf16"),
-                                      (16, 17408, 5120, "f16"), (3, 256, 40976, "f16"), (16, 256, 40976, "bf16"), (16, 128, 19472, "f16")])
+                                      (16, 17408, 5120, "f16"), (3, 256, 40976, "f16"), (16, 256, 40976, "bf16"), (16, 128, 19472, "f16"),
+                                      (1, 256, 33792, "bf16"), (1, 128, 34000, "f16"), (4, 384, 29696, "f16"), (2, 128, 30000, "bf16"), (8, 256, 25600, "bf16"),
+                                      (5, 640, 20496, "f16"), (16, 256, 29696, "f16"), (12, 1152, 24576, "bf16"), (9, 128, 18432, "f16"), (1, 128, 70000, "f16")])
 def test_layer_sizes(M, K, N, xt):
     print(f"[matvec] M={M} K={K} N={N} {xt}", flush=True)
     layer = Layer(K, N, 520 + M)
@@ -128,7 +130,8 @@ def test_layer_sizes(M, K, N, xt):
 
 @gpu
 @pytest.mark.parametrize("M,K,cuts,xt", [(4, 5120, (6144, 1024, 1024), "bf16"), (1, 384, (128, 48), "f16"), (16, 640, (256, 128, 144), "bf16"),
-                                         (7, 1024, (1280, 128), "f16")])
+                                         (7, 1024, (1280, 128), "f16"), (6, 256, (3584, 15616, 3136), "bf16"), (16, 256, (8192, 8192, 1040), "f16"),
+                                         (1, 128, (16384, 384, 16624), "bf16"), (12, 384, (128, 20352, 16), "bf16")])
 def test_partitions(M, K, cuts, xt):
     N, ends = sum(cuts), np.cumsum(cuts).tolist()
     layer = Layer(K, N, 540 + M)
