@@ -167,3 +167,41 @@ def test_subclass_parameter_and_streams(through_python):
     assert torch.equal(a, want) and torch.equal(b, want)
     with torch.inference_mode():
         assert torch.equal(pq.matvec(x, w["wpk"], w["sz"], 2 * w["F"]), want)
+
+
+@gpu
+def test_two_threads_and_a_graph():
+    """Calls from two Python threads on streams of their own, and captured with their outputs made in the capture, replayed between eager calls."""
+    import threading
+    w = _world()
+    calls = [c for n, c in _calls(w).items() if "no rows" not in n and "whole numbers" not in n]
+    flat = lambda r: [t for t in (r if isinstance(r, tuple) else (r,)) if t is not None]   # noqa: E731
+    want = [[t.clone() for t in flat(c())] for c in calls]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work():
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                for c, ref in zip(calls, want):
+                    if not all(torch.equal(a, b) for a, b in zip(flat(c()), ref)):
+                        failed.append(1)
+        s.synchronize()
+    threads = [threading.Thread(target=work) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs = [flat(c()) for c in calls]
+    for _ in range(3):
+        for o in outs:
+            for t in o:
+                t.fill_(7)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for o, ref in zip(outs, want) for a, b in zip(o, ref))
+        assert all(torch.equal(a, b) for c, ref in zip(calls, want) for a, b in zip(flat(c()), ref))
