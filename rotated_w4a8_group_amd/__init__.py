@@ -29,6 +29,7 @@ LIB_PATH = os.path.join(_HERE, "libpq.so")
 GROUP = 128
 LAYERS = 8
 NO_BOUNDARY = 0x7FFFFFFF
+INT_MAX = 0x7FFFFFFF
 
 PQ_OK = 0
 ERRORS = {
@@ -210,6 +211,12 @@ def _validate(specs, rows=()):
             raise TypeError(f"{name}: expected a contiguous tensor")
 
 
+def _too_large(**sizes):
+    """Raises for the sizes that the library's 32-bit arguments do not hold (ctypes would wrap them, and the library
+    would answer for another size). The callers compare first; this names which."""
+    raise ValueError(", ".join(f"{n}={v}" for n, v in sizes.items() if not -INT_MAX <= v <= INT_MAX) + ": at most 2^31 - 1 in one call")
+
+
 def _partitions(cs, K):
     """P from the channel-scale tensor: [P, K] or [K] (one partition)."""
     if cs.dim() == 2:
@@ -227,6 +234,8 @@ def _prologue_specs(x, rec, cs, K):
         raise ValueError("x: expected a [M, K] tensor")
     if K <= 0 or K % GROUP:
         raise ValueError(f"x: K={K} must be a positive multiple of {GROUP}")
+    if K > INT_MAX or x.shape[0] > INT_MAX:
+        _too_large(M=x.shape[0], K=K)
     P = _partitions(cs, K)
     if not 1 <= P <= 3:
         raise ValueError(f"cs: {P} partitions, expected 1..3")
@@ -333,6 +342,8 @@ def pack_weights(qweight, qzeros, scales, stream=None):
     K, N = qweight.shape[0], qweight.shape[1] * 8
     if K % GROUP or N % 16 or K == 0:
         raise ValueError(f"qweight: K={K} must be a multiple of {GROUP} and N={N} of 16")
+    if K > INT_MAX or N > INT_MAX:
+        _too_large(K=K, N=N)
     _validate([(qweight, "qweight", torch.int32, (K, N // 8)), (qzeros, "qzeros", torch.int32, (K // GROUP, N // 8)),
                (scales, "scales", torch.float16, (K // GROUP, N))])
     wpk = torch.empty(lib().pq_packed_weight_bytes(K, N), dtype=torch.uint8, device=qweight.device)
@@ -352,6 +363,8 @@ def pack_weights5(qweight, qweight_hi, qzeros, qzeros_hi, scales, stream=None):
     K, N = qweight.shape[0], qweight.shape[1] * 8
     if K % GROUP or N % 32 or K == 0:
         raise ValueError(f"qweight: K={K} must be a multiple of {GROUP} and N={N} of 32")
+    if K > INT_MAX or N > INT_MAX:
+        _too_large(K=K, N=N)
     _validate([(qweight, "qweight", torch.int32, (K, N // 8)), (qweight_hi, "qweight_hi", torch.int32, (K, N // 32)),
                (qzeros, "qzeros", torch.int32, (K // GROUP, N // 8)),
                (qzeros_hi, "qzeros_hi", torch.int32, (K // GROUP, N // 32)),
@@ -438,6 +451,8 @@ def rotate(x, rec, cs, out=None, stream=None):
 
 
 def gemm_workspace_bytes(M, N, K):
+    if M > INT_MAX or N > INT_MAX or K > INT_MAX:
+        _too_large(M=M, N=N, K=K)
     return int(lib().pq_gemm_workspace_bytes(M, N, K))
 
 
@@ -450,6 +465,8 @@ def _gemm_common(fn, A, S, RS, wpk, sz, N, pb1, pb2, out, workspace, stream, *, 
     P, M, K = A.shape
     if K == 0 or K % GROUP:
         raise ValueError(f"A: K={K} must be a positive multiple of {GROUP}")
+    if M > INT_MAX or K > INT_MAX or N > INT_MAX or not -INT_MAX <= pb1 <= INT_MAX or not -INT_MAX <= pb2 <= INT_MAX:
+        _too_large(M=M, K=K, N=N, pb1=pb1, pb2=pb2)
     G = K // GROUP
     L = lib()
     need = L.pq_packed_weight5_bytes(K, N) if w5 else L.pq_packed_weight_bytes(K, N)
@@ -503,6 +520,8 @@ def matvec(x, wpk, sz, N, pb1=NO_BOUNDARY, pb2=NO_BOUNDARY, out=None, dtype=None
         raise ValueError(f"x: K={K} must be a positive multiple of {GROUP}")
     if M > 16:
         raise ValueError(f"x: M={M} rows, at most 16 (gemm takes more, quantised)")
+    if K > INT_MAX or N > INT_MAX or not -INT_MAX <= pb1 <= INT_MAX or not -INT_MAX <= pb2 <= INT_MAX:
+        _too_large(K=K, N=N, pb1=pb1, pb2=pb2)
     need = lib().pq_packed_weight_bytes(K, N)
     if need == 0:
         raise ValueError(f"N={N}: not a shape the library packs (N % 16 == 0 needed)")
@@ -562,6 +581,8 @@ def gemm_glu(A, ASG, RS, wpk, sz, F, act="silu", out=None, dtype=None, workspace
     code = GLU_ACTS.get(act)
     if code is None:
         raise ValueError(f"act: {act!r}, expected one of {', '.join(GLU_ACTS)}")
+    if M > INT_MAX or K > INT_MAX or 2 * F > INT_MAX:
+        _too_large(M=M, K=K, **{"2 F": 2 * F})
     L = lib()
     need = L.pq_packed_weight_bytes(K, 2 * F) if F % 16 == 0 else 0
     if need == 0:
@@ -604,6 +625,8 @@ def gemm_noalloc(A, ASG, RS, wpk, sz, N, pb1=NO_BOUNDARY, pb2=NO_BOUNDARY, out=N
     P, M, K = A.shape
     if K == 0 or K % GROUP:
         raise ValueError(f"A: K={K} must be a positive multiple of {GROUP}")
+    if M > INT_MAX or K > INT_MAX or N > INT_MAX or not -INT_MAX <= pb1 <= INT_MAX or not -INT_MAX <= pb2 <= INT_MAX:
+        _too_large(M=M, K=K, N=N, pb1=pb1, pb2=pb2)
     G = K // GROUP
     need = lib().pq_packed_weight_bytes(K, N)
     if need == 0:
@@ -680,6 +703,8 @@ def rotate_quant_tok(x, rec, cs, out=None, stream=None):
 
 
 def gemm_tok_workspace_bytes(M, N, K):
+    if M > INT_MAX or N > INT_MAX or K > INT_MAX:
+        _too_large(M=M, N=N, K=K)
     return int(lib().pq_gemm_tok_workspace_bytes(M, N, K))
 
 
@@ -714,6 +739,8 @@ def block_norms(x, residual, w_post=None, gate=None, w_pre=None, eps=1e-6, scale
     if not isinstance(residual, torch.Tensor):
         raise TypeError("residual: expected a tensor")
     M, K = x.shape
+    if M > INT_MAX or K > INT_MAX:
+        _too_large(M=M, K=K)
     xt = _type_code(x.dtype, "x")
     rt = _type_code(residual.dtype, "residual", 3)
     act = GATE_ACTS.get(gate_act)
