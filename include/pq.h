@@ -47,7 +47,8 @@ enum pq_status {
   PQ_ERR_PARTITION = -4, /* P or the partition boundaries are inconsistent */
   PQ_ERR_RECORDS = -5,   /* a 128-slice of `pairs` is not a permutation of 0..127 */
   PQ_ERR_WORKSPACE = -6, /* workspace smaller than pq_gemm_workspace_bytes() */
-  PQ_ERR_DEVICE = -7     /* the HIP runtime reported an error at launch */
+  PQ_ERR_DEVICE = -7     /* the HIP runtime refused a launch of this call (the kernel before it, where the call has
+                            several, may be queued); what other code left in the thread's last error is not looked at */
 };
 
 /* Element types of the entry points that take several. */

@@ -209,11 +209,11 @@ __global__ void zpe_act_kernel(const float* __restrict__ ASG, const float* __res
   zpa[idx] = u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
 }
 
-void zero_point_operands(const float* asg, const float* rs, int M, int G, int P, void* ws, int ws_parts, void* stream) {
+int zero_point_operands(const float* asg, const float* rs, int M, int G, int P, void* ws, int ws_parts, void* stream) {
   const int64_t zt = static_cast<int64_t>(P) * ((M + 15) / 16) * zpe_chunks(G) * 64;
   float* asgt = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + zpe_act_bytes(M, G, ws_parts));
-  hipLaunchKernelGGL(zpe_act_kernel<false>, dim3(static_cast<unsigned>((zt + 255) / 256)), dim3(256), 0,
-                     static_cast<hipStream_t>(stream), asg, rs, M, G, P, static_cast<u32x4*>(ws), asgt);
+  return launch_kernel(zpe_act_kernel<false>, dim3(static_cast<unsigned>((zt + 255) / 256)), dim3(256), 0,
+                       static_cast<hipStream_t>(stream), asg, rs, M, G, P, static_cast<u32x4*>(ws), asgt);
 }
 
 // Per-token scales broadcast to every group, [P][M][G], for the decode kernel.
@@ -487,20 +487,23 @@ int pq_pack_weights(const int32_t* qweight_d, const int32_t* qzeros_d, const uin
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const int G = K / PQ_GROUP;
   const int64_t words = static_cast<int64_t>(K) * N / 8;
-  hipLaunchKernelGGL(pack_weights_kernel, dim3(static_cast<unsigned>((words + 255) / 256)), dim3(256), 0, s,
-                     qweight_d, K, N, static_cast<uint32_t*>(wpk_d));
+  hipError_t launched = launch_kernel(pack_weights_kernel, dim3(static_cast<unsigned>((words + 255) / 256)), dim3(256), 0, s,
+                                      qweight_d, K, N, static_cast<uint32_t*>(wpk_d));
   const int64_t gn = static_cast<int64_t>(G) * N;
-  hipLaunchKernelGGL(pack_sz_kernel, dim3(static_cast<unsigned>((gn + 255) / 256)), dim3(256), 0, s,
-                     qzeros_d, scales_d, G, N, reinterpret_cast<uint32_t*>(sz_d));
+  if (launched == hipSuccess)
+    launched = launch_kernel(pack_sz_kernel, dim3(static_cast<unsigned>((gn + 255) / 256)), dim3(256), 0, s,
+                             qzeros_d, scales_d, G, N, reinterpret_cast<uint32_t*>(sz_d));
   const int64_t zl = static_cast<int64_t>(N / 16) * zpe_chunks(G) * 64;
   u32x4* zpe = reinterpret_cast<u32x4*>(static_cast<uint8_t*>(wpk_d) + static_cast<size_t>(K) * N / 2);
   auto zk = pack_zpe_kernel<false>;
-  hipLaunchKernelGGL(zk, dim3(static_cast<unsigned>((zl + 255) / 256)), dim3(256), 0, s,
-                     reinterpret_cast<const uint32_t*>(sz_d), G, N, zpe);
+  if (launched == hipSuccess)
+    launched = launch_kernel(zk, dim3(static_cast<unsigned>((zl + 255) / 256)), dim3(256), 0, s,
+                             reinterpret_cast<const uint32_t*>(sz_d), G, N, zpe);
   float* s9 = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(zpe) + static_cast<size_t>(N / 16) * zpe_chunks(G) * 1024);
-  hipLaunchKernelGGL(pack_s9_kernel, dim3(static_cast<unsigned>((gn + 255) / 256)), dim3(256), 0, s,
-                     reinterpret_cast<const uint32_t*>(sz_d), gn, s9);
-  return launch_status("pq_pack_weights");
+  if (launched == hipSuccess)
+    launched = launch_kernel(pack_s9_kernel, dim3(static_cast<unsigned>((gn + 255) / 256)), dim3(256), 0, s,
+                             reinterpret_cast<const uint32_t*>(sz_d), gn, s9);
+  return launch_status("pq_pack_weights", launched);
 }
 
 size_t pq_packed_weight5_bytes(int K, int N) {
@@ -526,23 +529,27 @@ int pq_pack_weights5(const int32_t* qweight_d, const int32_t* qweight_hi_d, cons
   const int G = K / PQ_GROUP;
   const int64_t words = static_cast<int64_t>(K) * N / 8;
   uint8_t* wb = static_cast<uint8_t*>(wpk_d);
-  hipLaunchKernelGGL(pack_weights_kernel, dim3(static_cast<unsigned>((words + 255) / 256)), dim3(256), 0, s,
-                     qweight_d, K, N, reinterpret_cast<uint32_t*>(wb));
+  hipError_t launched = launch_kernel(pack_weights_kernel, dim3(static_cast<unsigned>((words + 255) / 256)), dim3(256), 0, s,
+                                      qweight_d, K, N, reinterpret_cast<uint32_t*>(wb));
   const int64_t hw = static_cast<int64_t>(N / 16) * G * 64;
-  hipLaunchKernelGGL(pack_hi_kernel, dim3(static_cast<unsigned>((hw + 255) / 256)), dim3(256), 0, s,
-                     qweight_hi_d, K, N, reinterpret_cast<uint32_t*>(wb + static_cast<size_t>(K) * N / 2));
+  if (launched == hipSuccess)
+    launched = launch_kernel(pack_hi_kernel, dim3(static_cast<unsigned>((hw + 255) / 256)), dim3(256), 0, s,
+                             qweight_hi_d, K, N, reinterpret_cast<uint32_t*>(wb + static_cast<size_t>(K) * N / 2));
   const int64_t gn = static_cast<int64_t>(G) * N;
-  hipLaunchKernelGGL(pack_sz5_kernel, dim3(static_cast<unsigned>((gn + 255) / 256)), dim3(256), 0, s,
-                     qzeros_d, qzeros_hi_d, scales_d, G, N, reinterpret_cast<uint32_t*>(sz_d));
+  if (launched == hipSuccess)
+    launched = launch_kernel(pack_sz5_kernel, dim3(static_cast<unsigned>((gn + 255) / 256)), dim3(256), 0, s,
+                             qzeros_d, qzeros_hi_d, scales_d, G, N, reinterpret_cast<uint32_t*>(sz_d));
   const int64_t zl = static_cast<int64_t>(N / 16) * zpe_chunks(G) * 64;
   u32x4* zpe = reinterpret_cast<u32x4*>(wb + static_cast<size_t>(K) * N / 2 + static_cast<size_t>(K) * N / 8);
   auto zk = pack_zpe_kernel<true>;
-  hipLaunchKernelGGL(zk, dim3(static_cast<unsigned>((zl + 255) / 256)), dim3(256), 0, s,
-                     reinterpret_cast<const uint32_t*>(sz_d), G, N, zpe);
+  if (launched == hipSuccess)
+    launched = launch_kernel(zk, dim3(static_cast<unsigned>((zl + 255) / 256)), dim3(256), 0, s,
+                             reinterpret_cast<const uint32_t*>(sz_d), G, N, zpe);
   float* s9 = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(zpe) + static_cast<size_t>(N / 16) * zpe_chunks(G) * 1024);
-  hipLaunchKernelGGL(pack_s9_kernel, dim3(static_cast<unsigned>((gn + 255) / 256)), dim3(256), 0, s,
-                     reinterpret_cast<const uint32_t*>(sz_d), gn, s9);
-  return launch_status("pq_pack_weights5");
+  if (launched == hipSuccess)
+    launched = launch_kernel(pack_s9_kernel, dim3(static_cast<unsigned>((gn + 255) / 256)), dim3(256), 0, s,
+                             reinterpret_cast<const uint32_t*>(sz_d), gn, s9);
+  return launch_status("pq_pack_weights5", launched);
 }
 
 size_t pq_gemm_workspace_bytes(int M, int N, int K) {
@@ -583,22 +590,24 @@ static int gemm_launch(const char* what, const uint8_t* a_d, const float* a_scal
   const u32x4* zpe = reinterpret_cast<const u32x4*>(wb + static_cast<size_t>(K) * N / 2 + (kW5 ? static_cast<size_t>(K) * N / 8 : 0));
   const float* s9img = reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(zpe) +
                                                       static_cast<size_t>(N / 16) * zpe_chunks(G) * 1024);
+  hipError_t launched = hipSuccess;
   if (M <= 16) {
     const float* asg = a_scale;
     if (kTok) {
       // the decode kernel folds per group: give every group the token's scale
       float* ex = static_cast<float*>(ws_d);
       const int64_t n = static_cast<int64_t>(P) * M * G;
-      hipLaunchKernelGGL(tok_expand_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, s,
-                         a_scale, P * M, G, ex);
+      launched = launch_kernel(tok_expand_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, s,
+                               a_scale, P * M, G, ex);
       asg = ex;
     }
     DecodeMap map;
     decode_map(N, pb1, pb2, cu_count(), kDecMaxQ, &map);
     auto dec = gemm_decode_kernel<kI8, kW5>;
-    hipLaunchKernelGGL(dec, dim3(map.wg0[3]), dim3(64 * kDecWaves), 0, s,
-                       a_d, asg, rs_d, M, K, wpk, hi, sz, N, map, y_d, ldy);
-    return launch_status(what);
+    if (launched == hipSuccess)
+      launched = launch_kernel(dec, dim3(map.wg0[3]), dim3(64 * kDecWaves), 0, s,
+                               a_d, asg, rs_d, M, K, wpk, hi, sz, N, map, y_d, ldy);
+    return launch_status(what, launched);
   }
   // 256x256 tiles (one workgroup per CU) unless a partition boundary is not on
   // a 256-column line
@@ -616,15 +625,16 @@ static int gemm_launch(const char* what, const uint8_t* a_d, const float* a_scal
                      : reinterpret_cast<float*>(static_cast<uint8_t*>(ws_d) + zpe_act_bytes(M, G, ws_parts));
   if (!prepared) {
     const int64_t zt = static_cast<int64_t>(P) * ((M + 15) / 16) * zpe_chunks(G) * 64;
-    hipLaunchKernelGGL(zpe_act_kernel<kTok>, dim3(static_cast<unsigned>((zt + 255) / 256)), dim3(256), 0, s,
-                       a_scale, rs_d, M, G, P, zpa, asgt);
+    launched = launch_kernel(zpe_act_kernel<kTok>, dim3(static_cast<unsigned>((zt + 255) / 256)), dim3(256), 0, s,
+                             a_scale, rs_d, M, G, P, zpa, asgt);
   }
   // 16-byte output stores need a 16-byte aligned y and a row pitch of 8 elements
   const bool vec16 = aligned(y_d, 16) && ldy % 8 == 0;
   auto prefill = gemm_prefill_kernel<kTok, kI8, kW5>;
-  hipLaunchKernelGGL(prefill, dim3(static_cast<unsigned>(grid)), dim3(64 * kPfWaves), 0, s,
-                     a_d, kTok ? a_scale : asgt, M, K, wpk, hi, zpe, zpa, s9img, N, pb1, pb2, y_d, ldy, map, vec16);
-  return launch_status(what);
+  if (launched == hipSuccess)
+    launched = launch_kernel(prefill, dim3(static_cast<unsigned>(grid)), dim3(64 * kPfWaves), 0, s,
+                             a_d, kTok ? a_scale : asgt, M, K, wpk, hi, zpe, zpa, s9img, N, pb1, pb2, y_d, ldy, map, vec16);
+  return launch_status(what, launched);
 }
 
 // Shared validation of pq_gemm / pq_gemm_tok; returns PQ_OK to go on, 1 for the M == 0 no-op.

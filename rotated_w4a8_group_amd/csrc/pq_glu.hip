@@ -544,6 +544,7 @@ int pq_gemm_glu(const uint8_t* a_d, const float* asg_d, const float* rs_d, int M
   const size_t N = 2 * static_cast<size_t>(F);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const int out_bf16 = h_type == PQ_BF16;
+  hipError_t launched = hipSuccess;
   GluMidPlan plan;
   const bool mid = glu_mid_plan(M, F, P, G, cus, &plan);
   const int MA = M <= 8 ? 8 : 16, most = glu_max_columns(MA, P);
@@ -554,9 +555,9 @@ int pq_gemm_glu(const uint8_t* a_d, const float* asg_d, const float* rs_d, int M
   // either, M=8, F=1424 6.7 here, 7.4 there.
   if (M <= 16 && (rounds == 1 || !mid)) {
     const int64_t ranges = std::min<int64_t>(F / 2, rounds * cus);
-#define PQ_GLU_DECODE(MR, MA, PA)                                                                                     \
-  launch_kernel((glu_decode_kernel<MR, MA, PA>), dim3(static_cast<unsigned>(ranges)), dim3(64 * kGdWaves), 0, s, a_d, \
-                     asg_d, rs_d, M, K, wpk, reinterpret_cast<const uint32_t*>(sz_d), F, act, h_d, ldh, out_bf16)
+#define PQ_GLU_DECODE(MR, MA, PA)                                                                                                 \
+  launched = launch_kernel((glu_decode_kernel<MR, MA, PA>), dim3(static_cast<unsigned>(ranges)), dim3(64 * kGdWaves), 0, s, a_d, \
+                           asg_d, rs_d, M, K, wpk, reinterpret_cast<const uint32_t*>(sz_d), F, act, h_d, ldh, out_bf16)
     if (P == 1) {
       if (M == 1) PQ_GLU_DECODE(1, 8, 1);
       else if (M <= 8) PQ_GLU_DECODE(4, 8, 1);
@@ -567,15 +568,15 @@ int pq_gemm_glu(const uint8_t* a_d, const float* asg_d, const float* rs_d, int M
       else PQ_GLU_DECODE(4, 16, 2);
     }
 #undef PQ_GLU_DECODE
-    return launch_status(what);
+    return launch_status(what, launched);
   }
   if (mid) {
 #define PQ_GLU_MID(MF, PA, W)                                                                                                  \
   do {                                                                                                                         \
     const int lds = glu_mid_lds<MF, PA, W>(plan.nt);                                                                           \
-    launch_kernel((glu_mid_kernel<MF, PA, W>), dim3(static_cast<unsigned>(plan.blocks) * plan.ranges), dim3(64 * W), lds, s,   \
-                  a_d, asg_d, rs_d, M, K, wpk, reinterpret_cast<const uint32_t*>(sz_d), F, plan.ranges, plan.gran,             \
-                  plan.rows_fast ? plan.blocks : plan.ranges, plan.rows_fast ? 1 : 0, act, h_d, ldh, out_bf16);                \
+    launched = launch_kernel((glu_mid_kernel<MF, PA, W>), dim3(static_cast<unsigned>(plan.blocks) * plan.ranges), dim3(64 * W), lds, s, \
+                             a_d, asg_d, rs_d, M, K, wpk, reinterpret_cast<const uint32_t*>(sz_d), F, plan.ranges, plan.gran,  \
+                             plan.rows_fast ? plan.blocks : plan.ranges, plan.rows_fast ? 1 : 0, act, h_d, ldh, out_bf16);     \
   } while (0)
 #define PQ_GLU_MID_WAVES(MF, PA)          \
   do {                                    \
@@ -590,7 +591,7 @@ int pq_gemm_glu(const uint8_t* a_d, const float* asg_d, const float* rs_d, int M
     else PQ_GLU_MID_WAVES(4, 1);
 #undef PQ_GLU_MID_WAVES
 #undef PQ_GLU_MID
-    return launch_status(what);
+    return launch_status(what, launched);
   }
   if (static_cast<int64_t>((M + 127) / 128) * ((2 * F + 127) / 128) * 8 > 0x7FFFFFFF)
     return set_error(PQ_ERR_SHAPE, "%s: problem too large", what);
@@ -601,7 +602,10 @@ int pq_gemm_glu(const uint8_t* a_d, const float* asg_d, const float* rs_d, int M
   const float* s9img = reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(zpe) + (N / 16) * zpe_chunks(G) * 1024);
   const float* asgt = reinterpret_cast<const float*>(static_cast<const uint8_t*>(ws_d) + zpe_act_bytes(M, G, PQ_MAX_PARTITIONS));
   const bool vec16 = aligned(h_d, 16) && ldh % 8 == 0;
-  if (!prepared) zero_point_operands(asg_d, rs_d, M, G, P, ws_d, PQ_MAX_PARTITIONS, s);
+  if (!prepared) {
+    const int rc = launch_status(what, zero_point_operands(asg_d, rs_d, M, G, P, ws_d, PQ_MAX_PARTITIONS, s));
+    if (rc != PQ_OK) return rc;
+  }
   // Less than a round of 256 x 256 tiles, that the map above takes whole or in halves: 128 x 128 tiles, two at a time on a CU, up
   // to 2.25 per CU. K=5120, F=8704: M=256 52.9 against 53.4 us, M=300 51.9 / 81.1, M=384 51.6 / 81, M=512 76.0 / 81.5,
   // M=768 (3.2 per CU) 96.4 / 82.1; K=2048, F=4096: M=512 19.8 / 20.7. Also for one or two groups, where a tile is mostly its
@@ -610,14 +614,14 @@ int pq_gemm_glu(const uint8_t* a_d, const float* asg_d, const float* rs_d, int M
   const int rows128 = (M + 127) / 128, cols128 = (2 * F + 127) / 128;
   const int64_t small = static_cast<int64_t>(rows128) * cols128;
   if (P == 1 && (G <= 2 || (map.full == 0 && map.split < 4 && 4 * small <= 9 * static_cast<int64_t>(cus)))) {
-    launch_kernel(glu_small_tile_kernel, dim3(static_cast<unsigned>(small)), dim3(64 * kPfWaves), 0, s, a_d, asgt, M, K, wpk, zpe,
-                       static_cast<const u32x4*>(ws_d), s9img, F, act, h_d, ldh, out_bf16, rows128, cols128, vec16);
-    return launch_status(what);
+    launched = launch_kernel(glu_small_tile_kernel, dim3(static_cast<unsigned>(small)), dim3(64 * kPfWaves), 0, s, a_d, asgt, M, K, wpk, zpe,
+                             static_cast<const u32x4*>(ws_d), s9img, F, act, h_d, ldh, out_bf16, rows128, cols128, vec16);
+    return launch_status(what, launched);
   }
   auto kern = P == 1 ? glu_prefill_kernel<1> : glu_prefill_kernel<2>;
-  launch_kernel(kern, dim3(static_cast<unsigned>(grid)), dim3(64 * kPfWaves), 0, s, a_d, asgt, M, K, wpk, zpe,
-                     static_cast<const u32x4*>(ws_d), s9img, F, act, h_d, ldh, out_bf16, map, vec16);
-  return launch_status(what);
+  launched = launch_kernel(kern, dim3(static_cast<unsigned>(grid)), dim3(64 * kPfWaves), 0, s, a_d, asgt, M, K, wpk, zpe,
+                           static_cast<const u32x4*>(ws_d), s9img, F, act, h_d, ldh, out_bf16, map, vec16);
+  return launch_status(what, launched);
 }
 
 }  // extern "C"

@@ -33,10 +33,11 @@ int set_error(int code, const char* fmt, ...) {
 
 void clear_error() { g_last_error.clear(); }
 
-int launch_status(const char* what) {
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return set_error(PQ_ERR_DEVICE, "%s: launch failed: %s", what, hipGetErrorString(e));
-  return PQ_OK;
+int launch_status(const char* what, int hip_error) {
+  const hipError_t e = static_cast<hipError_t>(hip_error);
+  if (e == hipSuccess) return PQ_OK;
+  (void)hipGetLastError();   // reported here: not to be found again by the thread's next check
+  return set_error(PQ_ERR_DEVICE, "%s: launch failed: %s", what, hipGetErrorString(e));
 }
 
 int cu_count() {

@@ -14,8 +14,8 @@ void clear_error();
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// PQ_OK, or PQ_ERR_DEVICE with the message of the launch that just failed.
-int launch_status(const char* what);
+// PQ_OK, or PQ_ERR_DEVICE with the message of a launch that failed with this HIP error.
+int launch_status(const char* what, int hip_error);
 
 // Compute units of the current device (cached per device).
 int cu_count();
@@ -28,7 +28,7 @@ int check_partitions(int P, int pb1, int pb2, int N);
 size_t zpe_act_bytes(int M, int G, int P);
 size_t asgt_bytes(int M, int G, int P);
 
-// Fills the prefill GEMM's workspace from ASG and RS (P partitions, laid out for ws_parts).
-void zero_point_operands(const float* asg, const float* rs, int M, int G, int P, void* ws, int ws_parts, void* stream);
+// Fills the prefill GEMM's workspace from ASG and RS (P partitions, laid out for ws_parts). Returns the launch's HIP error.
+int zero_point_operands(const float* asg, const float* rs, int M, int G, int P, void* ws, int ws_parts, void* stream);
 
 }  // namespace pq

@@ -254,18 +254,19 @@ int pq_matvec(const uint16_t* x_d, int64_t ldx, int x_type, int M, int K, int P,
   const u32x4* wpk = static_cast<const u32x4*>(wpk_d);
   const uint32_t* sz = reinterpret_cast<const uint32_t*>(sz_d);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-#define PQ_MATVEC_LAUNCH(MR, MX)                                                                                  \
-  do {                                                                                                            \
-    auto kern = x_type == PQ_BF16 ? matvec_kernel<true, MR, MX> : matvec_kernel<false, MR, MX>;                   \
-    launch_kernel(kern, dim3(map.wg0[3]), dim3(64 * kMvWaves), 0, s, x_d, ldx, M, K, wpk, sz, N, map, y_d, ldy, \
-                       y_type == PQ_BF16 ? 1 : 0);                                                                 \
+  hipError_t launched;
+#define PQ_MATVEC_LAUNCH(MR, MX)                                                                                            \
+  do {                                                                                                                      \
+    auto kern = x_type == PQ_BF16 ? matvec_kernel<true, MR, MX> : matvec_kernel<false, MR, MX>;                             \
+    launched = launch_kernel(kern, dim3(map.wg0[3]), dim3(64 * kMvWaves), 0, s, x_d, ldx, M, K, wpk, sz, N, map, y_d, ldy, \
+                             y_type == PQ_BF16 ? 1 : 0);                                                                    \
   } while (0)
   if (M == 1) PQ_MATVEC_LAUNCH(1, 1);
   else if (M <= 4) PQ_MATVEC_LAUNCH(4, 4);
   else if (M <= 8) PQ_MATVEC_LAUNCH(4, 8);
   else PQ_MATVEC_LAUNCH(4, 16);
 #undef PQ_MATVEC_LAUNCH
-  return launch_status(what);
+  return launch_status(what, launched);
 }
 
 }  // extern "C"

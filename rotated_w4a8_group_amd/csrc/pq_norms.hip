@@ -276,31 +276,28 @@ static void norms_shape(int M, int K, int* nc, int* threads) {
 }
 
 template <bool kX, int kR, bool kO>
-static void norms_launch(const NormArgs& a, hipStream_t s) {
+static hipError_t norms_launch(const NormArgs& a, hipStream_t s) {
   int nc, threads;
   norms_shape(a.M, a.K, &nc, &threads);
 #define PQ_NORM_LAUNCH(NC) \
-  launch_kernel((block_norms_kernel<NC, kX, kR, kO>), dim3(static_cast<unsigned>(a.M)), dim3(threads), 0, s, a)
+  return launch_kernel((block_norms_kernel<NC, kX, kR, kO>), dim3(static_cast<unsigned>(a.M)), dim3(threads), 0, s, a)
   if (nc == 1) PQ_NORM_LAUNCH(1);
-  else if (nc == 2) PQ_NORM_LAUNCH(2);
-  else if (nc == 3) PQ_NORM_LAUNCH(3);
-  else PQ_NORM_LAUNCH(4);
+  if (nc == 2) PQ_NORM_LAUNCH(2);
+  if (nc == 3) PQ_NORM_LAUNCH(3);
+  PQ_NORM_LAUNCH(4);
 #undef PQ_NORM_LAUNCH
 }
 template <bool kX, int kR>
-static void norms_for_out(const NormArgs& a, int out_type, hipStream_t s) {
-  if (out_type == PQ_BF16) norms_launch<kX, kR, true>(a, s);
-  else norms_launch<kX, kR, false>(a, s);
+static hipError_t norms_for_out(const NormArgs& a, int out_type, hipStream_t s) {
+  return out_type == PQ_BF16 ? norms_launch<kX, kR, true>(a, s) : norms_launch<kX, kR, false>(a, s);
 }
 template <bool kX>
-static void norms_for_res(const NormArgs& a, int res_type, int out_type, hipStream_t s) {
-  if (res_type == PQ_F32) norms_for_out<kX, PQ_F32>(a, out_type, s);
-  else if (res_type == PQ_BF16) norms_for_out<kX, PQ_BF16>(a, out_type, s);
-  else norms_for_out<kX, PQ_F16>(a, out_type, s);
+static hipError_t norms_for_res(const NormArgs& a, int res_type, int out_type, hipStream_t s) {
+  if (res_type == PQ_F32) return norms_for_out<kX, PQ_F32>(a, out_type, s);
+  return res_type == PQ_BF16 ? norms_for_out<kX, PQ_BF16>(a, out_type, s) : norms_for_out<kX, PQ_F16>(a, out_type, s);
 }
-static void norms_for_x(const NormArgs& a, int x_type, int res_type, int out_type, hipStream_t s) {
-  if (x_type == PQ_BF16) norms_for_res<true>(a, res_type, out_type, s);
-  else norms_for_res<false>(a, res_type, out_type, s);
+static hipError_t norms_for_x(const NormArgs& a, int x_type, int res_type, int out_type, hipStream_t s) {
+  return x_type == PQ_BF16 ? norms_for_res<true>(a, res_type, out_type, s) : norms_for_res<false>(a, res_type, out_type, s);
 }
 
 // Whether any byte of the M rows of `wa` bytes every `lda` bytes at a is one of b's rows. Exact where
@@ -380,8 +377,7 @@ int pq_block_norms(const void* x_d, int64_t ldx, int x_type, const void* res_d, 
   NormArgs a{x_d, res_d, w_post_d, gate_d, w_pre_d, res_out_d, hs_d, ldx, ldr, ldg, ldo, ldh, M, K,
              gate_cols, gate_act, eps, scale, res_scale, gemma ? 1.0f : 0.0f};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  norms_for_x(a, x_type, res_type, out_type, s);
-  return launch_status(what);
+  return launch_status(what, norms_for_x(a, x_type, res_type, out_type, s));
 }
 
 }  // extern "C"

@@ -901,10 +901,9 @@ static int rotate_quant_launch(const char* what, const uint16_t* x_d, int64_t ld
     asgt = reinterpret_cast<float*>(static_cast<uint8_t*>(ws_d) + zpe_act_bytes(M, G, PQ_MAX_PARTITIONS));
   }
   auto kern = vec16 ? rotate_quant_kernel<true, kI8, kWs> : rotate_quant_kernel<false, kI8, kWs>;
-  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
-                     reinterpret_cast<hipStream_t>(stream), x_d, ldx, M, K, P,
-                     static_cast<const uint2*>(rec_d), cs_d, a_d, asg_d, rs_d, tok, chunks, zpa, asgt);
-  return launch_status(what);
+  return launch_status(what, launch_kernel(kern, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
+                                           reinterpret_cast<hipStream_t>(stream), x_d, ldx, M, K, P,
+                                           static_cast<const uint2*>(rec_d), cs_d, a_d, asg_d, rs_d, tok, chunks, zpa, asgt));
 }
 
 }  // namespace pq
@@ -945,9 +944,8 @@ int pq_rotate(const uint16_t* x_d, int64_t ldx, int x_type, int M, int K, int P,
   const bool vec16 = aligned(x_d, 16) && (ldx % 8) == 0;
   auto kern = x_type == PQ_BF16 ? (vec16 ? rotate_kernel<true, true> : rotate_kernel<false, true>)
                                 : (vec16 ? rotate_kernel<true, false> : rotate_kernel<false, false>);
-  launch_kernel(kern, dim3(static_cast<unsigned>(chunks) * G * P), dim3(64), 0, reinterpret_cast<hipStream_t>(stream),
-                     x_d, static_cast<uint32_t>(ldx), M, K, divisor(G), divisor(P), static_cast<const uint2*>(rec_d), cs_d, y_d, tok);
-  return launch_status(what);
+  return launch_status(what, launch_kernel(kern, dim3(static_cast<unsigned>(chunks) * G * P), dim3(64), 0, reinterpret_cast<hipStream_t>(stream), x_d,
+                                           static_cast<uint32_t>(ldx), M, K, divisor(G), divisor(P), static_cast<const uint2*>(rec_d), cs_d, y_d, tok));
 }
 
 int pq_rotate_quant_for_gemm(const uint16_t* x_d, int64_t ldx, int M, int K, int P, const void* rec_d,
@@ -998,18 +996,19 @@ int pq_rotate_quant_tok(const uint16_t* x_d, int64_t ldx, int M, int K, int P, c
   const int npg = (G + kTokWaves - 1) / kTokWaves;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const uint2* rec = static_cast<const uint2*>(rec_d);
+  hipError_t launched;
 #define PQ_TOK_LAUNCH(NPG)                                                                          \
   do {                                                                                              \
     auto kern = vec16 ? rotate_quant_tok_kernel<NPG, true> : rotate_quant_tok_kernel<NPG, false>;   \
-    hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(blocks)), dim3(64 * kTokWaves), 0, s, x_d, ldx, \
-                       M, K, P, rec, cs_d, a_d, as_d, rs_d);                                        \
+    launched = launch_kernel(kern, dim3(static_cast<unsigned>(blocks)), dim3(64 * kTokWaves), 0, s, \
+                             x_d, ldx, M, K, P, rec, cs_d, a_d, as_d, rs_d);                        \
   } while (0)
   if (npg <= 1) PQ_TOK_LAUNCH(1);
   else if (npg <= 3) PQ_TOK_LAUNCH(3);
   else if (npg <= 5) PQ_TOK_LAUNCH(5);
   else PQ_TOK_LAUNCH(9);
 #undef PQ_TOK_LAUNCH
-  return launch_status("pq_rotate_quant_tok");
+  return launch_status("pq_rotate_quant_tok", launched);
 }
 
 int pq_add_rms_rotate_quant(const uint16_t* x_d, int64_t ldx, const uint16_t* res_d, int64_t ldr,
@@ -1050,19 +1049,20 @@ int pq_add_rms_rotate_quant(const uint16_t* x_d, int64_t ldx, const uint16_t* re
   const int64_t blocks = static_cast<int64_t>((M + 3) / 4) * (chunked ? npg : 1);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const uint2* rec = static_cast<const uint2*>(rec_d);
+  hipError_t launched;
 #define PQ_PROD_LAUNCH(NPG)                                                                           \
   do {                                                                                                \
     auto kern = chunked ? add_rms_rotate_quant_kernel<NPG, true> : add_rms_rotate_quant_kernel<NPG, false>; \
-    hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(blocks)), dim3(64 * kTokWaves), 0, s, x_d, ldx, \
-                       res_d, ldr, w_d, eps, gemma ? 1 : 0, M, K, P, rec, cs_d, res_out_d, ldo, hs_d,   \
-                       a_d, asg_d, rs_d);                                                             \
+    launched = launch_kernel(kern, dim3(static_cast<unsigned>(blocks)), dim3(64 * kTokWaves), 0, s, x_d, ldx, \
+                             res_d, ldr, w_d, eps, gemma ? 1 : 0, M, K, P, rec, cs_d, res_out_d, ldo, \
+                             hs_d, a_d, asg_d, rs_d);                                                 \
   } while (0)
   if (npg <= 1) PQ_PROD_LAUNCH(1);
   else if (npg <= 3) PQ_PROD_LAUNCH(3);
   else if (npg <= 5) PQ_PROD_LAUNCH(5);
   else PQ_PROD_LAUNCH(9);
 #undef PQ_PROD_LAUNCH
-  return launch_status(what);
+  return launch_status(what, launched);
 }
 
 int pq_e4m3_encode(const float* q_d, uint8_t* codes_d, int64_t n, pq_stream_t stream) {
@@ -1075,9 +1075,8 @@ int pq_e4m3_encode(const float* q_d, uint8_t* codes_d, int64_t n, pq_stream_t st
   const int64_t threads = (n + 1) / 2;
   const int64_t blocks = (threads + 255) / 256;
   if (blocks > 0x7FFFFFFF) return set_error(PQ_ERR_SHAPE, "pq_e4m3_encode: n too large");
-  hipLaunchKernelGGL(e4m3_encode_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
-                     reinterpret_cast<hipStream_t>(stream), q_d, codes_d, n);
-  return launch_status("pq_e4m3_encode");
+  return launch_status("pq_e4m3_encode", launch_kernel(e4m3_encode_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
+                       reinterpret_cast<hipStream_t>(stream), q_d, codes_d, n));
 }
 
 int pq_recip_f32(const float* x_d, float* y_d, int64_t n, pq_stream_t stream) {
@@ -1089,9 +1088,8 @@ int pq_recip_f32(const float* x_d, float* y_d, int64_t n, pq_stream_t stream) {
   if (!aligned(x_d, 4) || !aligned(y_d, 4)) return set_error(PQ_ERR_ALIGN, "pq_recip_f32: misaligned pointer");
   const int64_t blocks = (n + 255) / 256;
   if (blocks > 0x7FFFFFFF) return set_error(PQ_ERR_SHAPE, "pq_recip_f32: n too large");
-  hipLaunchKernelGGL(recip_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
-                     reinterpret_cast<hipStream_t>(stream), x_d, y_d, n);
-  return launch_status("pq_recip_f32");
+  return launch_status("pq_recip_f32", launch_kernel(recip_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
+                       reinterpret_cast<hipStream_t>(stream), x_d, y_d, n));
 }
 
 int pq_bf16_round(const float* x_d, uint16_t* out_d, int64_t n, pq_stream_t stream) {
@@ -1104,9 +1102,8 @@ int pq_bf16_round(const float* x_d, uint16_t* out_d, int64_t n, pq_stream_t stre
   const int64_t threads = (n + 1) / 2;
   const int64_t blocks = (threads + 255) / 256;
   if (blocks > 0x7FFFFFFF) return set_error(PQ_ERR_SHAPE, "pq_bf16_round: n too large");
-  hipLaunchKernelGGL(bf16_round_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
-                     reinterpret_cast<hipStream_t>(stream), x_d, out_d, n);
-  return launch_status("pq_bf16_round");
+  return launch_status("pq_bf16_round", launch_kernel(bf16_round_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
+                       reinterpret_cast<hipStream_t>(stream), x_d, out_d, n));
 }
 
 }  // extern "C"
