@@ -593,10 +593,19 @@ int pq_gemm_glu(const uint8_t* a_d, const float* asg_d, const float* rs_d, int M
 #undef PQ_GLU_MID
     return launch_status(what, launched);
   }
-  if (static_cast<int64_t>((M + 127) / 128) * ((2 * F + 127) / 128) * 8 > 0x7FFFFFFF)
-    return set_error(PQ_ERR_SHAPE, "%s: problem too large", what);
+  // Less than a round of 256 x 256 tiles, that the map takes whole or in halves: 128 x 128 tiles, two at a time on a CU, up
+  // to 2.25 per CU. K=5120, F=8704: M=256 52.9 against 53.4 us, M=300 51.9 / 81.1, M=384 51.6 / 81, M=512 76.0 / 81.5,
+  // M=768 (3.2 per CU) 96.4 / 82.1; K=2048, F=4096: M=512 19.8 / 20.7. Also for one or two groups, where a tile is mostly its
+  // beginning and its end, which two workgroups overlap: M=1200, K=256, F=4640 16.9 against 18.8 us, M=2048, K=256, F=8704 32.2 /
+  // 33.4; at eight groups 58.1 / 56.1.
+  const int rows128 = (M + 127) / 128, cols128 = (2 * F + 127) / 128;
+  const int64_t small = static_cast<int64_t>(rows128) * cols128;
+  if (small * 8 > 0x7FFFFFFF) return set_error(PQ_ERR_SHAPE, "%s: problem too large", what);
   const PrefillMap map = prefill_map(M, 2 * F, P == 1 ? kPfWide : kPfPair, cus);
-  const int64_t grid = static_cast<int64_t>(map.full) + static_cast<int64_t>(map.ntiles - map.full) * map.split;
+  const bool small_tiles = P == 1 && (G <= 2 || (map.full == 0 && map.split < 4 && 4 * small <= 9 * static_cast<int64_t>(cus)));
+  const int64_t grid = small_tiles ? small : static_cast<int64_t>(map.full) + static_cast<int64_t>(map.ntiles - map.full) * map.split;
+  if (grid * 64 * kPfWaves > 0xFFFFFFFFll)   // the runtime counts a launch's threads in 32 bits
+    return set_error(PQ_ERR_SHAPE, "%s: M=%d rows too many for one call (split the rows)", what, M);
   const uint8_t* wb = static_cast<const uint8_t*>(wpk_d);
   const u32x4* zpe = reinterpret_cast<const u32x4*>(wb + static_cast<size_t>(K) * N / 2);
   const float* s9img = reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(zpe) + (N / 16) * zpe_chunks(G) * 1024);
@@ -606,15 +615,8 @@ int pq_gemm_glu(const uint8_t* a_d, const float* asg_d, const float* rs_d, int M
     const int rc = launch_status(what, zero_point_operands(asg_d, rs_d, M, G, P, ws_d, PQ_MAX_PARTITIONS, s));
     if (rc != PQ_OK) return rc;
   }
-  // Less than a round of 256 x 256 tiles, that the map above takes whole or in halves: 128 x 128 tiles, two at a time on a CU, up
-  // to 2.25 per CU. K=5120, F=8704: M=256 52.9 against 53.4 us, M=300 51.9 / 81.1, M=384 51.6 / 81, M=512 76.0 / 81.5,
-  // M=768 (3.2 per CU) 96.4 / 82.1; K=2048, F=4096: M=512 19.8 / 20.7. Also for one or two groups, where a tile is mostly its
-  // beginning and its end, which two workgroups overlap: M=1200, K=256, F=4640 16.9 against 18.8 us, M=2048, K=256, F=8704 32.2 /
-  // 33.4; at eight groups 58.1 / 56.1.
-  const int rows128 = (M + 127) / 128, cols128 = (2 * F + 127) / 128;
-  const int64_t small = static_cast<int64_t>(rows128) * cols128;
-  if (P == 1 && (G <= 2 || (map.full == 0 && map.split < 4 && 4 * small <= 9 * static_cast<int64_t>(cus)))) {
-    launched = launch_kernel(glu_small_tile_kernel, dim3(static_cast<unsigned>(small)), dim3(64 * kPfWaves), 0, s, a_d, asgt, M, K, wpk, zpe,
+  if (small_tiles) {
+    launched = launch_kernel(glu_small_tile_kernel, dim3(static_cast<unsigned>(grid)), dim3(64 * kPfWaves), 0, s, a_d, asgt, M, K, wpk, zpe,
                              static_cast<const u32x4*>(ws_d), s9img, F, act, h_d, ldh, out_bf16, rows128, cols128, vec16);
     return launch_status(what, launched);
   }

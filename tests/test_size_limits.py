@@ -67,3 +67,11 @@ def test_no_boundary_and_past_the_columns_are_taken():
             pq.matvec(_e(1, 128), *_layer(128, 256), 256, *pb)
         with pytest.raises(TypeError, match="CUDA"):
             pq.gemm(*_codes(1, 128), *_layer(128, 256), 256, *pb)
+
+
+@pytest.mark.parametrize("M,K,F,P", [(2 ** 20 + 1, 128, 65536, 1), (2 ** 21, 256, 32784, 1), (2 ** 23, 128, 2 ** 16, 2), (2 ** 20 - 128, 2048, 2 ** 18, 1)])
+def test_gemm_glu_of_more_threads_than_a_launch_counts(M, K, F, P):
+    """Refused before the pass over the scales is queued (no address is real, so nothing may be launched)."""
+    at = [(1 << 44) + (i << 40) for i in range(7)]
+    rc = pq.lib().pq_gemm_glu(at[0], at[1], at[2], M, K, P, at[3], at[4], F, 0, at[5], F, 0, at[6], 1 << 40, 0, None)
+    assert rc == -2 and b"too many for one call" in pq.lib().pq_last_error()
