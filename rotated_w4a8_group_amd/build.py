@@ -6,8 +6,10 @@ Every call recompiles. Objects go to ``_build/`` under the repository root.
 """
 import os
 import shutil
+import signal
 import subprocess
 import sys
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -58,34 +60,57 @@ def binding_command(out: str) -> list:
                   "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-o", out]
 
 
+def _start_binding(verbose: bool):
+    """(command, process, None), or (None, None, why it cannot be started)."""
+    try:
+        cmd = binding_command(BINDING + ".tmp")
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        return cmd, subprocess.Popen(cmd, start_new_session=True), None
+    except (ImportError, OSError, RuntimeError) as e:
+        return None, None, f"{type(e).__name__}: {e}"
+
+
 def build(verbose: bool = False) -> str:
+    """The library needs hipcc alone. Without torch, g++ or their headers there is no ``_binding.so``: a warning says why, an
+    older one is taken away, and every call goes through Python and ctypes."""
     cc = hipcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
     objs, jobs = [], []
-    for src, extra in SOURCES:
-        obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
-        lang = ["-x", "hip"]
-        cmd = [cc, "-c"] + lang + HIP_FLAGS + extra + ["-I", INCLUDE, "-I", CSRC,
-                                                       os.path.join(CSRC, src), "-o", obj]
+    binding, why = None, None
+    try:
+        for src, extra in SOURCES:
+            obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
+            lang = ["-x", "hip"]
+            cmd = [cc, "-c"] + lang + HIP_FLAGS + extra + ["-I", INCLUDE, "-I", CSRC,
+                                                           os.path.join(CSRC, src), "-o", obj]
+            if verbose:
+                print(" ".join(cmd), flush=True)
+            jobs.append((cmd, subprocess.Popen(cmd, start_new_session=True)))
+            objs.append(obj)
+        bcmd, binding, why = _start_binding(verbose)
+        failed = [(job.returncode, cmd) for cmd, job in jobs if job.wait() != 0]   # waits for every one
+        if failed:
+            raise subprocess.CalledProcessError(*failed[0])
+        tmp = OUT + ".tmp"
+        cmd = [cc, "-shared", "-fPIC", f"--offload-arch={ARCH}"] + objs + ["-o", tmp]
         if verbose:
             print(" ".join(cmd), flush=True)
-        jobs.append((cmd, subprocess.Popen(cmd)))
-        objs.append(obj)
-    btmp = BINDING + ".tmp"
-    cmd = binding_command(btmp)
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    jobs.append((cmd, subprocess.Popen(cmd)))
-    failed = [cmd for cmd, job in jobs if job.wait() != 0]   # waits for every one
-    if failed:
-        raise subprocess.CalledProcessError(1, failed[0])
-    tmp = OUT + ".tmp"
-    cmd = [cc, "-shared", "-fPIC", f"--offload-arch={ARCH}"] + objs + ["-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, OUT)
-    os.replace(btmp, BINDING)
+        subprocess.run(cmd, check=True)
+        os.replace(tmp, OUT)
+        if binding is not None and binding.wait() != 0:
+            why = f"exit status {binding.returncode} of {' '.join(bcmd)}"
+        if why is None:
+            os.replace(BINDING + ".tmp", BINDING)
+        else:
+            if os.path.exists(BINDING):
+                os.remove(BINDING)
+            warnings.warn(f"_binding.so is not built, calls go through Python: {why}")
+    finally:   # whatever was raised, no compiler runs on
+        for _, job in jobs + [(None, binding)]:
+            if job is not None and job.poll() is None:
+                os.killpg(job.pid, signal.SIGKILL)   # with what it started
+                job.wait()
     return OUT
 
 
