@@ -30,7 +30,8 @@
 extern "C" {
 #endif
 
-#define PQ_ABI_VERSION 1
+/* Raised with every entry point that is added or changed. 2: pq_rotate, pq_matvec, pq_gemm_glu and pq_block_norms. */
+#define PQ_ABI_VERSION 2
 #define PQ_GROUP 128
 #define PQ_LAYERS 8
 #define PQ_MAX_PARTITIONS 3

@@ -107,22 +107,21 @@ _fast = None
 def _native():
     """The compiled calls of rotate, matvec, gemm_glu and block_norms (``_binding.so``), which take the usual call - plain
     tensors that pass every check, on the current device and stream - and answer NotImplemented to any other; False where
-    they are not built for this interpreter and torch: the functions below then do every call, about 3 us slower each."""
+    they are not built for this interpreter, torch and library: the functions below then do every call, about 3 us slower each."""
     global _fast
     if _fast is None:
         import torch  # noqa: F401  (its libraries first)
         L = lib()
         try:
             from . import _binding as b
-        except ImportError as e:
+            b.bind(_check, L.pq_abi_version(), *(ctypes.cast(getattr(L, f), _P).value for f in (
+                "pq_rotate", "pq_matvec", "pq_gemm_glu", "pq_block_norms", "pq_packed_weight_bytes", "pq_gemm_workspace_bytes")))
+            _fast = b
+        except ImportError as e:   # not built, or not for this library
             if os.path.exists(os.path.join(_HERE, "_binding.so")):
                 import warnings
                 warnings.warn(f"_binding.so does not load ({e}): calls go through Python")
             _fast = False
-            return _fast
-        b.bind(_check, *(ctypes.cast(getattr(L, f), _P).value for f in (
-            "pq_rotate", "pq_matvec", "pq_gemm_glu", "pq_block_norms", "pq_packed_weight_bytes", "pq_gemm_workspace_bytes")))
-        _fast = b
     return _fast
 
 

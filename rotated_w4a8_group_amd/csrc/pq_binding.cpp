@@ -285,11 +285,17 @@ PyObject* block_norms(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// bind(check, rotate, matvec, gemm_glu, block_norms, packed_weight_bytes, gemm_workspace_bytes): addresses
+// bind(check, abi_version, rotate, matvec, gemm_glu, block_norms, packed_weight_bytes, gemm_workspace_bytes): addresses, of a
+// library of this ABI version. The signatures are the ones that pq.h had when this file was compiled, so another version raises.
 PyObject* bind(PyObject*, PyObject* args) {
   unsigned long long f[6];
   PyObject* c;
-  if (!PyArg_ParseTuple(args, "OKKKKKK", &c, f, f + 1, f + 2, f + 3, f + 4, f + 5)) return nullptr;
+  int version;
+  if (!PyArg_ParseTuple(args, "OiKKKKKK", &c, &version, f, f + 1, f + 2, f + 3, f + 4, f + 5)) return nullptr;
+  if (version != PQ_ABI_VERSION) {
+    PyErr_Format(PyExc_ImportError, "compiled for ABI version %d of the library, which has %d", PQ_ABI_VERSION, version);
+    return nullptr;
+  }
   Py_INCREF(c);
   Py_XDECREF(check);
   check = c;

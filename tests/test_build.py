@@ -100,3 +100,22 @@ def test_no_compiler_outlives_an_exception(tree, monkeypatch):
         else:
             pytest.fail(f"{p.args[-1]} still has processes")
     assert not os.path.exists(b.OUT)
+
+
+def test_the_compiled_calls_are_bound_to_a_library_of_their_version_only(monkeypatch):
+    """Built for another version of the library, they are left out with a warning, whatever its entry points' addresses."""
+    import rotated_w4a8_group_amd as pq
+    assert pq._native()
+    real = pq.lib()
+
+    class Other:
+        pq_abi_version = staticmethod(lambda: real.pq_abi_version() + 1)
+
+        def __getattr__(self, name):
+            return getattr(real, name)
+    monkeypatch.setattr(pq, "lib", Other)
+    monkeypatch.setattr(pq, "_fast", None)
+    with pytest.warns(UserWarning, match="ABI version"):
+        assert pq._native() is False
+    with pytest.raises(TypeError):       # without a version they are not bound at all
+        pq._binding.bind(pq._check, *[0] * 6)
