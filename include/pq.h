@@ -380,7 +380,8 @@ int pq_add_rms_rotate_quant(const uint16_t* x_d, int64_t ldx, const uint16_t* re
  *   h  = res_scale * res + scale * a(gate) * n        the new residual stream, type of res
  *   hs = h * rstd(h) * w_pre'                         from h as stored (w_pre_d NULL: not written)
  * with rstd(v) = 1 / sqrt(mean_k(v^2) + eps), w' = 1 + w (gemma != 0) or w, a = identity, sigmoid or tanh.
- * Rows whose squares overflow binary32 get rstd 0, as in any binary32 norm; NaN stays in its row.
+ * Rows whose squares overflow binary32 get rstd 0, as in any binary32 norm; NaN stays in its row. A sigmoid below
+ * 2^-126 (gates below -87.3) counts 0. The order of a row's sums depends on M and K: the same call gives the same bits.
  *
  * x_d        f16 or bf16 [M, ldx] (x_type), the block's output (pq_gemm's bf16 y, say).
  * res_d      f16, bf16 or f32 [M, ldr] (res_type); res_out_d the same type [M, ldo]: res_d itself with

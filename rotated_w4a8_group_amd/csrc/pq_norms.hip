@@ -87,8 +87,9 @@ __device__ __forceinline__ norm_u32x4 pack8(const float (&v)[8]) {
 }
 
 // The hardware's exp2 and reciprocal are within 1 ulp (2 u, u = 2^-24). Infinite gates give the functions' limits, NaN stays.
-//  - sigmoid: relative error at most (5 + 2 |t|) u, the exponent's two roundings counting |t| each. expf and a division made
-//    8192 rows of 5120 with a channel gate 68.4 us, this 61.5; one row with its own gates 4.5, this 3.8.
+//  - sigmoid: relative error at most (5 + 2 |t|) u, the exponent's two roundings counting |t| each, where it is a normal number
+//    (t > -87.3); below, the reciprocal's result is 0. expf and a division made 8192 rows of 5120 with a channel gate 68.4 us,
+//    this 61.5; one row with its own gates 4.5, this 3.8.
 //  - tanh: below 1/2 its Taylor series to t^13 (the next term is 1.5 u, the sum's roundings 3 u), above 1 - 2 / (1 + exp(2 |t|)),
 //    where at 1/2 the quotient's 6 u count 1.2 and the difference rounds once: at most 8 u. tanhf made the 8192 rows
 //    67.6 us, this 64.1; the one row 4.6, this 4.2.

@@ -65,8 +65,10 @@ __device__ __forceinline__ int pf_strip(int h0, int j, int F) {
 }
 
 // act(g) * u for silu and gelu (tanh form): both are g * sigmoid(t), t = g or 2 sqrt(2/pi) (g + 0.044715 g^3).
-// exp and the reciprocal by the hardware's instructions (1 ulp each; the product t log2(e) rounds by
-// |t| 2^-24, 2^-18 at the t where sigmoid leaves binary32): far below the 16-bit rounding of the result.
+// exp and the reciprocal by the hardware's instructions, 1 ulp (2 u, u = 2^-24) each. The exponent is off by the product's and
+// the constant's rounding, and for gelu by its polynomial's 4: 2 |t| u of the result for silu, 6 |t| u for gelu, so with the other
+// steps' 8 u at most 2^-14.9 wherever sigmoid is a normal number (t > -87.3), below the half step of f16 (2^-11) and bf16 (2^-8) that
+// the one rounding then takes; below that t the result is 0.
 __device__ __forceinline__ float glu_value(float g, float u, int act) {
   const float t = act == PQ_ACT_GELU ? g * __builtin_fmaf(0.0713548162726f * g, g, 1.59576912161f) : g;
   return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504089f * t)) * u;

@@ -255,3 +255,16 @@ def test_gate_extremes(xt):
         h, _ = pq.block_norms(x, res, gate=gate, gate_act=act)
         assert torch.equal(h[0], res[0] + x[0].float()) and torch.equal(h[1], res[1] if act == "sigmoid" else res[1] - x[1].float())
         assert torch.isnan(h).sum() == 1 and torch.isnan(h[2, 7])
+
+
+@gpu
+def test_sigmoid_ends_with_the_normal_numbers():
+    """(5 + 2 |t|) u of the sigmoid down to 2^-126, 0 below; with a stream of zeros nothing covers the gate's error. The product
+    with x is exact (a power of two), the f32 stream rounds nothing."""
+    gates = torch.tensor([-60.0, -80.0, -86.5, -87.0, -87.5, -88.0, -89.0, -104.0, -3e4], device="cuda").bfloat16()[:, None]
+    x = torch.full((9, 8), 2.0 ** 10, device="cuda").bfloat16()
+    for gate in (gates, gates.expand(9, 8).contiguous()):
+        h, _ = pq.block_norms(x, torch.zeros((9, 8), device="cuda"), gate=gate, gate_act="sigmoid")
+        t = gates[:4].double()
+        ref = torch.sigmoid(t) * 2.0 ** 10
+        assert ((h[:4].double() - ref).abs() <= (5 + 2 * t.abs()) * U * ref).all() and not h[4:].any()
