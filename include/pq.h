@@ -190,7 +190,9 @@ int pq_gemm(const uint8_t* a_d, const float* asg_d, const float* rs_d, int M, in
  *   y[m, n] = fl( sum_g ( sc[g,n] * sum_{k in g} x_p[m,k] (c[k,n] - 8)
  *                         - fl16(sc[g,n]*(zp[g,n]-8)) * sum_{k in g} x_p[m,k] ) )
  * pq_gemm's weights (the same wpk_d and sz_d) with activations that are not quantised; sums in binary32, one
- * rounding to the type of y. A row of x with an infinity or a NaN gives NaN in its whole row of y.
+ * rounding to the type of y. A row of x with an infinity or a NaN gives NaN in its whole row of y (the sum
+ * of x W itself would be an infinity in most columns); a bf16 row whose 15 sum |x| over a group passes binary32's range may
+ * give infinities or NaN.
  *
  * x_d     f16 or bf16 (x_type) [P, M, ldx] (first K columns of a row used; partition p starts at row
  *         p * M), 16-byte aligned, ldx a multiple of 8, K <= ldx <= 2^26. For weights of the rotated
@@ -242,6 +244,12 @@ int pq_gemm_prepared(const uint8_t* a_d, const float* asg_d, const float* rs_d, 
  *                    Small calls do without the workspace's contents; which is the library's choice.
  * Rows m >= M of h are never written. The order in which the groups are added depends on (M, K, F, P), so the same
  * call gives the same bits, and a row alone may differ from that row in a batch in the last bits of its sums.
+ *
+ * g and u are sums in binary32 of what the e4m3 matrix instruction gives, as in pq_gemm: of 8 neighbouring k it drops what lies
+ * below 2^-13 of the largest product's power of two, at most 7 * 2^-10 of sum asg sc (max |D| of the 8). The bf16 step of pq_gemm's y
+ * covers that; an f16 h shows it (1.1e-4 of the norm beside the 2.1e-4 of its own rounding, K=5120). The zero point is taken in
+ * binary32 up to 16 rows and in the row blocks of small calls, and as a product of bf16 pieces (2^-14 of its magnitude) in the
+ * tiles of long prompts, so a row may be less exact in a long prompt than in a short one.
  */
 enum pq_act { PQ_ACT_SILU = 0, PQ_ACT_GELU = 1 };
 int pq_gemm_glu(const uint8_t* a_d, const float* asg_d, const float* rs_d, int M, int K, int P, const void* wpk_d,

@@ -504,7 +504,7 @@ def gemm(A, ASG, RS, wpk, sz, N, pb1=NO_BOUNDARY, pb2=NO_BOUNDARY, out=None, wor
 def matvec(x, wpk, sz, N, pb1=NO_BOUNDARY, pb2=NO_BOUNDARY, out=None, dtype=None, stream=None):
     """Products of few 16-bit rows with the packed weights of ``gemm``: x f16 or bf16 [P, M, K] (or [M, K] for one
     partition; row stride may exceed K), M <= 16 -> y [M, N] of ``dtype`` (f16 or bf16; x's type by default), or into
-    ``out``, a [M, ldy >= N] view with unit column stride."""
+    ``out``, a [M, ldy >= N] view with unit column stride. A row with an infinity or a NaN gives NaN in its whole row of y."""
     f = _native() if _fast is None else _fast
     if f and stream is None:
         done = f.matvec(x, wpk, sz, N, pb1, pb2, out, dtype)
@@ -564,7 +564,10 @@ def gemm_glu(A, ASG, RS, wpk, sz, F, act="silu", out=None, dtype=None, workspace
     [P, M, G] with P = 1 (one rotation for both) or 2 (the gate's, the up projection's) -> h [M, F] of ``dtype`` (f16 by
     default, what the next prologue takes, or bf16), or into ``out``, a [M, ldh >= F] view with unit column stride.
     act "silu" or "gelu" (tanh form). workspace: gemm_workspace_bytes(M, 2 F, K) bytes; prepared: it holds
-    what ``rotate_quant_for_gemm`` wrote for these A, ASG and RS."""
+    what ``rotate_quant_for_gemm`` wrote for these A, ASG and RS.
+
+    g and u carry what ``gemm``'s products do (the e4m3 matrix instruction drops what lies below 2^-13 of the largest of 8
+    neighbours), and in the tiles of long prompts the zero point's bf16 pieces (2^-14 of it): an f16 h shows both, about 1e-4 of the norm."""
     f = _native() if _fast is None else _fast
     if f and stream is None:
         done = f.gemm_glu(A, ASG, RS, wpk, sz, F, GLU_ACTS.get(act), out, dtype, workspace, prepared)
