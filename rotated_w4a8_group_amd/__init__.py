@@ -107,7 +107,7 @@ _fast = None
 def _native():
     """The compiled calls of rotate, matvec, gemm_glu and block_norms (``_binding.so``), which take the usual call - plain
     tensors that pass every check, on the current device and stream - and answer NotImplemented to any other; False where
-    they are not built for this interpreter, torch and library: the functions below then do every call, about 3 us slower each."""
+    they are not built for this interpreter, torch and library: the functions below then do every call, 2 to 5 us slower each."""
     global _fast
     if _fast is None:
         import torch  # noqa: F401  (its libraries first)

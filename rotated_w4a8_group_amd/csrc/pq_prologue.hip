@@ -451,7 +451,8 @@ __global__ __launch_bounds__(256) void rotate_quant_kernel(
 // way: 8 x 11 or 11 x 11 significand bits). Bound, like the prologue, by the layers: their vector instructions (6 per
 // pair, token and layer, each rounding separately so that the rows are the prologue's) are 96 % of the vector
 // issue of M=1021 with three partitions before the steps below, and the LDS works 76 % of that time beside them.
-// M=8192, K=5120 takes 44 us (3.8 TB/s), M=1021 with three partitions 19.7; one row 3.3, the launch. What brought it there:
+// M=8192, K=5120 takes 43 us (3.9 TB/s), M=1021 with three partitions 17.3; one row 2.9, the launch (captured, three sets of
+// inputs in turn). What brought it there, each step's figures as measured then, before the later ones:
 //  - stores that stream past the caches: 44 against 48 us.
 //  - a workgroup of one wave (its LDS begins at 0, nothing to add to a row's address), scalar bases with 32-bit lane
 //    offsets, the unit's numbers by multiplication: 500 vector instructions a unit of 8 tokens against 586, 384 of
