@@ -424,7 +424,7 @@ __global__ __launch_bounds__(64 * W, 2) void glu_mid_kernel(
 // weights, 2 + 2 P of scales) and 2 nt MF products; two 4-wave workgroups side by side count as 1.6. The tallest blocks throughout
 // were slower wherever F is small: M=297, K=5504, F=208 12.6 against 6.6 us, M=68, K=8448, F=544 15.9 / 10.5, M=32, K=10240,
 // F=1024 12.4 / 8.4; M=18, K=7808, F=720 is one of the few the rule costs something, 8.4 / 9.3.
-// K=5120, F=8704: 13.0 to 13.4 us at M=17..32, 20.4 at 64, 30.6 at 128 (the tiles below take 50 at M=129..256, this kernel 58).
+// K=5120, F=8704: 12.8 to 13.2 us at M=17..32, 18.8 at 64, 29.3 at 128 (the tiles below take 50 at M=129..256, this kernel 58).
 struct GluMidPlan {
   int MF, blocks, ranges;
   int gran, nt;    // columns are dealt out gran at a time; tiles of a projection that a range may touch
