@@ -30,8 +30,9 @@
 extern "C" {
 #endif
 
-/* Raised with every entry point that is added or changed. 2: pq_rotate, pq_matvec, pq_gemm_glu and pq_block_norms. */
-#define PQ_ABI_VERSION 2
+/* Raised with every entry point that is added or changed. 2: pq_rotate, pq_matvec, pq_gemm_glu and pq_block_norms.
+   3: pq_kv_write, pq_kv_read, pq_attn_decode and pq_attn_prefill. */
+#define PQ_ABI_VERSION 3
 #define PQ_GROUP 128
 #define PQ_LAYERS 8
 #define PQ_MAX_PARTITIONS 3
@@ -406,6 +407,61 @@ int pq_block_norms(const void* x_d, int64_t ldx, int x_type, const void* res_d, 
                    const void* w_post_d, const void* gate_d, int64_t ldg, int gate_cols, int gate_act,
                    const void* w_pre_d, float eps, float scale, float res_scale, int gemma, int M, int K,
                    void* res_out_d, int64_t ldo, void* hs_d, int64_t ldh, int out_type, pq_stream_t stream);
+
+/*
+ * The key-value cache of the attention layers (device). A cache is two arrays [pages][Hkv][page][D], keys and values: a head's
+ * rows of one page are one contiguous run. With scales (ks_d, vs_d: f32 [pages][Hkv][page], one for each row of a head)
+ * it holds e4m3 codes, without them the 16-bit values of `type`. D is 64, 128 or 256, page a power of two in 16..1024.
+ *
+ * pq_kv_write: row t, head h of k and v into the place slots[t] = page number * page + row in the page.
+ *   s = fl32(max_i |x_i| * fl32(1/448)), code_i = E(fl32(x_i * fl32(1/s))) with the prologue's encoder (the scale of a group of
+ *   pq_rotate_quant); a row whose s is below 2^-126 counts as zero (codes 0, s 0); one with an infinity or a
+ *   NaN gets codes 0 and s NaN. Without scales the 16 bits are copied.
+ *   k_d, v_d  f16 or bf16 (type): element i of head h of row t at t ld + h hs + i; ld, hs multiples of 8, 16-byte aligned - the
+ *             columns of a merged projection's y, for instance. They overlap no cache.
+ *   slots_d   int64 [T]; a negative slot, or one past the cache, writes nothing (padding rows). Two rows of one call with
+ *             the same slot leave a mixture of both there.
+ * pq_kv_read: the rows of B sequences back, packed: row t belongs to the sequence b with cu[b] <= t < cu[b + 1], its position is
+ *   t - cu[b], found through the sequence's page numbers table[b][0..width). y = fl(code * s), one rounding to type.
+ *   cu_d      int32 [B + 1], ascending. Rows of no sequence are left as they were. A position past the width, or whose page is
+ *             not one of the cache's, reads as zeros.
+ *   k_d, v_d  out f16 or bf16 (type; for a 16-bit cache its own) [T, Hkv, D], 16-byte aligned; they overlap no input.
+ */
+int pq_kv_write(const uint16_t* k_d, int64_t ldk, int64_t hsk, const uint16_t* v_d, int64_t ldv, int64_t hsv, int type, int T, int Hkv,
+                int D, const int64_t* slots_d, void* kc_d, void* vc_d, float* ks_d, float* vs_d, int64_t pages, int page,
+                pq_stream_t stream);
+int pq_kv_read(const void* kc_d, const void* vc_d, const float* ks_d, const float* vs_d, int64_t pages, int page,
+               const int32_t* table_d, int width, const int32_t* cu_d, int B, int T, int Hkv, int D, uint16_t* k_d, uint16_t* v_d,
+               int type, pq_stream_t stream);
+
+/*
+ * Attention (device): o[h] = sum_j p_j v_j, p = softmax over the keys that the query sees of scale * q[h] . k_j, with query head h
+ * on key head h / (Hq / Hkv). Scores, maxima, sums and outputs are held in binary32; one rounding where o is stored. What a
+ * query does not see has no influence, infinities and NaN included; a query that sees no key gives zeros.
+ *
+ * pq_attn_decode: one query for each sequence over the paged cache, positions 0 .. lens[b] - 1 through table[b] (as in
+ *   pq_kv_read; a position whose page is not one of the cache's is left out, and no length passes width * page).
+ *   q_d       f16 or bf16 (type) [B rows], strides as pq_kv_write's k; a cache without scales holds this type.
+ *   lens_d    int32 [B].
+ *   o_d       out f16 or bf16 (out_type) [B, Hq, D], 16-byte aligned.
+ * pq_attn_prefill: packed prompts. Sequence b has the queries cu_q[b] .. cu_q[b + 1] - 1 and the keys cu_k[b] .. cu_k[b + 1] - 1
+ *   of the Tq and Tk rows; query i of nq sees the keys j <= i + nk - nq (causal != 0) or all nk of them.
+ *   cu_q_d, cu_k_d  int32 [B + 1], ascending; values past Tq and Tk count as those. Rows of o of no sequence are left as they were.
+ *   o_d       out f16 or bf16 (out_type) [Tq, Hq, D], 16-byte aligned.
+ *
+ * scale > 0 and finite. Outputs overlap no input. ws_d: at least pq_attn_*_workspace_bytes(), 16-byte aligned; its
+ * contents need no initialisation and are not kept, so calls that may run at the same time take one each.
+ * Errors: PQ_ERR_SHAPE, PQ_ERR_NULL, PQ_ERR_ALIGN, PQ_ERR_WORKSPACE, PQ_ERR_DEVICE.
+ */
+size_t pq_attn_decode_workspace_bytes(int B, int Hq, int Hkv, int D);
+int pq_attn_decode(const uint16_t* q_d, int64_t ldq, int64_t hsq, int type, const void* kc_d, const void* vc_d, const float* ks_d,
+                   const float* vs_d, int64_t pages, int page, const int32_t* table_d, int width, const int32_t* lens_d, int B, int Hq,
+                   int Hkv, int D, float scale, uint16_t* o_d, int out_type, void* ws_d, size_t ws_bytes, pq_stream_t stream);
+size_t pq_attn_prefill_workspace_bytes(int B, int Tq, int Tk, int Hq, int Hkv, int D);
+int pq_attn_prefill(const uint16_t* q_d, int64_t ldq, int64_t hsq, const uint16_t* k_d, int64_t ldk, int64_t hsk, const uint16_t* v_d,
+                    int64_t ldv, int64_t hsv, int type, const int32_t* cu_q_d, const int32_t* cu_k_d, int B, int Tq, int Tk, int Hq,
+                    int Hkv, int D, float scale, int causal, uint16_t* o_d, int out_type, void* ws_d, size_t ws_bytes,
+                    pq_stream_t stream);
 
 /*
  * Verification hooks: run the exact device arithmetic the prologue uses on plain arrays, so

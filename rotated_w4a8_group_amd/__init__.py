@@ -16,6 +16,10 @@ Calls (same names as the C entry points, without the ``pq_`` prefix):
 * ``matvec(x, wpk, sz, N, pb1, pb2)``        device; 16-bit rows (at most 16) -> y of their type
 * ``block_norms(x, residual, ...)``           device; -> (new residual, normalised row): the norms before
   and after a block with its gate and residual scale
+* ``kv_write(k, v, slots, ...)``             device; rows into a paged key-value cache, as e4m3 codes or as they are
+* ``kv_read(k_cache, v_cache, ...)``         device; the rows of its sequences back, packed
+* ``attn_decode(q, k_cache, v_cache, ...)``  device; attention of one new token of each sequence over the cache
+* ``attn_prefill(q, k, v, cu_q)``            device; attention over packed prompts, causal, grouped heads
 * ``e4m3_encode(q)``, ``recip_f32(x)``       device verification hooks
 """
 import ctypes
@@ -71,6 +75,13 @@ SIGNATURES = {
                                      _P, _P, _P, _P, _P]),
     "pq_block_norms": (_I, [_P, _I64, _I, _P, _I64, _I, _P, _P, _I64, _I, _I, _P, ctypes.c_float, ctypes.c_float,
                             ctypes.c_float, _I, _I, _I, _P, _I64, _P, _I64, _I, _P]),
+    "pq_kv_write": (_I, [_P, _I64, _I64, _P, _I64, _I64, _I, _I, _I, _I, _P, _P, _P, _P, _P, _I64, _I, _P]),
+    "pq_kv_read": (_I, [_P, _P, _P, _P, _I64, _I, _P, _I, _P, _I, _I, _I, _I, _P, _P, _I, _P]),
+    "pq_attn_decode_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
+    "pq_attn_decode": (_I, [_P, _I64, _I64, _I, _P, _P, _P, _P, _I64, _I, _P, _I, _P, _I, _I, _I, _I, ctypes.c_float, _P, _I, _P, _SZ, _P]),
+    "pq_attn_prefill_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "pq_attn_prefill": (_I, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I, _P, _P, _I, _I, _I, _I, _I, _I, ctypes.c_float, _I, _P, _I,
+                             _P, _SZ, _P]),
     "pq_e4m3_encode": (_I, [_P, _P, _I64, _P]),
     "pq_recip_f32": (_I, [_P, _P, _I64, _P]),
     "pq_bf16_round": (_I, [_P, _P, _I64, _P]),
@@ -782,6 +793,216 @@ def block_norms(x, residual, w_post=None, gate=None, w_pre=None, eps=1e-6, scale
             act, _addr(w_pre), float(eps), float(scale), float(res_scale), 1 if gemma else 0, M, K,
             residual_out.data_ptr(), _pitch(residual_out, M, K), _addr(out), K if out is None else _pitch(out, M, K), ot)
     return residual_out, out
+
+# ------------------------------------------------------------------------------------------
+def _heads(t, name, dtype=None, T=None, H=None, D=None):
+    """Checks rows of heads [T, H, D] with unit channel stride - the columns of a merged projection among them - and returns
+    (row stride, head stride)."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a tensor")
+    if dtype is None:
+        _type_code(t.dtype, name)
+    elif t.dtype != dtype:
+        raise TypeError(f"{name}: expected a tensor of {dtype}")
+    if t.dim() != 3 or any(w is not None and w != n for w, n in zip((T, H, D), t.shape)):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [{', '.join('any' if n is None else str(n) for n in (T, H, D))}]")
+    T, H, D = t.shape
+    if T > INT_MAX or H > INT_MAX or D > INT_MAX:
+        _too_large(**{f"{name} rows": T, f"{name} heads": H, f"{name} channels": D})
+    if T and H and D > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}: strides {t.stride()}, expected unit channel stride")
+    return t.stride(0) if T > 1 else H * D, t.stride(1) if H > 1 else D
+
+
+def _paged(k_cache, v_cache, k_scale, v_scale, dtype, Hkv=None, D=None):
+    """Checks a cache against the 16-bit type it is written from or read as; returns (pages, Hkv, page, D, specs)."""
+    import torch
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache: expected a [pages, Hkv, page, D] tensor")
+    pages, H, page, d = k_cache.shape
+    if (Hkv is not None and H != Hkv) or (D is not None and d != D):
+        raise ValueError(f"k_cache: shape {tuple(k_cache.shape)}, expected [pages, {H if Hkv is None else Hkv}, page, {d if D is None else D}]")
+    if pages > INT_MAX or H > INT_MAX or page > INT_MAX or d > INT_MAX:
+        _too_large(pages=pages, Hkv=H, page=page, D=d)
+    if (k_scale is None) != (v_scale is None):
+        raise ValueError("k_scale, v_scale: both for a cache of e4m3 codes, neither for one of 16-bit values")
+    kind = dtype if k_scale is None else torch.uint8
+    specs = [(k_cache, "k_cache", kind, (pages, H, page, d)), (v_cache, "v_cache", kind, (pages, H, page, d))]
+    if k_scale is not None:
+        specs += [(k_scale, "k_scale", torch.float32, (pages, H, page)), (v_scale, "v_scale", torch.float32, (pages, H, page))]
+    return pages, H, page, d, specs
+
+
+def _on_device(first, *tensors):
+    """The tensors that ``_validate`` does not see: on the GPU, and all on one device."""
+    for t, name in tensors:
+        if not t.is_cuda:
+            raise TypeError(f"{name}: expected a CUDA tensor")
+        if t.device != first.device:
+            raise TypeError(f"tensors on several devices: {sorted((str(first.device), str(t.device)))}")
+
+
+def _table(block_table):
+    """Checks a [B, width] page table; returns (B, width, spec)."""
+    import torch
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table: expected an int32 [B, width] tensor")
+    B, width = block_table.shape
+    if B > INT_MAX or width > INT_MAX:
+        _too_large(B=B, width=width)
+    return B, width, (block_table, "block_table", torch.int32, (B, width))
+
+
+def kv_write(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None, stream=None):
+    """Rows into a paged key-value cache: k, v f16 or bf16 [T, Hkv, D] (any row and head strides that are multiples of 8,
+    the columns of a merged projection's output among them), slots int64 [T], the place of each row: page * rows of a
+    page + row in the page; a row with a negative slot (or one past the cache) is not written. Slots of one call are distinct.
+
+    k_cache, v_cache [pages, Hkv, page, D]: uint8 e4m3 codes with k_scale, v_scale f32 [pages, Hkv, page] - per (row, head)
+    max |x| / 448, as ``rotate_quant`` encodes a group - or k's type without scales: the rows as they are. A row
+    with an infinity or a NaN gets the scale NaN. D 64, 128 or 256, page a power of two in 16..1024. Returns (k_cache, v_cache)."""
+    import torch
+    ldk, hsk = _heads(k, "k")
+    T, H, D = k.shape
+    ldv, hsv = _heads(v, "v", k.dtype, T, H, D)
+    pages, _, page, _, specs = _paged(k_cache, v_cache, k_scale, v_scale, k.dtype, H, D)
+    _validate(specs + [(slots, "slots", torch.int64, (T,))])
+    _on_device(k_cache, (k, "k"), (v, "v"))
+    _launch("pq_kv_write", k.device, stream, k.data_ptr(), ldk, hsk, v.data_ptr(), ldv, hsv, _type_code(k.dtype, "k"), T, H, D, slots.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale), pages, page)
+    return k_cache, v_cache
+
+
+def kv_read(k_cache, v_cache, block_table, cu, T, k_scale=None, v_scale=None, out=None, dtype=None, stream=None):
+    """The rows of sequences back from a paged cache (``kv_write``'s): block_table int32 [B, width], the pages of each
+    sequence in order; cu int32 [B + 1], where its rows begin in the packed output -> (k, v) [T, Hkv, D] of ``dtype`` (f16 or
+    bf16; the cache's own type where it holds 16-bit values, f16 by default otherwise), or into ``out``, a pair of those.
+    Rows of no sequence are left as they were; a position whose page is not one of the cache's reads as zeros."""
+    import torch
+    if out is not None:
+        if not isinstance(out, (tuple, list)) or len(out) != 2:
+            raise ValueError("out: expected a (k, v) pair")
+        if dtype is not None and any(isinstance(o, torch.Tensor) and o.dtype != dtype for o in out):
+            raise TypeError(f"out: dtype says {dtype}")
+        dtype = out[0].dtype if isinstance(out[0], torch.Tensor) else dtype
+    if dtype is None:
+        dtype = k_cache.dtype if k_scale is None and isinstance(k_cache, torch.Tensor) else torch.float16
+    code = _type_code(dtype, "out" if out is not None else "dtype")
+    pages, H, page, D, specs = _paged(k_cache, v_cache, k_scale, v_scale, dtype)
+    B, width, spec = _table(block_table)
+    if T > INT_MAX:
+        _too_large(T=T)
+    if T < 0:
+        raise ValueError(f"T={T}: negative")
+    specs += [spec, (cu, "cu", torch.int32, (B + 1,))]
+    if out is not None:
+        specs += [(out[0], "out k", dtype, (T, H, D)), (out[1], "out v", dtype, (T, H, D))]
+    _validate(specs)
+    if out is None:
+        out = tuple(_new((T, H, D), dtype, k_cache.device, stream) for _ in range(2))
+    _launch("pq_kv_read", k_cache.device, stream, k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale), pages, page,
+            block_table.data_ptr(), width, cu.data_ptr(), B, T, H, D, out[0].data_ptr(), out[1].data_ptr(), code)
+    return out
+
+
+def _attn_out(out, dtype, q, what="out"):
+    """Type code of an attention's output and the spec of a given one."""
+    import torch
+    if out is not None and dtype is not None and isinstance(out, torch.Tensor) and out.dtype != dtype:
+        raise TypeError(f"{what}: {out.dtype}, dtype says {dtype}")
+    dtype = out.dtype if isinstance(out, torch.Tensor) else dtype or q.dtype
+    return dtype, _type_code(dtype, what), [] if out is None else [(out, what, dtype, tuple(q.shape))]
+
+
+def attn_decode_workspace_bytes(B, Hq, Hkv, D):
+    """Bytes of the workspace of ``attn_decode``."""
+    if B > INT_MAX or Hq > INT_MAX or Hkv > INT_MAX or D > INT_MAX:
+        _too_large(B=B, Hq=Hq, Hkv=Hkv, D=D)
+    return int(lib().pq_attn_decode_workspace_bytes(B, Hq, Hkv, D))
+
+
+def attn_decode(q, k_cache, v_cache, block_table, lengths, k_scale=None, v_scale=None, scale=None, out=None, dtype=None, workspace=None,
+                stream=None):
+    """Attention of one new token of each sequence over the paged cache: q f16 or bf16 [B, Hq, D] (any row and head
+    strides that are multiples of 8), the cache as ``kv_write`` fills it (16-bit caches of q's type), Hq a multiple of Hkv
+    (query head h reads key head h // (Hq / Hkv)), block_table int32 [B, width], lengths int32 [B], the positions that each
+    sequence holds, the new token's own among them -> [B, Hq, D] of ``dtype`` (f16, as the next prologue takes it, or bf16; q's
+    type by default), or into ``out``. scale: of the scores, D ** -0.5 by default.
+
+    A sequence of length 0 gives zeros; positions whose page is not one of the cache's are left out, and no length passes the
+    table's width. What the cache holds behind a sequence's end - infinities and NaN too - does not count."""
+    import torch
+    ldq, hsq = _heads(q, "q")
+    B, Hq, D = q.shape
+    pages, Hkv, page, _, specs = _paged(k_cache, v_cache, k_scale, v_scale, q.dtype, None, D)
+    if Hkv == 0 or Hq % Hkv:
+        raise ValueError(f"q: {Hq} heads, expected a multiple of the cache's {Hkv}")
+    rows, width, spec = _table(block_table)
+    if rows != B:
+        raise ValueError(f"block_table: {rows} rows, expected {B}")
+    odt, code, ospec = _attn_out(out, dtype, q)
+    specs += [spec, (lengths, "lengths", torch.int32, (B,))] + ospec
+    need = lib().pq_attn_decode_workspace_bytes(B, Hq, Hkv, D)
+    if workspace is not None:
+        specs.append((workspace, "workspace", torch.uint8, need))
+    _validate(specs)
+    _on_device(k_cache, (q, "q"))
+    if out is None:
+        out = _new((B, Hq, D), odt, q.device, stream)
+    if workspace is None and need:
+        workspace = _new((need,), torch.uint8, q.device, stream)
+    _launch("pq_attn_decode", q.device, stream, q.data_ptr(), ldq, hsq, _type_code(q.dtype, "q"), k_cache.data_ptr(), v_cache.data_ptr(),
+            _addr(k_scale), _addr(v_scale), pages, page, block_table.data_ptr(), width, lengths.data_ptr(), B, Hq, Hkv, D,
+            D ** -0.5 if scale is None else float(scale), out.data_ptr(), code, _addr(workspace), workspace.numel() if workspace is not None else 0)
+    return out
+
+
+def attn_prefill_workspace_bytes(B, Tq, Tk, Hq, Hkv, D):
+    """Bytes of the workspace of ``attn_prefill``."""
+    if any(n > INT_MAX for n in (B, Tq, Tk, Hq, Hkv, D)):
+        _too_large(B=B, Tq=Tq, Tk=Tk, Hq=Hq, Hkv=Hkv, D=D)
+    return int(lib().pq_attn_prefill_workspace_bytes(B, Tq, Tk, Hq, Hkv, D))
+
+
+def attn_prefill(q, k, v, cu_q, cu_k=None, scale=None, causal=True, out=None, dtype=None, workspace=None, stream=None):
+    """Attention over packed prompts: q f16 or bf16 [Tq, Hq, D], k, v of its type [Tk, Hkv, D] (any row and head strides that
+    are multiples of 8, the columns of a merged projection's output among them), Hq a multiple of Hkv; cu_q int32 [B + 1], where each sequence's
+    rows begin, cu_k the same for its keys (cu_q by default) -> [Tq, Hq, D] of ``dtype`` (f16, as the next prologue takes
+    it, or bf16; q's type by default), or into ``out``. Query i of a sequence of nq queries and nk keys sees the keys j <= i + nk - nq
+    (all with causal=False): the chunk of a prompt whose earlier keys came back through ``kv_read`` is the last nq of nk.
+
+    A query that sees no key gives zeros, whatever it does not see does not count (infinities and NaN too), and rows of no
+    sequence are left as they were. scale: of the scores, D ** -0.5 by default."""
+    import torch
+    ldq, hsq = _heads(q, "q")
+    Tq, Hq, D = q.shape
+    ldk, hsk = _heads(k, "k", q.dtype, None, None, D)
+    Tk, Hkv, _ = k.shape
+    ldv, hsv = _heads(v, "v", q.dtype, Tk, Hkv, D)
+    if Hkv == 0 or Hq % Hkv:
+        raise ValueError(f"q: {Hq} heads, expected a multiple of k's {Hkv}")
+    cu_k = cu_q if cu_k is None else cu_k
+    if not isinstance(cu_q, torch.Tensor) or cu_q.dim() != 1 or cu_q.numel() < 1:
+        raise ValueError("cu_q: expected an int32 [B + 1] tensor")
+    B = cu_q.shape[0] - 1
+    if B > INT_MAX:
+        _too_large(B=B)
+    odt, code, ospec = _attn_out(out, dtype, q)
+    specs = [(cu_q, "cu_q", torch.int32, (B + 1,)), (cu_k, "cu_k", torch.int32, (B + 1,))] + ospec
+    need = lib().pq_attn_prefill_workspace_bytes(B, Tq, Tk, Hq, Hkv, D)
+    if workspace is not None:
+        specs.append((workspace, "workspace", torch.uint8, need))
+    _validate(specs)
+    _on_device(cu_q, (q, "q"), (k, "k"), (v, "v"))
+    if out is None:
+        out = _new((Tq, Hq, D), odt, q.device, stream)
+    if workspace is None and need:
+        workspace = _new((need,), torch.uint8, q.device, stream)
+    _launch("pq_attn_prefill", q.device, stream, q.data_ptr(), ldq, hsq, k.data_ptr(), ldk, hsk, v.data_ptr(), ldv, hsv, _type_code(q.dtype, "q"),
+            cu_q.data_ptr(), cu_k.data_ptr(), B, Tq, Tk, Hq, Hkv, D, D ** -0.5 if scale is None else float(scale), 1 if causal else 0,
+            out.data_ptr(), code, _addr(workspace), workspace.numel() if workspace is not None else 0)
+    return out
 
 
 def e4m3_encode(q, stream=None):

@@ -31,6 +31,8 @@ SOURCES = [
     # the prologue's results are defined by binary32 ops that each round: no contraction
     ("pq_prologue.hip", ["-ffp-contract=off"]),
     ("pq_norms.hip", []),
+    ("pq_kv.hip", []),
+    ("pq_attn.hip", []),
     # matrix-core results land in VGPRs (the fold reads them there; no AGPR copies)
     ("pq_matvec.hip", ["-mllvm", "-amdgpu-mfma-vgpr-form"]),
     ("pq_glu.hip", ["-mllvm", "-amdgpu-mfma-vgpr-form"]),

@@ -1,0 +1,198 @@
+// The key-value cache of the attention layers: rows quantised as they are written into its pages (pq_kv_write)
+// and sequences read back (pq_kv_read).
+//
+// A cache is [pages][Hkv][page][D], so a head's rows of one page are one contiguous run, which is what the
+// attention streams. Rows are e4m3 codes with one binary32 scale for each (row, head) in [pages][Hkv][page], or the
+// 16-bit values themselves. Per row x of D values (the encoder and the scale are those of the prologue's groups):
+//   s = fl32(max |x| * fl32(1/448)),  code_i = E(fl32(x_i * fl32(1/s))),  read back as fl(code_i * s).
+//
+// Both kernels move bytes: D / 8 lanes hold a row, 16 bytes of 16-bit values each, so a wave takes 8 rows of 64, 4 of
+// 128 or 2 of 256 values, and the row's maximum is a reduction over those lanes.
+#include <algorithm>
+
+#include "pq_attn.h"
+
+namespace pq {
+
+struct KvWriteArgs {
+  const uint16_t* src[2];   // k, v
+  int64_t ld[2], hs[2];
+  void* cache[2];
+  float* scale[2];
+  const int64_t* slots;
+  int64_t nslots;           // pages * page
+  int T, Hkv, page_shift;
+};
+
+// The largest of a non-negative value over the L lanes of a row.
+template <int L>
+__device__ __forceinline__ float row_max(float v) {
+#pragma unroll
+  for (int m = 1; m < L; m *= 2) v = __builtin_fmaxf(v, __shfl_xor(v, m));
+  return v;
+}
+
+template <int D, bool kBf16, bool kQuant>
+__global__ __launch_bounds__(256) void kv_write_kernel(KvWriteArgs a) {
+  constexpr int L = D / 8, R = 256 / L;   // lanes of a row, rows of a workgroup
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * R + threadIdx.x / L;
+  const int lane = threadIdx.x % L;
+  // unit = (token, k or v, head): the heads of a token stand next to each other in the source
+  const int64_t t = unit / (2 * a.Hkv);
+  const int r = static_cast<int>(unit - t * 2 * a.Hkv), which = r >= a.Hkv, h = r - which * a.Hkv;
+  if (t >= a.T) return;     // whole rows leave: the lanes of a row stay together
+  const int64_t slot = a.slots[t];
+  if (slot < 0 || slot >= a.nslots) return;
+  const attn_u32x4 q = *reinterpret_cast<const attn_u32x4*>(a.src[which] + t * a.ld[which] + h * a.hs[which] + 8 * lane);
+  const int64_t row = (((slot >> a.page_shift) * a.Hkv + h) << a.page_shift) + (slot & ((1 << a.page_shift) - 1));
+  if constexpr (!kQuant) {
+    *reinterpret_cast<attn_u32x4*>(static_cast<uint16_t*>(a.cache[which]) + row * D + 8 * lane) = q;
+  } else {
+    float v[8];
+    unpack16x8<kBf16>(q, v);
+    // a row with an infinity or a NaN gets the scale NaN and the codes 0: it reads back as NaN
+    float most = 0.0f;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      most = __builtin_fmaxf(most, __builtin_fabsf(v[i]));
+      bad = bad || !(__builtin_fabsf(v[i]) <= 3.4e38f);
+    }
+    most = row_max<L>(bad ? __builtin_inff() : most);
+    float s = most * (1.0f / 448.0f);
+    if (s < 1.17549435e-38f) s = 0.0f;   // its reciprocal would overflow: such a row counts as zero
+    const float inv = s > 0.0f && most <= 3.4e38f ? 1.0f / s : 0.0f;
+    if (!(most <= 3.4e38f)) s = __builtin_nanf("");
+    uint32_t c[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      c[i] = e4m3_encode2(v[4 * i] * inv, v[4 * i + 1] * inv) | e4m3_encode2(v[4 * i + 2] * inv, v[4 * i + 3] * inv) << 16;
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.cache[which]) + row * D + 8 * lane) = make_uint2(c[0], c[1]);
+    if (lane == 0) a.scale[which][row] = s;
+  }
+}
+
+struct KvReadArgs {
+  CacheArgs c;
+  const int32_t* cu;
+  int B, T;
+  uint16_t* out[2];
+};
+
+template <int D, bool kBf16, bool kQuant>
+__global__ __launch_bounds__(256) void kv_read_kernel(KvReadArgs a) {
+  constexpr int L = D / 8, R = 256 / L;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * R + threadIdx.x / L;
+  const int lane = threadIdx.x % L;
+  const int64_t t = unit / (2 * a.c.Hkv);
+  const int r = static_cast<int>(unit - t * 2 * a.c.Hkv), which = r >= a.c.Hkv, h = r - which * a.c.Hkv;
+  if (t >= a.T) return;
+  // the sequence of row t: the last b with cu[b] <= t
+  int lo = 0, hi = a.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.cu[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  const int64_t first = a.cu[lo];
+  if (t < first || t >= a.cu[lo + 1]) return;   // rows of no sequence stay as they are
+  const int64_t pos = t - first, row = cache_row(a.c, lo, h, pos);
+  attn_u32x4 q = {0, 0, 0, 0};                  // a page outside the cache reads as zeros
+  if (row >= 0) {
+    if constexpr (!kQuant) {
+      q = *reinterpret_cast<const attn_u32x4*>(static_cast<const uint16_t*>(which ? a.c.v : a.c.k) + row * D + 8 * lane);
+    } else {
+      const uint2 c = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(which ? a.c.v : a.c.k) + row * D + 8 * lane);
+      const float s = (which ? a.c.vs : a.c.ks)[row];
+      float v[8];
+      decode8(c, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= s;
+      q = pack16x8<kBf16>(v);
+    }
+  }
+  *reinterpret_cast<attn_u32x4*>(a.out[which] + (t * a.c.Hkv + h) * D + 8 * lane) = q;
+}
+
+template <int D>
+static hipError_t write_launch(const KvWriteArgs& a, int type, unsigned grid, hipStream_t s) {
+  if (a.scale[0] && type == PQ_BF16) return launch_kernel((kv_write_kernel<D, true, true>), dim3(grid), dim3(256), 0, s, a);
+  if (a.scale[0]) return launch_kernel((kv_write_kernel<D, false, true>), dim3(grid), dim3(256), 0, s, a);
+  return launch_kernel((kv_write_kernel<D, false, false>), dim3(grid), dim3(256), 0, s, a);   // bits are copied, whatever their type
+}
+template <int D>
+static hipError_t read_launch(const KvReadArgs& a, int type, unsigned grid, hipStream_t s) {
+  if (a.c.ks && type == PQ_BF16) return launch_kernel((kv_read_kernel<D, true, true>), dim3(grid), dim3(256), 0, s, a);
+  if (a.c.ks) return launch_kernel((kv_read_kernel<D, false, true>), dim3(grid), dim3(256), 0, s, a);
+  return launch_kernel((kv_read_kernel<D, false, false>), dim3(grid), dim3(256), 0, s, a);
+}
+
+int check_cache(const char* what, const void* kc, const void* vc, const float* ks, const float* vs, int64_t pages, int page, int Hkv, int D) {
+  if (D != 64 && D != 128 && D != 256) return set_error(PQ_ERR_SHAPE, "%s: head size D=%d must be 64, 128 or 256", what, D);
+  if (Hkv <= 0 || Hkv > kAttnMaxHeads) return set_error(PQ_ERR_SHAPE, "%s: Hkv=%d must be in 1..%d", what, Hkv, kAttnMaxHeads);
+  if (page < 16 || page > 1024 || (page & (page - 1)))
+    return set_error(PQ_ERR_SHAPE, "%s: page=%d must be a power of two in 16..1024", what, page);
+  if (pages < 0 || pages > INT32_MAX) return set_error(PQ_ERR_SHAPE, "%s: pages=%lld must be in 0..2^31-1", what, static_cast<long long>(pages));
+  if (!ks != !vs) return set_error(PQ_ERR_NULL, "%s: k and v scales go together", what);
+  if (pages && (!kc || !vc)) return set_error(PQ_ERR_NULL, "%s: NULL cache", what);
+  if (!aligned(kc, 16) || !aligned(vc, 16) || !aligned(ks, 4) || !aligned(vs, 4)) return set_error(PQ_ERR_ALIGN, "%s: misaligned cache", what);
+  return PQ_OK;
+}
+
+int check_heads(const char* what, const char* name, const void* p, int64_t ld, int64_t hs, int T, int H, int D) {
+  if (ld % 8 || hs % 8 || ld < 0 || hs < 0 || ld > kAttnMaxStride || hs > kAttnMaxStride)
+    return set_error(PQ_ERR_SHAPE, "%s: strides of %s (%lld, %lld) must be multiples of 8 in 0..2^31 - 8", what, name,
+                     static_cast<long long>(ld), static_cast<long long>(hs));
+  if (T > 0 && !p) return set_error(PQ_ERR_NULL, "%s: %s is NULL", what, name);
+  if (!aligned(p, 16)) return set_error(PQ_ERR_ALIGN, "%s: %s must be 16-byte aligned", what, name);
+  return PQ_OK;
+}
+
+}  // namespace pq
+
+extern "C" {
+
+int pq_kv_write(const uint16_t* k_d, int64_t ldk, int64_t hsk, const uint16_t* v_d, int64_t ldv, int64_t hsv, int type, int T, int Hkv, int D,
+                const int64_t* slots_d, void* kc_d, void* vc_d, float* ks_d, float* vs_d, int64_t pages, int page, pq_stream_t stream) {
+  using namespace pq;
+  clear_error();
+  const char* what = "pq_kv_write";
+  if (T < 0) return set_error(PQ_ERR_SHAPE, "%s: T=%d < 0", what, T);
+  if (type != PQ_F16 && type != PQ_BF16) return set_error(PQ_ERR_SHAPE, "%s: type %d, expected f16 or bf16", what, type);
+  int rc = check_cache(what, kc_d, vc_d, ks_d, vs_d, pages, page, Hkv, D);
+  if (rc == PQ_OK) rc = check_heads(what, "k", k_d, ldk, hsk, T, Hkv, D);
+  if (rc == PQ_OK) rc = check_heads(what, "v", v_d, ldv, hsv, T, Hkv, D);
+  if (rc != PQ_OK) return rc;
+  const int64_t rows = 2ll * T * Hkv, per = 256 / (D / 8), grid = (rows + per - 1) / per;
+  if (grid * 256 > 0xFFFFFFFFll) return set_error(PQ_ERR_SHAPE, "%s: T=%d rows too many for one call (split the rows)", what, T);
+  if (T == 0) return PQ_OK;
+  if (!slots_d) return set_error(PQ_ERR_NULL, "%s: slots is NULL", what);
+  if (!aligned(slots_d, 8)) return set_error(PQ_ERR_ALIGN, "%s: slots must be 8-byte aligned", what);
+  if (pages == 0) return PQ_OK;   // no slot exists
+  KvWriteArgs a{{k_d, v_d}, {ldk, ldv}, {hsk, hsv}, {kc_d, vc_d}, {ks_d, vs_d}, slots_d, pages * page, T, Hkv, __builtin_ctz(page)};
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const unsigned g = static_cast<unsigned>(grid);
+  return launch_status(what, D == 64 ? write_launch<64>(a, type, g, s) : D == 128 ? write_launch<128>(a, type, g, s) : write_launch<256>(a, type, g, s));
+}
+
+int pq_kv_read(const void* kc_d, const void* vc_d, const float* ks_d, const float* vs_d, int64_t pages, int page, const int32_t* table_d, int width,
+               const int32_t* cu_d, int B, int T, int Hkv, int D, uint16_t* k_d, uint16_t* v_d, int type, pq_stream_t stream) {
+  using namespace pq;
+  clear_error();
+  const char* what = "pq_kv_read";
+  if (T < 0 || B < 0 || width < 0) return set_error(PQ_ERR_SHAPE, "%s: T=%d, B=%d, width=%d: negative", what, T, B, width);
+  if (type != PQ_F16 && type != PQ_BF16) return set_error(PQ_ERR_SHAPE, "%s: type %d, expected f16 or bf16", what, type);
+  const int rc = check_cache(what, kc_d, vc_d, ks_d, vs_d, pages, page, Hkv, D);
+  if (rc != PQ_OK) return rc;
+  const int64_t rows = 2ll * T * Hkv, per = 256 / (D / 8), grid = (rows + per - 1) / per;
+  if (grid * 256 > 0xFFFFFFFFll) return set_error(PQ_ERR_SHAPE, "%s: T=%d rows too many for one call (split the sequences)", what, T);
+  if (T == 0 || B == 0) return PQ_OK;
+  if (!k_d || !v_d || !cu_d || (width && !table_d)) return set_error(PQ_ERR_NULL, "%s: NULL pointer", what);
+  if (!aligned(k_d, 16) || !aligned(v_d, 16) || !aligned(cu_d, 4) || !aligned(table_d, 4)) return set_error(PQ_ERR_ALIGN, "%s: misaligned pointer", what);
+  KvReadArgs a{{kc_d, vc_d, ks_d, vs_d, table_d, pages, width, Hkv, __builtin_ctz(page)}, cu_d, B, T, {k_d, v_d}};
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const unsigned g = static_cast<unsigned>(grid);
+  return launch_status(what, D == 64 ? read_launch<64>(a, type, g, s) : D == 128 ? read_launch<128>(a, type, g, s) : read_launch<256>(a, type, g, s));
+}
+
+}  // extern "C"
