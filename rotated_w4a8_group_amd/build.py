@@ -32,7 +32,8 @@ SOURCES = [
     ("pq_prologue.hip", ["-ffp-contract=off"]),
     ("pq_norms.hip", []),
     ("pq_kv.hip", []),
-    ("pq_attn.hip", []),
+    ("pq_attn_decode.hip", ["-mllvm", "-amdgpu-mfma-vgpr-form"]),
+    ("pq_attn_prefill.hip", ["-mllvm", "-amdgpu-mfma-vgpr-form"]),
     # matrix-core results land in VGPRs (the fold reads them there; no AGPR copies)
     ("pq_matvec.hip", ["-mllvm", "-amdgpu-mfma-vgpr-form"]),
     ("pq_glu.hip", ["-mllvm", "-amdgpu-mfma-vgpr-form"]),

@@ -7,7 +7,7 @@
 namespace pq {
 
 constexpr int kAttnMaxHeads = 1 << 16;
-constexpr int64_t kAttnMaxStride = (1ll << 31) - 8;
+constexpr int64_t kAttnMaxStride = 1ll << 24;   // elements: 64 rows stay within 32-bit offsets
 
 typedef uint32_t attn_u32x4 __attribute__((ext_vector_type(4)));
 
@@ -65,8 +65,68 @@ __device__ __forceinline__ int64_t cache_row(const CacheArgs& c, int b, int h, i
   return ((page * c.Hkv + h) << c.page_shift) + (pos & ((1ll << c.page_shift) - 1));
 }
 
+// Sum over the wave, the same value in every lane.
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int m = 1; m < 64; m *= 2) v += __shfl_xor(v, m);
+  return v;
+}
+
+// The D / 64 values of this lane in a 16-bit row.
+template <int D, bool kBf16>
+__device__ __forceinline__ void lane_values(const uint16_t* row, float (&v)[D / 64]) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) {
+    const uint32_t w = row[lane * (D / 64) + i];
+    v[i] = kBf16 ? bf16_to_f32(w) : f16_to_f32(w);
+  }
+}
+template <int D>
+__device__ __forceinline__ void lane_values(const uint8_t* row, float s, float (&v)[D / 64]) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) v[i] = s * __builtin_amdgcn_cvt_f32_fp8(row[lane * (D / 64) + i], 0);
+}
+
+// Running softmax of one query row: the largest score so far, the sum of exp2(c (score - largest)) and the weighted values.
+template <int D>
+struct RowState {
+  float m = -__builtin_inff(), l = 0.0f, o[D / 64] = {};
+  __device__ __forceinline__ void add(float s, float c, const float (&v)[D / 64]) {
+    const float n = s > m ? s : m;   // a NaN score leaves m and makes the sum NaN
+    const float f = m == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(c * (m - n));
+    const float p = s == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(c * (s - n));
+    m = n;
+    l = l * f + p;
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) o[i] = o[i] * f + p * v[i];
+  }
+};
+
+template <int D>
+__device__ __forceinline__ void store_row(uint16_t* out, const RowState<D>& r, bool any, int out_type) {
+  const int lane = threadIdx.x & 63;
+  const float inv = any ? 1.0f / r.l : 0.0f;
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) {
+    const float v = any ? r.o[i] * inv : 0.0f;
+    out[lane * (D / 64) + i] = static_cast<uint16_t>(out_type == PQ_BF16 ? pack2<true>(v, v) : pack2<false>(v, v));
+  }
+}
+
 // Checks shared by the entry points: PQ_OK, or an error code with its message.
 int check_cache(const char* what, const void* kc, const void* vc, const float* ks, const float* vs, int64_t pages, int page, int Hkv, int D);
 int check_heads(const char* what, const char* name, const void* p, int64_t ld, int64_t hs, int T, int H, int D);
+inline int check_attention(const char* what, int type, int out_type, int Hq, int Hkv, int D, float scale) {
+  if ((type != PQ_F16 && type != PQ_BF16) || (out_type != PQ_F16 && out_type != PQ_BF16))
+    return set_error(PQ_ERR_SHAPE, "%s: types (%d, out %d): f16 or bf16", what, type, out_type);
+  if (D != 64 && D != 128 && D != 256) return set_error(PQ_ERR_SHAPE, "%s: head size D=%d must be 64, 128 or 256", what, D);
+  if (Hkv <= 0 || Hkv > kAttnMaxHeads || Hq <= 0 || Hq > kAttnMaxHeads || Hq % Hkv)
+    return set_error(PQ_ERR_SHAPE, "%s: Hq=%d must be a multiple of Hkv=%d, both in 1..%d", what, Hq, Hkv, kAttnMaxHeads);
+  if (!(scale > 0.0f) || !(scale < __builtin_inff())) return set_error(PQ_ERR_SHAPE, "%s: scale must be positive and finite", what);
+  return PQ_OK;
+}
+
 
 }  // namespace pq

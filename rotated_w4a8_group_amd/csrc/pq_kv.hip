@@ -141,7 +141,7 @@ int check_cache(const char* what, const void* kc, const void* vc, const float* k
 
 int check_heads(const char* what, const char* name, const void* p, int64_t ld, int64_t hs, int T, int H, int D) {
   if (ld % 8 || hs % 8 || ld < 0 || hs < 0 || ld > kAttnMaxStride || hs > kAttnMaxStride)
-    return set_error(PQ_ERR_SHAPE, "%s: strides of %s (%lld, %lld) must be multiples of 8 in 0..2^31 - 8", what, name,
+    return set_error(PQ_ERR_SHAPE, "%s: strides of %s (%lld, %lld) must be multiples of 8 in 0..2^24", what, name,
                      static_cast<long long>(ld), static_cast<long long>(hs));
   if (T > 0 && !p) return set_error(PQ_ERR_NULL, "%s: %s is NULL", what, name);
   if (!aligned(p, 16)) return set_error(PQ_ERR_ALIGN, "%s: %s must be 16-byte aligned", what, name);
