@@ -1,7 +1,7 @@
 // Helpers shared by the key-value cache and the attention kernels (gfx950).
 #pragma once
 
-#include "pq_device.h"
+#include "pq_gemm_device.h"
 #include "pq_internal.h"
 
 namespace pq {
@@ -10,6 +10,8 @@ constexpr int kAttnMaxHeads = 1 << 16;
 constexpr int64_t kAttnMaxStride = 1ll << 24;   // elements: 64 rows stay within 32-bit offsets
 
 typedef uint32_t attn_u32x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 // 8 values of a 16-bit type from 16 loaded bytes.
 template <bool kBf16>
@@ -44,6 +46,24 @@ __device__ __forceinline__ void decode8(const uint2& c, float (&v)[8]) {
     v[4 * i + 3] = hi.y;
   }
 }
+
+// 4 keys of one channel a lane: lane l gives the address of key l % 16 / 4 and channels 4 (l % 4) .. + 3 of its 16 lanes' 4 x 16 block
+// and gets channel l % 16 of the 4 keys.
+__device__ __forceinline__ uint2 lds_read_transposed(const uint8_t* p) {
+  typedef __attribute__((address_space(3))) s16x4* lds_ptr;
+  return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(uintptr_t)lds_addr(p)));
+}
+
+// A value of this lane and of the same lane of the other half of the wave, the lower half's first.
+struct Halves { float lo, hi; };
+__device__ __forceinline__ Halves both_halves(float v) {
+  const uint32_t w = __builtin_bit_cast(uint32_t, v);
+  const auto r = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+  const uint32_t lo = r[0], hi = r[1];
+  return {__builtin_bit_cast(float, lo), __builtin_bit_cast(float, hi)};
+}
+__device__ __forceinline__ float both_halves_max(float v) { const Halves x = both_halves(v); return __builtin_fmaxf(x.lo, x.hi); }
+__device__ __forceinline__ float both_halves_sum(float v) { const Halves x = both_halves(v); return x.lo + x.hi; }
 
 // A paged cache and the pages of its sequences.
 struct CacheArgs {

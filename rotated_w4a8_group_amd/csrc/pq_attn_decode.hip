@@ -1,6 +1,21 @@
-// Attention of one new token of each sequence over the paged cache (pq_attn_decode).
+// Attention of one new token of each sequence over the paged cache (pq_attn_decode): the heads that share a key head are
+// the rows of one small product, so every cached row is read once.
 //
-// One wave per (row, query head): D / 64 channels per lane, the keys one by one with a running maximum and sum.
+// The cache is the traffic and bounds it; the arithmetic only has to stay beside it. A wave walks tiles of 32 keys, which go
+// global -> LDS by direct loads into its own two slots, K and V of one tile: while a tile's scores are computed its V is
+// in flight, while its V is used the next tile's K is. Nothing in the loop waits for another wave.
+//   S^T = K Q^T   (16x16x32, twice: 16 keys x 32 channels times 32 channels x 16 query heads): lane l holds head l % 16 and, of
+//                 each 16 keys, the 4 from 4 (l / 16) on;
+//   O^T = V^T P^T (16 channels x 32 keys times 32 keys x 16 heads), the keys in the order in which a lane holds them, V^T by
+//                 transposing LDS reads of that order.
+// Codes become 16-bit values, exactly, on their way from LDS to the matrix core (of q's type for K, bf16 for V); a key's
+// scale multiplies its score, a value's its weight. p is held in two 16-bit pieces, hi + lo, each with a product of its
+// own: the matrix core has the time, and no rounding of p shows in an f16 output (2^-16 of it is left).
+//
+// Work is split over the cache's length: the sequences' tiles, key head by key head, are one line that is cut into equal
+// shares, a workgroup each (at least 8 tiles), whatever the lengths. Where a share ends inside a sequence the workgroup leaves
+// its maximum, sum and O in the workspace, and attn_join_kernel puts the pieces together in the order of the line. Which shares
+// exist follows from the lengths on the device; the host only bounds them.
 #include <algorithm>
 
 #include "pq_attn.h"
@@ -12,53 +27,505 @@ struct DecodeArgs {
   const uint16_t* q;
   int64_t ldq, hsq;
   const int32_t* lens;
-  int B, Hq;
+  int B, Hq, G;             // G: query heads of a key head
+  int hv, tiles_of_heads;   // virtual heads: a key head once for each 16 query heads that share it
+  int split;                // 0: a workgroup for each sequence and virtual head
   float scale_log2;
   uint16_t* o;
   int out_type;
+  float* ws;
 };
 
-template <int D, bool kBf16, bool kQuant>
-__global__ __launch_bounds__(64) void attn_decode_kernel(DecodeArgs a) {
-  const int b = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq, h = hq / (a.Hq / a.c.Hkv);
-  float q[D / 64], k[D / 64], v[D / 64];
-  lane_values<D, kBf16>(a.q + b * a.ldq + hq * a.hsq, q);
-  RowState<D> r;
-  const int64_t len = std::min<int64_t>(a.lens[b], static_cast<int64_t>(a.c.width) << a.c.page_shift);
-  bool any = false;
-  for (int64_t j = 0; j < len; ++j) {
-    const int64_t row = cache_row(a.c, b, h, j);
-    if (row < 0) continue;
-    any = true;
-    if constexpr (kQuant) {
-      lane_values<D>(static_cast<const uint8_t*>(a.c.k) + row * D, a.c.ks[row], k);
-      lane_values<D>(static_cast<const uint8_t*>(a.c.v) + row * D, a.c.vs[row], v);
-    } else {
-      lane_values<D, kBf16>(static_cast<const uint16_t*>(a.c.k) + row * D, k);
-      lane_values<D, kBf16>(static_cast<const uint16_t*>(a.c.v) + row * D, v);
-    }
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i) s += q[i] * k[i];
-    r.add(lanes_sum(s), a.scale_log2, v);
+constexpr int kTileKeys = 32;
+constexpr int kLeastTiles = 8;      // of a share
+constexpr int kTableHalves = 256;   // 16-key halves whose pages a wave holds at a time
+
+template <int D, bool kQuant>
+struct DecodeTile {
+  static constexpr int kRow = D * (kQuant ? 1 : 2);        // bytes of a row
+  static constexpr int kPart = kTileKeys * kRow;           // a tile's K, or V
+  static constexpr int kWaves = 2 * kPart > 16384 ? 4 : 8;
+  static constexpr int kThreads = 64 * kWaves;
+  static constexpr int kLoads = kPart / 1024;              // direct loads of it
+  static constexpr int kChunks = kRow / 16;                // 16-byte chunks of a row
+  static constexpr int kTable = 4 * kTableHalves;
+  static constexpr int kScale = kQuant ? 256 : 0;          // 32 scales of K, 32 of V
+  static constexpr int kWave = 2 * kPart + 2 * kScale + kTable;
+  static constexpr int kState = kWaves * 16 * 16;          // maximum, sum, seen of every wave and head
+  static constexpr int kLds = kWaves * kWave + kState;
+  static constexpr int kPerCu = std::min(160 * 1024 / kLds, 2048 / kThreads);
+  static constexpr int kSlot = 16 * D + 64;                // floats of a piece in the workspace
+  static_assert(2 * kPart >= 16 * D * 4, "O of a wave fits its slots");
+
+  // Places of chunk c of row r in a slot, so that the 16 lanes of an operand read lie in different banks: K reads the same
+  // chunk of 16 rows; V 32 bytes of the 8 rows 4 g .. of two neighbouring lane groups (codes: 16 bytes of those and of the
+  // rows 16 further on).
+  static __device__ __forceinline__ int kswizzle(int r) { return kRow >= 256 ? r & 15 : kRow == 128 ? (r >> 1) & 7 : (r >> 2) & 3; }
+  static __device__ __forceinline__ int vswizzle(int r) {
+    if constexpr (kQuant) return kRow == 256 ? (r & 7) | (r >> 4 & 1) << 3 : kRow == 128 ? (r >> 1 & 3) | (r >> 4 & 1) << 2 : (r >> 2 & 1) | (r >> 4 & 1) << 1;
+    else return kRow >= 256 ? (r & 7) << 1 : (r >> 1 & 3) << 1;
   }
-  store_row<D>(a.o + (static_cast<int64_t>(b) * a.Hq + hq) * D, r, any, a.out_type);
+};
+
+template <bool kBf16>
+__device__ __forceinline__ v4f mfma_16(const attn_u32x4& a, const attn_u32x4& b, const v4f& c) {
+  if constexpr (kBf16) return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  else return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-template <int D>
-static hipError_t decode_launch(const DecodeArgs& a, int type, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(a.B * a.Hq)), block(64);
-  if (a.c.ks)
-    return type == PQ_BF16 ? launch_kernel((attn_decode_kernel<D, true, true>), grid, block, 0, s, a)
-                           : launch_kernel((attn_decode_kernel<D, false, true>), grid, block, 0, s, a);
-  return type == PQ_BF16 ? launch_kernel((attn_decode_kernel<D, true, false>), grid, block, 0, s, a)
-                         : launch_kernel((attn_decode_kernel<D, false, false>), grid, block, 0, s, a);
+// 4 codes as 16-bit values (exact).
+template <bool kBf16>
+__device__ __forceinline__ uint2 widen4(uint32_t w) {
+  if constexpr (kBf16)
+    return make_uint2(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true)));
+  else
+    return make_uint2(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true)));
 }
+template <bool kBf16>
+__device__ __forceinline__ attn_u32x4 widen8(uint32_t lo, uint32_t hi) {
+  const uint2 a = widen4<kBf16>(lo), b = widen4<kBf16>(hi);
+  return attn_u32x4{a.x, a.y, b.x, b.y};
+}
+
+// 8 bytes a lane: lanes 2 r and 2 r + 1 of 16 give the halves of row r's 16 bytes; lane i gets byte i of the 8 rows.
+__device__ __forceinline__ uint2 lds_read_transposed8(const uint8_t* p) {
+  typedef int i32x2 __attribute__((ext_vector_type(2)));
+  typedef __attribute__((address_space(3))) i32x2* lds_ptr;
+  return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_ptr)(uintptr_t)lds_addr(p)));
+}
+
+// The lanes l, l ^ 16, l ^ 32, l ^ 48 combined.
+template <typename F>
+__device__ __forceinline__ float four_groups(float v, F f) {
+  const uint32_t w = __builtin_bit_cast(uint32_t, v);
+  const auto r = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+  const uint32_t a = r[0], b = r[1];
+  const Halves x = both_halves(f(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)));
+  return f(x.lo, x.hi);
+}
+
+// Tiles of a sequence.
+__device__ __forceinline__ int64_t seq_len(const DecodeArgs& a, int b) {
+  return std::min<int64_t>(std::max(a.lens[b], 0), static_cast<int64_t>(a.c.width) << a.c.page_shift);
+}
+__device__ __forceinline__ int seq_tiles(const DecodeArgs& a, int b) { return static_cast<int>((seq_len(a, b) + kTileKeys - 1) / kTileKeys); }
+
+// Sum over the wave's lanes, everywhere.
+__device__ __forceinline__ int64_t wave_total(int64_t v) {
+#pragma unroll
+  for (int m = 1; m < 64; m *= 2) v += __shfl_xor(v, m);
+  return v;
+}
+
+// All tiles of all sequences and virtual heads, and tiles of one share.
+__device__ __forceinline__ int64_t all_tiles(const DecodeArgs& a) {
+  int64_t n = 0;
+  for (int b = threadIdx.x & 63; b < a.B; b += 64) n += seq_tiles(a, b);
+  return wave_total(n) * a.hv;
+}
+__device__ __forceinline__ int64_t share_tiles(int64_t all, int shares) {
+  return std::max<int64_t>(kLeastTiles, (all + shares - 1) / shares);
+}
+
+// The sequence that tile x of the line belongs to, its first tile and its tiles per virtual head: x is below all_tiles.
+struct Place {
+  int b, n;
+  int64_t first;
+};
+__device__ __forceinline__ Place find_place(const DecodeArgs& a, int64_t x) {
+  const int lane = threadIdx.x & 63;
+  int64_t before = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 64) {
+    const int n = b0 + lane < a.B ? seq_tiles(a, b0 + lane) : 0;
+    int64_t sum = static_cast<int64_t>(n) * a.hv;
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) {
+      const int64_t o = __shfl_up(sum, m);
+      sum += lane >= m ? o : 0;
+    }
+    const uint64_t here = __ballot(before + sum > x);
+    if (here) {
+      const int f = __builtin_ctzll(here), nf = __shfl(n, f);
+      return {b0 + f, nf, before + __shfl(sum, f) - static_cast<int64_t>(nf) * a.hv};
+    }
+    before += __shfl(sum, 63);
+  }
+  return {a.B, 0, before};
+}
+
+template <int D, bool kBf16, bool kQuant>
+__global__ __launch_bounds__((DecodeTile<D, kQuant>::kThreads), (DecodeTile<D, kQuant>::kPerCu * DecodeTile<D, kQuant>::kWaves / 4)) void attn_decode_kernel(DecodeArgs a) {
+  using Tile = DecodeTile<D, kQuant>;
+  constexpr int kDB = D / 16, kSteps = D / 32;
+  constexpr bool kVBf16 = kQuant || kBf16;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[Tile::kLds];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n = lane & 15, g = lane >> 4;
+  uint8_t* const mine = smem + wave * Tile::kWave;
+  uint8_t* const kslot = mine;
+  uint8_t* const vslot = mine + Tile::kPart;
+  float* const scales = reinterpret_cast<float*>(mine + 2 * Tile::kPart);      // two tiles' worth
+  int32_t* const table = reinterpret_cast<int32_t*>(mine + 2 * Tile::kPart + 2 * Tile::kScale);
+  float* const state = reinterpret_cast<float*>(smem + Tile::kWaves * Tile::kWave);
+  const float c = a.scale_log2;
+  const int64_t page_mask = (1ll << a.c.page_shift) - 1;
+
+  // this workgroup's share of the line
+  int64_t x, end, per = 0, all = 0;
+  if (a.split) {
+    all = all_tiles(a);
+    per = share_tiles(all, gridDim.x);
+    x = blockIdx.x * per;
+    end = std::min(x + per, all);
+  } else {
+    x = 0;
+    end = 1;
+  }
+  while (x < end) {
+    // the segment of one sequence and virtual head at x: its tiles t0 .. t1 - 1 of nt
+    int b, hv, t0, t1, nt;
+    if (a.split) {
+      const Place p = find_place(a, x);
+      const int64_t in = x - p.first;
+      b = __builtin_amdgcn_readfirstlane(p.b);
+      nt = __builtin_amdgcn_readfirstlane(p.n);
+      hv = __builtin_amdgcn_readfirstlane(static_cast<int>(in / p.n));
+      t0 = __builtin_amdgcn_readfirstlane(static_cast<int>(in % p.n));
+      t1 = __builtin_amdgcn_readfirstlane(static_cast<int>(std::min<int64_t>(nt, t0 + (end - x))));
+      x += t1 - t0;
+    } else {
+      b = blockIdx.x / a.hv;
+      hv = blockIdx.x % a.hv;
+      nt = __builtin_amdgcn_readfirstlane(seq_tiles(a, b));
+      t0 = 0;
+      t1 = nt;
+      x = end;
+    }
+    const int64_t len = seq_len(a, b);
+    const int h = hv / a.tiles_of_heads, first_head = hv % a.tiles_of_heads * 16, heads = std::min(a.G - first_head, 16);
+    const int hq0 = h * a.G + first_head;
+    const uint8_t* const kc = static_cast<const uint8_t*>(a.c.k);
+    const uint8_t* const vc = static_cast<const uint8_t*>(a.c.v);
+
+    // this wave's tiles
+    const int count = t1 - t0, ta = t0 + static_cast<int>(static_cast<int64_t>(count) * wave / Tile::kWaves),
+              tb = t0 + static_cast<int>(static_cast<int64_t>(count) * (wave + 1) / Tile::kWaves);
+
+    // query heads: for 16-bit rows channels 32 s + 8 g .. + 7 of step s; for codes 64 t + 16 g .. + 7 and .. + 15 of steps 2 t, 2 t + 1
+    attn_u32x4 q[kSteps];
+    if (ta < tb) {
+      const uint16_t* p = a.q + b * a.ldq + (hq0 + std::min(n, heads - 1)) * a.hsq;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) q[s] = *reinterpret_cast<const attn_u32x4*>(p + (kQuant ? 64 * (s / 2) + 16 * g + 8 * (s % 2) : 32 * s + 8 * g));
+    }
+
+    int held = ta;   // the tile that the held page numbers begin with
+    auto fill = [&](int t) {
+      held = t;
+      wait_lds_reads();
+#pragma unroll
+      for (int i = 0; i < kTableHalves / 64; ++i) {
+        const int64_t key = (static_cast<int64_t>(t) * 2 + 64 * i + lane) * 16, at = key >> a.c.page_shift;
+        int page = -1;
+        if (key < len) {                                    // positions past the width do not exist: len stops there
+          page = a.c.table[static_cast<int64_t>(b) * a.c.width + at];
+          if (page < 0 || page >= a.c.pages) page = -1;
+        }
+        table[64 * i + lane] = page;
+      }
+      wait_lds_reads();
+    };
+    auto page_of = [&](int t, int i) { return __builtin_amdgcn_readfirstlane(table[2 * (t - held) + i]); };
+    // first cache row of half i of tile t, and whether it exists; where it does not, row 0 of the cache stands in
+    auto row_of = [&](int t, int i, int page) {
+      const int64_t key = static_cast<int64_t>(t) * kTileKeys + 16 * i;
+      return page < 0 ? 0 : ((static_cast<int64_t>(page) * a.c.Hkv + h) << a.c.page_shift) + (key & page_mask);
+    };
+    auto load = [&](const uint8_t* cache, uint8_t* slot, int t, bool is_k) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const void* base = scalar_addr(cache + row_of(t, i, page_of(t, i)) * Tile::kRow);
+#pragma unroll
+        for (int j = 0; j < Tile::kLoads / 2; ++j) {
+          const int at = 64 * j + lane, r = at / Tile::kChunks, ch = at % Tile::kChunks;
+          lds_dma16_s(base, r * Tile::kRow + 16 * (ch ^ (is_k ? Tile::kswizzle(16 * i + r) : Tile::vswizzle(16 * i + r))),
+                      lds_addr(slot) + (i * Tile::kLoads / 2 + j) * 1024);
+        }
+      }
+    };
+    auto load_k = [&](int t) {
+      load(kc, kslot, t, true);
+      if constexpr (kQuant) {   // lanes 0..31 the scales of K, 32..63 those of V
+        const int64_t r0 = row_of(t, 0, page_of(t, 0)), r1 = row_of(t, 1, page_of(t, 1));
+        lds_dma4((lane < 32 ? a.c.ks : a.c.vs) + ((lane & 16) ? r1 : r0) + n, lds_addr(scales + 64 * (t & 1)));
+      }
+    };
+    auto load_v = [&](int t) { load(vc, vslot, t, false); };
+
+    v4f o[kDB];
+#pragma unroll
+    for (int i = 0; i < kDB; ++i) o[i] = v4f{0.f, 0.f, 0.f, 0.f};
+    float m = -__builtin_inff(), mc = 0.0f, l = 0.0f;
+    bool any = false;
+
+    if (ta < tb) {
+      fill(ta);
+      load_k(ta);
+      load_v(ta);
+    }
+    for (int t = ta; t < tb; ++t) {
+      const bool more = t + 1 < tb;
+      // which of the tile's keys exist
+      const int left = static_cast<int>(std::min<int64_t>(len - static_cast<int64_t>(t) * kTileKeys, kTileKeys));
+      uint32_t valid = left >= 32 ? 0xFFFFFFFFu : (1u << left) - 1;
+      if (page_of(t, 0) < 0) valid &= 0xFFFF0000u;
+      if (page_of(t, 1) < 0) valid &= 0x0000FFFFu;
+      any = any || valid;
+
+      wait_vm<Tile::kLoads>();          // K of this tile and its scales; V may be in flight
+      v4f s[2];
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        s[kb] = v4f{0.f, 0.f, 0.f, 0.f};
+        const int r = 16 * kb + n;
+        if constexpr (kQuant) {
+#pragma unroll
+          for (int st = 0; st < kSteps / 2; ++st) {
+            const attn_u32x4 w = *reinterpret_cast<const attn_u32x4*>(kslot + r * Tile::kRow + 16 * ((4 * st + g) ^ Tile::kswizzle(r)));
+            s[kb] = mfma_16<kBf16>(widen8<kBf16>(w.x, w.y), q[2 * st], s[kb]);
+            s[kb] = mfma_16<kBf16>(widen8<kBf16>(w.z, w.w), q[2 * st + 1], s[kb]);
+          }
+        } else {
+#pragma unroll
+          for (int st = 0; st < kSteps; ++st) {
+            const attn_u32x4 w = *reinterpret_cast<const attn_u32x4*>(kslot + r * Tile::kRow + 16 * ((4 * st + g) ^ Tile::kswizzle(r)));
+            s[kb] = mfma_16<kBf16>(w, q[st], s[kb]);
+          }
+        }
+      }
+      float vs[2][4];
+      if constexpr (kQuant) {
+        const float* sc = scales + 64 * (t & 1);
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+          const float4 ks4 = *reinterpret_cast<const float4*>(sc + 16 * kb + 4 * g), vs4 = *reinterpret_cast<const float4*>(sc + 32 + 16 * kb + 4 * g);
+          s[kb] = v4f{s[kb][0] * ks4.x, s[kb][1] * ks4.y, s[kb][2] * ks4.z, s[kb][3] * ks4.w};
+          vs[kb][0] = vs4.x, vs[kb][1] = vs4.y, vs[kb][2] = vs4.z, vs[kb][3] = vs4.w;
+        }
+      }
+      wait_lds_reads();                 // K's slot is free
+      if (more) {
+        if (t + 1 - held >= kTableHalves / 2) fill(t + 1);
+        load_k(t + 1);
+      }
+      if (valid != 0xFFFFFFFFu) {
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool is = valid >> (16 * kb + 4 * g + i) & 1;
+            s[kb][i] = is ? s[kb][i] : -__builtin_inff();
+            if constexpr (kQuant) vs[kb][i] = is ? vs[kb][i] : 0.0f;
+          }
+      }
+      float mt = m;
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mt = __builtin_fmaxf(mt, s[kb][i]);
+      mt = four_groups(mt, [](float u, float v) { return __builtin_fmaxf(u, v); });
+      if (__any((mt - m) * c > 8.0f)) {
+        const float f = m == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m * c - mt * c);
+        m = mt;
+        mc = m == -__builtin_inff() ? 0.0f : m * c;
+        l *= f;
+#pragma unroll
+        for (int i = 0; i < kDB; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[i][j] *= f;
+      }
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          float p[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            p[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i + k], c, -mc));
+            l += p[k];
+            if constexpr (kQuant) p[k] *= vs[kb][i + k];
+          }
+          const uint32_t w = pack2<kVBf16>(p[0], p[1]);
+          hi[2 * kb + i / 2] = w;
+          lo[2 * kb + i / 2] = kVBf16 ? pack2<true>(p[0] - bf16_to_f32(w), p[1] - bf16_to_f32(w >> 16)) : pack2<false>(p[0] - f16_to_f32(w), p[1] - f16_to_f32(w >> 16));
+        }
+      const attn_u32x4 ph = {hi[0], hi[1], hi[2], hi[3]}, pl = {lo[0], lo[1], lo[2], lo[3]};
+
+      if (more) wait_vm<Tile::kLoads + (kQuant ? 1 : 0)>();   // V of this tile; the next K may be in flight
+      else wait_vm<0>();
+      if (valid != 0xFFFFFFFFu) {       // rows that do not exist enter the product with weight 0: as zeros, whatever the cache holds there
+#pragma unroll
+        for (int j = 0; j < Tile::kLoads; ++j) {
+          const int r = (64 * j + lane) / Tile::kChunks;
+          if (!(valid >> r & 1)) *reinterpret_cast<attn_u32x4*>(vslot + 1024 * j + 16 * lane) = attn_u32x4{0, 0, 0, 0};
+        }
+        wait_lds_reads();
+      }
+#pragma unroll
+      for (int db = 0; db < kDB; ++db) {
+        attn_u32x4 w;
+        if constexpr (kQuant) {
+          const int i = (lane & 15) >> 1, r = 4 * g + (i & 3) + (i >> 2) * 16;
+          const uint2 v = lds_read_transposed8(vslot + r * Tile::kRow + 16 * (db ^ Tile::vswizzle(r)) + 8 * (lane & 1));
+          w = widen8<true>(v.x, v.y);
+        } else {
+          const int r = 4 * g + ((lane & 15) >> 2), ch = 2 * db + ((lane & 3) >> 1);
+          const uint2 v0 = lds_read_transposed(vslot + r * Tile::kRow + 16 * (ch ^ Tile::vswizzle(r)) + 8 * (lane & 1));
+          const uint2 v1 = lds_read_transposed(vslot + (r + 16) * Tile::kRow + 16 * (ch ^ Tile::vswizzle(r + 16)) + 8 * (lane & 1));
+          w = attn_u32x4{v0.x, v0.y, v1.x, v1.y};
+        }
+        o[db] = mfma_16<kVBf16>(w, ph, o[db]);
+        o[db] = mfma_16<kVBf16>(w, pl, o[db]);
+      }
+      wait_lds_reads();                 // V's slot is free
+      if (more) load_v(t + 1);
+    }
+
+    // The waves' states meet in LDS: O [16 heads][D] in each wave's own slots, its 16-byte chunks permuted by the head.
+    l = four_groups(l, [](float u, float v) { return u + v; });
+    float* const po = reinterpret_cast<float*>(mine);
+#pragma unroll
+    for (int db = 0; db < kDB; ++db)
+      *reinterpret_cast<float4*>(po + n * D + 4 * ((4 * db + g) ^ n)) = make_float4(o[db][0], o[db][1], o[db][2], o[db][3]);
+    if (g == 0) *reinterpret_cast<float4*>(state + (wave * 16 + n) * 4) = make_float4(m == -__builtin_inff() ? m : mc, l, any ? 1.0f : 0.0f, 0.0f);
+    __syncthreads();
+    const bool whole = t0 == 0 && t1 == nt;
+    const int slot = 2 * blockIdx.x + (t0 == 0);    // at most one segment of a share began before it, and one goes on behind it
+    for (int e = tid; e < heads * (D / 4); e += Tile::kThreads) {
+      const int r = e / (D / 4), ch = e % (D / 4);
+      float most = -__builtin_inff(), sum = 0.0f, seen = 0.0f;
+#pragma unroll
+      for (int w = 0; w < Tile::kWaves; ++w) most = __builtin_fmaxf(most, state[(w * 16 + r) * 4]);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < Tile::kWaves; ++w) {
+        const float4 st = *reinterpret_cast<const float4*>(state + (w * 16 + r) * 4);
+        const float f = st.x == -__builtin_inff() ? (st.y == st.y ? 0.0f : st.y) : __builtin_amdgcn_exp2f(st.x - most);
+        const float4 u = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + w * Tile::kWave) + r * D + 4 * (ch ^ r));
+        sum += f * st.y;
+        seen += st.z;
+        v.x += f * u.x, v.y += f * u.y, v.z += f * u.z, v.w += f * u.w;
+      }
+      if (whole) {
+        const float inv = seen > 0.0f ? 1.0f / sum : 0.0f;
+        const float4 y = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+        *reinterpret_cast<uint2*>(a.o + (static_cast<int64_t>(b) * a.Hq + hq0 + r) * D + 4 * ch) =
+            a.out_type == PQ_BF16 ? make_uint2(pack2<true>(y.x, y.y), pack2<true>(y.z, y.w)) : make_uint2(pack2<false>(y.x, y.y), pack2<false>(y.z, y.w));
+      } else {
+        float* const p = a.ws + static_cast<int64_t>(slot) * Tile::kSlot;
+        *reinterpret_cast<float4*>(p + r * D + 4 * ch) = v;
+        if (ch == 0) *reinterpret_cast<float4*>(p + 16 * D + 4 * r) = make_float4(most, sum, seen, 0.0f);
+      }
+    }
+    __syncthreads();   // before the slots are loaded again
+  }
+}
+
+// The pieces of one sequence and query head, in the order of the line: D / 4 threads each take 4 channels of every kParts-th piece.
+template <int D, bool kQuant>
+__global__ __launch_bounds__(256) void attn_join_kernel(DecodeArgs a, int shares) {
+  using Tile = DecodeTile<D, kQuant>;
+  constexpr int kLanes = D / 4, kParts = 256 / kLanes;
+  __shared__ __attribute__((aligned(16))) float part[kParts][D];
+  __shared__ float sums[kParts][4];
+  const int b = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq;
+  const int h = hq / a.G, hv = h * a.tiles_of_heads + hq % a.G / 16, r = hq % a.G % 16;
+  const int64_t all = all_tiles(a), per = share_tiles(all, shares);
+  int64_t before = 0;
+  for (int i = threadIdx.x & 63; i < b; i += 64) before += seq_tiles(a, i);
+  const int nt = seq_tiles(a, b);
+  const int64_t s0 = wave_total(before) * a.hv + static_cast<int64_t>(hv) * nt, s1 = s0 + nt;
+  uint16_t* const out = a.o + (static_cast<int64_t>(b) * a.Hq + hq) * D;
+  const int lane = threadIdx.x % kLanes, p = threadIdx.x / kLanes;
+  if (nt == 0) {
+    if (p == 0) *reinterpret_cast<uint2*>(out + 4 * lane) = make_uint2(0, 0);
+    return;
+  }
+  const int64_t w0 = s0 / per, w1 = (s1 - 1) / per;
+  if (w0 == w1) return;   // one share holds it whole, and has written it
+  float m = -__builtin_inff(), l = 0.0f, seen = 0.0f;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int64_t w = w0 + p; w <= w1; w += kParts) {
+    const float* q = a.ws + (2 * w + (w == w0)) * Tile::kSlot;
+    const float4 st = *reinterpret_cast<const float4*>(q + 16 * D + 4 * r), u = *reinterpret_cast<const float4*>(q + r * D + 4 * lane);
+    const float n = __builtin_fmaxf(m, st.x);
+    const float f = m == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m - n), e = st.x == -__builtin_inff() ? (st.y == st.y ? 0.0f : st.y) : __builtin_amdgcn_exp2f(st.x - n);
+    m = n;
+    l = l * f + st.y * e;
+    seen += st.z;
+    v.x = v.x * f + u.x * e, v.y = v.y * f + u.y * e, v.z = v.z * f + u.z * e, v.w = v.w * f + u.w * e;
+  }
+  *reinterpret_cast<float4*>(&part[p][4 * lane]) = v;
+  if (lane == 0) sums[p][0] = m, sums[p][1] = l, sums[p][2] = seen;
+  __syncthreads();
+  if (p) return;
+  float most = -__builtin_inff(), sum = 0.0f;
+  seen = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kParts; ++i) most = __builtin_fmaxf(most, sums[i][0]);
+  v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < kParts; ++i) {
+    const float f = sums[i][0] == -__builtin_inff() ? (sums[i][1] == sums[i][1] ? 0.0f : sums[i][1]) : __builtin_amdgcn_exp2f(sums[i][0] - most);
+    const float4 u = *reinterpret_cast<const float4*>(&part[i][4 * lane]);
+    sum += f * sums[i][1];
+    seen += sums[i][2];
+    v.x += f * u.x, v.y += f * u.y, v.z += f * u.z, v.w += f * u.w;
+  }
+  const float inv = seen > 0.0f ? 1.0f / sum : 0.0f;
+  *reinterpret_cast<uint2*>(out + 4 * lane) = a.out_type == PQ_BF16 ? make_uint2(pack2<true>(v.x * inv, v.y * inv), pack2<true>(v.z * inv, v.w * inv))
+                                                                    : make_uint2(pack2<false>(v.x * inv, v.y * inv), pack2<false>(v.z * inv, v.w * inv));
+}
+
+// Shares that a device holds at once, of every cache type.
+template <int D>
+static int most_shares() { return cu_count() * std::max(DecodeTile<D, true>::kPerCu, DecodeTile<D, false>::kPerCu); }
+// Up to this many positions a sequence's head stays in one workgroup, and no join follows.
+constexpr int64_t kWholeLength = 1024;
+
+template <int D>
+static size_t decode_workspace(int64_t) { return 2ull * most_shares<D>() * DecodeTile<D, true>::kSlot * sizeof(float); }
+
+template <int D, bool kBf16, bool kQuant>
+static hipError_t decode_launch(DecodeArgs a, hipStream_t s) {
+  using Tile = DecodeTile<D, kQuant>;
+  const int64_t length = static_cast<int64_t>(a.c.width) << a.c.page_shift, heads = static_cast<int64_t>(a.B) * a.hv;
+  const int64_t tiles = heads * ((length + kTileKeys - 1) / kTileKeys);
+  a.split = length > kWholeLength;
+  const int64_t grid = a.split ? std::min<int64_t>(cu_count() * Tile::kPerCu, (tiles + kLeastTiles - 1) / kLeastTiles) : heads;
+  hipError_t e = launch_kernel((attn_decode_kernel<D, kBf16, kQuant>), dim3(static_cast<unsigned>(grid)), dim3(Tile::kThreads), 0, s, a);
+  if (e == hipSuccess && a.split)
+    e = launch_kernel((attn_join_kernel<D, kQuant>), dim3(static_cast<unsigned>(a.B * a.Hq)), dim3(256), 0, s, a, static_cast<int>(grid));
+  return e;
+}
+template <int D>
+static hipError_t decode_for(const DecodeArgs& a, int type, hipStream_t s) {
+  if (a.c.ks) return type == PQ_BF16 ? decode_launch<D, true, true>(a, s) : decode_launch<D, false, true>(a, s);
+  return type == PQ_BF16 ? decode_launch<D, true, false>(a, s) : decode_launch<D, false, false>(a, s);
+}
+
 }  // namespace pq
 
 extern "C" {
 
-size_t pq_attn_decode_workspace_bytes(int B, int Hq, int Hkv, int D) { return 0; }
+size_t pq_attn_decode_workspace_bytes(int B, int Hq, int Hkv, int D) {
+  using namespace pq;
+  if (B <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv) return 0;
+  return D == 64 ? decode_workspace<64>(B) : D == 128 ? decode_workspace<128>(B) : D == 256 ? decode_workspace<256>(B) : 0;
+}
 
 int pq_attn_decode(const uint16_t* q_d, int64_t ldq, int64_t hsq, int type, const void* kc_d, const void* vc_d, const float* ks_d, const float* vs_d,
                    int64_t pages, int page, const int32_t* table_d, int width, const int32_t* lens_d, int B, int Hq, int Hkv, int D, float scale,
@@ -71,14 +538,20 @@ int pq_attn_decode(const uint16_t* q_d, int64_t ldq, int64_t hsq, int type, cons
   if (rc == PQ_OK) rc = check_cache(what, kc_d, vc_d, ks_d, vs_d, pages, page, Hkv, D);
   if (rc == PQ_OK) rc = check_heads(what, "q", q_d, ldq, hsq, B, Hq, D);
   if (rc != PQ_OK) return rc;
-  if (static_cast<int64_t>(B) * Hq * 64 > 0xFFFFFFFFll) return set_error(PQ_ERR_SHAPE, "%s: B=%d sequences too many for one call", what, B);
+  if (static_cast<int64_t>(B) * Hq * 512 > 0xFFFFFFFFll)   // the runtime counts a launch's threads in 32 bits
+    return set_error(PQ_ERR_SHAPE, "%s: B=%d sequences of %d heads too many for one call", what, B, Hq);
+  if (static_cast<int64_t>(width) * page > INT32_MAX)
+    return set_error(PQ_ERR_SHAPE, "%s: width=%d pages of %d rows: sequences of at most 2^31 - 1 positions", what, width, page);
   if (B == 0) return PQ_OK;
   if (!o_d || !lens_d || (width && !table_d)) return set_error(PQ_ERR_NULL, "%s: NULL pointer", what);
-  if (!aligned(o_d, 16) || !aligned(lens_d, 4) || !aligned(table_d, 4)) return set_error(PQ_ERR_ALIGN, "%s: misaligned pointer", what);
-  DecodeArgs a{{kc_d, vc_d, ks_d, vs_d, table_d, pages, width, Hkv, __builtin_ctz(page)}, q_d, ldq, hsq, lens_d, B, Hq,
-               scale * 1.44269504088896340736f, o_d, out_type};
+  if (!aligned(o_d, 16) || !aligned(lens_d, 4) || !aligned(table_d, 4) || !aligned(ws_d, 16)) return set_error(PQ_ERR_ALIGN, "%s: misaligned pointer", what);
+  const size_t need = pq_attn_decode_workspace_bytes(B, Hq, Hkv, D);
+  if (!ws_d || ws_bytes < need) return set_error(PQ_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", what, ws_d ? ws_bytes : 0, need);
+  const int G = Hq / Hkv, tiles_of_heads = (G + 15) / 16;
+  DecodeArgs a{{kc_d, vc_d, ks_d, vs_d, table_d, pages, pages ? width : 0, Hkv, __builtin_ctz(page)}, q_d, ldq, hsq, lens_d, B, Hq, G,
+               Hkv * tiles_of_heads, tiles_of_heads, 0, scale * 1.44269504088896340736f, o_d, out_type, static_cast<float*>(ws_d)};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  return launch_status(what, D == 64 ? decode_launch<64>(a, type, s) : D == 128 ? decode_launch<128>(a, type, s) : decode_launch<256>(a, type, s));
+  return launch_status(what, D == 64 ? decode_for<64>(a, type, s) : D == 128 ? decode_for<128>(a, type, s) : decode_for<256>(a, type, s));
 }
 
 }  // extern "C"

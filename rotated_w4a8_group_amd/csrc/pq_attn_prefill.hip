@@ -21,13 +21,10 @@
 #include <algorithm>
 
 #include "pq_attn.h"
-#include "pq_gemm_device.h"
 
 namespace pq {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 struct PrefillArgs {
   const uint16_t* q;
@@ -52,24 +49,6 @@ __device__ __forceinline__ f32x16 mfma_32(const attn_u32x4& a, const attn_u32x4&
   if constexpr (kBf16) return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
   else return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
-
-// 4 keys of one channel a lane: lane l gives the address of key l % 16 / 4 and channels 4 (l % 4) .. + 3 of its 16 lanes' 4 x 16 block
-// and gets channel l % 16 of the 4 keys.
-__device__ __forceinline__ uint2 lds_read_transposed(const uint8_t* p) {
-  typedef __attribute__((address_space(3))) s16x4* lds_ptr;
-  return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(uintptr_t)lds_addr(p)));
-}
-
-// A value of this lane and of the same lane of the other half of the wave, the lower half's first.
-struct Halves { float lo, hi; };
-__device__ __forceinline__ Halves both_halves(float v) {
-  const uint32_t w = __builtin_bit_cast(uint32_t, v);
-  const auto r = __builtin_amdgcn_permlane32_swap(w, w, false, false);
-  const uint32_t lo = r[0], hi = r[1];
-  return {__builtin_bit_cast(float, lo), __builtin_bit_cast(float, hi)};
-}
-__device__ __forceinline__ float both_halves_max(float v) { const Halves x = both_halves(v); return __builtin_fmaxf(x.lo, x.hi); }
-__device__ __forceinline__ float both_halves_sum(float v) { const Halves x = both_halves(v); return x.lo + x.hi; }
 
 template <int D>
 struct PrefillTile {
