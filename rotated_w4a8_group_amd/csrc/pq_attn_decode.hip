@@ -12,10 +12,10 @@
 // scale multiplies its score, a value's its weight. p is held in two 16-bit pieces, hi + lo, each with a product of its
 // own: the matrix core has the time, and no rounding of p shows in an f16 output (2^-16 of it is left).
 //
-// Work is split over the cache's length: the sequences' tiles, key head by key head, are one line that is cut into equal
-// shares, a workgroup each (at least 8 tiles), whatever the lengths. Where a share ends inside a sequence the workgroup leaves
-// its maximum, sum and O in the workspace, and attn_join_kernel puts the pieces together in the order of the line. Which shares
-// exist follows from the lengths on the device; the host only bounds them.
+// Work is split over the cache's length: each head's tiles of a sequence are cut into pieces of at most a share of all of them
+// (Cut), a workgroup each, whatever the lengths. A piece that is not the whole head leaves its maximum, sum and O in the
+// workspace, and attn_join_kernel puts the pieces together in their order. Which pieces exist follows from the lengths on
+// the device; the host only bounds them.
 #include <algorithm>
 
 #include "pq_attn.h"
@@ -29,7 +29,7 @@ struct DecodeArgs {
   const int32_t* lens;
   int B, Hq, G;             // G: query heads of a key head
   int hv, tiles_of_heads;   // virtual heads: a key head once for each 16 query heads that share it
-  int split;                // 0: a workgroup for each sequence and virtual head
+  int pieces;               // pieces to cut the whole line into, about; 0: a workgroup for each sequence and virtual head
   float scale_log2;
   uint16_t* o;
   int out_type;
@@ -38,13 +38,15 @@ struct DecodeArgs {
 
 constexpr int kTileKeys = 32;
 constexpr int kLeastTiles = 8;      // of a share
-constexpr int kTableHalves = 256;   // 16-key halves whose pages a wave holds at a time
+constexpr int kTableHalves = 128;   // 16-key halves whose pages a wave holds at a time
+constexpr int kMostPieces = 4096;   // of one head
 
-template <int D, bool kQuant>
+// kWide: as many waves as the LDS holds, for the calls with fewer workgroups than CUs; else several workgroups a CU.
+template <int D, bool kQuant, bool kWide>
 struct DecodeTile {
   static constexpr int kRow = D * (kQuant ? 1 : 2);        // bytes of a row
   static constexpr int kPart = kTileKeys * kRow;           // a tile's K, or V
-  static constexpr int kWaves = 2 * kPart > 16384 ? 4 : 8;
+  static constexpr int kWaves = (2 * kPart > 16384 ? 2 : 2 * kPart > 8192 || !kWide ? 4 : 8) * (kWide ? 2 : 1);
   static constexpr int kThreads = 64 * kWaves;
   static constexpr int kLoads = kPart / 1024;              // direct loads of it
   static constexpr int kChunks = kRow / 16;                // 16-byte chunks of a row
@@ -53,7 +55,7 @@ struct DecodeTile {
   static constexpr int kWave = 2 * kPart + 2 * kScale + kTable;
   static constexpr int kState = kWaves * 16 * 16;          // maximum, sum, seen of every wave and head
   static constexpr int kLds = kWaves * kWave + kState;
-  static constexpr int kPerCu = std::min(160 * 1024 / kLds, 2048 / kThreads);
+  static constexpr int kPerCu = std::min(160 * 1024 / kLds, 16 / kWaves);
   static constexpr int kSlot = 16 * D + 64;                // floats of a piece in the workspace
   static_assert(2 * kPart >= 16 * D * 4, "O of a wave fits its slots");
 
@@ -96,6 +98,13 @@ __device__ __forceinline__ uint2 lds_read_transposed8(const uint8_t* p) {
   return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_ptr)(uintptr_t)lds_addr(p)));
 }
 
+// The same number, where the compiler may not know it: what an address takes from it is computed where it is used, a few vector
+// instructions, and not kept in a register for the whole loop.
+__device__ __forceinline__ int opaque(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 // The lanes l, l ^ 16, l ^ 32, l ^ 48 combined.
 template <typename F>
 __device__ __forceinline__ float four_groups(float v, F f) {
@@ -106,58 +115,43 @@ __device__ __forceinline__ float four_groups(float v, F f) {
   return f(x.lo, x.hi);
 }
 
-// Tiles of a sequence.
-__device__ __forceinline__ int64_t seq_len(const DecodeArgs& a, int b) {
-  return std::min<int64_t>(std::max(a.lens[b], 0), static_cast<int64_t>(a.c.width) << a.c.page_shift);
-}
-__device__ __forceinline__ int seq_tiles(const DecodeArgs& a, int b) { return static_cast<int>((seq_len(a, b) + kTileKeys - 1) / kTileKeys); }
+// Positions and tiles of a sequence.
+__device__ __forceinline__ int seq_len(const DecodeArgs& a, int b) { return std::min(std::max(a.lens[b], 0), a.c.width << a.c.page_shift); }
+__device__ __forceinline__ int tiles_of(int len) { return static_cast<int>((static_cast<uint32_t>(len) + kTileKeys - 1) / kTileKeys); }
 
-// Sum over the wave's lanes, everywhere.
-__device__ __forceinline__ int64_t wave_total(int64_t v) {
-#pragma unroll
-  for (int m = 1; m < 64; m *= 2) v += __shfl_xor(v, m);
+// Sum over the lanes up to this one.
+__device__ __forceinline__ int lanes_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // within 16 lanes: 1, 2, 4, 8 back
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // the last lane of 16 to the next 16
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // that of 32 to the upper 32
   return v;
 }
+__device__ __forceinline__ int lanes_total(int v) { return __builtin_amdgcn_readlane(lanes_scan(v), 63); }
 
-// All tiles of all sequences and virtual heads, and tiles of one share.
-__device__ __forceinline__ int64_t all_tiles(const DecodeArgs& a) {
-  int64_t n = 0;
-  for (int b = threadIdx.x & 63; b < a.B; b += 64) n += seq_tiles(a, b);
-  return wave_total(n) * a.hv;
-}
-__device__ __forceinline__ int64_t share_tiles(int64_t all, int shares) {
-  return std::max<int64_t>(kLeastTiles, (all + shares - 1) / shares);
-}
-
-// The sequence that tile x of the line belongs to, its first tile and its tiles per virtual head: x is below all_tiles.
-struct Place {
-  int b, n;
-  int64_t first;
-};
-__device__ __forceinline__ Place find_place(const DecodeArgs& a, int64_t x) {
-  const int lane = threadIdx.x & 63;
-  int64_t before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 64) {
-    const int n = b0 + lane < a.B ? seq_tiles(a, b0 + lane) : 0;
-    int64_t sum = static_cast<int64_t>(n) * a.hv;
-#pragma unroll
-    for (int m = 1; m < 64; m *= 2) {
-      const int64_t o = __shfl_up(sum, m);
-      sum += lane >= m ? o : 0;
-    }
-    const uint64_t here = __ballot(before + sum > x);
-    if (here) {
-      const int f = __builtin_ctzll(here), nf = __shfl(n, f);
-      return {b0 + f, nf, before + __shfl(sum, f) - static_cast<int64_t>(nf) * a.hv};
-    }
-    before += __shfl(sum, 63);
+// How the sequences are cut: a head's nt tiles into pieces of at most `per`, alike in size; the pieces stand in one line,
+// sequence by sequence and head by head. The host bounds their number (a.pieces + sequences x heads), the lengths decide it.
+// Sequence b is lane b % 64's of round b / 64.
+struct Cut {
+  int per, first_len;   // this lane's length in the first round
+  __device__ __forceinline__ explicit Cut(const DecodeArgs& a) {
+    const int lane = threadIdx.x & 63;
+    first_len = lane < a.B ? seq_len(a, lane) : 0;
+    int n = tiles_of(first_len);
+    for (int b = lane + 64; b < a.B; b += 64) n += tiles_of(seq_len(a, b));
+    const int all = lanes_total(n) * a.hv;
+    per = std::max(kLeastTiles, (all + a.pieces - 1) / a.pieces);
   }
-  return {a.B, 0, before};
-}
+  __device__ __forceinline__ int len(const DecodeArgs& a, int b) const { return b < 64 ? first_len : b < a.B ? seq_len(a, b) : 0; }
+  __device__ __forceinline__ int pieces(int len) const { return (tiles_of(len) + per - 1) / per; }
+};
 
-template <int D, bool kBf16, bool kQuant>
-__global__ __launch_bounds__((DecodeTile<D, kQuant>::kThreads), (DecodeTile<D, kQuant>::kPerCu * DecodeTile<D, kQuant>::kWaves / 4)) void attn_decode_kernel(DecodeArgs a) {
-  using Tile = DecodeTile<D, kQuant>;
+template <int D, bool kBf16, bool kQuant, bool kWide>
+__global__ __launch_bounds__((DecodeTile<D, kQuant, kWide>::kThreads), (std::max(1, DecodeTile<D, kQuant, kWide>::kPerCu * DecodeTile<D, kQuant, kWide>::kWaves / 4)))
+void attn_decode_kernel(DecodeArgs a) {
+  using Tile = DecodeTile<D, kQuant, kWide>;
   constexpr int kDB = D / 16, kSteps = D / 32;
   constexpr bool kVBf16 = kQuant || kBf16;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[Tile::kLds];
@@ -172,38 +166,38 @@ __global__ __launch_bounds__((DecodeTile<D, kQuant>::kThreads), (DecodeTile<D, k
   const float c = a.scale_log2;
   const int64_t page_mask = (1ll << a.c.page_shift) - 1;
 
-  // this workgroup's share of the line
-  int64_t x, end, per = 0, all = 0;
-  if (a.split) {
-    all = all_tiles(a);
-    per = share_tiles(all, gridDim.x);
-    x = blockIdx.x * per;
-    end = std::min(x + per, all);
-  } else {
-    x = 0;
-    end = 1;
-  }
-  while (x < end) {
-    // the segment of one sequence and virtual head at x: its tiles t0 .. t1 - 1 of nt
-    int b, hv, t0, t1, nt;
-    if (a.split) {
-      const Place p = find_place(a, x);
-      const int64_t in = x - p.first;
-      b = __builtin_amdgcn_readfirstlane(p.b);
-      nt = __builtin_amdgcn_readfirstlane(p.n);
-      hv = __builtin_amdgcn_readfirstlane(static_cast<int>(in / p.n));
-      t0 = __builtin_amdgcn_readfirstlane(static_cast<int>(in % p.n));
-      t1 = __builtin_amdgcn_readfirstlane(static_cast<int>(std::min<int64_t>(nt, t0 + (end - x))));
-      x += t1 - t0;
-    } else {
-      b = blockIdx.x / a.hv;
-      hv = blockIdx.x % a.hv;
-      nt = __builtin_amdgcn_readfirstlane(seq_tiles(a, b));
-      t0 = 0;
-      t1 = nt;
-      x = end;
+  // this workgroup's piece: tiles t0 .. t1 - 1 of the nt of sequence b and virtual head hv
+  int b, hv, len, t0 = 0, t1, nt;
+  if (a.pieces) {
+    const Cut cut(a);
+    int before = 0, f = 0, np = 0;
+    uint64_t here = 0;
+    for (int b0 = 0; b0 < a.B && !here; b0 += 64) {
+      const int ln = cut.len(a, b0 + lane), n = cut.pieces(ln), sum = lanes_scan(n * a.hv);
+      here = __ballot(before + sum > static_cast<int>(blockIdx.x));
+      if (here) {
+        f = __builtin_ctzll(here);
+        b = b0 + f;
+        len = __builtin_amdgcn_readlane(ln, f);
+        np = __builtin_amdgcn_readlane(n, f);
+        before += __builtin_amdgcn_readlane(sum, f) - np * a.hv;
+      } else {
+        before += __builtin_amdgcn_readlane(sum, 63);
+      }
     }
-    const int64_t len = seq_len(a, b);
+    if (!here) return;   // fewer pieces than the host allowed for
+    const int in = blockIdx.x - before, i = in % np;
+    hv = in / np;
+    nt = tiles_of(len);
+    t0 = static_cast<int>(static_cast<int64_t>(nt) * i / np);
+    t1 = static_cast<int>(static_cast<int64_t>(nt) * (i + 1) / np);
+  } else {
+    b = blockIdx.x / a.hv;
+    hv = blockIdx.x % a.hv;
+    len = __builtin_amdgcn_readfirstlane(seq_len(a, b));
+    t1 = nt = tiles_of(len);
+  }
+  {
     const int h = hv / a.tiles_of_heads, first_head = hv % a.tiles_of_heads * 16, heads = std::min(a.G - first_head, 16);
     const int hq0 = h * a.G + first_head;
     const uint8_t* const kc = static_cast<const uint8_t*>(a.c.k);
@@ -227,10 +221,10 @@ __global__ __launch_bounds__((DecodeTile<D, kQuant>::kThreads), (DecodeTile<D, k
       wait_lds_reads();
 #pragma unroll
       for (int i = 0; i < kTableHalves / 64; ++i) {
-        const int64_t key = (static_cast<int64_t>(t) * 2 + 64 * i + lane) * 16, at = key >> a.c.page_shift;
+        const int64_t key = (static_cast<int64_t>(t) * 2 + 64 * i + lane) * 16;
         int page = -1;
         if (key < len) {                                    // positions past the width do not exist: len stops there
-          page = a.c.table[static_cast<int64_t>(b) * a.c.width + at];
+          page = a.c.table[static_cast<int64_t>(b) * a.c.width + (key >> a.c.page_shift)];
           if (page < 0 || page >= a.c.pages) page = -1;
         }
         table[64 * i + lane] = page;
@@ -244,12 +238,13 @@ __global__ __launch_bounds__((DecodeTile<D, kQuant>::kThreads), (DecodeTile<D, k
       return page < 0 ? 0 : ((static_cast<int64_t>(page) * a.c.Hkv + h) << a.c.page_shift) + (key & page_mask);
     };
     auto load = [&](const uint8_t* cache, uint8_t* slot, int t, bool is_k) {
+      const int ln = opaque(lane), r0 = ln / Tile::kChunks, ch = ln % Tile::kChunks;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const void* base = scalar_addr(cache + row_of(t, i, page_of(t, i)) * Tile::kRow);
 #pragma unroll
         for (int j = 0; j < Tile::kLoads / 2; ++j) {
-          const int at = 64 * j + lane, r = at / Tile::kChunks, ch = at % Tile::kChunks;
+          const int r = 64 / Tile::kChunks * j + r0;
           lds_dma16_s(base, r * Tile::kRow + 16 * (ch ^ (is_k ? Tile::kswizzle(16 * i + r) : Tile::vswizzle(16 * i + r))),
                       lds_addr(slot) + (i * Tile::kLoads / 2 + j) * 1024);
         }
@@ -278,7 +273,7 @@ __global__ __launch_bounds__((DecodeTile<D, kQuant>::kThreads), (DecodeTile<D, k
     for (int t = ta; t < tb; ++t) {
       const bool more = t + 1 < tb;
       // which of the tile's keys exist
-      const int left = static_cast<int>(std::min<int64_t>(len - static_cast<int64_t>(t) * kTileKeys, kTileKeys));
+      const int left = std::min(len - t * kTileKeys, kTileKeys);
       uint32_t valid = left >= 32 ? 0xFFFFFFFFu : (1u << left) - 1;
       if (page_of(t, 0) < 0) valid &= 0xFFFF0000u;
       if (page_of(t, 1) < 0) valid &= 0x0000FFFFu;
@@ -286,10 +281,11 @@ __global__ __launch_bounds__((DecodeTile<D, kQuant>::kThreads), (DecodeTile<D, k
 
       wait_vm<Tile::kLoads>();          // K of this tile and its scales; V may be in flight
       v4f s[2];
+      const int ln = opaque(lane);
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
         s[kb] = v4f{0.f, 0.f, 0.f, 0.f};
-        const int r = 16 * kb + n;
+        const int r = 16 * kb + (ln & 15), g = ln >> 4;
         if constexpr (kQuant) {
 #pragma unroll
           for (int st = 0; st < kSteps / 2; ++st) {
@@ -374,9 +370,11 @@ __global__ __launch_bounds__((DecodeTile<D, kQuant>::kThreads), (DecodeTile<D, k
         }
         wait_lds_reads();
       }
+      const int lv = opaque(lane);
 #pragma unroll
       for (int db = 0; db < kDB; ++db) {
         attn_u32x4 w;
+        const int g = lv >> 4, lane = lv;
         if constexpr (kQuant) {
           const int i = (lane & 15) >> 1, r = 4 * g + (i & 3) + (i >> 2) * 16;
           const uint2 v = lds_read_transposed8(vslot + r * Tile::kRow + 16 * (db ^ Tile::vswizzle(r)) + 8 * (lane & 1));
@@ -389,6 +387,7 @@ __global__ __launch_bounds__((DecodeTile<D, kQuant>::kThreads), (DecodeTile<D, k
         }
         o[db] = mfma_16<kVBf16>(w, ph, o[db]);
         o[db] = mfma_16<kVBf16>(w, pl, o[db]);
+        if (db % 4 == 3) __builtin_amdgcn_sched_barrier(0);   // no more operands in flight than this: registers
       }
       wait_lds_reads();                 // V's slot is free
       if (more) load_v(t + 1);
@@ -403,7 +402,6 @@ __global__ __launch_bounds__((DecodeTile<D, kQuant>::kThreads), (DecodeTile<D, k
     if (g == 0) *reinterpret_cast<float4*>(state + (wave * 16 + n) * 4) = make_float4(m == -__builtin_inff() ? m : mc, l, any ? 1.0f : 0.0f, 0.0f);
     __syncthreads();
     const bool whole = t0 == 0 && t1 == nt;
-    const int slot = 2 * blockIdx.x + (t0 == 0);    // at most one segment of a share began before it, and one goes on behind it
     for (int e = tid; e < heads * (D / 4); e += Tile::kThreads) {
       const int r = e / (D / 4), ch = e % (D / 4);
       float most = -__builtin_inff(), sum = 0.0f, seen = 0.0f;
@@ -425,91 +423,111 @@ __global__ __launch_bounds__((DecodeTile<D, kQuant>::kThreads), (DecodeTile<D, k
         *reinterpret_cast<uint2*>(a.o + (static_cast<int64_t>(b) * a.Hq + hq0 + r) * D + 4 * ch) =
             a.out_type == PQ_BF16 ? make_uint2(pack2<true>(y.x, y.y), pack2<true>(y.z, y.w)) : make_uint2(pack2<false>(y.x, y.y), pack2<false>(y.z, y.w));
       } else {
-        float* const p = a.ws + static_cast<int64_t>(slot) * Tile::kSlot;
+        float* const p = a.ws + static_cast<int64_t>(blockIdx.x) * Tile::kSlot;
         *reinterpret_cast<float4*>(p + r * D + 4 * ch) = v;
         if (ch == 0) *reinterpret_cast<float4*>(p + 16 * D + 4 * r) = make_float4(most, sum, seen, 0.0f);
       }
     }
-    __syncthreads();   // before the slots are loaded again
   }
 }
 
-// The pieces of one sequence and query head, in the order of the line: D / 4 threads each take 4 channels of every kParts-th piece.
-template <int D, bool kQuant>
-__global__ __launch_bounds__(256) void attn_join_kernel(DecodeArgs a, int shares) {
-  using Tile = DecodeTile<D, kQuant>;
-  constexpr int kLanes = D / 4, kParts = 256 / kLanes;
+// The pieces of one sequence and query head, in the order of the line: their weights first, then D / 4 threads each take 4
+// channels of every kParts-th piece.
+template <int D>
+__global__ __launch_bounds__(256) void attn_join_kernel(DecodeArgs a) {
+  constexpr int kLanes = D / 4, kParts = 256 / kLanes, kSlot = 16 * D + 64;
   __shared__ __attribute__((aligned(16))) float part[kParts][D];
-  __shared__ float sums[kParts][4];
+  __shared__ float weight[kMostPieces + 1];
+  __shared__ float sums[3][4];
   const int b = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq;
   const int h = hq / a.G, hv = h * a.tiles_of_heads + hq % a.G / 16, r = hq % a.G % 16;
-  const int64_t all = all_tiles(a), per = share_tiles(all, shares);
-  int64_t before = 0;
-  for (int i = threadIdx.x & 63; i < b; i += 64) before += seq_tiles(a, i);
-  const int nt = seq_tiles(a, b);
-  const int64_t s0 = wave_total(before) * a.hv + static_cast<int64_t>(hv) * nt, s1 = s0 + nt;
+  const int tid = threadIdx.x, lane = tid % kLanes, p = tid / kLanes;
+  const Cut cut(a);
+  int before = 0, pieces = 0;
+  for (int b0 = 0; b0 <= b; b0 += 64) {
+    const int i = b0 + (tid & 63), n = cut.pieces(cut.len(a, i));
+    before += i < b ? n : 0;
+    pieces = __builtin_amdgcn_readlane(n, b & 63);   // of sequence b in the last round
+  }
   uint16_t* const out = a.o + (static_cast<int64_t>(b) * a.Hq + hq) * D;
-  const int lane = threadIdx.x % kLanes, p = threadIdx.x / kLanes;
-  if (nt == 0) {
+  if (pieces == 0) {
     if (p == 0) *reinterpret_cast<uint2*>(out + 4 * lane) = make_uint2(0, 0);
     return;
   }
-  const int64_t w0 = s0 / per, w1 = (s1 - 1) / per;
-  if (w0 == w1) return;   // one share holds it whole, and has written it
-  float m = -__builtin_inff(), l = 0.0f, seen = 0.0f;
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int64_t w = w0 + p; w <= w1; w += kParts) {
-    const float* q = a.ws + (2 * w + (w == w0)) * Tile::kSlot;
-    const float4 st = *reinterpret_cast<const float4*>(q + 16 * D + 4 * r), u = *reinterpret_cast<const float4*>(q + r * D + 4 * lane);
-    const float n = __builtin_fmaxf(m, st.x);
-    const float f = m == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m - n), e = st.x == -__builtin_inff() ? (st.y == st.y ? 0.0f : st.y) : __builtin_amdgcn_exp2f(st.x - n);
-    m = n;
-    l = l * f + st.y * e;
+  if (pieces == 1) return;   // one workgroup held it whole, and has written it
+  const float* const first = a.ws + (static_cast<int64_t>(lanes_total(before)) * a.hv + static_cast<int64_t>(hv) * pieces) * kSlot;
+  auto piece = [&](int i) { return first + static_cast<int64_t>(i) * kSlot; };
+  auto over = [&](float v, float* to, auto f) {                        // over the workgroup, everywhere
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) v = f(v, __shfl_xor(v, m));
+    if ((tid & 63) == 0) to[tid >> 6] = v;
+    __syncthreads();
+    return f(f(to[0], to[1]), f(to[2], to[3]));
+  };
+  auto larger = [](float u, float v) { return __builtin_fmaxf(u, v); };
+  auto plus = [](float u, float v) { return u + v; };
+  float most = -__builtin_inff();
+  for (int i = tid; i < pieces; i += 256) most = larger(most, piece(i)[16 * D + 4 * r]);
+  most = over(most, sums[0], larger);
+  float sum = 0.0f, seen = 0.0f;
+  for (int i = tid; i < pieces; i += 256) {
+    const float4 st = *reinterpret_cast<const float4*>(piece(i) + 16 * D + 4 * r);
+    const float f = st.x == -__builtin_inff() ? (st.y == st.y ? 0.0f : st.y) : __builtin_amdgcn_exp2f(st.x - most);
+    weight[i] = f;
+    sum += f * st.y;
     seen += st.z;
-    v.x = v.x * f + u.x * e, v.y = v.y * f + u.y * e, v.z = v.z * f + u.z * e, v.w = v.w * f + u.w * e;
+  }
+  sum = over(sum, sums[1], plus);
+  seen = over(seen, sums[2], plus);
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = p; i < pieces; i += kParts) {
+    const float4 u = *reinterpret_cast<const float4*>(piece(i) + r * D + 4 * lane);
+    const float f = weight[i];
+    v.x += f * u.x, v.y += f * u.y, v.z += f * u.z, v.w += f * u.w;
   }
   *reinterpret_cast<float4*>(&part[p][4 * lane]) = v;
-  if (lane == 0) sums[p][0] = m, sums[p][1] = l, sums[p][2] = seen;
   __syncthreads();
   if (p) return;
-  float most = -__builtin_inff(), sum = 0.0f;
-  seen = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kParts; ++i) most = __builtin_fmaxf(most, sums[i][0]);
-  v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-  for (int i = 0; i < kParts; ++i) {
-    const float f = sums[i][0] == -__builtin_inff() ? (sums[i][1] == sums[i][1] ? 0.0f : sums[i][1]) : __builtin_amdgcn_exp2f(sums[i][0] - most);
+  for (int i = 1; i < kParts; ++i) {
     const float4 u = *reinterpret_cast<const float4*>(&part[i][4 * lane]);
-    sum += f * sums[i][1];
-    seen += sums[i][2];
-    v.x += f * u.x, v.y += f * u.y, v.z += f * u.z, v.w += f * u.w;
+    v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
   }
   const float inv = seen > 0.0f ? 1.0f / sum : 0.0f;
   *reinterpret_cast<uint2*>(out + 4 * lane) = a.out_type == PQ_BF16 ? make_uint2(pack2<true>(v.x * inv, v.y * inv), pack2<true>(v.z * inv, v.w * inv))
                                                                     : make_uint2(pack2<false>(v.x * inv, v.y * inv), pack2<false>(v.z * inv, v.w * inv));
 }
 
-// Shares that a device holds at once, of every cache type.
-template <int D>
-static int most_shares() { return cu_count() * std::max(DecodeTile<D, true>::kPerCu, DecodeTile<D, false>::kPerCu); }
 // Up to this many positions a sequence's head stays in one workgroup, and no join follows.
-constexpr int64_t kWholeLength = 1024;
+constexpr int kWholeLength = 1024;
 
+// Pieces that the line is cut into: kRounds for every workgroup that the device holds at once, so that those that get their
+// data later than others get fewer.
+constexpr int kRounds = 2;
+template <int D, bool kQuant>
+static int wanted_pieces() { return std::min(kMostPieces, kRounds * cu_count() * DecodeTile<D, kQuant, false>::kPerCu); }
+
+// A slot for each piece; every sequence and virtual head adds at most one to the wanted number.
 template <int D>
-static size_t decode_workspace(int64_t) { return 2ull * most_shares<D>() * DecodeTile<D, true>::kSlot * sizeof(float); }
+static size_t decode_workspace(int64_t B, int64_t hv) {
+  return (std::max(wanted_pieces<D, true>(), wanted_pieces<D, false>()) + static_cast<size_t>(B * hv)) * DecodeTile<D, true, false>::kSlot * sizeof(float);
+}
 
+template <int D, bool kBf16, bool kQuant, bool kWide>
+static hipError_t decode_kernel(const DecodeArgs& a, int64_t grid, hipStream_t s) {
+  return launch_kernel((attn_decode_kernel<D, kBf16, kQuant, kWide>), dim3(static_cast<unsigned>(grid)), dim3(DecodeTile<D, kQuant, kWide>::kThreads), 0, s, a);
+}
 template <int D, bool kBf16, bool kQuant>
 static hipError_t decode_launch(DecodeArgs a, hipStream_t s) {
-  using Tile = DecodeTile<D, kQuant>;
-  const int64_t length = static_cast<int64_t>(a.c.width) << a.c.page_shift, heads = static_cast<int64_t>(a.B) * a.hv;
-  const int64_t tiles = heads * ((length + kTileKeys - 1) / kTileKeys);
-  a.split = length > kWholeLength;
-  const int64_t grid = a.split ? std::min<int64_t>(cu_count() * Tile::kPerCu, (tiles + kLeastTiles - 1) / kLeastTiles) : heads;
-  hipError_t e = launch_kernel((attn_decode_kernel<D, kBf16, kQuant>), dim3(static_cast<unsigned>(grid)), dim3(Tile::kThreads), 0, s, a);
-  if (e == hipSuccess && a.split)
-    e = launch_kernel((attn_join_kernel<D, kQuant>), dim3(static_cast<unsigned>(a.B * a.Hq)), dim3(256), 0, s, a, static_cast<int>(grid));
-  return e;
+  const int length = a.c.width << a.c.page_shift;
+  const int64_t heads = static_cast<int64_t>(a.B) * a.hv;
+  if (length <= kWholeLength)
+    return heads <= cu_count() ? decode_kernel<D, kBf16, kQuant, true>(a, heads, s) : decode_kernel<D, kBf16, kQuant, false>(a, heads, s);
+  a.pieces = wanted_pieces<D, kQuant>();
+  const int64_t most = heads * ((length + kTileKeys * kLeastTiles - 1) / (kTileKeys * kLeastTiles));
+  const hipError_t e = decode_kernel<D, kBf16, kQuant, false>(a, std::min<int64_t>(a.pieces + heads, most), s);
+  return e != hipSuccess ? e : launch_kernel((attn_join_kernel<D>), dim3(static_cast<unsigned>(a.B * a.Hq)), dim3(256), 0, s, a);
 }
 template <int D>
 static hipError_t decode_for(const DecodeArgs& a, int type, hipStream_t s) {
@@ -524,7 +542,8 @@ extern "C" {
 size_t pq_attn_decode_workspace_bytes(int B, int Hq, int Hkv, int D) {
   using namespace pq;
   if (B <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv) return 0;
-  return D == 64 ? decode_workspace<64>(B) : D == 128 ? decode_workspace<128>(B) : D == 256 ? decode_workspace<256>(B) : 0;
+  const int64_t hv = Hkv * ((Hq / Hkv + 15ll) / 16);
+  return D == 64 ? decode_workspace<64>(B, hv) : D == 128 ? decode_workspace<128>(B, hv) : D == 256 ? decode_workspace<256>(B, hv) : 0;
 }
 
 int pq_attn_decode(const uint16_t* q_d, int64_t ldq, int64_t hsq, int type, const void* kc_d, const void* vc_d, const float* ks_d, const float* vs_d,
@@ -542,12 +561,14 @@ int pq_attn_decode(const uint16_t* q_d, int64_t ldq, int64_t hsq, int type, cons
     return set_error(PQ_ERR_SHAPE, "%s: B=%d sequences of %d heads too many for one call", what, B, Hq);
   if (static_cast<int64_t>(width) * page > INT32_MAX)
     return set_error(PQ_ERR_SHAPE, "%s: width=%d pages of %d rows: sequences of at most 2^31 - 1 positions", what, width, page);
+  const int G = Hq / Hkv, tiles_of_heads = (G + 15) / 16;
+  if (static_cast<int64_t>(B) * Hkv * tiles_of_heads > INT32_MAX / (static_cast<int64_t>(width) * page / kTileKeys + 1))   // tiles are counted in 32 bits
+    return set_error(PQ_ERR_SHAPE, "%s: B=%d tables of %d pages of %d rows too large for one call", what, B, width, page);
   if (B == 0) return PQ_OK;
   if (!o_d || !lens_d || (width && !table_d)) return set_error(PQ_ERR_NULL, "%s: NULL pointer", what);
   if (!aligned(o_d, 16) || !aligned(lens_d, 4) || !aligned(table_d, 4) || !aligned(ws_d, 16)) return set_error(PQ_ERR_ALIGN, "%s: misaligned pointer", what);
   const size_t need = pq_attn_decode_workspace_bytes(B, Hq, Hkv, D);
   if (!ws_d || ws_bytes < need) return set_error(PQ_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", what, ws_d ? ws_bytes : 0, need);
-  const int G = Hq / Hkv, tiles_of_heads = (G + 15) / 16;
   DecodeArgs a{{kc_d, vc_d, ks_d, vs_d, table_d, pages, pages ? width : 0, Hkv, __builtin_ctz(page)}, q_d, ldq, hsq, lens_d, B, Hq, G,
                Hkv * tiles_of_heads, tiles_of_heads, 0, scale * 1.44269504088896340736f, o_d, out_type, static_cast<float*>(ws_d)};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
