@@ -245,7 +245,7 @@ void attn_decode_kernel(DecodeArgs a) {
 #pragma unroll
         for (int j = 0; j < Tile::kLoads / 2; ++j) {
           const int r = 64 / Tile::kChunks * j + r0;
-          lds_dma16_s(base, r * Tile::kRow + 16 * (ch ^ (is_k ? Tile::kswizzle(16 * i + r) : Tile::vswizzle(16 * i + r))),
+          lds_dma16_nt(base, r * Tile::kRow + 16 * (ch ^ (is_k ? Tile::kswizzle(16 * i + r) : Tile::vswizzle(16 * i + r))),
                       lds_addr(slot) + (i * Tile::kLoads / 2 + j) * 1024);
         }
       }
@@ -457,34 +457,51 @@ __global__ __launch_bounds__(256) void attn_join_kernel(DecodeArgs a) {
   if (pieces == 1) return;   // one workgroup held it whole, and has written it
   const float* const first = a.ws + (static_cast<int64_t>(lanes_total(before)) * a.hv + static_cast<int64_t>(hv) * pieces) * kSlot;
   auto piece = [&](int i) { return first + static_cast<int64_t>(i) * kSlot; };
-  auto over = [&](float v, float* to, auto f) {                        // over the workgroup, everywhere
+  // the first pieces' channels and states are requested together: one wait for both
+  constexpr int kAhead = 8;
+  float4 u[kAhead];
 #pragma unroll
-    for (int m = 1; m < 64; m *= 2) v = f(v, __shfl_xor(v, m));
-    if ((tid & 63) == 0) to[tid >> 6] = v;
-    __syncthreads();
-    return f(f(to[0], to[1]), f(to[2], to[3]));
-  };
-  auto larger = [](float u, float v) { return __builtin_fmaxf(u, v); };
-  auto plus = [](float u, float v) { return u + v; };
-  float most = -__builtin_inff();
-  for (int i = tid; i < pieces; i += 256) most = larger(most, piece(i)[16 * D + 4 * r]);
-  most = over(most, sums[0], larger);
+  for (int j = 0; j < kAhead; ++j) u[j] = *reinterpret_cast<const float4*>(piece(std::min(p + j * kParts, pieces - 1)) + r * D + 4 * lane);
+  auto state = [&](int i) { return *reinterpret_cast<const float4*>(piece(i) + 16 * D + 4 * r); };
+  const float4 mine = state(std::min(tid, pieces - 1));
+  float most = mine.x;
+  for (int i = tid + 256; i < pieces; i += 256) most = __builtin_fmaxf(most, state(i).x);
+#pragma unroll
+  for (int m = 1; m < 64; m *= 2) most = __builtin_fmaxf(most, __shfl_xor(most, m));
+  if ((tid & 63) == 0) sums[0][tid >> 6] = most;
+  __syncthreads();
+  most = __builtin_fmaxf(__builtin_fmaxf(sums[0][0], sums[0][1]), __builtin_fmaxf(sums[0][2], sums[0][3]));
   float sum = 0.0f, seen = 0.0f;
   for (int i = tid; i < pieces; i += 256) {
-    const float4 st = *reinterpret_cast<const float4*>(piece(i) + 16 * D + 4 * r);
+    const float4 st = i == tid ? mine : state(i);
     const float f = st.x == -__builtin_inff() ? (st.y == st.y ? 0.0f : st.y) : __builtin_amdgcn_exp2f(st.x - most);
     weight[i] = f;
     sum += f * st.y;
     seen += st.z;
   }
-  sum = over(sum, sums[1], plus);
-  seen = over(seen, sums[2], plus);
+#pragma unroll
+  for (int m = 1; m < 64; m *= 2) {
+    sum += __shfl_xor(sum, m);
+    seen += __shfl_xor(seen, m);
+  }
+  if ((tid & 63) == 0) sums[1][tid >> 6] = sum, sums[2][tid >> 6] = seen;
+  __syncthreads();
+  sum = (sums[1][0] + sums[1][1]) + (sums[1][2] + sums[1][3]);
+  seen = (sums[2][0] + sums[2][1]) + (sums[2][2] + sums[2][3]);
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = p; i < pieces; i += kParts) {
-    const float4 u = *reinterpret_cast<const float4*>(piece(i) + r * D + 4 * lane);
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) {
+    const int i = p + j * kParts;
+    if (i < pieces) {
+      const float f = weight[i];
+      v.x += f * u[j].x, v.y += f * u[j].y, v.z += f * u[j].z, v.w += f * u[j].w;
+    }
+  }
+#pragma unroll 8
+  for (int i = p + kAhead * kParts; i < pieces; i += kParts) {
+    const float4 w = *reinterpret_cast<const float4*>(piece(i) + r * D + 4 * lane);
     const float f = weight[i];
-    v.x += f * u.x, v.y += f * u.y, v.z += f * u.z, v.w += f * u.w;
+    v.x += f * w.x, v.y += f * w.y, v.z += f * w.z, v.w += f * w.w;
   }
   *reinterpret_cast<float4*>(&part[p][4 * lane]) = v;
   __syncthreads();
@@ -502,16 +519,15 @@ __global__ __launch_bounds__(256) void attn_join_kernel(DecodeArgs a) {
 // Up to this many positions a sequence's head stays in one workgroup, and no join follows.
 constexpr int kWholeLength = 1024;
 
-// Pieces that the line is cut into: kRounds for every workgroup that the device holds at once, so that those that get their
-// data later than others get fewer.
-constexpr int kRounds = 2;
-template <int D, bool kQuant>
-static int wanted_pieces() { return std::min(kMostPieces, kRounds * cu_count() * DecodeTile<D, kQuant, false>::kPerCu); }
+// Pieces that the line is cut into: so many that those workgroups that get their data later than others get fewer, and few enough
+// for the join. (64 ragged sequences of up to 8192, 16-bit, two workgroups a CU: 2, 4, 6, 8 pieces a CU 191, 178, 184, 184 us; one
+// of 131071, e4m3, four a CU: 4, 8, 12, 16 pieces 53.7, 58.9, 64, 67.)
+static int wanted_pieces() { return std::min(kMostPieces, 4 * cu_count()); }
 
 // A slot for each piece; every sequence and virtual head adds at most one to the wanted number.
 template <int D>
 static size_t decode_workspace(int64_t B, int64_t hv) {
-  return (std::max(wanted_pieces<D, true>(), wanted_pieces<D, false>()) + static_cast<size_t>(B * hv)) * DecodeTile<D, true, false>::kSlot * sizeof(float);
+  return (wanted_pieces() + static_cast<size_t>(B * hv)) * DecodeTile<D, true, false>::kSlot * sizeof(float);
 }
 
 template <int D, bool kBf16, bool kQuant, bool kWide>
@@ -524,7 +540,7 @@ static hipError_t decode_launch(DecodeArgs a, hipStream_t s) {
   const int64_t heads = static_cast<int64_t>(a.B) * a.hv;
   if (length <= kWholeLength)
     return heads <= cu_count() ? decode_kernel<D, kBf16, kQuant, true>(a, heads, s) : decode_kernel<D, kBf16, kQuant, false>(a, heads, s);
-  a.pieces = wanted_pieces<D, kQuant>();
+  a.pieces = wanted_pieces();
   const int64_t most = heads * ((length + kTileKeys * kLeastTiles - 1) / (kTileKeys * kLeastTiles));
   const hipError_t e = decode_kernel<D, kBf16, kQuant, false>(a, std::min<int64_t>(a.pieces + heads, most), s);
   return e != hipSuccess ? e : launch_kernel((attn_join_kernel<D>), dim3(static_cast<unsigned>(a.B * a.Hq)), dim3(256), 0, s, a);
