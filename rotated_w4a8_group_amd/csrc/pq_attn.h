@@ -34,6 +34,11 @@ __device__ __forceinline__ attn_u32x4 pack16x8(const float (&v)[8]) {
   return attn_u32x4{pack2<kBf16>(v[0], v[1]), pack2<kBf16>(v[2], v[3]), pack2<kBf16>(v[4], v[5]), pack2<kBf16>(v[6], v[7])};
 }
 
+// Four values rounded to the type of an output.
+__device__ __forceinline__ uint2 pack4(int type, float x, float y, float z, float w) {
+  return type == PQ_BF16 ? make_uint2(pack2<true>(x, y), pack2<true>(z, w)) : make_uint2(pack2<false>(x, y), pack2<false>(z, w));
+}
+
 // 8 e4m3 codes as the values they stand for.
 __device__ __forceinline__ void decode8(const uint2& c, float (&v)[8]) {
   const uint32_t w[2] = {c.x, c.y};
@@ -46,6 +51,25 @@ __device__ __forceinline__ void decode8(const uint2& c, float (&v)[8]) {
     v[4 * i + 3] = hi.y;
   }
 }
+
+// The same number, where the compiler may not know it: what an address takes from it is computed where it is used, a few vector
+// instructions, and not kept in a register for the whole loop.
+__device__ __forceinline__ int opaque(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// Sum over the lanes up to this one.
+__device__ __forceinline__ int lanes_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // within 16 lanes: 1, 2, 4, 8 back
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // the last lane of 16 to the next 16
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // that of 32 to the upper 32
+  return v;
+}
+__device__ __forceinline__ int lanes_total(int v) { return __builtin_amdgcn_readlane(lanes_scan(v), 63); }
 
 // 4 keys of one channel a lane: lane l gives the address of key l % 16 / 4 and channels 4 (l % 4) .. + 3 of its 16 lanes' 4 x 16 block
 // and gets channel l % 16 of the 4 keys.

@@ -98,13 +98,6 @@ __device__ __forceinline__ uint2 lds_read_transposed8(const uint8_t* p) {
   return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_ptr)(uintptr_t)lds_addr(p)));
 }
 
-// The same number, where the compiler may not know it: what an address takes from it is computed where it is used, a few vector
-// instructions, and not kept in a register for the whole loop.
-__device__ __forceinline__ int opaque(int v) {
-  asm volatile("" : "+v"(v));
-  return v;
-}
-
 // The lanes l, l ^ 16, l ^ 32, l ^ 48 combined.
 template <typename F>
 __device__ __forceinline__ float four_groups(float v, F f) {
@@ -118,18 +111,6 @@ __device__ __forceinline__ float four_groups(float v, F f) {
 // Positions and tiles of a sequence.
 __device__ __forceinline__ int seq_len(const DecodeArgs& a, int b) { return std::min(std::max(a.lens[b], 0), a.c.width << a.c.page_shift); }
 __device__ __forceinline__ int tiles_of(int len) { return static_cast<int>((static_cast<uint32_t>(len) + kTileKeys - 1) / kTileKeys); }
-
-// Sum over the lanes up to this one.
-__device__ __forceinline__ int lanes_scan(int v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // within 16 lanes: 1, 2, 4, 8 back
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // the last lane of 16 to the next 16
-  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // that of 32 to the upper 32
-  return v;
-}
-__device__ __forceinline__ int lanes_total(int v) { return __builtin_amdgcn_readlane(lanes_scan(v), 63); }
 
 // How the sequences are cut: a head's nt tiles into pieces of at most `per`, alike in size; the pieces stand in one line,
 // sequence by sequence and head by head. The host bounds their number (a.pieces + sequences x heads), the lengths decide it.
@@ -419,9 +400,7 @@ void attn_decode_kernel(DecodeArgs a) {
       }
       if (whole) {
         const float inv = seen > 0.0f ? 1.0f / sum : 0.0f;
-        const float4 y = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-        *reinterpret_cast<uint2*>(a.o + (static_cast<int64_t>(b) * a.Hq + hq0 + r) * D + 4 * ch) =
-            a.out_type == PQ_BF16 ? make_uint2(pack2<true>(y.x, y.y), pack2<true>(y.z, y.w)) : make_uint2(pack2<false>(y.x, y.y), pack2<false>(y.z, y.w));
+        *reinterpret_cast<uint2*>(a.o + (static_cast<int64_t>(b) * a.Hq + hq0 + r) * D + 4 * ch) = pack4(a.out_type, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
       } else {
         float* const p = a.ws + static_cast<int64_t>(blockIdx.x) * Tile::kSlot;
         *reinterpret_cast<float4*>(p + r * D + 4 * ch) = v;
@@ -512,8 +491,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(DecodeArgs a) {
     v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
   }
   const float inv = seen > 0.0f ? 1.0f / sum : 0.0f;
-  *reinterpret_cast<uint2*>(out + 4 * lane) = a.out_type == PQ_BF16 ? make_uint2(pack2<true>(v.x * inv, v.y * inv), pack2<true>(v.z * inv, v.w * inv))
-                                                                    : make_uint2(pack2<false>(v.x * inv, v.y * inv), pack2<false>(v.z * inv, v.w * inv));
+  *reinterpret_cast<uint2*>(out + 4 * lane) = pack4(a.out_type, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
 }
 
 // Up to this many positions a sequence's head stays in one workgroup, and no join follows.

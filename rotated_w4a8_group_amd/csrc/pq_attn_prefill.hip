@@ -37,11 +37,18 @@ struct PrefillArgs {
   float scale_log2;
   uint16_t* o;
   int out_type;
+  int line;      // places for a head's items, or with `pieces` for the pieces of its items
+  int pieces;    // pieces that a head's key tiles are cut into, about; 0: items are whole
+  float* ws;
 };
 
-// What a workgroup works on: rows r0 .. of sequence b, whose queries start at q0 (nq of them) and keys at k0 (nk of them).
+// What a workgroup works on: rows r0 .. of a sequence whose queries start at q0 (nq of them) and keys at k0 (nk of them), and of the
+// items' key tiles the `piece`th of `pieces` parts.
 struct PrefillItem {
-  int r0, q0, nq, k0, nk;
+  int r0, q0, nq, k0, nk, piece, pieces;
+  __device__ __forceinline__ int shift(bool causal) const { return causal ? nk - nq + 1 : nk; }
+  // Keys that row r sees.
+  __device__ __forceinline__ int keys(int r, bool causal) const { return causal ? std::max(std::min(nk, r + nk - nq + 1), 0) : nk; }
 };
 
 template <bool kBf16>
@@ -49,6 +56,8 @@ __device__ __forceinline__ f32x16 mfma_32(const attn_u32x4& a, const attn_u32x4&
   if constexpr (kBf16) return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
   else return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
+
+constexpr int kLeastTiles = 8;   // key tiles of a piece
 
 template <int D>
 struct PrefillTile {
@@ -60,6 +69,7 @@ struct PrefillTile {
   static constexpr int kPart = kKeys * kRowBytes;       // bytes of K, or of V, of one tile
   static constexpr int kLds = 2 * 2 * kPart;
   static constexpr int kLoads = kPart / 1024 / kWaves;  // direct loads a wave makes for K, or for V
+  static constexpr int kSlot = (D + 2) * kRows;         // floats of a piece in the workspace
 
   // The place of chunk c of row r: 16 rows (a K read: the same chunk of 16 rows) and 4 rows (a V read: 64 bytes of each) in
   // different banks of the 256-byte line.
@@ -69,7 +79,7 @@ struct PrefillTile {
 
 // One row key by key, exactly as the formula reads: keys j < keys.
 template <int D, bool kBf16>
-__device__ __attribute__((noinline)) void attend_row(const PrefillArgs& a, int64_t t, int hq, int k0, int keys) {
+__device__ __forceinline__ void attend_row(const PrefillArgs& a, int64_t t, int hq, int k0, int keys) {
   const int h = hq / (a.Hq / a.Hkv);
   float q[D / 64], k[D / 64], v[D / 64];
   lane_values<D, kBf16>(a.q + t * a.ldq + hq * a.hsq, q);
@@ -85,40 +95,83 @@ __device__ __attribute__((noinline)) void attend_row(const PrefillArgs& a, int64
   store_row<D>(a.o + (t * a.Hq + hq) * D, r, keys > 0, a.out_type);
 }
 
-// The item of tile number `tile` (rows of kRows; a sequence's tiles from its end, where a causal one is longest): false past the last.
-template <int kRows>
-__device__ __forceinline__ bool find_item(const PrefillArgs& a, int tile, PrefillItem* it) {
-  const int lane = threadIdx.x & 63;
-  int before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 64) {
-    const int b = b0 + lane;
-    int q0 = 0, nq = 0;
+// Sequence b's queries and keys, clamped to the rows that exist.
+struct Sequence {
+  int q0, nq, k0, nk;
+  __device__ __forceinline__ Sequence(const PrefillArgs& a, int b) : q0(0), nq(0), k0(0), nk(0) {
     if (b < a.B) {
       q0 = std::min(std::max(a.cu_q[b], 0), a.Tq);
       nq = std::max(std::min(a.cu_q[b + 1], a.Tq) - q0, 0);
+      k0 = std::min(std::max(a.cu_k[b], 0), a.Tk);
+      nk = std::max(std::min(a.cu_k[b + 1], a.Tk) - k0, 0);
     }
-    const int n = (nq + kRows - 1) / kRows;
-    int sum = n;   // inclusive prefix sum
-#pragma unroll
-    for (int m = 1; m < 64; m *= 2) {
-      const int o = __shfl_up(sum, m);
-      sum += lane >= m ? o : 0;
+  }
+};
+
+// The item at a place of a head's line: false past the last. kRows: queries of an item, kKeys: keys of a tile.
+//  - Up to 64 sequences, whole items: those that see the most keys first, so that no long one begins when the others end. An item's
+//    cost is the number of key blocks of kRows before its end; `from(x)` items cost x or more, and the place's own cost is
+//    found by bisection, a sum over the wave each (packed prompts of 4093 rows: 110 us in the sequences' order, see the kernel).
+//  - More sequences: in their order, each from its end. Pieces: likewise, an item's pieces next to each other.
+template <int kRows, int kKeys>
+__device__ __forceinline__ bool find_item(const PrefillArgs& a, int place, PrefillItem* it) {
+  const int lane = threadIdx.x & 63;
+  auto lane_of = [](int v, int l) { return __builtin_amdgcn_readlane(v, l); };
+  if (a.B <= 64 && !a.pieces) {
+    const Sequence s(a, lane);
+    const int n = (s.nq + kRows - 1) / kRows;
+    // cost of the sequence's first item, and of the one past its last (without the mask all cost the same)
+    const int first = a.causal ? std::max(s.nk - s.nq, 0) / kRows : (s.nk + kRows - 1) / kRows, last = a.causal ? first + n : first + 1;
+    auto from = [&](int x) { return lanes_total(a.causal ? std::min(std::max(last - x, 0), n) : last > x ? n : 0); };
+    if (place >= lanes_total(n)) return false;
+    int lo = 0, hi = (a.Tk + kRows - 1) / kRows + (a.Tq + kRows - 1) / kRows + 1;   // from(lo) > place >= from(hi)
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (from(mid) > place) lo = mid;
+      else hi = mid;
     }
-    const uint64_t here = __ballot(before + sum > tile);
+    const int rank = place - from(lo + 1);
+    const int mine = a.causal ? (first <= lo && lo < last ? 1 : 0) : first == lo ? n : 0, sum = lanes_scan(mine);
+    const int f = __builtin_ctzll(__ballot(sum > rank));
+    const int at = a.causal ? lo - lane_of(first, f) : rank - (lane_of(sum, f) - lane_of(mine, f));
+    *it = {at * kRows, lane_of(s.q0, f), lane_of(s.nq, f), lane_of(s.k0, f), lane_of(s.nk, f), 0, 1};
+    return true;
+  }
+  int per = 1;
+  if (a.pieces) {
+    int all = 0;
+    for (int b = lane; b < a.B; b += 64) {
+      const Sequence s(a, b);
+      all += (s.nq + kRows - 1) / kRows * ((s.nk + kKeys - 1) / kKeys);
+    }
+    per = std::max(kLeastTiles, (lanes_total(all) + a.pieces - 1) / a.pieces);
+  }
+  int before = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 64) {
+    const Sequence s(a, b0 + lane);
+    const int n = (s.nq + kRows - 1) / kRows, np = a.pieces ? std::max(((s.nk + kKeys - 1) / kKeys + per - 1) / per, 1) : 1, sum = lanes_scan(n * np);
+    const uint64_t here = __ballot(before + sum > place);
     if (here) {
-      const int first = __builtin_ctzll(here);
-      const int at = tile - before - (__builtin_amdgcn_readlane(sum, first) - __builtin_amdgcn_readlane(n, first));
-      const int s = b0 + first;
-      it->q0 = __builtin_amdgcn_readlane(q0, first);
-      it->nq = __builtin_amdgcn_readlane(nq, first);
-      it->r0 = (__builtin_amdgcn_readlane(n, first) - 1 - at) * kRows;
-      it->k0 = __builtin_amdgcn_readfirstlane(std::min(std::max(a.cu_k[s], 0), a.Tk));
-      it->nk = __builtin_amdgcn_readfirstlane(std::max(std::min(a.cu_k[s + 1], a.Tk) - it->k0, 0));
+      const int f = __builtin_ctzll(here), parts = lane_of(np, f), in = place - before - (lane_of(sum, f) - lane_of(n, f) * parts);
+      *it = {(lane_of(n, f) - 1 - in / parts) * kRows, lane_of(s.q0, f), lane_of(s.nq, f), lane_of(s.k0, f), lane_of(s.nk, f), in % parts, parts};
       return true;
     }
-    before += __builtin_amdgcn_readlane(sum, 63);
+    before += lane_of(sum, 63);
   }
   return false;
+}
+
+// A workgroup's head and place. Workgroups go round the 8 XCDs, so with Hq a multiple of 8 each XCD keeps its own Hq / 8 heads
+// (the queries that share a key head meet in one L2).
+__device__ __forceinline__ void head_and_place(const PrefillArgs& a, int block, int* hq, int* place) {
+  if (a.Hq % 8 == 0) {
+    const int per = a.Hq / 8, i = block >> 3;
+    *hq = (block & 7) * per + i % per;
+    *place = i / per;
+  } else {
+    *hq = block % a.Hq;
+    *place = block / a.Hq;
+  }
 }
 
 template <int D, bool kBf16>
@@ -129,30 +182,20 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(PrefillArgs a) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 31, half = lane >> 5;
 
-  // Workgroup -> (tile, head). Workgroups go round the 8 XCDs, so with Hq a multiple of 8 each XCD keeps its own Hq / 8 heads (the
-  // queries that share a key head meet in one L2).
-  int hq, tile;
-  if (a.Hq % 8 == 0) {
-    const int per = a.Hq / 8, i = blockIdx.x >> 3;
-    hq = (blockIdx.x & 7) * per + i % per;
-    tile = i / per;
-  } else {
-    hq = blockIdx.x % a.Hq;
-    tile = blockIdx.x / a.Hq;
-  }
+  int hq, place;
+  head_and_place(a, blockIdx.x, &hq, &place);
   PrefillItem it;
-  if (!find_item<Tile::kRows>(a, tile, &it)) return;
+  if (!find_item<Tile::kRows, Tile::kKeys>(a, place, &it)) return;
   const int h = hq / (a.Hq / a.Hkv);
-  const int shift = a.causal ? it.nk - it.nq + 1 : it.nk;              // row r sees min(nk, r + shift) keys (causal)
+  const bool causal = a.causal;
   const int row = it.r0 + 32 * wave + n;                               // this lane's query; rows past the end repeat the last
-  const int seen = a.causal ? std::max(std::min(it.nk, std::min(row, it.nq - 1) + shift), 0) : it.nk;
-  const int last_row = std::min(it.r0 + Tile::kRows, it.nq) - 1;
-  const int keys = a.causal ? std::max(std::min(it.nk, last_row + shift), 0) : it.nk;
-  const int tiles = (keys + Tile::kKeys - 1) / Tile::kKeys;
+  const int seen = it.keys(std::min(row, it.nq - 1), causal);
+  const int all_tiles = (it.keys(std::min(it.r0 + Tile::kRows, it.nq) - 1, causal) + Tile::kKeys - 1) / Tile::kKeys;
+  const int first = static_cast<int>(static_cast<int64_t>(all_tiles) * it.piece / it.pieces);
+  const int tiles = static_cast<int>(static_cast<int64_t>(all_tiles) * (it.piece + 1) / it.pieces);
   // of this wave's rows: the fewest and the most keys that one sees
-  const int wr0 = std::min(it.r0 + 32 * wave, it.nq - 1), wr1 = std::min(it.r0 + 32 * wave + 31, it.nq - 1);
-  const int least = a.causal ? std::max(std::min(it.nk, wr0 + shift), 0) : it.nk;
-  const int most = it.r0 + 32 * wave >= it.nq ? 0 : a.causal ? std::max(std::min(it.nk, wr1 + shift), 0) : it.nk;
+  const int least = it.keys(std::min(it.r0 + 32 * wave, it.nq - 1), causal);
+  const int most = it.r0 + 32 * wave >= it.nq ? 0 : it.keys(std::min(it.r0 + 32 * wave + 31, it.nq - 1), causal);
 
   // queries: channels 16 s + 8 half .. + 7 of step s
   attn_u32x4 q[kSteps];
@@ -165,23 +208,36 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(PrefillArgs a) {
   const uint16_t* kbase = a.k + static_cast<int64_t>(it.k0) * a.ldk + h * a.hsk;
   const uint16_t* vbase = a.v + static_cast<int64_t>(it.k0) * a.ldv + h * a.hsv;
   const uint32_t lds0 = lds_addr(smem);
-  // Direct loads of tile j into buffer j % 2: load i of a wave fills 1 KiB, 64 chunks in LDS order; rows past the last key repeat it.
+  // Direct loads of tile j into buffer j % 2: load i of a wave fills 1 KiB, kStep rows, 64 chunks in LDS order. A lane's row of
+  // the kStep and its chunk are fixed; the load's own rows are in the scalar base, and change the chunk's place by an exclusive or.
+  constexpr int kStep = 64 / Tile::kChunks;
+  const int lr = lane / Tile::kChunks, lc = lane % Tile::kChunks;
+  const uint32_t krow = lr * static_cast<uint32_t>(a.ldk) * 2, vrow = lr * static_cast<uint32_t>(a.ldv) * 2;
+  const uint32_t kch = 16 * (lc ^ Tile::kswizzle(lr)), vch = 16 * (lc ^ Tile::vswizzle(lr));
   auto load = [&](int j) {
-    const int left = it.nk - j * Tile::kKeys - 1;
-    const void* kb = scalar_addr(kbase + static_cast<int64_t>(j) * Tile::kKeys * a.ldk);
-    const void* vb = scalar_addr(vbase + static_cast<int64_t>(j) * Tile::kKeys * a.ldv);
+    const int left = it.nk - j * Tile::kKeys;
+    const uint16_t* kb = kbase + static_cast<int64_t>(j) * Tile::kKeys * a.ldk;
+    const uint16_t* vb = vbase + static_cast<int64_t>(j) * Tile::kKeys * a.ldv;
     const uint32_t to = lds0 + (j & 1) * 2 * Tile::kPart;
+    if (left >= Tile::kKeys) {
 #pragma unroll
-    for (int i = 0; i < Tile::kLoads; ++i) {
-      const int piece = wave * Tile::kLoads + i, at = piece * 64 + lane, r = at / Tile::kChunks, c = at % Tile::kChunks;
-      const uint32_t from = static_cast<uint32_t>(std::min(r, left));
-      lds_dma16_s(kb, (from * static_cast<uint32_t>(a.ldk) + 8 * (c ^ Tile::kswizzle(r))) * 2, to + piece * 1024);
-    }
+      for (int i = 0; i < Tile::kLoads; ++i) {
+        const int r = (wave * Tile::kLoads + i) * kStep;
+        lds_dma16_s(scalar_addr(kb + r * a.ldk), krow + (kch ^ (16 * Tile::kswizzle(r))), to + r * Tile::kRowBytes);
+      }
 #pragma unroll
-    for (int i = 0; i < Tile::kLoads; ++i) {
-      const int piece = wave * Tile::kLoads + i, at = piece * 64 + lane, r = at / Tile::kChunks, c = at % Tile::kChunks;
-      const uint32_t from = static_cast<uint32_t>(std::min(r, left));
-      lds_dma16_s(vb, (from * static_cast<uint32_t>(a.ldv) + 8 * (c ^ Tile::vswizzle(r))) * 2, to + Tile::kPart + piece * 1024);
+      for (int i = 0; i < Tile::kLoads; ++i) {
+        const int r = (wave * Tile::kLoads + i) * kStep;
+        lds_dma16_s(scalar_addr(vb + r * a.ldv), vrow + (vch ^ (16 * Tile::vswizzle(r))), to + Tile::kPart + r * Tile::kRowBytes);
+      }
+    } else {   // rows past the last key repeat it
+#pragma unroll
+      for (int i = 0; i < Tile::kLoads; ++i) {
+        const int r = (wave * Tile::kLoads + i) * kStep;
+        const uint32_t from = static_cast<uint32_t>(std::min(r + lr, left - 1)) * 2;
+        lds_dma16_s(scalar_addr(kb), from * static_cast<uint32_t>(a.ldk) + (kch ^ (16 * Tile::kswizzle(r))), to + r * Tile::kRowBytes);
+        lds_dma16_s(scalar_addr(vb), from * static_cast<uint32_t>(a.ldv) + (vch ^ (16 * Tile::vswizzle(r))), to + Tile::kPart + r * Tile::kRowBytes);
+      }
     }
   };
 
@@ -189,8 +245,8 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(PrefillArgs a) {
   float m = -__builtin_inff(), mc = 0.0f, l = 0.0f;   // the maximum that p is taken against, m * c, the sum of this lane's keys
   const float c = a.scale_log2;
 
-  if (tiles > 0) load(0);
-  for (int j = 0; j < tiles; ++j) {
+  if (first < tiles) load(first);
+  for (int j = first; j < tiles; ++j) {
     // this wave's loads of tile j have landed and its reads of tile j - 1 are done; behind the barrier every wave's
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     if (j + 1 < tiles) load(j + 1);
@@ -200,10 +256,11 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(PrefillArgs a) {
     const uint8_t* vt = kt + Tile::kPart;
 
     f32x16 s[kKB];
+    const int ln = D == 256 ? opaque(lane) : lane;   // (registers; at 128 channels the 1 % that it costs buys nothing)
 #pragma unroll
     for (int kb = 0; kb < kKB; ++kb) {
       s[kb] = f32x16{};
-      const int r = 32 * kb + n;
+      const int r = 32 * kb + (ln & 31), half = ln >> 5;
 #pragma unroll
       for (int st = 0; st < kSteps; ++st) {
         const attn_u32x4 k = *reinterpret_cast<const attn_u32x4*>(kt + r * Tile::kRowBytes + 16 * ((2 * st + half) ^ Tile::kswizzle(r)));
@@ -242,8 +299,10 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(PrefillArgs a) {
         l += x + y;
         p[kb][i / 2] = pack2<kBf16>(x, y);
       }
+    const int lv = D == 256 ? opaque(lane) : lane;
 #pragma unroll
     for (int kb = 0; kb < 2 * kKB; ++kb) {             // 16 keys each
+      const int lane = lv, half = lv >> 5;
       const attn_u32x4 w = {p[kb / 2][4 * (kb % 2)], p[kb / 2][4 * (kb % 2) + 1], p[kb / 2][4 * (kb % 2) + 2], p[kb / 2][4 * (kb % 2) + 3]};
       const int r = 16 * kb + 4 * half + ((lane & 15) >> 2);   // this lane's key of the first transposing read; r + 8 of the second
 #pragma unroll
@@ -257,6 +316,18 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(PrefillArgs a) {
   }
 
   l = both_halves_sum(l);
+  if (it.pieces > 1) {
+    // A piece: O as 16-byte chunks [D / 4][rows], then the maximum and the sum of every row. 32 rows' chunks are one run.
+    float* const p = a.ws + static_cast<int64_t>(blockIdx.x) * Tile::kSlot + 4 * (32 * wave + n);
+#pragma unroll
+    for (int db = 0; db < kDB; ++db)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        *reinterpret_cast<float4*>(p + (8 * db + 2 * g + half) * 4 * Tile::kRows) = make_float4(o[db][4 * g], o[db][4 * g + 1], o[db][4 * g + 2], o[db][4 * g + 3]);
+    if (half == 0) *reinterpret_cast<float2*>(a.ws + static_cast<int64_t>(blockIdx.x) * Tile::kSlot + D * Tile::kRows + 2 * (32 * wave + n)) =
+        make_float2(m == -__builtin_inff() ? m : mc, l);
+    return;
+  }
   // Rows that saw a key and whose values are not all finite: key by key. (A sum of 0 has every score at -inf: NaN by the formula.)
   float t = l > 0.0f ? 0.0f : __builtin_nanf("");
 #pragma unroll
@@ -271,30 +342,107 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(PrefillArgs a) {
 #pragma unroll
     for (int db = 0; db < kDB; ++db)
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {                    // channels 32 db + 8 g + 4 half .. + 3
-        const float x[4] = {o[db][4 * g] * inv, o[db][4 * g + 1] * inv, o[db][4 * g + 2] * inv, o[db][4 * g + 3] * inv};
-        const uint2 w = a.out_type == PQ_BF16 ? make_uint2(pack2<true>(x[0], x[1]), pack2<true>(x[2], x[3])) : make_uint2(pack2<false>(x[0], x[1]), pack2<false>(x[2], x[3]));
-        *reinterpret_cast<uint2*>(out + 32 * db + 8 * g + 4 * half) = w;
-      }
+      for (int g = 0; g < 4; ++g)                      // channels 32 db + 8 g + 4 half .. + 3
+        *reinterpret_cast<uint2*>(out + 32 * db + 8 * g + 4 * half) = pack4(a.out_type, o[db][4 * g] * inv, o[db][4 * g + 1] * inv, o[db][4 * g + 2] * inv, o[db][4 * g + 3] * inv);
   }
   for (uint32_t left = again; left; left &= left - 1) {
     const int r = it.r0 + 32 * wave + __builtin_ctz(left);
-    attend_row<D, kBf16>(a, it.q0 + r, hq, it.k0, a.causal ? std::max(std::min(it.nk, r + shift), 0) : it.nk);
+    attend_row<D, kBf16>(a, it.q0 + r, hq, it.k0, it.keys(r, causal));
   }
 }
 
+// The pieces of 32 rows of an item together: thread (row, part) takes the 16-byte chunks part, part + 8, ... of its row.
+template <int D, bool kBf16>
+__global__ __launch_bounds__(256) void attn_prefill_join_kernel(PrefillArgs a) {
+  using Tile = PrefillTile<D>;
+  constexpr int kGroups = Tile::kRows / 32;
+  __shared__ uint32_t odd;
+  int hq, place;
+  head_and_place(a, blockIdx.x / kGroups, &hq, &place);
+  PrefillItem it;
+  if (!find_item<Tile::kRows, Tile::kKeys>(a, place, &it)) return;
+  if (it.pieces == 1 || it.piece) return;     // the first piece's place stands for the item
+  const int n = threadIdx.x & 31, part = threadIdx.x >> 5, in = 32 * (blockIdx.x % kGroups) + n, row = it.r0 + in;
+  if (it.r0 + in - n >= it.nq) return;
+  if (threadIdx.x == 0) odd = 0;
+  __syncthreads();
+  // a head's places are workgroups 8 Hq / 8 apart, or Hq: Hq either way
+  auto slot = [&](int i) { return a.ws + (static_cast<int64_t>(blockIdx.x / kGroups) + static_cast<int64_t>(i) * a.Hq) * Tile::kSlot; };
+  auto state = [&](int i) { return *reinterpret_cast<const float2*>(slot(i) + D * Tile::kRows + 2 * in); };
+  float most = -__builtin_inff();
+  for (int i = 0; i < it.pieces; ++i) most = __builtin_fmaxf(most, state(i).x);
+  float sum = 0.0f;
+  float4 v[D / 32] = {};
+  for (int i = 0; i < it.pieces; ++i) {
+    const float2 st = state(i);
+    const float f = st.x == -__builtin_inff() ? (st.y == st.y ? 0.0f : st.y) : __builtin_amdgcn_exp2f(st.x - most);
+    sum += f * st.y;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+      const float4 u = *reinterpret_cast<const float4*>(slot(i) + (8 * c + part) * 4 * Tile::kRows + 4 * in);
+      v[c].x += f * u.x, v[c].y += f * u.y, v[c].z += f * u.z, v[c].w += f * u.w;
+    }
+  }
+  const int seen = it.keys(std::min(row, it.nq - 1), a.causal);
+  float t = sum > 0.0f ? 0.0f : __builtin_nanf("");
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) t += 0.0f * v[c].x + 0.0f * v[c].y + 0.0f * v[c].z + 0.0f * v[c].w;
+  if (row < it.nq && seen > 0 && !(t == 0.0f)) atomicOr(&odd, 1u << n);
+  __syncthreads();
+  const uint32_t again = odd;
+  if (row < it.nq && !(again >> n & 1)) {
+    const float inv = seen > 0 ? 1.0f / sum : 0.0f;
+    uint16_t* out = a.o + (static_cast<int64_t>(it.q0 + row) * a.Hq + hq) * D;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c)
+      *reinterpret_cast<uint2*>(out + 4 * (8 * c + part)) = pack4(a.out_type, v[c].x * inv, v[c].y * inv, v[c].z * inv, v[c].w * inv);
+  }
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  for (int i = wave; i < 32; i += 4)
+    if (again >> i & 1) attend_row<D, kBf16>(a, it.q0 + row - n + i, hq, it.k0, it.keys(row - n + i, a.causal));
+}
+
+// Whether the keys are cut, and the places of a head's line: an item for every kRows queries of a sequence, and when they are cut one
+// more place for every piece. Cut where the items are fewer than the workgroups that the device holds (two a CU) and a row may see more
+// than kWholeKeys keys.
+constexpr int kWholeKeys = 1024;
 template <int D>
-static hipError_t prefill_launch(const PrefillArgs& a, int type, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>((a.Tq / PrefillTile<D>::kRows + a.B) * static_cast<int64_t>(a.Hq))), block(256);
-  return type == PQ_BF16 ? launch_kernel((attn_prefill_kernel<D, true>), grid, block, 0, s, a)
-                         : launch_kernel((attn_prefill_kernel<D, false>), grid, block, 0, s, a);
+static void prefill_shape(int B, int Tq, int Tk, int Hq, int* pieces, int64_t* line) {
+  const int64_t items = Tq / PrefillTile<D>::kRows + static_cast<int64_t>(B), room = 2 * cu_count();
+  *pieces = items * Hq < room && Tk > kWholeKeys ? static_cast<int>((room + Hq - 1) / Hq) : 0;
+  *line = items + *pieces;
+}
+template <int D>
+static size_t prefill_workspace(int B, int Tq, int Tk, int Hq) {
+  int pieces;
+  int64_t line;
+  prefill_shape<D>(B, Tq, Tk, Hq, &pieces, &line);
+  return pieces ? static_cast<size_t>(line * Hq) * PrefillTile<D>::kSlot * sizeof(float) : 0;
+}
+
+template <int D, bool kBf16>
+static hipError_t prefill_kernels(const PrefillArgs& a, hipStream_t s) {
+  const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(a.line) * a.Hq);
+  const hipError_t e = launch_kernel((attn_prefill_kernel<D, kBf16>), dim3(grid), dim3(64 * PrefillTile<D>::kWaves), 0, s, a);
+  return e != hipSuccess || !a.pieces ? e : launch_kernel((attn_prefill_join_kernel<D, kBf16>), dim3(grid * (PrefillTile<D>::kRows / 32)), dim3(256), 0, s, a);
+}
+template <int D>
+static hipError_t prefill_launch(PrefillArgs a, int type, hipStream_t s) {
+  int64_t line;
+  prefill_shape<D>(a.B, a.Tq, a.Tk, a.Hq, &a.pieces, &line);
+  a.line = static_cast<int>(line);
+  return type == PQ_BF16 ? prefill_kernels<D, true>(a, s) : prefill_kernels<D, false>(a, s);
 }
 
 }  // namespace pq
 
 extern "C" {
 
-size_t pq_attn_prefill_workspace_bytes(int B, int Tq, int Tk, int Hq, int Hkv, int D) { return 0; }
+size_t pq_attn_prefill_workspace_bytes(int B, int Tq, int Tk, int Hq, int Hkv, int D) {
+  using namespace pq;
+  if (B <= 0 || Tq <= 0 || Tk <= 0 || Hq <= 0) return 0;
+  return D == 64 ? prefill_workspace<64>(B, Tq, Tk, Hq) : D == 128 ? prefill_workspace<128>(B, Tq, Tk, Hq) : D == 256 ? prefill_workspace<256>(B, Tq, Tk, Hq) : 0;
+}
 
 int pq_attn_prefill(const uint16_t* q_d, int64_t ldq, int64_t hsq, const uint16_t* k_d, int64_t ldk, int64_t hsk, const uint16_t* v_d, int64_t ldv,
                     int64_t hsv, int type, const int32_t* cu_q_d, const int32_t* cu_k_d, int B, int Tq, int Tk, int Hq, int Hkv, int D, float scale,
@@ -312,8 +460,11 @@ int pq_attn_prefill(const uint16_t* q_d, int64_t ldq, int64_t hsq, const uint16_
     return set_error(PQ_ERR_SHAPE, "%s: Tq=%d rows of B=%d sequences too many for one call", what, Tq, B);
   if (Tq == 0 || B == 0) return PQ_OK;
   if (!o_d || !cu_q_d || !cu_k_d) return set_error(PQ_ERR_NULL, "%s: NULL pointer", what);
-  if (!aligned(o_d, 16) || !aligned(cu_q_d, 4) || !aligned(cu_k_d, 4)) return set_error(PQ_ERR_ALIGN, "%s: misaligned pointer", what);
-  PrefillArgs a{q_d, k_d, v_d, ldq, hsq, ldk, hsk, ldv, hsv, cu_q_d, cu_k_d, B, Tq, Tk, Hq, Hkv, causal, scale * 1.44269504088896340736f, o_d, out_type};
+  if (!aligned(o_d, 16) || !aligned(cu_q_d, 4) || !aligned(cu_k_d, 4) || !aligned(ws_d, 16)) return set_error(PQ_ERR_ALIGN, "%s: misaligned pointer", what);
+  const size_t need = pq_attn_prefill_workspace_bytes(B, Tq, Tk, Hq, Hkv, D);
+  if (need && (!ws_d || ws_bytes < need)) return set_error(PQ_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", what, ws_d ? ws_bytes : 0, need);
+  PrefillArgs a{q_d, k_d, v_d, ldq, hsq, ldk, hsk, ldv, hsv, cu_q_d, cu_k_d, B, Tq, Tk, Hq, Hkv, causal, scale * 1.44269504088896340736f, o_d, out_type,
+                0, 0, static_cast<float*>(ws_d)};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   return launch_status(what, D == 64 ? prefill_launch<64>(a, type, s) : D == 128 ? prefill_launch<128>(a, type, s) : prefill_launch<256>(a, type, s));
 }
