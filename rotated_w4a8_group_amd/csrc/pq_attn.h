@@ -29,6 +29,12 @@ template <bool kBf16>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return kBf16 ? bf16x2_rn(a, b) : f16x2_rn(a, b);
 }
+// sum + the two values of a word
+template <bool kBf16>
+__device__ __forceinline__ float add_pair(uint32_t w, float sum) {
+  if constexpr (kBf16) return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(pq_bf16x2, w), pq_bf16x2{1.0f, 1.0f}, sum, false);
+  else return __builtin_amdgcn_fdot2(__builtin_bit_cast(pq_f16x2, w), pq_f16x2{1.0f, 1.0f}, sum, false);
+}
 template <bool kBf16>
 __device__ __forceinline__ attn_u32x4 pack16x8(const float (&v)[8]) {
   return attn_u32x4{pack2<kBf16>(v[0], v[1]), pack2<kBf16>(v[2], v[3]), pack2<kBf16>(v[4], v[5]), pack2<kBf16>(v[6], v[7])};

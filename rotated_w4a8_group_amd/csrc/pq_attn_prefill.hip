@@ -9,13 +9,15 @@
 //                 the contraction is free, a lane's own 8 are taken as they lie - P never leaves its registers - and V^T
 //                 follows that order: two transposing LDS reads of 4 keys each per 16 keys and 32 channels.
 // Scores, sums and O are binary32. P is rounded to v's type for the second product (half a step of it, 2^-8 or 2^-11 of each
-// weight); the sum takes the unrounded p.
+// weight).
 //
 // K and V tiles go global -> LDS by direct loads, row-major with the 16-byte chunks of a row permuted (kswizzle, vswizzle) so
 // that the 16 lanes of an operand read, and the 4 keys of a transposing one, lie in different banks.
 //
-// The maximum that p is taken against is raised only when a score passes it by more than 2^8 (a wave-wide vote): p stays below
-// 2^8, and the 16 D / 32 multiplications of O are rare. Keys that a query does not see get the score -inf, in the tiles
+// The score m that p = exp2(c (s - m)) is taken against is the largest of the first tile and is raised only where the weights of a
+// tile pass what their type holds with room to spare (their sum 2^60, f16 2^15: a wave-wide vote): the softmax does not depend
+// on m, sums and O are binary32, and neither the maximum nor a rescaling of O is part of an ordinary tile. The sum takes the rounded p, so
+// a rounding moves weight between values and leaves their sum at 1. Keys that a query does not see get the score -inf, in the tiles
 // that need it only. Their values still enter the product, with weight 0: a row whose result is not finite is
 // recomputed key by key (attend_row), so that an infinity or a NaN in a row that it does not see cannot reach it.
 #include <algorithm>
@@ -178,6 +180,7 @@ template <int D, bool kBf16>
 __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(PrefillArgs a) {
   using Tile = PrefillTile<D>;
   constexpr int kDB = D / 32, kKB = Tile::kKeys / 32, kSteps = D / 16;
+  constexpr bool kOpaque = D == 256;   // registers: at 128 channels the 1 % that it costs buys nothing
   __shared__ __attribute__((aligned(1024))) uint8_t smem[Tile::kLds];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 31, half = lane >> 5;
@@ -205,68 +208,73 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(PrefillArgs a) {
     for (int s = 0; s < kSteps; ++s) q[s] = *reinterpret_cast<const attn_u32x4*>(p + 16 * s);
   }
 
-  const uint16_t* kbase = a.k + static_cast<int64_t>(it.k0) * a.ldk + h * a.hsk;
-  const uint16_t* vbase = a.v + static_cast<int64_t>(it.k0) * a.ldv + h * a.hsv;
-  const uint32_t lds0 = lds_addr(smem);
-  // Direct loads of tile j into buffer j % 2: load i of a wave fills 1 KiB, kStep rows, 64 chunks in LDS order. A lane's row of
-  // the kStep and its chunk are fixed; the load's own rows are in the scalar base, and change the chunk's place by an exclusive or.
+  // Direct loads of a tile: load i of a wave fills 1 KiB, kStep rows, 64 chunks in LDS order. A lane's row of the kStep and its
+  // chunk are fixed; the load's own rows are in the scalar base, and change the chunk's place by an exclusive or.
   constexpr int kStep = 64 / Tile::kChunks;
-  const int lr = lane / Tile::kChunks, lc = lane % Tile::kChunks;
+  const int lr = lane / Tile::kChunks, lc = lane % Tile::kChunks, wr = wave * Tile::kLoads * kStep;   // wr: the wave's first row
   const uint32_t krow = lr * static_cast<uint32_t>(a.ldk) * 2, vrow = lr * static_cast<uint32_t>(a.ldv) * 2;
   const uint32_t kch = 16 * (lc ^ Tile::kswizzle(lr)), vch = 16 * (lc ^ Tile::vswizzle(lr));
+  const uint16_t* const kbase = a.k + static_cast<int64_t>(it.k0) * a.ldk + h * a.hsk;
+  const uint16_t* const vbase = a.v + static_cast<int64_t>(it.k0) * a.ldv + h * a.hsv;
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(smem) + wave * Tile::kLoads * 1024);
   auto load = [&](int j) {
     const int left = it.nk - j * Tile::kKeys;
-    const uint16_t* kb = kbase + static_cast<int64_t>(j) * Tile::kKeys * a.ldk;
-    const uint16_t* vb = vbase + static_cast<int64_t>(j) * Tile::kKeys * a.ldv;
     const uint32_t to = lds0 + (j & 1) * 2 * Tile::kPart;
+    const uint16_t* const kb = kbase + static_cast<int64_t>(j) * Tile::kKeys * a.ldk;
+    const uint16_t* const vb = vbase + static_cast<int64_t>(j) * Tile::kKeys * a.ldv;
     if (left >= Tile::kKeys) {
 #pragma unroll
-      for (int i = 0; i < Tile::kLoads; ++i) {
-        const int r = (wave * Tile::kLoads + i) * kStep;
-        lds_dma16_s(scalar_addr(kb + r * a.ldk), krow + (kch ^ (16 * Tile::kswizzle(r))), to + r * Tile::kRowBytes);
-      }
+      for (int i = 0; i < Tile::kLoads; ++i)
+        lds_dma16_s(scalar_addr(kb + (wr + i * kStep) * a.ldk), krow + (kch ^ (16 * Tile::kswizzle(wr + i * kStep))), to + i * 1024);
 #pragma unroll
-      for (int i = 0; i < Tile::kLoads; ++i) {
-        const int r = (wave * Tile::kLoads + i) * kStep;
-        lds_dma16_s(scalar_addr(vb + r * a.ldv), vrow + (vch ^ (16 * Tile::vswizzle(r))), to + Tile::kPart + r * Tile::kRowBytes);
-      }
+      for (int i = 0; i < Tile::kLoads; ++i)
+        lds_dma16_s(scalar_addr(vb + (wr + i * kStep) * a.ldv), vrow + (vch ^ (16 * Tile::vswizzle(wr + i * kStep))), to + Tile::kPart + i * 1024);
     } else {   // rows past the last key repeat it
 #pragma unroll
       for (int i = 0; i < Tile::kLoads; ++i) {
-        const int r = (wave * Tile::kLoads + i) * kStep;
-        const uint32_t from = static_cast<uint32_t>(std::min(r + lr, left - 1)) * 2;
-        lds_dma16_s(scalar_addr(kb), from * static_cast<uint32_t>(a.ldk) + (kch ^ (16 * Tile::kswizzle(r))), to + r * Tile::kRowBytes);
-        lds_dma16_s(scalar_addr(vb), from * static_cast<uint32_t>(a.ldv) + (vch ^ (16 * Tile::vswizzle(r))), to + Tile::kPart + r * Tile::kRowBytes);
+        const int r = wr + i * kStep;
+        const uint32_t from = 2 * static_cast<uint32_t>(std::min(r + lr, left - 1));
+        lds_dma16_s(scalar_addr(kb), from * static_cast<uint32_t>(a.ldk) + (kch ^ (16 * Tile::kswizzle(r))), to + i * 1024);
+        lds_dma16_s(scalar_addr(vb), from * static_cast<uint32_t>(a.ldv) + (vch ^ (16 * Tile::vswizzle(r))), to + Tile::kPart + i * 1024);
       }
     }
   };
 
   f32x16 o[kDB] = {};
-  float m = -__builtin_inff(), mc = 0.0f, l = 0.0f;   // the maximum that p is taken against, m * c, the sum of this lane's keys
+  float m = -__builtin_inff(), mc = 0.0f, l = 0.0f;   // the score that p is taken against, m * c, the sum of this lane's keys
+  bool fresh = true;                                  // a row of the wave has no such score yet
   const float c = a.scale_log2;
+  const int wave_tiles = std::min(tiles, (most + Tile::kKeys - 1) / Tile::kKeys);   // behind these nothing for this wave's rows
 
-  if (first < tiles) load(first);
-  for (int j = first; j < tiles; ++j) {
-    // this wave's loads of tile j have landed and its reads of tile j - 1 are done; behind the barrier every wave's
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (j + 1 < tiles) load(j + 1);
+  // Tile j, which lies in buffer j % 2.
+  auto step = [&](int j) {
+    const uint8_t* const kt = smem + (j & 1) * 2 * Tile::kPart;
+    const uint8_t* const vt = kt + Tile::kPart;
     const int k0 = j * Tile::kKeys;
-    if (k0 >= most) continue;                          // nothing here for this wave's rows
-    const uint8_t* kt = smem + (j & 1) * 2 * Tile::kPart;
-    const uint8_t* vt = kt + Tile::kPart;
-
+    // Operands are read kRead products ahead of their use: an LDS read takes longer than a product.
+    constexpr int kProducts = kKB * kSteps, kRead = D == 256 ? 2 : 4;
     f32x16 s[kKB];
-    const int ln = D == 256 ? opaque(lane) : lane;   // (registers; at 128 channels the 1 % that it costs buys nothing)
+    const int ln = kOpaque ? opaque(lane) : lane;
+    auto read_k = [&](int e) {
+      const int r = 32 * (e / kSteps) + (ln & 31), st = e % kSteps;
+      return *reinterpret_cast<const attn_u32x4*>(kt + r * Tile::kRowBytes + 16 * ((2 * st + (ln >> 5)) ^ Tile::kswizzle(r)));
+    };
+    attn_u32x4 kf[kRead];
 #pragma unroll
-    for (int kb = 0; kb < kKB; ++kb) {
-      s[kb] = f32x16{};
-      const int r = 32 * kb + (ln & 31), half = ln >> 5;
+    for (int e = 0; e < kRead; ++e) kf[e] = read_k(e);
 #pragma unroll
-      for (int st = 0; st < kSteps; ++st) {
-        const attn_u32x4 k = *reinterpret_cast<const attn_u32x4*>(kt + r * Tile::kRowBytes + 16 * ((2 * st + half) ^ Tile::kswizzle(r)));
-        s[kb] = mfma_32<kBf16>(k, q[st], s[kb]);
-      }
+    for (int e = 0; e < kProducts; ++e) {
+      f32x16& t = s[e / kSteps];
+      t = mfma_32<kBf16>(kf[e % kRead], q[e % kSteps], e % kSteps ? t : f32x16{});
+      if (e + kRead < kProducts) kf[e % kRead] = read_k(e + kRead);
     }
+    __builtin_amdgcn_sched_group_barrier(0x100, kRead, 0);
+#pragma unroll
+    for (int e = 0; e < kProducts - kRead; ++e) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, kRead, 0);
     if (k0 + Tile::kKeys > least) {
       const int limit = seen - k0 - 4 * half;
 #pragma unroll
@@ -274,13 +282,13 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(PrefillArgs a) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[kb][i] = 32 * kb + (i & 3) + 8 * (i >> 2) < limit ? s[kb][i] : -__builtin_inff();
     }
-    float mt = s[0][0];
+    auto raise = [&] {
+      float mt = m;
 #pragma unroll
-    for (int kb = 0; kb < kKB; ++kb)
+      for (int kb = 0; kb < kKB; ++kb)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) mt = __builtin_fmaxf(mt, s[kb][i]);
-    mt = __builtin_fmaxf(both_halves_max(mt), m);
-    if (__any((mt - m) * c > 8.0f)) {
+        for (int i = 0; i < 16; ++i) mt = __builtin_fmaxf(mt, s[kb][i]);
+      mt = both_halves_max(mt);
       const float f = m == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m * c - mt * c);
       m = mt;
       mc = m == -__builtin_inff() ? 0.0f : m * c;
@@ -289,31 +297,66 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(PrefillArgs a) {
       for (int db = 0; db < kDB; ++db)
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[db][i] *= f;
-    }
+      fresh = __any(m == -__builtin_inff());
+    };
     uint32_t p[kKB][8];
+    float sum;
+    auto weights = [&] {
+      float part[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int kb = 0; kb < kKB; ++kb)
+      for (int kb = 0; kb < kKB; ++kb)
 #pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i], c, -mc)), y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i + 1], c, -mc));
-        l += x + y;
-        p[kb][i / 2] = pack2<kBf16>(x, y);
-      }
-    const int lv = D == 256 ? opaque(lane) : lane;
+        for (int i = 0; i < 8; ++i) {
+          p[kb][i] = pack2<kBf16>(__builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][2 * i], c, -mc)), __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][2 * i + 1], c, -mc)));
+          part[i & 1] = add_pair<kBf16>(p[kb][i], part[i & 1]);
+        }
+      sum = part[0] + part[1];
+    };
+    const int lv = kOpaque ? opaque(lane) : lane;
+    auto read_v = [&](int e) {                         // product e: 32 channels of 16 keys
+      const int kb = e / kDB, db = e % kDB;
+      const int r = 16 * kb + 4 * (lv >> 5) + ((lv & 15) >> 2);   // this lane's key of the first transposing read; r + 8 of the second
+      const int ch = 4 * db + 2 * ((lv >> 4) & 1) + ((lv & 3) >> 1), byte = 8 * (lv & 1);
+      const uint2 v0 = lds_read_transposed(vt + r * Tile::kRowBytes + 16 * (ch ^ Tile::vswizzle(r)) + byte);
+      const uint2 v1 = lds_read_transposed(vt + (r + 8) * Tile::kRowBytes + 16 * (ch ^ Tile::vswizzle(r + 8)) + byte);
+      return attn_u32x4{v0.x, v0.y, v1.x, v1.y};
+    };
+    constexpr int kValues = 2 * kKB * kDB, kReadV = D == 256 ? 2 : 6;
+    attn_u32x4 vf[kReadV];
 #pragma unroll
-    for (int kb = 0; kb < 2 * kKB; ++kb) {             // 16 keys each
-      const int lane = lv, half = lv >> 5;
-      const attn_u32x4 w = {p[kb / 2][4 * (kb % 2)], p[kb / 2][4 * (kb % 2) + 1], p[kb / 2][4 * (kb % 2) + 2], p[kb / 2][4 * (kb % 2) + 3]};
-      const int r = 16 * kb + 4 * half + ((lane & 15) >> 2);   // this lane's key of the first transposing read; r + 8 of the second
-#pragma unroll
-      for (int db = 0; db < kDB; ++db) {
-        const int ch = 4 * db + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1), byte = 8 * (lane & 1);
-        const uint2 v0 = lds_read_transposed(vt + r * Tile::kRowBytes + 16 * (ch ^ Tile::vswizzle(r)) + byte);
-        const uint2 v1 = lds_read_transposed(vt + (r + 8) * Tile::kRowBytes + 16 * (ch ^ Tile::vswizzle(r + 8)) + byte);
-        o[db] = mfma_32<kBf16>(attn_u32x4{v0.x, v0.y, v1.x, v1.y}, w, o[db]);
-      }
+    for (int e = 0; e < kReadV; ++e) vf[e] = read_v(e);
+    if (fresh) raise();
+    weights();
+    if (__any(!(sum <= (kBf16 ? 0x1p60f : 0x1p15f)))) {
+      raise();
+      weights();
     }
-  }
+    l += sum;
+#pragma unroll
+    for (int e = 0; e < kValues; ++e) {
+      const int kb = e / kDB;
+      const attn_u32x4 w = {p[kb / 2][4 * (kb % 2)], p[kb / 2][4 * (kb % 2) + 1], p[kb / 2][4 * (kb % 2) + 2], p[kb / 2][4 * (kb % 2) + 3]};
+      o[e % kDB] = mfma_32<kBf16>(vf[e % kReadV], w, o[e % kDB]);
+      if (e + kReadV < kValues) vf[e % kReadV] = read_v(e + kReadV);
+    }
+#pragma unroll
+    for (int e = 0; e < kValues - kReadV; ++e) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 1);
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 1);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, kReadV, 1);
+  };
+  auto turn = [&](int j) {
+    // this wave's loads of tile j have landed and its reads of tile j - 1 are done; behind the barrier every wave's
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (j + 1 < tiles) load(j + 1);
+    if (j < wave_tiles) step(j);
+  };
+  if (first < tiles) load(first);
+  // the queries have landed: or the loop would wait for them again, and with them for the loads it has just made
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) asm volatile("" : "+v"(q[i]));
+  for (int j = first; j < tiles; ++j) turn(j);
 
   l = both_halves_sum(l);
   if (it.pieces > 1) {
@@ -329,12 +372,12 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(PrefillArgs a) {
     return;
   }
   // Rows that saw a key and whose values are not all finite: key by key. (A sum of 0 has every score at -inf: NaN by the formula.)
-  float t = l > 0.0f ? 0.0f : __builtin_nanf("");
+  float odd_sum = l > 0.0f ? 0.0f : __builtin_nanf("");
 #pragma unroll
   for (int db = 0; db < kDB; ++db)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) t = __builtin_fmaf(o[db][i], 0.0f, t);
-  const uint64_t odd = __ballot(seen > 0 && row < it.nq && !(t == 0.0f));
+    for (int i = 0; i < 16; ++i) odd_sum = __builtin_fmaf(o[db][i], 0.0f, odd_sum);
+  const uint64_t odd = __ballot(seen > 0 && row < it.nq && !(odd_sum == 0.0f));
   const uint32_t again = static_cast<uint32_t>(odd | odd >> 32);
   const float inv = seen > 0 ? 1.0f / l : 0.0f;
   if (row < it.nq && !(again >> n & 1)) {

@@ -9,11 +9,12 @@ Tolerance, with u = 2^-24, c = scale, n keys, and in 64 bits Q = max_j c sum_i |
    most (2 D + 4) u Q, which is the relative error of exp; exp2 adds 2 u. Scores change only through their differences, so
    each p is off by at most E = 2 (2 D + 4) u Q + 4 u, the rounded maxima included.
  - The sum and the weighted sum have n terms each, in any order, with one rescaling a tile: 2 (2 n) u between them, 8 u for joining parts and dividing.
- - Prompts: p is rounded to the type of v for the matrix product, e(t). f16 reaches down to 2^-24 only: up to 2^-25 more for each p,
-   where the largest is at least 1. One token: p is held in two pieces of the type, (2^-8)^2 at most, and 2^-24 absolute for f16.
+ - Prompts: p is rounded to the type of v, e(t), and the rounded p are summed too: o' - o = sum_j p_j d_j (v_j - o) / sum_j p_j (1 + d_j)
+   with |d| <= e(t), at most e(t) (A + |o|) to first order. f16 reaches down to 2^-24 only: up to 2^-25 more for each p, where one of
+   them is at least 1: 2^-25 (sum_j |v_j| + n |o|). One token: p is held in two pieces of the type, (2^-8)^2 at most, f16's down to 2^-24.
  - o is stored with one rounding, e(out), and f16 subnormals 2^-25.
 
-    |o - o_ref| <= e(out) |o_ref| + 1.01 (2 E + (4 n + 8) u + e_p) A + (f16: 2^-24 sum_j |v_j|) + 2^-25
+    |o - o_ref| <= e(out) |o_ref| + 1.01 (2 E + (4 n + 8) u) A + 1.01 e_p (A + |o_ref|) + (f16: 1.01 2^-25 (sum_j |v_j| + n |o_ref|)) + 2^-25
 """
 import math
 
@@ -124,9 +125,9 @@ def _reference(q, k, v, scale, visible):
 
 def _check(o, ref, n, D, dtype, e_p, what):
     want, Q, A, S = ref
-    tol = E[o.dtype] * want.abs() + 1.01 * (2 * (2 * (2 * D + 4) * U * Q + 4 * U) + (4 * n + 8) * U + e_p) * A + 2.0 ** -25
+    tol = E[o.dtype] * want.abs() + 1.01 * (2 * (2 * (2 * D + 4) * U * Q + 4 * U) + (4 * n + 8) * U) * A + 1.01 * e_p * (A + want.abs()) + 2.0 ** -25
     if dtype == F16:
-        tol = tol + 2.0 ** -24 * S
+        tol = tol + 1.01 * 2.0 ** -25 * (S + n * want.abs())
     err = (o.double() - want).abs()
     worst = float((err / tol).max()) if err.numel() else 0.0
     assert bool((err <= tol).all()), f"{what}: {worst:.2f} of the tolerance"
