@@ -6,8 +6,10 @@
 // 16-bit values themselves. Per row x of D values (the encoder and the scale are those of the prologue's groups):
 //   s = fl32(max |x| * fl32(1/448)),  code_i = E(fl32(x_i * fl32(1/s))),  read back as fl(code_i * s).
 //
-// Both kernels move bytes: D / 8 lanes hold a row, 16 bytes of 16-bit values each, so a wave takes 8 rows of 64, 4 of
-// 128 or 2 of 256 values, and the row's maximum is a reduction over those lanes.
+// Both kernels move bytes. D / 8 lanes hold a (row, head) pair, 8 values of k and 8 of v each, so that a wave takes 8 pairs of 64, 4 of
+// 128 or 2 of 256 values, the heads of a row next to each other; a maximum is a reduction over those lanes. Writing 4038 rows
+// of 8 heads of 128 (25 MB) takes 7.9 us, of which a launch is 2.6 (k and v in lanes of their own: 9.2), and every
+// lane's one chain of loads, maximum, division and store most of the rest: all workgroups are on the device at once.
 #include <algorithm>
 
 #include "pq_attn.h"
@@ -35,40 +37,49 @@ __device__ __forceinline__ float row_max(float v) {
 template <int D, bool kBf16, bool kQuant>
 __global__ __launch_bounds__(256) void kv_write_kernel(KvWriteArgs a) {
   constexpr int L = D / 8, R = 256 / L;   // lanes of a row, rows of a workgroup
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * R + threadIdx.x / L;
+  // unit = (token, head): the heads of a token stand next to each other in the source
+  const uint32_t unit = blockIdx.x * R + threadIdx.x / L, t = unit / a.Hkv, h = unit - t * a.Hkv;
   const int lane = threadIdx.x % L;
-  // unit = (token, k or v, head): the heads of a token stand next to each other in the source
-  const int64_t t = unit / (2 * a.Hkv);
-  const int r = static_cast<int>(unit - t * 2 * a.Hkv), which = r >= a.Hkv, h = r - which * a.Hkv;
-  if (t >= a.T) return;     // whole rows leave: the lanes of a row stay together
+  if (t >= static_cast<uint32_t>(a.T)) return;     // whole rows leave: the lanes of a row stay together
   const int64_t slot = a.slots[t];
+  attn_u32x4 q[2];
+#pragma unroll
+  for (int w = 0; w < 2; ++w) q[w] = __builtin_nontemporal_load(reinterpret_cast<const attn_u32x4*>(a.src[w] + t * a.ld[w] + h * a.hs[w] + 8 * lane));
   if (slot < 0 || slot >= a.nslots) return;
-  const attn_u32x4 q = *reinterpret_cast<const attn_u32x4*>(a.src[which] + t * a.ld[which] + h * a.hs[which] + 8 * lane);
   const int64_t row = (((slot >> a.page_shift) * a.Hkv + h) << a.page_shift) + (slot & ((1 << a.page_shift) - 1));
   if constexpr (!kQuant) {
-    *reinterpret_cast<attn_u32x4*>(static_cast<uint16_t*>(a.cache[which]) + row * D + 8 * lane) = q;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) *reinterpret_cast<attn_u32x4*>(static_cast<uint16_t*>(a.cache[w]) + row * D + 8 * lane) = q[w];
   } else {
-    float v[8];
-    unpack16x8<kBf16>(q, v);
-    // a row with an infinity or a NaN gets the scale NaN and the codes 0: it reads back as NaN
-    float most = 0.0f;
-    bool bad = false;
+    float v[2][8], most[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      most = __builtin_fmaxf(most, __builtin_fabsf(v[i]));
-      bad = bad || !(__builtin_fabsf(v[i]) <= 3.4e38f);
+    for (int w = 0; w < 2; ++w) {
+      unpack16x8<kBf16>(q[w], v[w]);
+      // a row with an infinity or a NaN gets the scale NaN and the codes 0: it reads back as NaN
+      most[w] = 0.0f;
+      bool bad = false;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        most[w] = __builtin_fmaxf(most[w], __builtin_fabsf(v[w][i]));
+        bad = bad || !(__builtin_fabsf(v[w][i]) <= 3.4e38f);
+      }
+      if (bad) most[w] = __builtin_inff();
     }
-    most = row_max<L>(bad ? __builtin_inff() : most);
-    float s = most * (1.0f / 448.0f);
-    if (s < 1.17549435e-38f) s = 0.0f;   // its reciprocal would overflow: such a row counts as zero
-    const float inv = s > 0.0f && most <= 3.4e38f ? 1.0f / s : 0.0f;
-    if (!(most <= 3.4e38f)) s = __builtin_nanf("");
-    uint32_t c[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      c[i] = e4m3_encode2(v[4 * i] * inv, v[4 * i + 1] * inv) | e4m3_encode2(v[4 * i + 2] * inv, v[4 * i + 3] * inv) << 16;
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.cache[which]) + row * D + 8 * lane) = make_uint2(c[0], c[1]);
-    if (lane == 0) a.scale[which][row] = s;
+    for (int w = 0; w < 2; ++w) {
+      most[w] = row_max<L>(most[w]);
+      float s = most[w] * (1.0f / 448.0f);
+      if (s < 1.17549435e-38f) s = 0.0f;   // its reciprocal would overflow: such a row counts as zero
+      const bool finite = most[w] <= 3.4e38f;
+      const float inv = s > 0.0f && finite ? 1.0f / s : 0.0f;
+      if (!finite) s = __builtin_nanf("");
+      uint32_t c[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        c[i] = e4m3_encode2(v[w][4 * i] * inv, v[w][4 * i + 1] * inv) | e4m3_encode2(v[w][4 * i + 2] * inv, v[w][4 * i + 3] * inv) << 16;
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.cache[w]) + row * D + 8 * lane) = make_uint2(c[0], c[1]);
+      if (lane == 0) a.scale[w][row] = s;
+    }
   }
 }
 
@@ -79,39 +90,70 @@ struct KvReadArgs {
   uint16_t* out[2];
 };
 
-template <int D, bool kBf16, bool kQuant>
+// kReadUnits: (row, head) pairs of a lane, whose loads are in flight together.
+template <int D, bool kBf16, bool kQuant, int kReadUnits>
 __global__ __launch_bounds__(256) void kv_read_kernel(KvReadArgs a) {
-  constexpr int L = D / 8, R = 256 / L;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * R + threadIdx.x / L;
+  constexpr int kBytes = D * (kQuant ? 1 : 2), L = D / 8, R = 256 / L;   // bytes of a row, its lanes, rows of a workgroup at a time
+  const uint32_t unit0 = blockIdx.x * (R * kReadUnits) + threadIdx.x / L;
   const int lane = threadIdx.x % L;
-  const int64_t t = unit / (2 * a.c.Hkv);
-  const int r = static_cast<int>(unit - t * 2 * a.c.Hkv), which = r >= a.c.Hkv, h = r - which * a.c.Hkv;
-  if (t >= a.T) return;
+  uint32_t t = unit0 / a.c.Hkv;
+  if (t >= static_cast<uint32_t>(a.T)) return;
   // the sequence of row t: the last b with cu[b] <= t
   int lo = 0, hi = a.B;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (a.cu[mid] <= t) lo = mid;
+    if (a.cu[mid] <= static_cast<int64_t>(t)) lo = mid;
     else hi = mid;
   }
-  const int64_t first = a.cu[lo];
-  if (t < first || t >= a.cu[lo + 1]) return;   // rows of no sequence stay as they are
-  const int64_t pos = t - first, row = cache_row(a.c, lo, h, pos);
-  attn_u32x4 q = {0, 0, 0, 0};                  // a page outside the cache reads as zeros
-  if (row >= 0) {
-    if constexpr (!kQuant) {
-      q = *reinterpret_cast<const attn_u32x4*>(static_cast<const uint16_t*>(which ? a.c.v : a.c.k) + row * D + 8 * lane);
-    } else {
-      const uint2 c = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(which ? a.c.v : a.c.k) + row * D + 8 * lane);
-      const float s = (which ? a.c.vs : a.c.ks)[row];
-      float v[8];
-      decode8(c, v);
+  int64_t row[kReadUnits], to[kReadUnits];   // row -1: a page outside the cache; to -1: nothing to write
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= s;
-      q = pack16x8<kBf16>(v);
+  for (int i = 0; i < kReadUnits; ++i) {
+    const uint32_t unit = unit0 + i * R;
+    t = unit / a.c.Hkv;
+    const uint32_t h = unit - t * a.c.Hkv;
+    row[i] = to[i] = -1;
+    if (t < static_cast<uint32_t>(a.T)) {
+      while (lo + 1 < a.B && a.cu[lo + 1] <= static_cast<int64_t>(t)) ++lo;
+      const int64_t first = a.cu[lo];
+      if (t >= first && t < static_cast<int64_t>(a.cu[lo + 1])) {   // rows of no sequence stay as they are
+        to[i] = static_cast<int64_t>(unit) * D + 8 * lane;
+        row[i] = cache_row(a.c, lo, h, t - first);
+      }
     }
   }
-  *reinterpret_cast<attn_u32x4*>(a.out[which] + (t * a.c.Hkv + h) * D + 8 * lane) = q;
+  attn_u32x4 q[kReadUnits][2];
+  float s[kReadUnits][2];
+#pragma unroll
+  for (int i = 0; i < kReadUnits; ++i)
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      q[i][w] = attn_u32x4{0, 0, 0, 0};
+      s[i][w] = 0.0f;
+      if (row[i] >= 0) {
+        const uint8_t* const from = static_cast<const uint8_t*>(w ? a.c.v : a.c.k) + row[i] * kBytes + kBytes / L * lane;
+        if constexpr (kQuant) {
+          const uint2 c = __builtin_bit_cast(uint2, __builtin_nontemporal_load(reinterpret_cast<const uint64_t*>(from)));
+          q[i][w].x = c.x, q[i][w].y = c.y;
+          s[i][w] = (w ? a.c.vs : a.c.ks)[row[i]];
+        } else {
+          q[i][w] = __builtin_nontemporal_load(reinterpret_cast<const attn_u32x4*>(from));
+        }
+      }
+    }
+#pragma unroll
+  for (int i = 0; i < kReadUnits; ++i)
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      if (to[i] < 0) continue;
+      if constexpr (kQuant) {
+        float v[8];
+        decode8(make_uint2(q[i][w].x, q[i][w].y), v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] *= s[i][w];
+        q[i][w] = pack16x8<kBf16>(v);
+      }
+      __builtin_nontemporal_store(q[i][w], reinterpret_cast<attn_u32x4*>(a.out[w] + to[i]));
+    }
 }
 
 template <int D>
@@ -120,11 +162,20 @@ static hipError_t write_launch(const KvWriteArgs& a, int type, unsigned grid, hi
   if (a.scale[0]) return launch_kernel((kv_write_kernel<D, false, true>), dim3(grid), dim3(256), 0, s, a);
   return launch_kernel((kv_write_kernel<D, false, false>), dim3(grid), dim3(256), 0, s, a);   // bits are copied, whatever their type
 }
+// One pair a lane while all of them are on the device together (65 rows of 4 heads of 256: 2.8 us, with four 4.6), else four (7
+// sequences of up to 8191 rows, 268 MB: 53.6 us, 5.0 TB/s; with one, two, eight 64, 60, 57; stores that stay in the caches 57.5; heads
+// of a page one after the other instead of a row's heads side by side, so that stores are a head wide, 60 to 63).
+template <int D, bool kBf16, bool kQuant>
+static hipError_t read_kernel(const KvReadArgs& a, hipStream_t s) {
+  constexpr int R = 256 / (D / 8);
+  const int64_t pairs = static_cast<int64_t>(a.T) * a.c.Hkv, blocks = (pairs + R - 1) / R;
+  if (blocks <= 8 * cu_count()) return launch_kernel((kv_read_kernel<D, kBf16, kQuant, 1>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a);
+  return launch_kernel((kv_read_kernel<D, kBf16, kQuant, 4>), dim3(static_cast<unsigned>((blocks + 3) / 4)), dim3(256), 0, s, a);
+}
 template <int D>
-static hipError_t read_launch(const KvReadArgs& a, int type, unsigned grid, hipStream_t s) {
-  if (a.c.ks && type == PQ_BF16) return launch_kernel((kv_read_kernel<D, true, true>), dim3(grid), dim3(256), 0, s, a);
-  if (a.c.ks) return launch_kernel((kv_read_kernel<D, false, true>), dim3(grid), dim3(256), 0, s, a);
-  return launch_kernel((kv_read_kernel<D, false, false>), dim3(grid), dim3(256), 0, s, a);
+static hipError_t read_launch(const KvReadArgs& a, int type, hipStream_t s) {
+  if (a.c.ks) return type == PQ_BF16 ? read_kernel<D, true, true>(a, s) : read_kernel<D, false, true>(a, s);
+  return read_kernel<D, false, false>(a, s);
 }
 
 int check_cache(const char* what, const void* kc, const void* vc, const float* ks, const float* vs, int64_t pages, int page, int Hkv, int D) {
@@ -163,7 +214,7 @@ int pq_kv_write(const uint16_t* k_d, int64_t ldk, int64_t hsk, const uint16_t* v
   if (rc == PQ_OK) rc = check_heads(what, "k", k_d, ldk, hsk, T, Hkv, D);
   if (rc == PQ_OK) rc = check_heads(what, "v", v_d, ldv, hsv, T, Hkv, D);
   if (rc != PQ_OK) return rc;
-  const int64_t rows = 2ll * T * Hkv, per = 256 / (D / 8), grid = (rows + per - 1) / per;
+  const int64_t rows = static_cast<int64_t>(T) * Hkv, per = 256 / (D / 8), grid = (rows + per - 1) / per;
   if (grid * 256 > 0xFFFFFFFFll) return set_error(PQ_ERR_SHAPE, "%s: T=%d rows too many for one call (split the rows)", what, T);
   if (T == 0) return PQ_OK;
   if (!slots_d) return set_error(PQ_ERR_NULL, "%s: slots is NULL", what);
@@ -184,15 +235,14 @@ int pq_kv_read(const void* kc_d, const void* vc_d, const float* ks_d, const floa
   if (type != PQ_F16 && type != PQ_BF16) return set_error(PQ_ERR_SHAPE, "%s: type %d, expected f16 or bf16", what, type);
   const int rc = check_cache(what, kc_d, vc_d, ks_d, vs_d, pages, page, Hkv, D);
   if (rc != PQ_OK) return rc;
-  const int64_t rows = 2ll * T * Hkv, per = 256 / (D / 8), grid = (rows + per - 1) / per;
-  if (grid * 256 > 0xFFFFFFFFll) return set_error(PQ_ERR_SHAPE, "%s: T=%d rows too many for one call (split the sequences)", what, T);
+  if (static_cast<int64_t>(T) * Hkv * (D / 8) > 0xFFFF0000ll)   // the runtime counts a launch's threads in 32 bits
+    return set_error(PQ_ERR_SHAPE, "%s: T=%d rows of %d heads too many for one call (split the sequences)", what, T, Hkv);
   if (T == 0 || B == 0) return PQ_OK;
   if (!k_d || !v_d || !cu_d || (width && !table_d)) return set_error(PQ_ERR_NULL, "%s: NULL pointer", what);
   if (!aligned(k_d, 16) || !aligned(v_d, 16) || !aligned(cu_d, 4) || !aligned(table_d, 4)) return set_error(PQ_ERR_ALIGN, "%s: misaligned pointer", what);
   KvReadArgs a{{kc_d, vc_d, ks_d, vs_d, table_d, pages, width, Hkv, __builtin_ctz(page)}, cu_d, B, T, {k_d, v_d}};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  const unsigned g = static_cast<unsigned>(grid);
-  return launch_status(what, D == 64 ? read_launch<64>(a, type, g, s) : D == 128 ? read_launch<128>(a, type, g, s) : read_launch<256>(a, type, g, s));
+  return launch_status(what, D == 64 ? read_launch<64>(a, type, s) : D == 128 ? read_launch<128>(a, type, s) : read_launch<256>(a, type, s));
 }
 
 }  // extern "C"
