@@ -116,8 +116,8 @@ _fast = None
 
 
 def _native():
-    """The compiled calls of rotate, matvec, gemm_glu and block_norms (``_binding.so``), which take the usual call - plain
-    tensors that pass every check, on the current device and stream - and answer NotImplemented to any other; False where
+    """The compiled calls of rotate, matvec, gemm_glu, block_norms, kv_write, kv_read, attn_decode and attn_prefill (``_binding.so``), which
+    take the usual call - plain tensors that pass every check, on the current device and stream - and answer NotImplemented to any other; False where
     they are not built for this interpreter, torch and library: the functions below then do every call, 2 to 5 us slower each."""
     global _fast
     if _fast is None:
@@ -126,7 +126,9 @@ def _native():
         try:
             from . import _binding as b
             b.bind(_check, L.pq_abi_version(), *(ctypes.cast(getattr(L, f), _P).value for f in (
-                "pq_rotate", "pq_matvec", "pq_gemm_glu", "pq_block_norms", "pq_packed_weight_bytes", "pq_gemm_workspace_bytes")))
+                "pq_rotate", "pq_matvec", "pq_gemm_glu", "pq_block_norms", "pq_packed_weight_bytes", "pq_gemm_workspace_bytes",
+                "pq_kv_write", "pq_kv_read", "pq_attn_decode", "pq_attn_prefill", "pq_attn_decode_workspace_bytes",
+                "pq_attn_prefill_workspace_bytes")))
             _fast = b
         except ImportError as e:   # not built, or not for this library
             if os.path.exists(os.path.join(_HERE, "_binding.so")):
@@ -862,6 +864,11 @@ def kv_write(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None, stream=N
     k_cache, v_cache [pages, Hkv, page, D]: uint8 e4m3 codes with k_scale, v_scale f32 [pages, Hkv, page] - per (row, head)
     max |x| / 448, as ``rotate_quant`` encodes a group - or k's type without scales: the rows as they are. A row
     with an infinity or a NaN gets the scale NaN. D 64, 128 or 256, page a power of two in 16..1024. Returns (k_cache, v_cache)."""
+    f = _native() if _fast is None else _fast
+    if f and stream is None:
+        done = f.kv_write(k, v, slots, k_cache, v_cache, k_scale, v_scale)
+        if done is not NotImplemented:
+            return done
     import torch
     ldk, hsk = _heads(k, "k")
     T, H, D = k.shape
@@ -879,6 +886,11 @@ def kv_read(k_cache, v_cache, block_table, cu, T, k_scale=None, v_scale=None, ou
     sequence in order; cu int32 [B + 1], where its rows begin in the packed output -> (k, v) [T, Hkv, D] of ``dtype`` (f16 or
     bf16; the cache's own type where it holds 16-bit values, f16 by default otherwise), or into ``out``, a pair of those.
     Rows of no sequence are left as they were; a position whose page is not one of the cache's reads as zeros."""
+    f = _native() if _fast is None else _fast
+    if f and stream is None:
+        done = f.kv_read(k_cache, v_cache, block_table, cu, T, k_scale, v_scale, out, dtype)
+        if done is not NotImplemented:
+            return done
     import torch
     if out is not None:
         if not isinstance(out, (tuple, list)) or len(out) != 2:
@@ -932,6 +944,11 @@ def attn_decode(q, k_cache, v_cache, block_table, lengths, k_scale=None, v_scale
 
     A sequence of length 0 gives zeros; positions whose page is not one of the cache's are left out, and no length passes the
     table's width. What the cache holds behind a sequence's end - infinities and NaN too - does not count."""
+    f = _native() if _fast is None else _fast
+    if f and stream is None:
+        done = f.attn_decode(q, k_cache, v_cache, block_table, lengths, k_scale, v_scale, scale, out, dtype, workspace)
+        if done is not NotImplemented:
+            return done
     import torch
     ldq, hsq = _heads(q, "q")
     B, Hq, D = q.shape
@@ -974,6 +991,11 @@ def attn_prefill(q, k, v, cu_q, cu_k=None, scale=None, causal=True, out=None, dt
 
     A query that sees no key gives zeros, whatever it does not see does not count (infinities and NaN too), and rows of no
     sequence are left as they were. scale: of the scores, D ** -0.5 by default."""
+    f = _native() if _fast is None else _fast
+    if f and stream is None:
+        done = f.attn_prefill(q, k, v, cu_q, cu_k, scale, causal, out, dtype, workspace)
+        if done is not NotImplemented:
+            return done
     import torch
     ldq, hsq = _heads(q, "q")
     Tq, Hq, D = q.shape

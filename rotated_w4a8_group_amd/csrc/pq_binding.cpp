@@ -1,5 +1,5 @@
-// The usual call of rotate, matvec, gemm_glu and block_norms without the interpreter's part: strided tensors of
-// the expected types and shapes, all on the current device, on its current stream. Anything else - another
+// The usual call of rotate, matvec, gemm_glu, block_norms, kv_write, kv_read, attn_decode and attn_prefill without the
+// interpreter's part: strided tensors of the expected types and shapes, all on the current device, on its current stream. Anything else - another
 // stream or device, a subclass of Tensor, an argument that is to be refused - returns NotImplemented, and the
 // Python function of the same name does the call or names what is wrong, so every refusal is worded in one place.
 //
@@ -17,6 +17,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <climits>
+#include <cmath>
 
 #include "pq.h"
 
@@ -30,6 +31,12 @@ struct Entries {
   decltype(&pq_block_norms) block_norms;
   decltype(&pq_packed_weight_bytes) packed_weight_bytes;
   decltype(&pq_gemm_workspace_bytes) gemm_workspace_bytes;
+  decltype(&pq_kv_write) kv_write;
+  decltype(&pq_kv_read) kv_read;
+  decltype(&pq_attn_decode) attn_decode;
+  decltype(&pq_attn_prefill) attn_prefill;
+  decltype(&pq_attn_decode_workspace_bytes) attn_decode_workspace_bytes;
+  decltype(&pq_attn_prefill_workspace_bytes) attn_prefill_workspace_bytes;
 };
 Entries pq{};
 PyObject* check = nullptr;
@@ -286,13 +293,166 @@ PyObject* block_norms(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// bind(check, abi_version, rotate, matvec, gemm_glu, block_norms, packed_weight_bytes, gemm_workspace_bytes): addresses, of a
-// library of this ABI version. The signatures are the ones that pq.h had when this file was compiled, so another version raises.
+// [T, H, D] rows of heads with unit channel stride; the row and head strides that the library takes
+bool heads(const Arg& a, at::ScalarType t, int64_t T, int64_t H, int64_t D) {
+  return a->scalar_type() == t && a->dim() == 3 && a->size(0) == T && a->size(1) == H && a->size(2) == D && (T == 0 || H == 0 || D <= 1 || a->stride(2) == 1);
+}
+struct Strides { int64_t row, head; };
+Strides strides(const at::Tensor& t) {
+  const int64_t H = t.size(1), D = t.size(2);
+  return {t.size(0) > 1 ? t.stride(0) : H * D, H > 1 ? t.stride(1) : D};
+}
+// A cache of `type` values, or of codes with scales, [pages, Hkv, page, D].
+bool paged(const Arg& kc, const Arg& vc, const Arg& ks, const Arg& vs, at::ScalarType type) {
+  if (kc->dim() != 4 || static_cast<bool>(ks) != static_cast<bool>(vs)) return false;
+  for (int i = 0; i < 4; ++i)
+    if (!fits(kc->size(i))) return false;
+  const at::ScalarType t = ks ? kU8 : type;
+  return dense(kc, t, kc->sizes()) && dense(vc, t, kc->sizes()) &&
+         (!ks || (dense(ks, kF32, kc->sizes().slice(0, 3)) && dense(vs, kF32, kc->sizes().slice(0, 3))));
+}
+const float* floats(const Arg& a) { return static_cast<const float*>(a.ptr()); }
+const int32_t* ints(const Arg& a) { return static_cast<const int32_t*>(a.ptr()); }
+// The scale of the scores: a number, or None for D^-1/2.
+bool get_scale(PyObject* o, int64_t D, float* v) {
+  if (o != Py_None) return get_float(o, v);
+  *v = static_cast<float>(1.0 / std::sqrt(static_cast<double>(D)));
+  return true;
+}
+PyObject* pair(PyObject* a, PyObject* b) {   // takes both references
+  PyObject* r = a && b ? PyTuple_Pack(2, a, b) : nullptr;
+  Py_XDECREF(a);
+  Py_XDECREF(b);
+  return r;
+}
+
+// kv_write(k, v, slots, k_cache, v_cache, k_scale, v_scale)
+PyObject* kv_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 7) return unusual();
+  const Arg k(a[0]), v(a[1]), slots(a[2]), kc(a[3]), vc(a[4]), ks(a[5]), vs(a[6]);
+  Device d;
+  if (!k || !v || !slots || !kc || !vc || !all_on(d, k, v, slots, kc, vc, ks, vs) || k->dim() != 3) return unusual();
+  const at::ScalarType t = k->scalar_type();
+  const int64_t T = k->size(0), H = k->size(1), D = k->size(2);
+  if (!half_type(t) || !fits(T) || !heads(k, t, T, H, D) || !heads(v, t, T, H, D) || !dense(slots, at::kLong, {T}) || !paged(kc, vc, ks, vs, t) ||
+      kc->size(1) != H || kc->size(3) != D)
+    return unusual();
+  const Strides sk = strides(*k.t), sv = strides(*v.t);
+  const int rc = call(pq.kv_write, static_cast<const uint16_t*>(k.ptr()), sk.row, sk.head, static_cast<const uint16_t*>(v.ptr()), sv.row, sv.head, type_code(t),
+                      static_cast<int>(T), static_cast<int>(H), static_cast<int>(D), static_cast<const int64_t*>(slots.ptr()), kc.ptr(), vc.ptr(),
+                      static_cast<float*>(ks.ptr()), static_cast<float*>(vs.ptr()), kc->size(0), static_cast<int>(kc->size(2)), d.stream());
+  if (!ok("pq_kv_write", rc)) return nullptr;
+  return PyTuple_Pack(2, a[3], a[4]);
+  END_HANDLE_TH_ERRORS
+}
+
+// kv_read(k_cache, v_cache, block_table, cu, T, k_scale, v_scale, out, dtype)
+PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  int T;
+  if (n != 9 || !get_int(a[4], &T) || T < 0) return unusual();
+  const bool given = a[7] != Py_None;
+  if (given && (!PyTuple_CheckExact(a[7]) || PyTuple_GET_SIZE(a[7]) != 2)) return unusual();
+  const Arg kc(a[0]), vc(a[1]), table(a[2]), cu(a[3]), ks(a[5]), vs(a[6]);
+  const Arg ok_(given ? PyTuple_GET_ITEM(a[7], 0) : Py_None), ov(given ? PyTuple_GET_ITEM(a[7], 1) : Py_None);
+  Device d;
+  if (!kc || !vc || !table || !cu || (given && (!ok_ || !ov)) || !all_on(d, kc, vc, table, cu, ks, vs, ok_, ov)) return unusual();
+  at::ScalarType t;
+  if (!out_type(ok_, a[8], ks ? kF16 : kc->scalar_type(), &t) || !paged(kc, vc, ks, vs, t)) return unusual();
+  const int64_t H = kc->size(1), D = kc->size(3);
+  if (table->dim() != 2 || !fits(table->size(0)) || !fits(table->size(1)) || !dense(table, at::kInt, table->sizes()) || !dense(cu, at::kInt, {table->size(0) + 1}) ||
+      (given && (!dense(ok_, t, {T, H, D}) || !dense(ov, t, {T, H, D}))))
+    return unusual();
+  at::Tensor mk, mv;
+  if (!given) {
+    const auto options = kc->options().dtype(t);
+    mk = at::empty({T, H, D}, options);
+    mv = at::empty({T, H, D}, options);
+  }
+  const int rc = call(pq.kv_read, static_cast<const void*>(kc.ptr()), static_cast<const void*>(vc.ptr()), floats(ks), floats(vs), kc->size(0),
+                      static_cast<int>(kc->size(2)), ints(table), static_cast<int>(table->size(1)), ints(cu), static_cast<int>(table->size(0)), T,
+                      static_cast<int>(H), static_cast<int>(D), static_cast<uint16_t*>(given ? ok_.ptr() : mk.data_ptr()),
+                      static_cast<uint16_t*>(given ? ov.ptr() : mv.data_ptr()), type_code(t), d.stream());
+  if (!ok("pq_kv_read", rc)) return nullptr;
+  if (given) {
+    Py_INCREF(a[7]);
+    return a[7];
+  }
+  return pair(THPVariable_Wrap(mk), THPVariable_Wrap(mv));
+  END_HANDLE_TH_ERRORS
+}
+
+// attn_decode(q, k_cache, v_cache, block_table, lengths, k_scale, v_scale, scale, out, dtype, workspace)
+PyObject* attn_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 11) return unusual();
+  const Arg q(a[0]), kc(a[1]), vc(a[2]), table(a[3]), lens(a[4]), ks(a[5]), vs(a[6]), out(a[8]), ws(a[10]);
+  Device d;
+  if (!q || !kc || !vc || !table || !lens || !all_on(d, q, kc, vc, table, lens, ks, vs, out, ws) || q->dim() != 3) return unusual();
+  const at::ScalarType t = q->scalar_type();
+  const int64_t B = q->size(0), H = q->size(1), D = q->size(2);
+  float scale;
+  at::ScalarType ot;
+  if (!half_type(t) || !fits(B) || !fits(H) || !heads(q, t, B, H, D) || !paged(kc, vc, ks, vs, t) || kc->size(3) != D || kc->size(1) == 0 ||
+      H % kc->size(1) || table->dim() != 2 || !fits(table->size(1)) || !dense(table, at::kInt, {B, table->size(1)}) || !dense(lens, at::kInt, {B}) ||
+      !get_scale(a[7], D, &scale) || !out_type(out, a[9], t, &ot) || (out && !dense(out, ot, {B, H, D})))
+    return unusual();
+  const int Hkv = static_cast<int>(kc->size(1));
+  const size_t need = pq.attn_decode_workspace_bytes(static_cast<int>(B), static_cast<int>(H), Hkv, static_cast<int>(D));
+  if (ws && !bytes(ws, need)) return unusual();
+  at::Tensor o, made;
+  if (!out) o = at::empty({B, H, D}, q->options().dtype(ot));
+  if (!ws && need) made = at::empty({static_cast<int64_t>(need)}, q->options().dtype(kU8));
+  const Strides sq = strides(*q.t);
+  const int rc = call(pq.attn_decode, static_cast<const uint16_t*>(q.ptr()), sq.row, sq.head, type_code(t), static_cast<const void*>(kc.ptr()),
+                      static_cast<const void*>(vc.ptr()), floats(ks), floats(vs), kc->size(0), static_cast<int>(kc->size(2)), ints(table),
+                      static_cast<int>(table->size(1)), ints(lens), static_cast<int>(B), static_cast<int>(H), Hkv, static_cast<int>(D), scale,
+                      static_cast<uint16_t*>(out ? out.ptr() : o.data_ptr()), type_code(ot), ws ? ws.ptr() : need ? made.data_ptr() : nullptr,
+                      ws ? static_cast<size_t>(ws->numel()) : need, d.stream());
+  return ok("pq_attn_decode", rc) ? result(a[8], o) : nullptr;
+  END_HANDLE_TH_ERRORS
+}
+
+// attn_prefill(q, k, v, cu_q, cu_k, scale, causal, out, dtype, workspace)
+PyObject* attn_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 10 || !PyBool_Check(a[6])) return unusual();
+  const Arg q(a[0]), k(a[1]), v(a[2]), cu_q(a[3]), cu_k(a[4] == Py_None ? a[3] : a[4]), out(a[7]), ws(a[9]);
+  Device d;
+  if (!q || !k || !v || !cu_q || !cu_k || !all_on(d, q, k, v, cu_q, cu_k, out, ws) || q->dim() != 3 || k->dim() != 3 || cu_q->dim() != 1) return unusual();
+  const at::ScalarType t = q->scalar_type();
+  const int64_t Tq = q->size(0), H = q->size(1), D = q->size(2), Tk = k->size(0), Hkv = k->size(1), B = cu_q->size(0) - 1;
+  float scale;
+  at::ScalarType ot;
+  if (!half_type(t) || !fits(Tq) || !fits(Tk) || !fits(H) || !fits(B) || Hkv == 0 || H % Hkv || !heads(q, t, Tq, H, D) || !heads(k, t, Tk, Hkv, D) ||
+      !heads(v, t, Tk, Hkv, D) || !dense(cu_q, at::kInt, {B + 1}) || !dense(cu_k, at::kInt, {B + 1}) || !get_scale(a[5], D, &scale) ||
+      !out_type(out, a[8], t, &ot) || (out && !dense(out, ot, {Tq, H, D})))
+    return unusual();
+  const size_t need = pq.attn_prefill_workspace_bytes(static_cast<int>(B), static_cast<int>(Tq), static_cast<int>(Tk), static_cast<int>(H),
+                                                      static_cast<int>(Hkv), static_cast<int>(D));
+  if (ws && !bytes(ws, need)) return unusual();
+  at::Tensor o, made;
+  if (!out) o = at::empty({Tq, H, D}, q->options().dtype(ot));
+  if (!ws && need) made = at::empty({static_cast<int64_t>(need)}, q->options().dtype(kU8));
+  const Strides sq = strides(*q.t), sk = strides(*k.t), sv = strides(*v.t);
+  const int rc = call(pq.attn_prefill, static_cast<const uint16_t*>(q.ptr()), sq.row, sq.head, static_cast<const uint16_t*>(k.ptr()), sk.row, sk.head,
+                      static_cast<const uint16_t*>(v.ptr()), sv.row, sv.head, type_code(t), ints(cu_q), ints(cu_k), static_cast<int>(B),
+                      static_cast<int>(Tq), static_cast<int>(Tk), static_cast<int>(H), static_cast<int>(Hkv), static_cast<int>(D), scale,
+                      a[6] == Py_True ? 1 : 0, static_cast<uint16_t*>(out ? out.ptr() : o.data_ptr()), type_code(ot),
+                      ws ? ws.ptr() : need ? made.data_ptr() : nullptr, ws ? static_cast<size_t>(ws->numel()) : need, d.stream());
+  return ok("pq_attn_prefill", rc) ? result(a[7], o) : nullptr;
+  END_HANDLE_TH_ERRORS
+}
+
+// bind(check, abi_version, rotate, matvec, gemm_glu, block_norms, packed_weight_bytes, gemm_workspace_bytes, kv_write, kv_read, attn_decode,
+// attn_prefill, attn_decode_workspace_bytes, attn_prefill_workspace_bytes): addresses, of a library of this ABI version. The signatures
+// are the ones that pq.h had when this file was compiled, so another version raises.
 PyObject* bind(PyObject*, PyObject* args) {
-  unsigned long long f[6];
+  unsigned long long f[12];
   PyObject* c;
   int version;
-  if (!PyArg_ParseTuple(args, "OiKKKKKK", &c, &version, f, f + 1, f + 2, f + 3, f + 4, f + 5)) return nullptr;
+  if (!PyArg_ParseTuple(args, "OiKKKKKKKKKKKK", &c, &version, f, f + 1, f + 2, f + 3, f + 4, f + 5, f + 6, f + 7, f + 8, f + 9, f + 10, f + 11)) return nullptr;
   if (version != PQ_ABI_VERSION) {
     PyErr_Format(PyExc_ImportError, "compiled for ABI version %d of the library, which has %d", PQ_ABI_VERSION, version);
     return nullptr;
@@ -306,6 +466,12 @@ PyObject* bind(PyObject*, PyObject* args) {
   pq.block_norms = reinterpret_cast<decltype(pq.block_norms)>(f[3]);
   pq.packed_weight_bytes = reinterpret_cast<decltype(pq.packed_weight_bytes)>(f[4]);
   pq.gemm_workspace_bytes = reinterpret_cast<decltype(pq.gemm_workspace_bytes)>(f[5]);
+  pq.kv_write = reinterpret_cast<decltype(pq.kv_write)>(f[6]);
+  pq.kv_read = reinterpret_cast<decltype(pq.kv_read)>(f[7]);
+  pq.attn_decode = reinterpret_cast<decltype(pq.attn_decode)>(f[8]);
+  pq.attn_prefill = reinterpret_cast<decltype(pq.attn_prefill)>(f[9]);
+  pq.attn_decode_workspace_bytes = reinterpret_cast<decltype(pq.attn_decode_workspace_bytes)>(f[10]);
+  pq.attn_prefill_workspace_bytes = reinterpret_cast<decltype(pq.attn_prefill_workspace_bytes)>(f[11]);
   Py_RETURN_NONE;
 }
 
@@ -315,6 +481,10 @@ PyMethodDef methods[] = {{"bind", bind, METH_VARARGS, nullptr},
                          {"matvec", PQ_FAST(matvec), nullptr},
                          {"gemm_glu", PQ_FAST(gemm_glu), nullptr},
                          {"block_norms", PQ_FAST(block_norms), nullptr},
+                         {"kv_write", PQ_FAST(kv_write), nullptr},
+                         {"kv_read", PQ_FAST(kv_read), nullptr},
+                         {"attn_decode", PQ_FAST(attn_decode), nullptr},
+                         {"attn_prefill", PQ_FAST(attn_prefill), nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
