@@ -39,7 +39,7 @@ struct PrefillArgs {
   float scale_log2;
   uint16_t* o;
   int out_type;
-  int line;      // places for a head's items, or with `pieces` for the pieces of its items
+  int items;     // places for a head's items
   int pieces;    // pieces that a head's key tiles are cut into, about; 0: items are whole
   float* ws;
 };
@@ -47,7 +47,7 @@ struct PrefillArgs {
 // What a workgroup works on: rows r0 .. of a sequence whose queries start at q0 (nq of them) and keys at k0 (nk of them), and of the
 // items' key tiles the `piece`th of `pieces` parts.
 struct PrefillItem {
-  int r0, q0, nq, k0, nk, piece, pieces;
+  int r0, q0, nq, k0, nk, piece, pieces, place;   // place: of the first piece
   __device__ __forceinline__ int shift(bool causal) const { return causal ? nk - nq + 1 : nk; }
   // Keys that row r sees.
   __device__ __forceinline__ int keys(int r, bool causal) const { return causal ? std::max(std::min(nk, r + nk - nq + 1), 0) : nk; }
@@ -115,7 +115,8 @@ struct Sequence {
 //    cost is the number of key blocks of kRows before its end; `from(x)` items cost x or more, and the place's own cost is
 //    found by bisection, a sum over the wave each (packed prompts of 4093 rows: 110 us in the sequences' order, see the kernel).
 //  - More sequences: in their order, each from its end. Pieces: likewise, an item's pieces next to each other.
-template <int kRows, int kKeys>
+//  kItems: `place` counts the items instead.
+template <int kRows, int kKeys, bool kItems = false>
 __device__ __forceinline__ bool find_item(const PrefillArgs& a, int place, PrefillItem* it) {
   const int lane = threadIdx.x & 63;
   auto lane_of = [](int v, int l) { return __builtin_amdgcn_readlane(v, l); };
@@ -136,29 +137,43 @@ __device__ __forceinline__ bool find_item(const PrefillArgs& a, int place, Prefi
     const int mine = a.causal ? (first <= lo && lo < last ? 1 : 0) : first == lo ? n : 0, sum = lanes_scan(mine);
     const int f = __builtin_ctzll(__ballot(sum > rank));
     const int at = a.causal ? lo - lane_of(first, f) : rank - (lane_of(sum, f) - lane_of(mine, f));
-    *it = {at * kRows, lane_of(s.q0, f), lane_of(s.nq, f), lane_of(s.k0, f), lane_of(s.nk, f), 0, 1};
+    *it = {at * kRows, lane_of(s.q0, f), lane_of(s.nq, f), lane_of(s.k0, f), lane_of(s.nk, f), 0, 1, place};
     return true;
   }
+  // Pieces: the smallest share of key tiles with which a head's items make no more pieces than wanted (one more would be a round
+  // of workgroups for itself: 512 rows behind 8191 keys, 576 pieces for 512 places 169 us, 480 144), or each stays whole.
   int per = 1;
   if (a.pieces) {
-    int all = 0;
-    for (int b = lane; b < a.B; b += 64) {
-      const Sequence s(a, b);
-      all += (s.nq + kRows - 1) / kRows * ((s.nk + kKeys - 1) / kKeys);
+    const Sequence mine(a, lane);
+    auto parts = [&](const Sequence& s, int share) { return (s.nq + kRows - 1) / kRows * std::max(((s.nk + kKeys - 1) / kKeys + share - 1) / share, 1); };
+    auto count = [&](int share) {
+      int n = parts(mine, share);
+      for (int b = lane + 64; b < a.B; b += 64) n += parts(Sequence(a, b), share);
+      return lanes_total(n);
+    };
+    int lo = kLeastTiles - 1, hi = (a.Tk + kKeys - 1) / kKeys;   // with hi every item is whole; with lo, but for kLeastTiles - 1, too many
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (count(mid) > a.pieces) lo = mid;
+      else hi = mid;
     }
-    per = std::max(kLeastTiles, (lanes_total(all) + a.pieces - 1) / a.pieces);
+    per = hi;
   }
-  int before = 0;
+  int before = 0, places = 0;
   for (int b0 = 0; b0 < a.B; b0 += 64) {
     const Sequence s(a, b0 + lane);
-    const int n = (s.nq + kRows - 1) / kRows, np = a.pieces ? std::max(((s.nk + kKeys - 1) / kKeys + per - 1) / per, 1) : 1, sum = lanes_scan(n * np);
+    const int n = (s.nq + kRows - 1) / kRows, np = a.pieces ? std::max(((s.nk + kKeys - 1) / kKeys + per - 1) / per, 1) : 1;
+    const int mine = kItems ? n : n * np, sum = lanes_scan(mine), all = kItems ? lanes_scan(n * np) : sum;
     const uint64_t here = __ballot(before + sum > place);
     if (here) {
-      const int f = __builtin_ctzll(here), parts = lane_of(np, f), in = place - before - (lane_of(sum, f) - lane_of(n, f) * parts);
-      *it = {(lane_of(n, f) - 1 - in / parts) * kRows, lane_of(s.q0, f), lane_of(s.nq, f), lane_of(s.k0, f), lane_of(s.nk, f), in % parts, parts};
+      const int f = __builtin_ctzll(here), parts = lane_of(np, f), in = place - before - (lane_of(sum, f) - lane_of(mine, f));
+      const int item = kItems ? in : in / parts;
+      *it = {(lane_of(n, f) - 1 - item) * kRows, lane_of(s.q0, f), lane_of(s.nq, f), lane_of(s.k0, f), lane_of(s.nk, f), kItems ? 0 : in % parts, parts,
+             places + lane_of(all, f) - lane_of(n, f) * parts + item * parts};
       return true;
     }
     before += lane_of(sum, 63);
+    places += lane_of(all, 63);
   }
   return false;
 }
@@ -174,6 +189,14 @@ __device__ __forceinline__ void head_and_place(const PrefillArgs& a, int block, 
     *hq = block % a.Hq;
     *place = block / a.Hq;
   }
+}
+
+__device__ __forceinline__ int block_of(const PrefillArgs& a, int hq, int place) {
+  if (a.Hq % 8 == 0) {
+    const int per = a.Hq / 8;
+    return 8 * (place * per + hq % per) + hq / per;
+  }
+  return place * a.Hq + hq;
 }
 
 template <int D, bool kBf16>
@@ -394,42 +417,43 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(PrefillArgs a) {
   }
 }
 
-// The pieces of 32 rows of an item together: thread (row, part) takes the 16-byte chunks part, part + 8, ... of its row.
+// The pieces of 16 rows of an item together: thread (row, part) takes the 16-byte chunks part, part + 16, ... of its row.
+constexpr int kJoinRows = 16;
 template <int D, bool kBf16>
 __global__ __launch_bounds__(256) void attn_prefill_join_kernel(PrefillArgs a) {
   using Tile = PrefillTile<D>;
-  constexpr int kGroups = Tile::kRows / 32;
+  constexpr int kGroups = Tile::kRows / kJoinRows, kEach = D / 64;
   __shared__ uint32_t odd;
-  int hq, place;
-  head_and_place(a, blockIdx.x / kGroups, &hq, &place);
+  const int hq = blockIdx.x / kGroups % a.Hq;
   PrefillItem it;
-  if (!find_item<Tile::kRows, Tile::kKeys>(a, place, &it)) return;
-  if (it.pieces == 1 || it.piece) return;     // the first piece's place stands for the item
-  const int n = threadIdx.x & 31, part = threadIdx.x >> 5, in = 32 * (blockIdx.x % kGroups) + n, row = it.r0 + in;
-  if (it.r0 + in - n >= it.nq) return;
+  if (!find_item<Tile::kRows, Tile::kKeys, true>(a, blockIdx.x / kGroups / a.Hq, &it) || it.pieces == 1) return;
+  const int n = threadIdx.x % kJoinRows, part = threadIdx.x / kJoinRows, in = kJoinRows * (blockIdx.x % kGroups) + n, row = it.r0 + in;
+  if (row - n >= it.nq) return;
   if (threadIdx.x == 0) odd = 0;
   __syncthreads();
-  // a head's places are workgroups 8 Hq / 8 apart, or Hq: Hq either way
-  auto slot = [&](int i) { return a.ws + (static_cast<int64_t>(blockIdx.x / kGroups) + static_cast<int64_t>(i) * a.Hq) * Tile::kSlot; };
+  const float* const first = a.ws + static_cast<int64_t>(block_of(a, hq, it.place)) * Tile::kSlot;   // a head's places are Hq workgroups apart
+  auto slot = [&](int i) { return first + static_cast<int64_t>(i) * a.Hq * Tile::kSlot; };
   auto state = [&](int i) { return *reinterpret_cast<const float2*>(slot(i) + D * Tile::kRows + 2 * in); };
   float most = -__builtin_inff();
+#pragma unroll 4
   for (int i = 0; i < it.pieces; ++i) most = __builtin_fmaxf(most, state(i).x);
   float sum = 0.0f;
-  float4 v[D / 32] = {};
+  float4 v[kEach] = {};
+#pragma unroll 4
   for (int i = 0; i < it.pieces; ++i) {
     const float2 st = state(i);
     const float f = st.x == -__builtin_inff() ? (st.y == st.y ? 0.0f : st.y) : __builtin_amdgcn_exp2f(st.x - most);
     sum += f * st.y;
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
-      const float4 u = *reinterpret_cast<const float4*>(slot(i) + (8 * c + part) * 4 * Tile::kRows + 4 * in);
+    for (int c = 0; c < kEach; ++c) {
+      const float4 u = *reinterpret_cast<const float4*>(slot(i) + (16 * c + part) * 4 * Tile::kRows + 4 * in);
       v[c].x += f * u.x, v[c].y += f * u.y, v[c].z += f * u.z, v[c].w += f * u.w;
     }
   }
   const int seen = it.keys(std::min(row, it.nq - 1), a.causal);
   float t = sum > 0.0f ? 0.0f : __builtin_nanf("");
 #pragma unroll
-  for (int c = 0; c < D / 32; ++c) t += 0.0f * v[c].x + 0.0f * v[c].y + 0.0f * v[c].z + 0.0f * v[c].w;
+  for (int c = 0; c < kEach; ++c) t += 0.0f * v[c].x + 0.0f * v[c].y + 0.0f * v[c].z + 0.0f * v[c].w;
   if (row < it.nq && seen > 0 && !(t == 0.0f)) atomicOr(&odd, 1u << n);
   __syncthreads();
   const uint32_t again = odd;
@@ -437,43 +461,43 @@ __global__ __launch_bounds__(256) void attn_prefill_join_kernel(PrefillArgs a) {
     const float inv = seen > 0 ? 1.0f / sum : 0.0f;
     uint16_t* out = a.o + (static_cast<int64_t>(it.q0 + row) * a.Hq + hq) * D;
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c)
-      *reinterpret_cast<uint2*>(out + 4 * (8 * c + part)) = pack4(a.out_type, v[c].x * inv, v[c].y * inv, v[c].z * inv, v[c].w * inv);
+    for (int c = 0; c < kEach; ++c)
+      *reinterpret_cast<uint2*>(out + 4 * (16 * c + part)) = pack4(a.out_type, v[c].x * inv, v[c].y * inv, v[c].z * inv, v[c].w * inv);
   }
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  for (int i = wave; i < 32; i += 4)
+  for (int i = wave; i < kJoinRows; i += 4)
     if (again >> i & 1) attend_row<D, kBf16>(a, it.q0 + row - n + i, hq, it.k0, it.keys(row - n + i, a.causal));
 }
 
-// Whether the keys are cut, and the places of a head's line: an item for every kRows queries of a sequence, and when they are cut one
-// more place for every piece. Cut where the items are fewer than the workgroups that the device holds (two a CU) and a row may see more
-// than kWholeKeys keys.
+// The most items that a head can have, an item for every kRows queries of a sequence, and the pieces that they are cut into. Cut where the items are fewer than the workgroups that the device holds (two a CU) and a row may see more than
+// kWholeKeys keys.
 constexpr int kWholeKeys = 1024;
 template <int D>
-static void prefill_shape(int B, int Tq, int Tk, int Hq, int* pieces, int64_t* line) {
-  const int64_t items = Tq / PrefillTile<D>::kRows + static_cast<int64_t>(B), room = 2 * cu_count();
-  *pieces = items * Hq < room && Tk > kWholeKeys ? static_cast<int>((room + Hq - 1) / Hq) : 0;
-  *line = items + *pieces;
+static void prefill_shape(int B, int Tq, int Tk, int Hq, int* pieces, int64_t* items) {
+  const int64_t room = 2 * cu_count();
+  *items = Tq / PrefillTile<D>::kRows + static_cast<int64_t>(B);
+  *pieces = *items * Hq < room && Tk > kWholeKeys ? static_cast<int>(room / Hq) : 0;
 }
 template <int D>
 static size_t prefill_workspace(int B, int Tq, int Tk, int Hq) {
   int pieces;
-  int64_t line;
-  prefill_shape<D>(B, Tq, Tk, Hq, &pieces, &line);
-  return pieces ? static_cast<size_t>(line * Hq) * PrefillTile<D>::kSlot * sizeof(float) : 0;
+  int64_t items;
+  prefill_shape<D>(B, Tq, Tk, Hq, &pieces, &items);
+  return pieces ? static_cast<size_t>(std::max<int64_t>(items, pieces) * Hq) * PrefillTile<D>::kSlot * sizeof(float) : 0;
 }
 
 template <int D, bool kBf16>
 static hipError_t prefill_kernels(const PrefillArgs& a, hipStream_t s) {
-  const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(a.line) * a.Hq);
+  const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(std::max(a.items, a.pieces)) * a.Hq);
   const hipError_t e = launch_kernel((attn_prefill_kernel<D, kBf16>), dim3(grid), dim3(64 * PrefillTile<D>::kWaves), 0, s, a);
-  return e != hipSuccess || !a.pieces ? e : launch_kernel((attn_prefill_join_kernel<D, kBf16>), dim3(grid * (PrefillTile<D>::kRows / 32)), dim3(256), 0, s, a);
+  if (e != hipSuccess || !a.pieces) return e;
+  return launch_kernel((attn_prefill_join_kernel<D, kBf16>), dim3(static_cast<unsigned>(a.items * a.Hq) * (PrefillTile<D>::kRows / kJoinRows)), dim3(256), 0, s, a);
 }
 template <int D>
 static hipError_t prefill_launch(PrefillArgs a, int type, hipStream_t s) {
-  int64_t line;
-  prefill_shape<D>(a.B, a.Tq, a.Tk, a.Hq, &a.pieces, &line);
-  a.line = static_cast<int>(line);
+  int64_t items;
+  prefill_shape<D>(a.B, a.Tq, a.Tk, a.Hq, &a.pieces, &items);
+  a.items = static_cast<int>(items);
   return type == PQ_BF16 ? prefill_kernels<D, true>(a, s) : prefill_kernels<D, false>(a, s);
 }
 
