@@ -418,14 +418,14 @@ int pq_block_norms(const void* x_d, int64_t ldx, int x_type, const void* res_d, 
  *   pq_rotate_quant); a row whose s is below 2^-126 counts as zero (codes 0, s 0); one with an infinity or a
  *   NaN gets codes 0 and s NaN. Without scales the 16 bits are copied.
  *   k_d, v_d  f16 or bf16 (type): element i of head h of row t at t ld + h hs + i; ld, hs multiples of 8, 16-byte aligned - the
- *             columns of a merged projection's y, for instance. They overlap no cache.
+ *             columns of a merged projection's y, for instance. Strides up to 2^24. Outputs overlap no input (PQ_ERR_SHAPE).
  *   slots_d   int64 [T]; a negative slot, or one past the cache, writes nothing (padding rows). Two rows of one call with
  *             the same slot leave a mixture of both there.
  * pq_kv_read: the rows of B sequences back, packed: row t belongs to the sequence b with cu[b] <= t < cu[b + 1], its position is
  *   t - cu[b], found through the sequence's page numbers table[b][0..width). y = fl(code * s), one rounding to type.
  *   cu_d      int32 [B + 1], ascending. Rows of no sequence are left as they were. A position past the width, or whose page is
  *             not one of the cache's, reads as zeros.
- *   k_d, v_d  out f16 or bf16 (type; for a 16-bit cache its own) [T, Hkv, D], 16-byte aligned; they overlap no input.
+ *   k_d, v_d  out f16 or bf16 (type; for a 16-bit cache its own) [T, Hkv, D], 16-byte aligned; they overlap no input (PQ_ERR_SHAPE).
  */
 int pq_kv_write(const uint16_t* k_d, int64_t ldk, int64_t hsk, const uint16_t* v_d, int64_t ldv, int64_t hsv, int type, int T, int Hkv,
                 int D, const int64_t* slots_d, void* kc_d, void* vc_d, float* ks_d, float* vs_d, int64_t pages, int page,
@@ -449,8 +449,10 @@ int pq_kv_read(const void* kc_d, const void* vc_d, const float* ks_d, const floa
  *   cu_q_d, cu_k_d  int32 [B + 1], ascending; values past Tq and Tk count as those. Rows of o of no sequence are left as they were.
  *   o_d       out f16 or bf16 (out_type) [Tq, Hq, D], 16-byte aligned.
  *
- * scale > 0 and finite. Outputs overlap no input. ws_d: at least pq_attn_*_workspace_bytes(), 16-byte aligned; its
- * contents need no initialisation and are not kept, so calls that may run at the same time take one each.
+ * 0 < scale <= 2^64. Outputs and the workspace overlap no input and each other (PQ_ERR_SHAPE). ws_d: at least pq_attn_*_workspace_bytes(),
+ * 16-byte aligned (may be NULL where that is 0); its contents need no initialisation and are not kept, so calls that may run at the same
+ * time take one each. The order of a row's sums depends on the lengths of all sequences, and its last bits in a prompt on
+ * the rows beside it: the same call gives the same bits.
  * Errors: PQ_ERR_SHAPE, PQ_ERR_NULL, PQ_ERR_ALIGN, PQ_ERR_WORKSPACE, PQ_ERR_DEVICE.
  */
 size_t pq_attn_decode_workspace_bytes(int B, int Hq, int Hkv, int D);

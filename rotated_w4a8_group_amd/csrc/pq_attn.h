@@ -7,6 +7,7 @@
 namespace pq {
 
 constexpr int kAttnMaxHeads = 1 << 16;
+constexpr float kAttnMaxScale = 0x1p64f;
 constexpr int64_t kAttnMaxStride = 1ll << 24;   // elements: 64 rows stay within 32-bit offsets
 
 typedef uint32_t attn_u32x4 __attribute__((ext_vector_type(4)));
@@ -165,8 +166,19 @@ __device__ __forceinline__ void store_row(uint16_t* out, const RowState<D>& r, b
   }
 }
 
+// Bytes that T rows of H heads reach over from their first element on.
+inline int64_t heads_span(int64_t ld, int64_t hs, int64_t T, int64_t H, int64_t D) { return T <= 0 ? 0 : 2 * ((T - 1) * ld + (H - 1) * hs + D); }
+// Whether two ranges of bytes have one in common; an output shares none with an input.
+inline bool ranges_meet(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return na > 0 && nb > 0 && p < q + static_cast<uintptr_t>(nb) && q < p + static_cast<uintptr_t>(na);
+}
+inline int overlap(const char* what) { return set_error(PQ_ERR_SHAPE, "%s: an output overlaps an input or another output", what); }
+
 // Checks shared by the entry points: PQ_OK, or an error code with its message.
 int check_cache(const char* what, const void* kc, const void* vc, const float* ks, const float* vs, int64_t pages, int page, int Hkv, int D);
+int64_t cache_bytes(const float* scales, int64_t pages, int page, int Hkv, int D);
+int64_t scale_bytes(const float* scales, int64_t pages, int page, int Hkv);
 int check_heads(const char* what, const char* name, const void* p, int64_t ld, int64_t hs, int T, int H, int D);
 inline int check_attention(const char* what, int type, int out_type, int Hq, int Hkv, int D, float scale) {
   if ((type != PQ_F16 && type != PQ_BF16) || (out_type != PQ_F16 && out_type != PQ_BF16))
@@ -174,7 +186,7 @@ inline int check_attention(const char* what, int type, int out_type, int Hq, int
   if (D != 64 && D != 128 && D != 256) return set_error(PQ_ERR_SHAPE, "%s: head size D=%d must be 64, 128 or 256", what, D);
   if (Hkv <= 0 || Hkv > kAttnMaxHeads || Hq <= 0 || Hq > kAttnMaxHeads || Hq % Hkv)
     return set_error(PQ_ERR_SHAPE, "%s: Hq=%d must be a multiple of Hkv=%d, both in 1..%d", what, Hq, Hkv, kAttnMaxHeads);
-  if (!(scale > 0.0f) || !(scale < __builtin_inff())) return set_error(PQ_ERR_SHAPE, "%s: scale must be positive and finite", what);
+  if (!(scale > 0.0f) || !(scale <= kAttnMaxScale)) return set_error(PQ_ERR_SHAPE, "%s: scale must be positive, at most 2^64", what);
   return PQ_OK;
 }
 

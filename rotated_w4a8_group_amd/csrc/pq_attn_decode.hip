@@ -17,6 +17,7 @@
 // workspace, and attn_join_kernel puts the pieces together in their order. Which pieces exist follows from the lengths on
 // the device; the host only bounds them.
 #include <algorithm>
+#include <utility>
 
 #include "pq_attn.h"
 
@@ -37,7 +38,7 @@ struct DecodeArgs {
 };
 
 constexpr int kTileKeys = 32;
-constexpr int kLeastTiles = 8;      // of a share
+constexpr int kLeastTiles = 8;      // of a piece (1 x 2048 of 8 heads: 10.5 us, with 4 9.2, with 16 14; 17 sequences of 4 wide heads 17.4, 20.0, 18.8)
 constexpr int kTableHalves = 128;   // 16-key halves whose pages a wave holds at a time
 constexpr int kMostPieces = 4096;   // of one head
 
@@ -494,9 +495,6 @@ __global__ __launch_bounds__(256) void attn_join_kernel(DecodeArgs a) {
   *reinterpret_cast<uint2*>(out + 4 * lane) = pack4(a.out_type, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
 }
 
-// Up to this many positions a sequence's head stays in one workgroup, and no join follows.
-constexpr int kWholeLength = 1024;
-
 // Pieces that the line is cut into: so many that those workgroups that get their data later than others get fewer, and few enough
 // for the join. (64 ragged sequences of up to 8192, 16-bit, two workgroups a CU: 2, 4, 6, 8 pieces a CU 191, 178, 184, 184 us; one
 // of 131071, e4m3, four a CU: 4, 8, 12, 16 pieces 53.7, 58.9, 64, 67.)
@@ -516,7 +514,11 @@ template <int D, bool kBf16, bool kQuant>
 static hipError_t decode_launch(DecodeArgs a, hipStream_t s) {
   const int length = a.c.width << a.c.page_shift;
   const int64_t heads = static_cast<int64_t>(a.B) * a.hv;
-  if (length <= kWholeLength)
+  // A head stays in one workgroup, and no join follows, while a wide one's waves have two tiles each (1 x 1000 of 8 heads of 128, e4m3:
+  // 10.5 us, cut 10.8; 1 x 1000 of 4 of 256, 16-bit, four waves: 24.7, cut 16.8; 8 x 1000 of 8 of 128, 16-bit, eight waves: 13.1, cut
+  // 11.5; 1 x 2000, e4m3: 16.5, cut 11.0), or where there are heads enough to fill the device with (128 x 2000 of 8 heads: 56,
+  // cut 62.8) and none takes so long that the others' end leaves it alone.
+  if (length <= (heads >= wanted_pieces() ? 2048 : 2 * kTileKeys * DecodeTile<D, kQuant, true>::kWaves))
     return heads <= cu_count() ? decode_kernel<D, kBf16, kQuant, true>(a, heads, s) : decode_kernel<D, kBf16, kQuant, false>(a, heads, s);
   a.pieces = wanted_pieces();
   const int64_t most = heads * ((length + kTileKeys * kLeastTiles - 1) / (kTileKeys * kLeastTiles));
@@ -563,6 +565,12 @@ int pq_attn_decode(const uint16_t* q_d, int64_t ldq, int64_t hsq, int type, cons
   if (!aligned(o_d, 16) || !aligned(lens_d, 4) || !aligned(table_d, 4) || !aligned(ws_d, 16)) return set_error(PQ_ERR_ALIGN, "%s: misaligned pointer", what);
   const size_t need = pq_attn_decode_workspace_bytes(B, Hq, Hkv, D);
   if (!ws_d || ws_bytes < need) return set_error(PQ_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", what, ws_d ? ws_bytes : 0, need);
+  const int64_t ob = 2ll * B * Hq * D, cb = cache_bytes(ks_d, pages, page, Hkv, D), sb = scale_bytes(ks_d, pages, page, Hkv), qb = heads_span(ldq, hsq, B, Hq, D);
+  for (const auto& [o, n] : {std::pair<const void*, int64_t>{o_d, ob}, {ws_d, static_cast<int64_t>(need)}})
+    if (ranges_meet(o, n, q_d, qb) || ranges_meet(o, n, kc_d, cb) || ranges_meet(o, n, vc_d, cb) || ranges_meet(o, n, ks_d, sb) || ranges_meet(o, n, vs_d, sb) ||
+        ranges_meet(o, n, table_d, 4ll * B * width) || ranges_meet(o, n, lens_d, 4ll * B))
+      return overlap(what);
+  if (ranges_meet(o_d, ob, ws_d, static_cast<int64_t>(need))) return overlap(what);
   DecodeArgs a{{kc_d, vc_d, ks_d, vs_d, table_d, pages, pages ? width : 0, Hkv, __builtin_ctz(page)}, q_d, ldq, hsq, lens_d, B, Hq, G,
                Hkv * tiles_of_heads, tiles_of_heads, 0, scale * 1.44269504088896340736f, o_d, out_type, static_cast<float*>(ws_d)};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);

@@ -21,6 +21,7 @@
 // that need it only. Their values still enter the product, with weight 0: a row whose result is not finite is
 // recomputed key by key (attend_row), so that an infinity or a NaN in a row that it does not see cannot reach it.
 #include <algorithm>
+#include <utility>
 
 #include "pq_attn.h"
 
@@ -79,20 +80,34 @@ struct PrefillTile {
   static __device__ __forceinline__ int vswizzle(int r) { return D == 64 ? ((r >> 1) & 1) << 2 : (r & 3) << 2; }
 };
 
-// One row key by key, exactly as the formula reads: keys j < keys.
+// One row key by key, exactly as the formula reads: keys j < keys, four of them loaded together. A query that is not finite has no
+// finite weight: its result is NaN.
 template <int D, bool kBf16>
 __device__ __forceinline__ void attend_row(const PrefillArgs& a, int64_t t, int hq, int k0, int keys) {
   const int h = hq / (a.Hq / a.Hkv);
-  float q[D / 64], k[D / 64], v[D / 64];
+  float q[D / 64], k[4][D / 64], v[4][D / 64];
   lane_values<D, kBf16>(a.q + t * a.ldq + hq * a.hsq, q);
-  RowState<D> r;
-  for (int j = 0; j < keys; ++j) {
-    lane_values<D, kBf16>(a.k + static_cast<int64_t>(k0 + j) * a.ldk + h * a.hsk, k);
-    lane_values<D, kBf16>(a.v + static_cast<int64_t>(k0 + j) * a.ldv + h * a.hsv, v);
-    float s = 0.0f;
+  float finite = 0.0f;
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) s += q[i] * k[i];
-    r.add(lanes_sum(s), a.scale_log2, v);
+  for (int i = 0; i < D / 64; ++i) finite = __builtin_fmaf(q[i], 0.0f, finite);
+  finite = lanes_sum(finite);
+  RowState<D> r;
+  if (!(finite == 0.0f)) r.l = finite;
+  for (int j0 = 0; j0 < (finite == 0.0f ? keys : 0); j0 += 4) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t row = k0 + std::min(j0 + j, keys - 1);
+      lane_values<D, kBf16>(a.k + row * a.ldk + h * a.hsk, k[j]);
+      lane_values<D, kBf16>(a.v + row * a.ldv + h * a.hsv, v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j0 + j >= keys) break;
+      float s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) s += q[i] * k[j][i];
+      r.add(lanes_sum(s), a.scale_log2, v[j]);
+    }
   }
   store_row<D>(a.o + (t * a.Hq + hq) * D, r, keys > 0, a.out_type);
 }
@@ -530,6 +545,12 @@ int pq_attn_prefill(const uint16_t* q_d, int64_t ldq, int64_t hsq, const uint16_
   if (!aligned(o_d, 16) || !aligned(cu_q_d, 4) || !aligned(cu_k_d, 4) || !aligned(ws_d, 16)) return set_error(PQ_ERR_ALIGN, "%s: misaligned pointer", what);
   const size_t need = pq_attn_prefill_workspace_bytes(B, Tq, Tk, Hq, Hkv, D);
   if (need && (!ws_d || ws_bytes < need)) return set_error(PQ_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", what, ws_d ? ws_bytes : 0, need);
+  const int64_t ob = 2ll * Tq * Hq * D, qb = heads_span(ldq, hsq, Tq, Hq, D), kb = heads_span(ldk, hsk, Tk, Hkv, D), vb = heads_span(ldv, hsv, Tk, Hkv, D);
+  for (const auto& [o, n] : {std::pair<const void*, int64_t>{o_d, ob}, {ws_d, static_cast<int64_t>(need)}})
+    if (ranges_meet(o, n, q_d, qb) || ranges_meet(o, n, k_d, kb) || ranges_meet(o, n, v_d, vb) || ranges_meet(o, n, cu_q_d, 4ll * (B + 1ll)) ||
+        ranges_meet(o, n, cu_k_d, 4ll * (B + 1ll)))
+      return overlap(what);
+  if (ranges_meet(o_d, ob, ws_d, static_cast<int64_t>(need))) return overlap(what);
   PrefillArgs a{q_d, k_d, v_d, ldq, hsq, ldk, hsk, ldv, hsv, cu_q_d, cu_k_d, B, Tq, Tk, Hq, Hkv, causal, scale * 1.44269504088896340736f, o_d, out_type,
                 0, 0, static_cast<float*>(ws_d)};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);

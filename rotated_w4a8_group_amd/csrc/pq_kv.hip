@@ -178,6 +178,9 @@ static hipError_t read_launch(const KvReadArgs& a, int type, hipStream_t s) {
   return read_kernel<D, false, false>(a, s);
 }
 
+int64_t cache_bytes(const float* scales, int64_t pages, int page, int Hkv, int D) { return pages * page * Hkv * D * (scales ? 1 : 2); }
+int64_t scale_bytes(const float* scales, int64_t pages, int page, int Hkv) { return scales ? 4 * pages * page * Hkv : 0; }
+
 int check_cache(const char* what, const void* kc, const void* vc, const float* ks, const float* vs, int64_t pages, int page, int Hkv, int D) {
   if (D != 64 && D != 128 && D != 256) return set_error(PQ_ERR_SHAPE, "%s: head size D=%d must be 64, 128 or 256", what, D);
   if (Hkv <= 0 || Hkv > kAttnMaxHeads) return set_error(PQ_ERR_SHAPE, "%s: Hkv=%d must be in 1..%d", what, Hkv, kAttnMaxHeads);
@@ -220,6 +223,14 @@ int pq_kv_write(const uint16_t* k_d, int64_t ldk, int64_t hsk, const uint16_t* v
   if (!slots_d) return set_error(PQ_ERR_NULL, "%s: slots is NULL", what);
   if (!aligned(slots_d, 8)) return set_error(PQ_ERR_ALIGN, "%s: slots must be 8-byte aligned", what);
   if (pages == 0) return PQ_OK;   // no slot exists
+  const int64_t cb = cache_bytes(ks_d, pages, page, Hkv, D), sb = scale_bytes(ks_d, pages, page, Hkv), kb = heads_span(ldk, hsk, T, Hkv, D), vb = heads_span(ldv, hsv, T, Hkv, D);
+  const void* const out[4] = {kc_d, vc_d, ks_d, vs_d};
+  const int64_t size[4] = {cb, cb, sb, sb};
+  for (int i = 0; i < 4; ++i) {
+    if (ranges_meet(out[i], size[i], k_d, kb) || ranges_meet(out[i], size[i], v_d, vb) || ranges_meet(out[i], size[i], slots_d, 8ll * T)) return overlap(what);
+    for (int j = 0; j < i; ++j)
+      if (ranges_meet(out[i], size[i], out[j], size[j])) return overlap(what);
+  }
   KvWriteArgs a{{k_d, v_d}, {ldk, ldv}, {hsk, hsv}, {kc_d, vc_d}, {ks_d, vs_d}, slots_d, pages * page, T, Hkv, __builtin_ctz(page)};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const unsigned g = static_cast<unsigned>(grid);
@@ -240,6 +251,12 @@ int pq_kv_read(const void* kc_d, const void* vc_d, const float* ks_d, const floa
   if (T == 0 || B == 0) return PQ_OK;
   if (!k_d || !v_d || !cu_d || (width && !table_d)) return set_error(PQ_ERR_NULL, "%s: NULL pointer", what);
   if (!aligned(k_d, 16) || !aligned(v_d, 16) || !aligned(cu_d, 4) || !aligned(table_d, 4)) return set_error(PQ_ERR_ALIGN, "%s: misaligned pointer", what);
+  const int64_t cb = cache_bytes(ks_d, pages, page, Hkv, D), sb = scale_bytes(ks_d, pages, page, Hkv), ob = 2ll * T * Hkv * D;
+  for (const void* o : {static_cast<const void*>(k_d), static_cast<const void*>(v_d)})
+    if (ranges_meet(o, ob, kc_d, cb) || ranges_meet(o, ob, vc_d, cb) || ranges_meet(o, ob, ks_d, sb) || ranges_meet(o, ob, vs_d, sb) ||
+        ranges_meet(o, ob, table_d, 4ll * B * width) || ranges_meet(o, ob, cu_d, 4ll * (B + 1ll)))
+      return overlap(what);
+  if (ranges_meet(k_d, ob, v_d, ob)) return overlap(what);
   KvReadArgs a{{kc_d, vc_d, ks_d, vs_d, table_d, pages, width, Hkv, __builtin_ctz(page)}, cu_d, B, T, {k_d, v_d}};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   return launch_status(what, D == 64 ? read_launch<64>(a, type, s) : D == 128 ? read_launch<128>(a, type, s) : read_launch<256>(a, type, s));

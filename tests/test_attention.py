@@ -47,7 +47,9 @@ def _decode(**kw):
     (dict(page=48), -2), (dict(pages=-1), -2), (dict(ldq=6148), -2), (dict(hsq=4), -2), (dict(ldq=-8), -2),
     (dict(q=None), -1), (dict(o=None), -1), (dict(lens=None), -1), (dict(table=None), -1), (dict(ks=None), -1), (dict(vc=None), -1),
     (dict(q=FAKE + 2), -3), (dict(o=FAKE + 8), -3), (dict(lens=FAKE + 2), -3), (dict(table=FAKE + 2), -3), (dict(kc=FAKE + 8), -3),
-    (dict(B=2**31 - 1), -2), (dict(B=0), 0), (dict(B=0, q=None, o=None, ws=None, wsb=0), 0),
+    (dict(B=2**31 - 1), -2), (dict(B=0), 0), (dict(B=0, q=None, o=None, ws=None, wsb=0), 0), (dict(scale=2.0**65), -2), (dict(scale=3e38), -2),
+    (dict(o=FAKE), -2), (dict(o=FAKE + (1 << 24) + 16), -2), (dict(o=FAKE + (4 << 24)), -2), (dict(o=FAKE + (6 << 24)), -2), (dict(o=FAKE + (8 << 24)), -2),
+    (dict(ws=FAKE + (1 << 24)), -2), (dict(o=FAKE + 2 * (6144 + 47 * 128 + 128) - 16), -2),
 ])
 def test_decode_refusals(kw, code):
     assert _decode(**kw) == code
@@ -67,7 +69,9 @@ def _prefill(**kw):
     (dict(scale=0.0), -2), (dict(scale=float("nan")), -2), (dict(ldq=8196), -2), (dict(hsk=2), -2), (dict(ldv=-8), -2), (dict(ldk=2**31), -2),
     (dict(q=None), -1), (dict(k=None), -1), (dict(v=None), -1), (dict(o=None), -1), (dict(cu_q=None), -1), (dict(cu_k=None), -1),
     (dict(q=FAKE + 8), -3), (dict(k=FAKE + 2), -3), (dict(v=FAKE + 4), -3), (dict(o=FAKE + 8), -3), (dict(cu_q=FAKE + 1), -3),
-    (dict(Tq=2**31 - 1), -2), (dict(Tq=0), 0), (dict(B=0), 0), (dict(Tq=0, q=None, o=None), 0),
+    (dict(Tq=2**31 - 1), -2), (dict(Tq=0), 0), (dict(B=0), 0), (dict(Tq=0, q=None, o=None), 0), (dict(scale=2.0**65), -2),
+    (dict(o=FAKE), -2), (dict(o=FAKE + (1 << 24) + 16), -2), (dict(o=FAKE + (2 << 24) - 16), -2), (dict(o=FAKE + (3 << 24)), -2), (dict(o=FAKE + (4 << 24)), -2),
+    (dict(Tk=2000, ws=FAKE + (2 << 24) + 16), -2), (dict(Tk=2000, ws=FAKE + (5 << 24)), -2),
 ])
 def test_prefill_refusals(kw, code):
     assert _prefill(**kw) == code
@@ -256,6 +260,41 @@ def test_prefill_values_that_a_query_does_not_see(kind, D, bad):
         assert bool((seen[:, :, 5][weight].float() == bad).all() | torch.isnan(seen[:, :, 5]).any())
     lens2, sane = [(70, 70), (at, at)], slice(0, 70 + at)
     _check_prompts(o[sane], q[sane], k[sane], v[sane], lens2, 0, True, D ** -0.5, "unseen")
+
+
+@gpu
+@pytest.mark.parametrize("nk", [70, 3000])
+def test_prefill_queries_that_are_not_finite(nk):
+    """NaN and infinities in a query make its own row NaN, and no other one."""
+    g = torch.Generator().manual_seed(12)
+    lens = [(70, nk), (40, 40)]
+    q, k, v, cu_q, cu_k = _prompts(g, lens, 2, 1, 128, BF16)
+    q[5, 0, 7], q[33, 1, 0], q[64] = math.nan, math.inf, -math.inf
+    o = pq.attn_prefill(q, k, v, cu_q, cu_k)
+    bad = torch.zeros(o.shape[:2], dtype=torch.bool, device="cuda")
+    bad[5, 0] = bad[33, 1] = bad[64, 0] = bad[64, 1] = True
+    assert bool(torch.isnan(o[bad]).all()) and bool(torch.isfinite(o[~bad]).all())
+    # the others within their tolerance (their last bits may differ: rows of a wave raise what their weights are taken against together)
+    at = kat = 0
+    for nq, n in lens:
+        visible = torch.ones((nq, n), dtype=torch.bool, device="cuda").tril(n - nq)
+        for h in range(2):
+            good = ~bad[at:at + nq, h]
+            ref = _reference(q[at:at + nq, h][good].double(), k[kat:kat + n, 0].double(), v[kat:kat + n, 0].double(), 128 ** -0.5, visible[good])
+            _check(o[at:at + nq, h][good], ref, n, 128, BF16, E[BF16], f"beside queries that are not finite, head {h}")
+        at, kat = at + nq, kat + n
+
+
+@gpu
+def test_prefill_largest_values():
+    """Values that a weight above 1 would carry past binary32, and scores whose maximum keeps rising along the keys."""
+    g = torch.Generator().manual_seed(13)
+    T, D = 200, 64
+    q, k, v, cu, _ = _prompts(g, [(T, T)], 2, 1, D, BF16)
+    v *= 1e36
+    k[:, 0, 0] = torch.linspace(-40, 40, T, device="cuda")
+    q[:, :, 0] = 30
+    _check_prompts(pq.attn_prefill(q, k, v, cu), q, k, v, [(T, T)], 0, True, D ** -0.5, "largest values")
 
 
 @gpu

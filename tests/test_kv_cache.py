@@ -30,6 +30,9 @@ def _write(**kw):
     (dict(ks=None), -1), (dict(vs=None), -1), (dict(kc=None), -1), (dict(vc=None), -1), (dict(k=None), -1), (dict(v=None), -1), (dict(slots=None), -1),
     (dict(k=FAKE + 8), -3), (dict(v=FAKE + 2), -3), (dict(kc=FAKE + 8), -3), (dict(vs=FAKE + 2), -3), (dict(slots=FAKE + 4), -3),
     (dict(T=2**31 - 1), -2), (dict(T=0), 0), (dict(T=0, k=None, v=None, slots=None), 0), (dict(pages=0, kc=None, vc=None), 0),
+    # an output over an input, or over another output
+    (dict(kc=FAKE), -2), (dict(vc=FAKE + (1 << 24) - 16), -2), (dict(kc=FAKE + 2 * (3 * 1024 + 1024) - 16), -2), (dict(vc=FAKE + (3 << 24) + 16), -2),
+    (dict(ks=FAKE + (3 << 24) + 64), -2), (dict(vs=FAKE + (5 << 24)), -2), (dict(kc=FAKE + (2 << 24)), -2), (dict(ks=FAKE + (2 << 24) + 16), -2),
 ])
 def test_write_refusals(kw, code):
     assert _write(**kw) == code
@@ -48,6 +51,8 @@ def _read(**kw):
     (dict(pages=-5), -2), (dict(ks=None), -1), (dict(kc=None), -1), (dict(table=None), -1), (dict(cu=None), -1), (dict(k=None), -1), (dict(v=None), -1),
     (dict(k=FAKE + 8), -3), (dict(cu=FAKE + 2), -3), (dict(table=FAKE + 1), -3), (dict(vc=FAKE + 4), -3), (dict(T=2**31 - 1), -2),
     (dict(T=0), 0), (dict(B=0), 0),
+    (dict(k=FAKE + 16), -2), (dict(v=FAKE + (2 << 24)), -2), (dict(v=FAKE + (6 << 24)), -2), (dict(k=FAKE + (4 << 24) + 16), -2), (dict(v=FAKE + (5 << 24)), -2),
+    (dict(k=FAKE + (1 << 24) - 2 * 4 * 8 * 128 + 16), -2),
 ])
 def test_read_refusals(kw, code):
     assert _read(**kw) == code
