@@ -59,6 +59,12 @@ __device__ __forceinline__ void decode8(const uint2& c, float (&v)[8]) {
   }
 }
 
+// A direct load of 16 bytes a lane (LDS address uniform, lane i lands 16 i bytes in) of data that is read once: it does not stay
+// in the caches.
+__device__ __forceinline__ void lds_dma16_nt(const void* sbase, uint32_t voff, uint32_t lds) {
+  asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1 nt" ::"v"(voff), "s"(sbase), "{m0}"(lds) : "memory");
+}
+
 // The same number, where the compiler may not know it: what an address takes from it is computed where it is used, a few vector
 // instructions, and not kept in a register for the whole loop.
 __device__ __forceinline__ int opaque(int v) {
@@ -189,6 +195,5 @@ inline int check_attention(const char* what, int type, int out_type, int Hq, int
   if (!(scale > 0.0f) || !(scale <= kAttnMaxScale)) return set_error(PQ_ERR_SHAPE, "%s: scale must be positive, at most 2^64", what);
   return PQ_OK;
 }
-
 
 }  // namespace pq

@@ -127,10 +127,6 @@ __device__ __forceinline__ void lds_dma16_s(const void* sbase, uint32_t voff, ui
 __device__ __forceinline__ void lds_dma4_s(const void* sbase, uint32_t voff, uint32_t lds) {
   asm volatile("s_nop 4\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(sbase), "{m0}"(lds) : "memory");
 }
-// the same for data that is read once: it does not stay in the caches
-__device__ __forceinline__ void lds_dma16_nt(const void* sbase, uint32_t voff, uint32_t lds) {
-  asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1 nt" ::"v"(voff), "s"(sbase), "{m0}"(lds) : "memory");
-}
 // A wave-uniform address in scalar registers, where the compiler computed it on the vector ALU.
 __device__ __forceinline__ const void* scalar_addr(const void* p) {
   const uint64_t a = reinterpret_cast<uint64_t>(p);
