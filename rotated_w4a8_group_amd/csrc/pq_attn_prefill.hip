@@ -60,7 +60,9 @@ __device__ __forceinline__ f32x16 mfma_32(const attn_u32x4& a, const attn_u32x4&
   else return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-constexpr int kLeastTiles = 8;   // key tiles of a piece
+// Key tiles of a piece, at least. (4, 8, 16: 256 rows behind 1280 keys, 24 heads of 128 23.8, 23.3, 26.2 us; 8 heads of 256 25.6, 26.1,
+// 32.6; 64 behind 1500, 12 of 64 15.0, 14.9, 19.2.)
+constexpr int kLeastTiles = 8;
 
 template <int D>
 struct PrefillTile {
@@ -125,36 +127,14 @@ struct Sequence {
   }
 };
 
-// The item at a place of a head's line: false past the last. kRows: queries of an item, kKeys: keys of a tile.
-//  - Up to 64 sequences, whole items: those that see the most keys first, so that no long one begins when the others end. An item's
-//    cost is the number of key blocks of kRows before its end; `from(x)` items cost x or more, and the place's own cost is
-//    found by bisection, a sum over the wave each (packed prompts of 4093 rows: 110 us in the sequences' order, see the kernel).
-//  - More sequences: in their order, each from its end. Pieces: likewise, an item's pieces next to each other.
-//  kItems: `place` counts the items instead.
+// The item at a place of a head's line: false past the last. kRows: queries of an item, kKeys: keys of a tile. Sequence by
+// sequence, each from its end, so that its items that see the most keys begin first, and an item's pieces next to each other. (All
+// items of a head by the keys that they see, found by bisection: 9 packed prompts of 4093 rows 96 us, in this order 92; 40 of 8000 87,
+// 81; 5 of 6000 behind 700 keys each 102, 104.) kItems: `place` counts the items instead of their pieces.
 template <int kRows, int kKeys, bool kItems = false>
 __device__ __forceinline__ bool find_item(const PrefillArgs& a, int place, PrefillItem* it) {
   const int lane = threadIdx.x & 63;
   auto lane_of = [](int v, int l) { return __builtin_amdgcn_readlane(v, l); };
-  if (a.B <= 64 && !a.pieces) {
-    const Sequence s(a, lane);
-    const int n = (s.nq + kRows - 1) / kRows;
-    // cost of the sequence's first item, and of the one past its last (without the mask all cost the same)
-    const int first = a.causal ? std::max(s.nk - s.nq, 0) / kRows : (s.nk + kRows - 1) / kRows, last = a.causal ? first + n : first + 1;
-    auto from = [&](int x) { return lanes_total(a.causal ? std::min(std::max(last - x, 0), n) : last > x ? n : 0); };
-    if (place >= lanes_total(n)) return false;
-    int lo = 0, hi = (a.Tk + kRows - 1) / kRows + (a.Tq + kRows - 1) / kRows + 1;   // from(lo) > place >= from(hi)
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (from(mid) > place) lo = mid;
-      else hi = mid;
-    }
-    const int rank = place - from(lo + 1);
-    const int mine = a.causal ? (first <= lo && lo < last ? 1 : 0) : first == lo ? n : 0, sum = lanes_scan(mine);
-    const int f = __builtin_ctzll(__ballot(sum > rank));
-    const int at = a.causal ? lo - lane_of(first, f) : rank - (lane_of(sum, f) - lane_of(mine, f));
-    *it = {at * kRows, lane_of(s.q0, f), lane_of(s.nq, f), lane_of(s.k0, f), lane_of(s.nk, f), 0, 1, place};
-    return true;
-  }
   // Pieces: the smallest share of key tiles with which a head's items make no more pieces than wanted (one more would be a round
   // of workgroups for itself: 512 rows behind 8191 keys, 576 pieces for 512 places 169 us, 480 144), or each stays whole.
   int per = 1;
@@ -289,7 +269,9 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(PrefillArgs a) {
     const uint8_t* const kt = smem + (j & 1) * 2 * Tile::kPart;
     const uint8_t* const vt = kt + Tile::kPart;
     const int k0 = j * Tile::kKeys;
-    // Operands are read kRead products ahead of their use: an LDS read takes longer than a product.
+    // Operands are read kRead products ahead of their use: an LDS read takes longer than a product. (K and V 2 and 4 ahead, 4 and 6, 8
+    // and 8: 8192 rows of 48 heads of 128 779, 772, 783 us; at 256 channels registers allow 2 and 1 130, 2 and 2 127, 4 and 4, which
+    // spills, 167.)
     constexpr int kProducts = kKB * kSteps, kRead = D == 256 ? 2 : 4;
     f32x16 s[kKB];
     const int ln = kOpaque ? opaque(lane) : lane;
@@ -484,14 +466,16 @@ __global__ __launch_bounds__(256) void attn_prefill_join_kernel(PrefillArgs a) {
     if (again >> i & 1) attend_row<D, kBf16>(a, it.q0 + row - n + i, hq, it.k0, it.keys(row - n + i, a.causal));
 }
 
-// The most items that a head can have, an item for every kRows queries of a sequence, and the pieces that they are cut into. Cut where the items are fewer than the workgroups that the device holds (two a CU) and a row may see more than
-// kWholeKeys keys.
-constexpr int kWholeKeys = 1024;
+// The most items that a head can have, an item for every kRows queries of a sequence, and the pieces that they are cut into. Cut where
+// the items are fewer than the workgroups that the device holds (two a CU) and a row may see more than kWholeTiles key tiles: the
+// join costs what some tiles do. (256 rows behind 1280 keys, 24 heads of 128: whole 32.4 us, cut 23.3; 1000 rows of 16 heads of 128:
+// 23.8, 24.9; 256 behind 768, 8 heads of 256: 43, 24.)
+constexpr int kWholeTiles = 16;
 template <int D>
 static void prefill_shape(int B, int Tq, int Tk, int Hq, int* pieces, int64_t* items) {
   const int64_t room = 2 * cu_count();
   *items = Tq / PrefillTile<D>::kRows + static_cast<int64_t>(B);
-  *pieces = *items * Hq < room && Tk > kWholeKeys ? static_cast<int>(room / Hq) : 0;
+  *pieces = *items * Hq < room && Tk > kWholeTiles * PrefillTile<D>::kKeys ? static_cast<int>(room / Hq) : 0;
 }
 template <int D>
 static size_t prefill_workspace(int B, int Tq, int Tk, int Hq) {
