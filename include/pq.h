@@ -411,7 +411,8 @@ int pq_block_norms(const void* x_d, int64_t ldx, int x_type, const void* res_d, 
 /*
  * The key-value cache of the attention layers (device). A cache is two arrays [pages][Hkv][page][D], keys and values: a head's
  * rows of one page are one contiguous run. With scales (ks_d, vs_d: f32 [pages][Hkv][page], one for each row of a head)
- * it holds e4m3 codes, without them the 16-bit values of `type`. D is 64, 128 or 256, page a power of two in 16..1024.
+ * it holds e4m3 codes, without them the 16-bit values of `type`. D is 64, 128 or 256, page a power of two in 16..1024,
+ * pages * Hkv * page at most 2^40.
  *
  * pq_kv_write: row t, head h of k and v into the place slots[t] = page number * page + row in the page.
  *   s = fl32(max_i |x_i| * fl32(1/448)), code_i = E(fl32(x_i * fl32(1/s))) with the prologue's encoder (the scale of a group of
@@ -445,11 +446,11 @@ int pq_kv_read(const void* kc_d, const void* vc_d, const float* ks_d, const floa
  *   lens_d    int32 [B].
  *   o_d       out f16 or bf16 (out_type) [B, Hq, D], 16-byte aligned.
  * pq_attn_prefill: packed prompts. Sequence b has the queries cu_q[b] .. cu_q[b + 1] - 1 and the keys cu_k[b] .. cu_k[b + 1] - 1
- *   of the Tq and Tk rows; query i of nq sees the keys j <= i + nk - nq (causal != 0) or all nk of them.
+ *   of the Tq and Tk rows (at most 2^30 of each); query i of nq sees the keys j <= i + nk - nq (causal != 0) or all nk of them.
  *   cu_q_d, cu_k_d  int32 [B + 1], ascending; values past Tq and Tk count as those. Rows of o of no sequence are left as they were.
  *   o_d       out f16 or bf16 (out_type) [Tq, Hq, D], 16-byte aligned.
  *
- * 0 < scale <= 2^64. Outputs and the workspace overlap no input and each other (PQ_ERR_SHAPE). ws_d: at least pq_attn_*_workspace_bytes(),
+ * 0 < scale <= 2^64. Outputs and the workspace overlap no input and each other (PQ_ERR_SHAPE). ws_d: at least pq_attn_*_workspace_bytes() of the device in use,
  * 16-byte aligned (may be NULL where that is 0); its contents need no initialisation and are not kept, so calls that may run at the same
  * time take one each. The order of a row's sums depends on the lengths of all sequences, and its last bits in a prompt on
  * the rows beside it: the same call gives the same bits.

@@ -515,7 +515,7 @@ static hipError_t decode_kernel(const DecodeArgs& a, int64_t grid, hipStream_t s
 }
 template <int D, bool kBf16, bool kQuant>
 static hipError_t decode_launch(DecodeArgs a, hipStream_t s) {
-  const int length = a.c.width << a.c.page_shift;
+  const int64_t length = static_cast<int64_t>(a.c.width) << a.c.page_shift;
   const int64_t heads = static_cast<int64_t>(a.B) * a.hv;
   // A head stays in one workgroup, and no join follows, while a wide one's waves have two tiles each (1 x 1000 of 8 heads of 128, e4m3:
   // 10.5 us, cut 10.8; 1 x 1000 of 4 of 256, 16-bit, four waves: 24.7, cut 16.8; 8 x 1000 of 8 of 128, 16-bit, eight waves: 13.1, cut
@@ -561,7 +561,7 @@ int pq_attn_decode(const uint16_t* q_d, int64_t ldq, int64_t hsq, int type, cons
   if (static_cast<int64_t>(width) * page > INT32_MAX)
     return set_error(PQ_ERR_SHAPE, "%s: width=%d pages of %d rows: sequences of at most 2^31 - 1 positions", what, width, page);
   const int G = Hq / Hkv, tiles_of_heads = (G + 15) / 16;
-  if (static_cast<int64_t>(B) * Hkv * tiles_of_heads > INT32_MAX / (static_cast<int64_t>(width) * page / kTileKeys + 1))   // tiles are counted in 32 bits
+  if (static_cast<int64_t>(B) * Hkv * tiles_of_heads > (1 << 30) / (static_cast<int64_t>(width) * page / kTileKeys + 1))   // tiles are counted in 32 bits
     return set_error(PQ_ERR_SHAPE, "%s: B=%d tables of %d pages of %d rows too large for one call", what, B, width, page);
   if (B == 0) return PQ_OK;
   if (!o_d || !lens_d || (width && !table_d)) return set_error(PQ_ERR_NULL, "%s: NULL pointer", what);

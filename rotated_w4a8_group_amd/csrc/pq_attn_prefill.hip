@@ -49,7 +49,6 @@ struct PrefillArgs {
 // items' key tiles the `piece`th of `pieces` parts.
 struct PrefillItem {
   int r0, q0, nq, k0, nk, piece, pieces, place;   // place: of the first piece
-  __device__ __forceinline__ int shift(bool causal) const { return causal ? nk - nq + 1 : nk; }
   // Keys that row r sees.
   __device__ __forceinline__ int keys(int r, bool causal) const { return causal ? std::max(std::min(nk, r + nk - nq + 1), 0) : nk; }
 };
@@ -471,6 +470,7 @@ __global__ __launch_bounds__(256) void attn_prefill_join_kernel(PrefillArgs a) {
 // join costs what some tiles do. (256 rows behind 1280 keys, 24 heads of 128: whole 32.4 us, cut 23.3; 1000 rows of 16 heads of 128:
 // 23.8, 24.9; 256 behind 768, 8 heads of 256: 43, 24.)
 constexpr int kWholeTiles = 16;
+constexpr int kMostRows = 1 << 30;   // of queries, and of keys: their sum stays within 32 bits
 template <int D>
 static void prefill_shape(int B, int Tq, int Tk, int Hq, int* pieces, int64_t* items) {
   const int64_t room = 2 * cu_count();
@@ -522,6 +522,7 @@ int pq_attn_prefill(const uint16_t* q_d, int64_t ldq, int64_t hsq, const uint16_
   if (rc == PQ_OK) rc = check_heads(what, "k", k_d, ldk, hsk, Tk, Hkv, D);
   if (rc == PQ_OK) rc = check_heads(what, "v", v_d, ldv, hsv, Tk, Hkv, D);
   if (rc != PQ_OK) return rc;
+  if (Tq > kMostRows || Tk > kMostRows) return set_error(PQ_ERR_SHAPE, "%s: Tq=%d, Tk=%d: at most 2^30 rows", what, Tq, Tk);
   if ((Tq / 128 + static_cast<int64_t>(B)) * Hq * 256 > 0xFFFFFFFFll)   // the runtime counts a launch's threads in 32 bits
     return set_error(PQ_ERR_SHAPE, "%s: Tq=%d rows of B=%d sequences too many for one call", what, Tq, B);
   if (Tq == 0 || B == 0) return PQ_OK;

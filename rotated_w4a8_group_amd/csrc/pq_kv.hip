@@ -178,6 +178,8 @@ static hipError_t read_launch(const KvReadArgs& a, int type, hipStream_t s) {
   return read_kernel<D, false, false>(a, s);
 }
 
+constexpr int64_t kMostCacheRows = 1ll << 40;   // 70 TB of them: its bytes are counted in 64 bits
+
 int64_t cache_bytes(const float* scales, int64_t pages, int page, int Hkv, int D) { return pages * page * Hkv * D * (scales ? 1 : 2); }
 int64_t scale_bytes(const float* scales, int64_t pages, int page, int Hkv) { return scales ? 4 * pages * page * Hkv : 0; }
 
@@ -187,6 +189,7 @@ int check_cache(const char* what, const void* kc, const void* vc, const float* k
   if (page < 16 || page > 1024 || (page & (page - 1)))
     return set_error(PQ_ERR_SHAPE, "%s: page=%d must be a power of two in 16..1024", what, page);
   if (pages < 0 || pages > INT32_MAX) return set_error(PQ_ERR_SHAPE, "%s: pages=%lld must be in 0..2^31-1", what, static_cast<long long>(pages));
+  if (pages * page * Hkv > kMostCacheRows) return set_error(PQ_ERR_SHAPE, "%s: %lld pages of %d rows and %d heads: at most 2^40 rows of heads", what, static_cast<long long>(pages), page, Hkv);
   if (!ks != !vs) return set_error(PQ_ERR_NULL, "%s: k and v scales go together", what);
   if (pages && (!kc || !vc)) return set_error(PQ_ERR_NULL, "%s: NULL cache", what);
   if (!aligned(kc, 16) || !aligned(vc, 16) || !aligned(ks, 4) || !aligned(vs, 4)) return set_error(PQ_ERR_ALIGN, "%s: misaligned cache", what);

@@ -49,7 +49,7 @@ def _decode(**kw):
     (dict(q=FAKE + 2), -3), (dict(o=FAKE + 8), -3), (dict(lens=FAKE + 2), -3), (dict(table=FAKE + 2), -3), (dict(kc=FAKE + 8), -3),
     (dict(B=2**31 - 1), -2), (dict(B=0), 0), (dict(B=0, q=None, o=None, ws=None, wsb=0), 0), (dict(scale=2.0**65), -2), (dict(scale=3e38), -2),
     (dict(o=FAKE), -2), (dict(o=FAKE + (1 << 24) + 16), -2), (dict(o=FAKE + (4 << 24)), -2), (dict(o=FAKE + (6 << 24)), -2), (dict(o=FAKE + (8 << 24)), -2),
-    (dict(ws=FAKE + (1 << 24)), -2), (dict(o=FAKE + 2 * (6144 + 47 * 128 + 128) - 16), -2),
+    (dict(ws=FAKE + (1 << 24)), -2), (dict(o=FAKE + 2 * (6144 + 47 * 128 + 128) - 16), -2), (dict(pages=2**31 - 1, page=1024), -2),
 ])
 def test_decode_refusals(kw, code):
     assert _decode(**kw) == code
@@ -72,6 +72,7 @@ def _prefill(**kw):
     (dict(Tq=2**31 - 1), -2), (dict(Tq=0), 0), (dict(B=0), 0), (dict(Tq=0, q=None, o=None), 0), (dict(scale=2.0**65), -2),
     (dict(o=FAKE), -2), (dict(o=FAKE + (1 << 24) + 16), -2), (dict(o=FAKE + (2 << 24) - 16), -2), (dict(o=FAKE + (3 << 24)), -2), (dict(o=FAKE + (4 << 24)), -2),
     (dict(Tk=2000, ws=FAKE + (2 << 24) + 16), -2), (dict(Tk=2000, ws=FAKE + (5 << 24)), -2),
+    (dict(Tk=2**30 + 1, ldk=0, ldv=0), -2), (dict(Tq=2**30 + 1, Hq=1, Hkv=1, ldq=0), -2),
 ])
 def test_prefill_refusals(kw, code):
     assert _prefill(**kw) == code

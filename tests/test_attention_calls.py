@@ -76,6 +76,7 @@ def test_sizes_past_31_bits(name):
 @pytest.mark.parametrize("B,width,page,Hq,Hkv,code", [
     (1, 2 ** 21, 1024, 8, 8, -2),            # 2^31 positions
     (2 ** 12, 2 ** 17, 256, 64, 64, -2),     # 2^38 tiles
+    (1, 2 ** 21 - 1, 1024, 32, 32, -2),      # 2^31 tiles, and the pieces' rounding past them
     (2 ** 16, 16, 16, 16, 16, -6),           # passes these checks: the workspace is next
 ])
 def test_decode_tables_that_are_too_large(B, width, page, Hq, Hkv, code):

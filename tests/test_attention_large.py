@@ -78,3 +78,19 @@ def test_rows_past_2_31_elements():
     for got, rows in ((kr, k), (vr, v)):
         codes, s = tk._codes(rows[T - tail:].float().cpu().numpy())
         assert torch.equal(got.cpu(), (torch.from_numpy(codes).view(torch.float8_e4m3fn).float() * torch.from_numpy(s.copy())[..., None]).bfloat16())
+
+
+def test_the_widest_table():
+    """2^31 - 16 positions that a table could hold, a thousand that the sequence has."""
+    width, n, D = 2 ** 27 - 1, 1000, 64
+    g = torch.Generator().manual_seed(3)
+    x = [torch.randn((n, 1, D), generator=g).bfloat16().cuda() for _ in range(2)]
+    cache = [torch.empty((64, 1, 16, D), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    pq.kv_write(*x, torch.arange(n, device="cuda"), *cache)
+    table = torch.full((1, width), -1, dtype=I32, device="cuda")
+    table[0, :64] = torch.arange(64, dtype=I32, device="cuda")
+    q = ta._heads(g, 1, 4, D, torch.bfloat16)
+    o = pq.attn_decode(q, *cache, table, torch.tensor([n], dtype=I32, device="cuda"))
+    ta._check_decode(o, q, [[t.double()] for t in x], [n], D ** -0.5, "widest table")
+    k, v = pq.kv_read(*cache, table, ta._cu([n]), n)
+    assert torch.equal(k, x[0]) and torch.equal(v, x[1])
