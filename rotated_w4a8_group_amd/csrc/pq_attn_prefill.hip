@@ -9,7 +9,9 @@
 //                 the contraction is free, a lane's own 8 are taken as they lie - P never leaves its registers - and V^T
 //                 follows that order: two transposing LDS reads of 4 keys each per 16 keys and 32 channels.
 // Scores, sums and O are binary32. P is rounded to v's type for the second product (half a step of it, 2^-8 or 2^-11 of each
-// weight).
+// weight), which is what the output's own rounding costs. Only where o is f16 and v bf16 would it be the larger by far (6.6e-4 of the norm
+// against 1.9e-4): there P is held in two bf16 pieces (2^-16), each with a product of its own, for 27 to 42 % more time (9 packed
+// prompts 92 -> 117 us, 8192 rows 780 -> 1087, 512 of 256 channels behind 8191 128 -> 167, 4096 rows of 24 heads of 64 69 -> 99).
 //
 // K and V tiles go global -> LDS by direct loads, row-major with the 16-byte chunks of a row permuted (kswizzle, vswizzle) so
 // that the 16 lanes of an operand read, and the 4 keys of a transposing one, lie in different banks.
@@ -193,7 +195,8 @@ __device__ __forceinline__ int block_of(const PrefillArgs& a, int hq, int place)
   return place * a.Hq + hq;
 }
 
-template <int D, bool kBf16>
+// kSplit: the weights in two bf16 pieces, each with a product of its own.
+template <int D, bool kBf16, bool kSplit>
 __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(PrefillArgs a) {
   using Tile = PrefillTile<D>;
   constexpr int kDB = D / 32, kKB = Tile::kKeys / 32, kSteps = D / 16;
@@ -270,7 +273,7 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(PrefillArgs a) {
     const int k0 = j * Tile::kKeys;
     // Operands are read kRead products ahead of their use: an LDS read takes longer than a product. (K and V 2 and 4 ahead, 4 and 6, 8
     // and 8: 8192 rows of 48 heads of 128 779, 772, 783 us; at 256 channels registers allow 2 and 1 130, 2 and 2 127, 4 and 4, which
-    // spills, 167.)
+    // spills, 167; with weights in two pieces 2 and 1 167, 2 and 2 175.)
     constexpr int kProducts = kKB * kSteps, kRead = D == 256 ? 2 : 4;
     f32x16 s[kKB];
     const int ln = kOpaque ? opaque(lane) : lane;
@@ -318,7 +321,7 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(PrefillArgs a) {
         for (int i = 0; i < 16; ++i) o[db][i] *= f;
       fresh = __any(m == -__builtin_inff());
     };
-    uint32_t p[kKB][8];
+    uint32_t p[kKB][8], rest[kKB][kSplit ? 8 : 1];
     float sum;
     auto weights = [&] {
       float part[2] = {0.0f, 0.0f};
@@ -326,8 +329,15 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(PrefillArgs a) {
       for (int kb = 0; kb < kKB; ++kb)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          p[kb][i] = pack2<kBf16>(__builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][2 * i], c, -mc)), __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][2 * i + 1], c, -mc)));
-          part[i & 1] = add_pair<kBf16>(p[kb][i], part[i & 1]);
+          const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][2 * i], c, -mc)), p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][2 * i + 1], c, -mc));
+          const uint32_t w = pack2<kBf16>(p0, p1);
+          p[kb][i] = w;
+          if constexpr (kSplit) {
+            rest[kb][i] = pack2<kBf16>(p0 - bf16_to_f32(w), p1 - bf16_to_f32(w >> 16));
+            part[i & 1] += p0 + p1;
+          } else {
+            part[i & 1] = add_pair<kBf16>(w, part[i & 1]);
+          }
         }
       sum = part[0] + part[1];
     };
@@ -340,7 +350,7 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(PrefillArgs a) {
       const uint2 v1 = lds_read_transposed(vt + (r + 8) * Tile::kRowBytes + 16 * (ch ^ Tile::vswizzle(r + 8)) + byte);
       return attn_u32x4{v0.x, v0.y, v1.x, v1.y};
     };
-    constexpr int kValues = 2 * kKB * kDB, kReadV = D == 256 ? 2 : 6;
+    constexpr int kValues = 2 * kKB * kDB, kReadV = D == 256 ? (kSplit ? 1 : 2) : 6;
     attn_u32x4 vf[kReadV];
 #pragma unroll
     for (int e = 0; e < kReadV; ++e) vf[e] = read_v(e);
@@ -354,16 +364,17 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(PrefillArgs a) {
 #pragma unroll
     for (int e = 0; e < kValues; ++e) {
       const int kb = e / kDB;
-      const attn_u32x4 w = {p[kb / 2][4 * (kb % 2)], p[kb / 2][4 * (kb % 2) + 1], p[kb / 2][4 * (kb % 2) + 2], p[kb / 2][4 * (kb % 2) + 3]};
-      o[e % kDB] = mfma_32<kBf16>(vf[e % kReadV], w, o[e % kDB]);
+      auto of = [&](auto& p) { return attn_u32x4{p[kb / 2][4 * (kb % 2)], p[kb / 2][4 * (kb % 2) + 1], p[kb / 2][4 * (kb % 2) + 2], p[kb / 2][4 * (kb % 2) + 3]}; };
+      o[e % kDB] = mfma_32<kBf16>(vf[e % kReadV], of(p), o[e % kDB]);
+      if constexpr (kSplit) o[e % kDB] = mfma_32<kBf16>(vf[e % kReadV], of(rest), o[e % kDB]);
       if (e + kReadV < kValues) vf[e % kReadV] = read_v(e + kReadV);
     }
 #pragma unroll
     for (int e = 0; e < kValues - kReadV; ++e) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 1);
+      __builtin_amdgcn_sched_group_barrier(0x008, kSplit ? 2 : 1, 1);
       __builtin_amdgcn_sched_group_barrier(0x100, 2, 1);
     }
-    __builtin_amdgcn_sched_group_barrier(0x008, kReadV, 1);
+    __builtin_amdgcn_sched_group_barrier(0x008, kReadV * (kSplit ? 2 : 1), 1);
   };
   auto turn = [&](int j) {
     // this wave's loads of tile j have landed and its reads of tile j - 1 are done; behind the barrier every wave's
@@ -485,10 +496,10 @@ static size_t prefill_workspace(int B, int Tq, int Tk, int Hq) {
   return pieces ? static_cast<size_t>(std::max<int64_t>(items, pieces) * Hq) * PrefillTile<D>::kSlot * sizeof(float) : 0;
 }
 
-template <int D, bool kBf16>
+template <int D, bool kBf16, bool kSplit>
 static hipError_t prefill_kernels(const PrefillArgs& a, hipStream_t s) {
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(std::max(a.items, a.pieces)) * a.Hq);
-  const hipError_t e = launch_kernel((attn_prefill_kernel<D, kBf16>), dim3(grid), dim3(64 * PrefillTile<D>::kWaves), 0, s, a);
+  const hipError_t e = launch_kernel((attn_prefill_kernel<D, kBf16, kSplit>), dim3(grid), dim3(64 * PrefillTile<D>::kWaves), 0, s, a);
   if (e != hipSuccess || !a.pieces) return e;
   return launch_kernel((attn_prefill_join_kernel<D, kBf16>), dim3(static_cast<unsigned>(a.items * a.Hq) * (PrefillTile<D>::kRows / kJoinRows)), dim3(256), 0, s, a);
 }
@@ -497,7 +508,8 @@ static hipError_t prefill_launch(PrefillArgs a, int type, hipStream_t s) {
   int64_t items;
   prefill_shape<D>(a.B, a.Tq, a.Tk, a.Hq, &a.pieces, &items);
   a.items = static_cast<int>(items);
-  return type == PQ_BF16 ? prefill_kernels<D, true>(a, s) : prefill_kernels<D, false>(a, s);
+  if (type == PQ_F16) return prefill_kernels<D, false, false>(a, s);
+  return a.out_type == PQ_F16 ? prefill_kernels<D, true, true>(a, s) : prefill_kernels<D, true, false>(a, s);
 }
 
 }  // namespace pq

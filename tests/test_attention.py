@@ -11,7 +11,8 @@ Tolerance, with u = 2^-24, c = scale, n keys, and in 64 bits Q = max_j c sum_i |
  - The sum and the weighted sum have n terms each, in any order, with one rescaling a tile: 2 (2 n) u between them, 8 u for joining parts and dividing.
  - Prompts: p is rounded to the type of v, e(t), and the rounded p are summed too: o' - o = sum_j p_j d_j (v_j - o) / sum_j p_j (1 + d_j)
    with |d| <= e(t), at most e(t) (A + |o|) to first order. f16 reaches down to 2^-24 only: up to 2^-25 more for each p, where one of
-   them is at least 1: 2^-25 (sum_j |v_j| + n |o|). One token: p is held in two pieces of the type, (2^-8)^2 at most, f16's down to 2^-24.
+   them is at least 1: 2^-25 (sum_j |v_j| + n |o|). One token, and bf16 prompts with f16 outputs: p is held in two pieces of the type,
+   (2^-8)^2 at most, f16's down to 2^-24.
  - o is stored with one rounding, e(out), and f16 subnormals 2^-25.
 
     |o - o_ref| <= e(out) |o_ref| + 1.01 (2 E + (4 n + 8) u) A + 1.01 e_p (A + |o_ref|) + (f16: 1.01 2^-25 (sum_j |v_j| + n |o_ref|)) + 2^-25
@@ -128,6 +129,10 @@ def _reference(q, k, v, scale, visible):
     return p @ v, mag.amax(-1, keepdim=True), p @ v.abs(), visible.to(q.dtype) @ v.abs()
 
 
+def _e_p(q, o):
+    return 2.0 ** -16 if q.dtype == BF16 and o.dtype == F16 else E[q.dtype]
+
+
 def _check(o, ref, n, D, dtype, e_p, what):
     want, Q, A, S = ref
     tol = E[o.dtype] * want.abs() + 1.01 * (2 * (2 * (2 * D + 4) * U * Q + 4 * U) + (4 * n + 8) * U) * A + 1.01 * e_p * (A + want.abs()) + 2.0 ** -25
@@ -173,7 +178,7 @@ def _check_prompts(o, q, k, v, lens, ahead, causal, scale, what, hidden=None):
         for h in range(Hq):
             ks, vs = k[kat:kat + nk, h // G].double(), v[kat:kat + nk, h // G].double()
             ref = _reference(q[at:at + nq, h].double(), ks, vs, scale, visible)
-            worst = max(worst, _check(o[at:at + nq, h], ref, nk, D, q.dtype, E[q.dtype], f"{what}, sequence {b} ({nq}, {nk}), head {h}"))
+            worst = max(worst, _check(o[at:at + nq, h], ref, nk, D, q.dtype, _e_p(q, o), f"{what}, sequence {b} ({nq}, {nk}), head {h}"))
         at, kat = at + nq, kat + nk
     return worst
 
