@@ -425,7 +425,7 @@ PyObject* attn_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t Tq = q->size(0), H = q->size(1), D = q->size(2), Tk = k->size(0), Hkv = k->size(1), B = cu_q->size(0) - 1;
   float scale;
   at::ScalarType ot;
-  if (!half_type(t) || !fits(Tq) || !fits(Tk) || !fits(H) || !fits(B) || Hkv == 0 || H % Hkv || !heads(q, t, Tq, H, D) || !heads(k, t, Tk, Hkv, D) ||
+  if (!half_type(t) || !fits(Tq) || !fits(Tk) || !fits(H) || !fits(D) || !fits(B) || Hkv == 0 || H % Hkv || !heads(q, t, Tq, H, D) || !heads(k, t, Tk, Hkv, D) ||
       !heads(v, t, Tk, Hkv, D) || !dense(cu_q, at::kInt, {B + 1}) || !dense(cu_k, at::kInt, {B + 1}) || !get_scale(a[5], D, &scale) ||
       !out_type(out, a[8], t, &ot) || (out && !dense(out, ot, {Tq, H, D})))
     return unusual();

@@ -211,6 +211,7 @@ def test_refusals_are_the_same(through_python):
         lambda: pq.attn_prefill(q, odd, v, cu), lambda: pq.attn_prefill(q, k, apart, cu), lambda: pq.attn_prefill(q, k, v, cu, scale=float("nan")),
         lambda: pq.attn_prefill(q, k, v, cu, out=new(70, 12, 64)), lambda: pq.attn_prefill(q, k, v, cu, dtype=F32), lambda: pq.attn_prefill(q, k, v, cu, scale=None, out=q),
         lambda: pq.attn_prefill(q, w["kl"], w["vl"], cu, w["cu_k"], workspace=w["ws"][:16]), lambda: pq.attn_prefill(q[..., :32], k[..., :32], v[..., :32], cu),
+        lambda: pq.attn_prefill(*(new(0, 1, WRAP + 128) for _ in range(3)), cu),
     ]
     for i, call in enumerate(calls):
         said = []
