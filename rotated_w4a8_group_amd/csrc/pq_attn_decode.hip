@@ -19,7 +19,7 @@
 //
 // Measured: 64 sequences of up to 8191 positions (8 heads of 128, 16-bit, 1.04 GB of rows) 178 us, 5.84 TB/s; one of 131071, e4m3
 // (277 MB) 53 us, 5.2 TB/s; a read of as much memory and nothing else reaches 6.3. Small calls are the waits of one chain: length,
-// page, row, score, and the join's launch (17 sequences of up to 4000, 4 heads of 256, 36 MB: 17.5 us).
+// page, row, score, and the join's launch (17 sequences of up to 4000, 4 heads of 256, e4m3, 36 MB: 17.5 us).
 #include <algorithm>
 #include <utility>
 
@@ -35,6 +35,7 @@ struct DecodeArgs {
   int B, Hq, G;             // G: query heads of a key head
   int hv, tiles_of_heads;   // virtual heads: a key head once for each 16 query heads that share it
   int pieces;               // pieces to cut the whole line into, about; 0: a workgroup for each sequence and virtual head
+  int places, least;        // workgroups that the device holds at a time; tiles of a piece at least
   float scale_log2;
   uint16_t* o;
   int out_type;
@@ -42,7 +43,12 @@ struct DecodeArgs {
 };
 
 constexpr int kTileKeys = 32;
-constexpr int kLeastTiles = 8;      // of a piece (1 x 2048 of 8 heads: 10.5 us, with 4 9.2, with 16 14; 17 sequences of 4 wide heads 17.4, 20.0, 18.8)
+// While a piece for every place of the device is at most this many tiles, there are no more pieces than places, each a whole number of
+// tiles for every wave: what a second round costs is the wait of its first loads (8 x 3000 of 4 heads of 256, 16-bit: 2 tiles a piece, 750
+// pieces for 512 places 23 us, 4 tiles 17.2; 4 x 500, 2 tiles 9.9, 4 12, 8 16; 17 x up to 4000 of 4 of 256, e4m3, 5 tiles for 4 waves
+// 17.9, 8 17.5). Longer ones are cut into wanted_pieces() of two tiles a wave at least (16 x 8000 of 4 of 256, 16-bit, 12 tiles in one
+// round 61, 6 in two 51; 12 x 4000 of 8 of 128, 16-bit, 5 tiles 30.5, 8 27.9).
+constexpr int kOneRound = 8;
 constexpr int kTableHalves = 128;   // 16-key halves whose pages a wave holds at a time
 constexpr int kMostPieces = 4096;   // of one head
 
@@ -128,7 +134,8 @@ struct Cut {
     int n = tiles_of(first_len);
     for (int b = lane + 64; b < a.B; b += 64) n += tiles_of(seq_len(a, b));
     const int all = lanes_total(n) * a.hv;
-    per = std::max(kLeastTiles, (all + a.pieces - 1) / a.pieces);
+    const int one = (all + a.places - 1) / a.places;
+    per = one <= kOneRound ? std::max(one + a.least - 1, a.least) / a.least * a.least : std::max((all + a.pieces - 1) / a.pieces, 2 * a.least);
   }
   __device__ __forceinline__ int len(const DecodeArgs& a, int b) const { return b < 64 ? first_len : b < a.B ? seq_len(a, b) : 0; }
   __device__ __forceinline__ int pieces(int len) const { return (tiles_of(len) + per - 1) / per; }
@@ -517,14 +524,20 @@ template <int D, bool kBf16, bool kQuant>
 static hipError_t decode_launch(DecodeArgs a, hipStream_t s) {
   const int64_t length = static_cast<int64_t>(a.c.width) << a.c.page_shift;
   const int64_t heads = static_cast<int64_t>(a.B) * a.hv;
-  // A head stays in one workgroup, and no join follows, while a wide one's waves have two tiles each (1 x 1000 of 8 heads of 128, e4m3:
-  // 10.5 us, cut 10.8; 1 x 1000 of 4 of 256, 16-bit, four waves: 24.7, cut 16.8; 8 x 1000 of 8 of 128, 16-bit, eight waves: 13.1, cut
-  // 11.5; 1 x 2000, e4m3: 16.5, cut 11.0), or where there are heads enough to fill the device with (128 x 2000 of 8 heads: 56,
-  // cut 62.8) and none takes so long that the others' end leaves it alone.
-  if (length <= (heads >= wanted_pieces() ? 2048 : 2 * kTileKeys * DecodeTile<D, kQuant, true>::kWaves))
+  // A head stays in one workgroup, and no join follows, while a wide one's waves have two tiles each (60 x 1000 of 8 heads of 128,
+  // e4m3: 20.6 us, cut 25.9; 20 x 1000 11.1, 13.6; 2 x 500, 16-bit 8.8, 9.5) - one tile where sixteen waves would be few heads' only
+  // ones (1 x 1000, e4m3: 10.4, cut 9.0; 8 x 1000 10.7, 10.5; 1 x 509 7.5, 9.0) - or where there are heads enough to fill half of the
+  // places wanted and none takes so long that the others' end leaves it alone (128 x 2000 of 8 heads of 128, e4m3: 56, cut 63; 100 x 2000,
+  // 16-bit 77, 84; 60 x 2000 50, 55; 40 x 2000, e4m3 33, 29; 100 x 2000 of 4 of 256, 16-bit 91, 86).
+  using Wide = DecodeTile<D, kQuant, true>;
+  const int waves = Wide::kWaves, tiles = waves < 16 || heads > cu_count() / 8 ? 2 : 1;
+  if (length <= (heads >= wanted_pieces() / 2 ? 2048 : tiles * kTileKeys * waves))
     return heads <= cu_count() ? decode_kernel<D, kBf16, kQuant, true>(a, heads, s) : decode_kernel<D, kBf16, kQuant, false>(a, heads, s);
   a.pieces = wanted_pieces();
-  const int64_t most = heads * ((length + kTileKeys * kLeastTiles - 1) / (kTileKeys * kLeastTiles));
+  using Tile = DecodeTile<D, kQuant, false>;
+  a.places = std::min(a.pieces, Tile::kPerCu * cu_count());
+  a.least = Tile::kWaves;
+  const int64_t most = heads * ((length + kTileKeys * a.least - 1) / (kTileKeys * a.least));
   const hipError_t e = decode_kernel<D, kBf16, kQuant, false>(a, std::min<int64_t>(a.pieces + heads, most), s);
   return e != hipSuccess ? e : launch_kernel((attn_join_kernel<D>), dim3(static_cast<unsigned>(a.B * a.Hq)), dim3(256), 0, s, a);
 }
@@ -575,7 +588,7 @@ int pq_attn_decode(const uint16_t* q_d, int64_t ldq, int64_t hsq, int type, cons
       return overlap(what);
   if (ranges_meet(o_d, ob, ws_d, static_cast<int64_t>(need))) return overlap(what);
   DecodeArgs a{{kc_d, vc_d, ks_d, vs_d, table_d, pages, pages ? width : 0, Hkv, __builtin_ctz(page)}, q_d, ldq, hsq, lens_d, B, Hq, G,
-               Hkv * tiles_of_heads, tiles_of_heads, 0, scale * 1.44269504088896340736f, o_d, out_type, static_cast<float*>(ws_d)};
+               Hkv * tiles_of_heads, tiles_of_heads, 0, 0, 0, scale * 1.44269504088896340736f, o_d, out_type, static_cast<float*>(ws_d)};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   return launch_status(what, D == 64 ? decode_for<64>(a, type, s) : D == 128 ? decode_for<128>(a, type, s) : decode_for<256>(a, type, s));
 }
