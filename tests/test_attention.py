@@ -231,6 +231,18 @@ def test_prefill_few_rows_behind_many_keys(nq, nk, D):
 
 
 @gpu
+@pytest.mark.parametrize("B,Hq,longest", [(100, 1, 3000), (150, 2, 2500), (65, 6, 1300), (300, 1, 60)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_prefill_of_many_sequences(B, Hq, longest, D):
+    """More sequences than a wave has lanes, empty ones among them, some with their key tiles cut and some whole."""
+    g = torch.Generator().manual_seed(B + D)
+    nq = torch.randint(0, 6, (B,), generator=g).tolist()
+    lens = [(n, n + int(longest * float(torch.rand((), generator=g)) ** 4)) for n in nq[:-2]] + [(140, 140 + longest), (0, 9)]
+    q, k, v, cu_q, cu_k = _prompts(g, lens, Hq, 1, D, BF16)
+    _check_prompts(pq.attn_prefill(q, k, v, cu_q, cu_k), q, k, v, lens, 0, True, D ** -0.5, "many sequences")
+
+
+@gpu
 @pytest.mark.parametrize("scale", [1e-4, 0.02, 1.0, 30.0])
 def test_prefill_scales(scale):
     """From weights that hardly differ to one that takes all; scores whose maximum rises and falls along the keys."""

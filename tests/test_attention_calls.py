@@ -303,6 +303,33 @@ def test_captured_calls():
 
 
 @gpu
+def test_replays_follow_lengths_and_pages():
+    """A served model replays one graph while its sequences grow and change pages: the eager call's bits at every step."""
+    w = _world()
+    c, table, lens, cu, cu_k = w["cache"], w["table"].clone(), w["lens"].clone(), w["cu"].clone(), w["cu_k"].clone()
+    calls = [lambda: pq.attn_decode(w["q"][:3], c[0], c[1], table, lens, c[2], c[3]), lambda: pq.attn_prefill(w["q"], w["kl"], w["vl"], cu, cu_k),
+             lambda: pq.attn_prefill(w["q"], w["k"], w["v"], cu)]
+    for f in calls:
+        f()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs = [f() for f in calls]
+    for step in ([1, 1, 1], [0, 1728, 0], [300, 301, 1727], [1728, 1728, 1728], [5, 0, 64], [0, 0, 0]):
+        lens.copy_(torch.tensor(step))
+        table.copy_(table.flip(0).roll(1, 1))
+        a, b = sorted(n % 71 for n in step[:2])
+        cu.copy_(torch.tensor([0, a, b, 70]))
+        cu_k.copy_(torch.tensor([0, 70 + step[0], 70 + step[0], 2000]))
+        for o in outs:
+            o.fill_(7)
+        g.replay()
+        torch.cuda.synchronize()
+        for o, f in zip(outs, calls):
+            assert torch.equal(o, f()), step
+
+
+@gpu
 def test_two_graphs_with_one_workspace():
     """One after the other they may share a workspace: a call takes nothing from what it holds."""
     w = _world()
