@@ -65,6 +65,9 @@ __device__ __forceinline__ f32x16 mfma_32(const attn_u32x4& a, const attn_u32x4&
 // 32.6; 64 behind 1500, 12 of 64 15.0, 14.9, 19.2.)
 constexpr int kLeastTiles = 8;
 
+// Two buffers of K and V are 64 KB, 32 at 64 channels, and the registers are a wave's of two a SIMD: one workgroup's softmax runs under
+// the other's products. (256 channels with one wave a SIMD and 64 keys, before the pieces filled the places: 512 rows behind 8191 keys
+// 183 us against 167.)
 template <int D>
 struct PrefillTile {
   static constexpr int kWaves = 4;
