@@ -61,6 +61,9 @@ __device__ __forceinline__ f32x16 mfma_32(const attn_u32x4& a, const attn_u32x4&
   else return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
+// Four packed values, or zeros where the mask is 0: a factor of 0 would leave a NaN.
+__device__ __forceinline__ uint2 kept(const uint2& v, uint32_t mask) { return make_uint2(v.x & mask, v.y & mask); }
+
 // Key tiles of a piece, at least. (4, 8, 16: 256 rows behind 1280 keys, 24 heads of 128 23.8, 23.3, 26.2 us; 8 heads of 256 25.6, 26.1,
 // 32.6; 64 behind 1500, 12 of 64 15.0, 14.9, 19.2.)
 constexpr int kLeastTiles = 8;
@@ -427,14 +430,15 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(PrefillArgs a) {
     for (int i = 0; i < 16; ++i) odd_sum = __builtin_fmaf(o[db][i], 0.0f, odd_sum);
   const uint64_t odd = __ballot(seen > 0 && row < it.nq && !(odd_sum == 0.0f));
   const uint32_t again = static_cast<uint32_t>(odd | odd >> 32);
-  const float inv = seen > 0 ? 1.0f / l : 0.0f;
+  const float inv = 1.0f / l;
+  const uint32_t keep = seen > 0 ? ~0u : 0;   // a row without a key is zeros, whatever values its weights of 0 stand before
   if (row < it.nq && !(again >> n & 1)) {
     uint16_t* out = a.o + (static_cast<int64_t>(it.q0 + row) * a.Hq + hq) * D;
 #pragma unroll
     for (int db = 0; db < kDB; ++db)
 #pragma unroll
       for (int g = 0; g < 4; ++g)                      // channels 32 db + 8 g + 4 half .. + 3
-        *reinterpret_cast<uint2*>(out + 32 * db + 8 * g + 4 * half) = pack4(a.out_type, o[db][4 * g] * inv, o[db][4 * g + 1] * inv, o[db][4 * g + 2] * inv, o[db][4 * g + 3] * inv);
+        *reinterpret_cast<uint2*>(out + 32 * db + 8 * g + 4 * half) = kept(pack4(a.out_type, o[db][4 * g] * inv, o[db][4 * g + 1] * inv, o[db][4 * g + 2] * inv, o[db][4 * g + 3] * inv), keep);
   }
   for (uint32_t left = again; left; left &= left - 1) {
     const int r = it.r0 + 32 * wave + __builtin_ctz(left);
@@ -483,11 +487,12 @@ __global__ __launch_bounds__(256) void attn_prefill_join_kernel(PrefillArgs a) {
   __syncthreads();
   const uint32_t again = odd;
   if (row < it.nq && !(again >> n & 1)) {
-    const float inv = seen > 0 ? 1.0f / sum : 0.0f;
+    const float inv = 1.0f / sum;
+    const uint32_t keep = seen > 0 ? ~0u : 0;
     uint16_t* out = a.o + (static_cast<int64_t>(it.q0 + row) * a.Hq + hq) * D;
 #pragma unroll
     for (int c = 0; c < kEach; ++c)
-      *reinterpret_cast<uint2*>(out + 4 * (16 * c + part)) = pack4(a.out_type, v[c].x * inv, v[c].y * inv, v[c].z * inv, v[c].w * inv);
+      *reinterpret_cast<uint2*>(out + 4 * (16 * c + part)) = kept(pack4(a.out_type, v[c].x * inv, v[c].y * inv, v[c].z * inv, v[c].w * inv), keep);
   }
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   for (int i = wave; i < kJoinRows; i += 4)
