@@ -61,6 +61,12 @@ __device__ __forceinline__ f32x16 mfma_32(const attn_u32x4& a, const attn_u32x4&
   else return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
+// a b, rounded to binary32 and not fused with what follows.
+__device__ __forceinline__ float rounded_product(float a, float b) {
+#pragma clang fp contract(off)
+  return a * b;
+}
+
 // Four packed values, or zeros where the mask is 0: a factor of 0 would leave a NaN.
 __device__ __forceinline__ uint2 kept(const uint2& v, uint32_t mask) { return make_uint2(v.x & mask, v.y & mask); }
 
@@ -332,10 +338,14 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(PrefillArgs a) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) mt = __builtin_fmaxf(mt, s[kb][i]);
       mt = both_halves_max(mt);
-      const float f = m == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m * c - mt * c);
+      // The weights so far were taken against mc as it was rounded, so the factor is the difference of the rounded ones (fused with
+      // a product it would be that of others, off by 2^(half a step of mc)).
+      const float to = mt == -__builtin_inff() ? 0.0f : rounded_product(mt, c), f = m == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(mc - to);
       m = mt;
-      mc = m == -__builtin_inff() ? 0.0f : m * c;
+      mc = to;
       l *= f;
+      // Scores of 2^30 and more: the step of mc may carry every weight past its type. Such a row is computed again, key by key.
+      if (__builtin_fabsf(mc) >= 0x1p30f) l = __builtin_nanf("");
 #pragma unroll
       for (int db = 0; db < kDB; ++db)
 #pragma unroll

@@ -53,3 +53,29 @@ def test_queries_without_a_key_beside_values_that_are_not_finite(lens, D, kind, 
             ref = ta._reference(q[at:at + sane, h].double(), k[kat:kat + nk, 0].double(), torch.nan_to_num(v[kat:kat + nk, 0].double(), 0, 0, 0), D ** -0.5, visible)
             ta._check(o[at:at + sane, h], ref, nk, D, q.dtype, ta._e_p(q, o), f"beside bad values, {(nq, nk)}, head {h}")
         at, kat = at + nq, kat + nk
+
+
+# ------------------------------------------------------------------------------------------
+def _whole_numbers(g, *shape, most=3):
+    return torch.randint(-most, most + 1, shape, generator=g).float()
+
+
+@pytest.mark.parametrize("scale", [1e5, 3e6, 1e8, 1e9, 2.0 ** 40, 2.0 ** 64])
+@pytest.mark.parametrize("kind,out", [("bf16", "bf16"), ("f16", "f16"), ("bf16", "f16")])
+@pytest.mark.parametrize("nq,nk", [(70, 70), (40, 3000)])
+def test_prefill_scales_that_leave_one_weight(nq, nk, kind, out, scale):
+    """Scores are whole numbers, exactly; those below the largest are at least `scale` below it, where exp gives 0, and equal ones have equal
+    weights: the result is the mean over the largest, and scores leave no error."""
+    g = torch.Generator().manual_seed(nk)
+    D = 64
+    k, v = _whole_numbers(g, nk, 1, D).to(ta.TYPES[kind]).cuda(), _whole_numbers(g, nk, 1, D, most=8).to(ta.TYPES[kind]).cuda()
+    q = (_whole_numbers(g, nq, 2, D) * 7).to(ta.TYPES[kind]).cuda()
+    o = pq.attn_prefill(q, k, v, _i32(0, nq), _i32(0, nk), scale=scale, dtype=ta.TYPES[out])
+    visible = torch.ones((nq, nk), dtype=torch.bool, device="cuda").tril(nk - nq)
+    for h in range(2):
+        a = (q[:, h].double() @ k[:, 0].double().t()).masked_fill(~visible, -math.inf)
+        top = (a == a.amax(-1, keepdim=True)).double()
+        want, A = (top @ x / top.sum(-1, keepdim=True) for x in (v[:, 0].double(), v[:, 0].double().abs()))
+        tol = ta.E[o.dtype] * want.abs() + 1.01 * ta._e_p(q, o) * (A + want.abs()) + (4 * nk + 8) * U * A + 2.0 ** -25
+        err = (o[:, h].double() - want).abs()
+        assert bool((err <= tol).all()), f"{float((err / tol).max()):.3g} of the tolerance"
