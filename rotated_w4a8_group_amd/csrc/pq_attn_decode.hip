@@ -257,7 +257,7 @@ void attn_decode_kernel(DecodeArgs a) {
   v4f o[kDB];
 #pragma unroll
   for (int i = 0; i < kDB; ++i) o[i] = v4f{0.f, 0.f, 0.f, 0.f};
-  float m = -__builtin_inff(), mc = 0.0f, l = 0.0f;
+  float m = -__builtin_inff(), ref = 0.0f, l = 0.0f;   // ref: m, once there is one
   bool any = false;
 
   if (ta < tb) {
@@ -328,9 +328,9 @@ void attn_decode_kernel(DecodeArgs a) {
       for (int i = 0; i < 4; ++i) mt = __builtin_fmaxf(mt, s[kb][i]);
     mt = four_groups(mt, [](float u, float v) { return __builtin_fmaxf(u, v); });
     if (__any((mt - m) * c > 8.0f)) {
-      const float f = m == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m * c - mt * c);
+      const float f = m == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f((m - mt) * c);
       m = mt;
-      mc = m == -__builtin_inff() ? 0.0f : m * c;
+      ref = m == -__builtin_inff() ? 0.0f : m;
       l *= f;
 #pragma unroll
       for (int i = 0; i < kDB; ++i)
@@ -345,7 +345,7 @@ void attn_decode_kernel(DecodeArgs a) {
         float p[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          p[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i + k], c, -mc));
+          p[k] = __builtin_amdgcn_exp2f((s[kb][i + k] - ref) * c);   // the difference first: 0 at the largest score, whatever the scale
           l += p[k];
           if constexpr (kQuant) p[k] *= vs[kb][i + k];
         }
@@ -394,7 +394,7 @@ void attn_decode_kernel(DecodeArgs a) {
 #pragma unroll
   for (int db = 0; db < kDB; ++db)
     *reinterpret_cast<float4*>(po + n * D + 4 * ((4 * db + g) ^ n)) = make_float4(o[db][0], o[db][1], o[db][2], o[db][3]);
-  if (g == 0) *reinterpret_cast<float4*>(state + (wave * 16 + n) * 4) = make_float4(m == -__builtin_inff() ? m : mc, l, any ? 1.0f : 0.0f, 0.0f);
+  if (g == 0) *reinterpret_cast<float4*>(state + (wave * 16 + n) * 4) = make_float4(m, l, any ? 1.0f : 0.0f, 0.0f);
   __syncthreads();
   const bool whole = t0 == 0 && t1 == nt;
   for (int e = tid; e < heads * (D / 4); e += Tile::kThreads) {
@@ -406,7 +406,7 @@ void attn_decode_kernel(DecodeArgs a) {
 #pragma unroll
     for (int w = 0; w < Tile::kWaves; ++w) {
       const float4 st = *reinterpret_cast<const float4*>(state + (w * 16 + r) * 4);
-      const float f = st.x == -__builtin_inff() ? (st.y == st.y ? 0.0f : st.y) : __builtin_amdgcn_exp2f(st.x - most);
+      const float f = st.x == -__builtin_inff() ? (st.y == st.y ? 0.0f : st.y) : __builtin_amdgcn_exp2f((st.x - most) * c);
       const float4 u = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + w * Tile::kWave) + r * D + 4 * (ch ^ r));
       sum += f * st.y;
       seen += st.z;
@@ -434,6 +434,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(DecodeArgs a) {
   const int b = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq;
   const int h = hq / a.G, hv = h * a.tiles_of_heads + hq % a.G / 16, r = hq % a.G % 16;
   const int tid = threadIdx.x, lane = tid % kLanes, p = tid / kLanes;
+  const float c = a.scale_log2;
   const Cut cut(a);
   int before = 0, pieces = 0;
   for (int b0 = 0; b0 <= b; b0 += 64) {
@@ -466,7 +467,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(DecodeArgs a) {
   float sum = 0.0f, seen = 0.0f;
   for (int i = tid; i < pieces; i += 256) {
     const float4 st = i == tid ? mine : state(i);
-    const float f = st.x == -__builtin_inff() ? (st.y == st.y ? 0.0f : st.y) : __builtin_amdgcn_exp2f(st.x - most);
+    const float f = st.x == -__builtin_inff() ? (st.y == st.y ? 0.0f : st.y) : __builtin_amdgcn_exp2f((st.x - most) * c);
     weight[i] = f;
     sum += f * st.y;
     seen += st.z;

@@ -79,3 +79,38 @@ def test_prefill_scales_that_leave_one_weight(nq, nk, kind, out, scale):
         tol = ta.E[o.dtype] * want.abs() + 1.01 * ta._e_p(q, o) * (A + want.abs()) + (4 * nk + 8) * U * A + 2.0 ** -25
         err = (o[:, h].double() - want).abs()
         assert bool((err <= tol).all()), f"{float((err / tol).max()):.3g} of the tolerance"
+
+
+def _cache(g, n, D, kind, k, v, page=16):
+    """k, v [n, 1, D] on pages of their own: values that e4m3 holds, under scales that are powers of two."""
+    pages = -(-n // page)
+    order = torch.randperm(pages, generator=g)
+    at = torch.arange(n)
+    out, scales = [], []
+    for x, s in ((k, 0.5), (v, 2.0)):
+        c = torch.full((pages, 1, page, D), math.nan).to(E4M3 if kind == "e4m3" else ta.TYPES[kind])
+        y = (x / s).to(c.dtype) if kind == "e4m3" else x.to(c.dtype)
+        c.view(U8 if kind == "e4m3" else torch.int16)[order[at // page], :, at % page] = y.view(U8 if kind == "e4m3" else torch.int16)
+        out.append((c.view(U8) if kind == "e4m3" else c).cuda())
+        scales.append(torch.full((pages, 1, page), s, device="cuda") if kind == "e4m3" else None)
+    return out, order.to(I32)[None].cuda(), scales
+
+
+@pytest.mark.parametrize("scale", [1e5, 1e8, 1e9, 2.0 ** 40, 2.0 ** 64])
+@pytest.mark.parametrize("cache,kind", [("e4m3", "bf16"), ("e4m3", "f16"), ("f16", "f16"), ("bf16", "bf16")])
+@pytest.mark.parametrize("n", [37, 700, 9001])
+def test_decode_scales_that_leave_one_weight(n, cache, kind, scale):
+    """The same for single tokens, whose weights are held in two pieces."""
+    g = torch.Generator().manual_seed(n)
+    D, Hq = 64, 20
+    k, v = _whole_numbers(g, n, 1, D), _whole_numbers(g, n, 1, D, most=8)
+    q = (_whole_numbers(g, 1, Hq, D) * 7).to(ta.TYPES[kind]).cuda()
+    c, table, s = _cache(g, n, D, cache, k, v)
+    o = pq.attn_decode(q, *c, table, _i32(n), *s, scale=scale)
+    a = q[0].double() @ k[:, 0].double().cuda().t()
+    top = (a == a.amax(-1, keepdim=True)).double()
+    want = top @ v[:, 0].double().cuda() / top.sum(-1, keepdim=True)
+    A = top @ v[:, 0].double().abs().cuda() / top.sum(-1, keepdim=True)
+    tol = ta.E[o.dtype] * want.abs() + 1.01 * 2.0 ** -16 * (A + want.abs()) + (4 * n + 8) * U * A + 2.0 ** -25
+    err = (o[0].double() - want).abs()
+    assert bool((err <= tol).all()), f"{float((err / tol).max()):.3g} of the tolerance"
