@@ -67,7 +67,7 @@ struct DecodeTile {
   static constexpr int kScale = kQuant ? 256 : 0;          // 32 scales of K, 32 of V
   static constexpr int kWave = 2 * kPart + 2 * kScale + kTable;
   static constexpr int kState = kWaves * 16 * 16;          // maximum, sum, seen of every wave and head
-  static constexpr int kLds = kWaves * kWave + kState;
+  static constexpr int kLds = kWaves * kWave + 2 * kState + 16;   // states, factors of them, and a flag
   static constexpr int kPerCu = std::min(160 * 1024 / kLds, 16 / kWaves);
   static constexpr int kSlot = 16 * D + 64;                // floats of a piece in the workspace
   static_assert(2 * kPart >= 16 * D * 4, "O of a wave fits its slots");
@@ -121,6 +121,16 @@ __device__ __forceinline__ float four_groups(float v, F f) {
   return f(x.lo, x.hi);
 }
 
+// log2 of the factor of a second walk: 2^31 weights of up to 2^8 times values of up to 2^128 stay below 2^120, and the weights
+// are bf16 with 2^-78 of the largest one still normal.
+constexpr float kFar = -48.0f;
+
+// What a state (maximum, sum, seen, log2 of its weights' factor) counts beside others: with the largest maximum and the least factor.
+__device__ __forceinline__ float state_factor(const float4& st, float most, float c, float least) {
+  if (st.x == -__builtin_inff()) return st.y == st.y ? 0.0f : st.y;
+  return __builtin_amdgcn_exp2f(__builtin_fmaf(st.x - most, c, least - st.w));
+}
+
 // Positions and tiles of a sequence.
 __device__ __forceinline__ int seq_len(const DecodeArgs& a, int b) { return std::min(std::max(a.lens[b], 0), a.c.width << a.c.page_shift); }
 __device__ __forceinline__ int tiles_of(int len) { return static_cast<int>((static_cast<uint32_t>(len) + kTileKeys - 1) / kTileKeys); }
@@ -143,14 +153,29 @@ struct Cut {
   __device__ __forceinline__ int pieces(int len) const { return (tiles_of(len) + per - 1) / per; }
 };
 
+// A workgroup's piece: tiles t0 .. t1 - 1 of the nt of sequence b and virtual head hv.
+struct DecodePiece {
+  int b, hv, len, t0, t1, nt;
+};
+
+// Walks the piece's tiles and stores what they give, with all weights (and so sums and O) 2^shift times as large. Whether a sum passed 2^100, or a
+// NaN came: it may have passed binary32 on the way, or will beside other pieces', though the mean does not. Such a piece is walked a second
+// time with kFar. (The second call is code of its own: as a loop around one, its registers cost the first walk 5 %. What a thread's
+// number gives is computed in each, not kept for the second.)
 template <int D, bool kBf16, bool kQuant, bool kWide>
-__global__ __launch_bounds__((DecodeTile<D, kQuant, kWide>::kThreads), (std::max(1, DecodeTile<D, kQuant, kWide>::kPerCu * DecodeTile<D, kQuant, kWide>::kWaves / 4)))
-void attn_decode_kernel(DecodeArgs a) {
+__device__ __forceinline__ bool decode_walk(const DecodeArgs& a, const DecodePiece& piece, uint8_t* smem, float shift) {
   using Tile = DecodeTile<D, kQuant, kWide>;
   constexpr int kDB = D / 16, kSteps = D / 32;
   constexpr bool kVBf16 = kQuant || kBf16;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[Tile::kLds];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int b = piece.b, hv = piece.hv, len = piece.len, t0 = piece.t0, t1 = piece.t1, nt = piece.nt;
+  const float c = a.scale_log2;
+  const int64_t page_mask = (1ll << a.c.page_shift) - 1;
+  const int h = hv / a.tiles_of_heads, first_head = hv % a.tiles_of_heads * 16, heads = std::min(a.G - first_head, 16);
+  const int hq0 = h * a.G + first_head;
+  const uint8_t* const kc = static_cast<const uint8_t*>(a.c.k);
+  const uint8_t* const vc = static_cast<const uint8_t*>(a.c.v);
+
+  const int tid = opaque(threadIdx.x), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 15, g = lane >> 4;
   uint8_t* const mine = smem + wave * Tile::kWave;
   uint8_t* const kslot = mine;
@@ -158,45 +183,9 @@ void attn_decode_kernel(DecodeArgs a) {
   float* const scales = reinterpret_cast<float*>(mine + 2 * Tile::kPart);      // two tiles' worth
   int32_t* const table = reinterpret_cast<int32_t*>(mine + 2 * Tile::kPart + 2 * Tile::kScale);
   float* const state = reinterpret_cast<float*>(smem + Tile::kWaves * Tile::kWave);
-  const float c = a.scale_log2;
-  const int64_t page_mask = (1ll << a.c.page_shift) - 1;
-
-  // this workgroup's piece: tiles t0 .. t1 - 1 of the nt of sequence b and virtual head hv
-  int b, hv, len, t0 = 0, t1, nt;
-  if (a.pieces) {
-    const Cut cut(a);
-    int before = 0, f = 0, np = 0;
-    uint64_t here = 0;
-    for (int b0 = 0; b0 < a.B && !here; b0 += 64) {
-      const int ln = cut.len(a, b0 + lane), n = cut.pieces(ln), sum = lanes_scan(n * a.hv);
-      here = __ballot(before + sum > static_cast<int>(blockIdx.x));
-      if (here) {
-        f = __builtin_ctzll(here);
-        b = b0 + f;
-        len = __builtin_amdgcn_readlane(ln, f);
-        np = __builtin_amdgcn_readlane(n, f);
-        before += __builtin_amdgcn_readlane(sum, f) - np * a.hv;
-      } else {
-        before += __builtin_amdgcn_readlane(sum, 63);
-      }
-    }
-    if (!here) return;   // fewer pieces than the host allowed for
-    const int in = blockIdx.x - before, i = in % np;
-    hv = in / np;
-    nt = tiles_of(len);
-    t0 = static_cast<int>(static_cast<int64_t>(nt) * i / np);
-    t1 = static_cast<int>(static_cast<int64_t>(nt) * (i + 1) / np);
-  } else {
-    b = blockIdx.x / a.hv;
-    hv = blockIdx.x % a.hv;
-    len = __builtin_amdgcn_readfirstlane(seq_len(a, b));
-    t1 = nt = tiles_of(len);
-  }
-
-  const int h = hv / a.tiles_of_heads, first_head = hv % a.tiles_of_heads * 16, heads = std::min(a.G - first_head, 16);
-  const int hq0 = h * a.G + first_head;
-  const uint8_t* const kc = static_cast<const uint8_t*>(a.c.k);
-  const uint8_t* const vc = static_cast<const uint8_t*>(a.c.v);
+  float* const factors = state + Tile::kState / 4;
+  int* const flag = reinterpret_cast<int*>(factors + Tile::kState / 4);
+  if (shift == 0.0f && tid == 0) *flag = 0;   // not by the second walk: waves may still be reading it
 
   // this wave's tiles
   const int count = t1 - t0, ta = t0 + static_cast<int>(static_cast<int64_t>(count) * wave / Tile::kWaves),
@@ -345,7 +334,7 @@ void attn_decode_kernel(DecodeArgs a) {
         float p[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          p[k] = __builtin_amdgcn_exp2f((s[kb][i + k] - ref) * c);   // the difference first: 0 at the largest score, whatever the scale
+          p[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i + k] - ref, c, shift));   // the difference first: 0 at the largest score, whatever the scale
           l += p[k];
           if constexpr (kQuant) p[k] *= vs[kb][i + k];
         }
@@ -396,31 +385,87 @@ void attn_decode_kernel(DecodeArgs a) {
     *reinterpret_cast<float4*>(po + n * D + 4 * ((4 * db + g) ^ n)) = make_float4(o[db][0], o[db][1], o[db][2], o[db][3]);
   if (g == 0) *reinterpret_cast<float4*>(state + (wave * 16 + n) * 4) = make_float4(m, l, any ? 1.0f : 0.0f, 0.0f);
   __syncthreads();
+  // Each wave's factor of each head, once, beside what it gives to the sum.
+  if (tid < Tile::kWaves * 16) {
+    float most = -__builtin_inff();
+#pragma unroll
+    for (int w = 0; w < Tile::kWaves; ++w) most = __builtin_fmaxf(most, state[(w * 16 + (tid & 15)) * 4]);
+    const float4 st = *reinterpret_cast<const float4*>(state + tid * 4);
+    const float f = state_factor(st, most, c, 0.0f);
+    *reinterpret_cast<float4*>(factors + tid * 4) = make_float4(f, f * st.y, st.z, most);
+  }
+  __syncthreads();
   const bool whole = t0 == 0 && t1 == nt;
   for (int e = tid; e < heads * (D / 4); e += Tile::kThreads) {
     const int r = e / (D / 4), ch = e % (D / 4);
-    float most = -__builtin_inff(), sum = 0.0f, seen = 0.0f;
-#pragma unroll
-    for (int w = 0; w < Tile::kWaves; ++w) most = __builtin_fmaxf(most, state[(w * 16 + r) * 4]);
+    float sum = 0.0f, seen = 0.0f, most = 0.0f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < Tile::kWaves; ++w) {
-      const float4 st = *reinterpret_cast<const float4*>(state + (w * 16 + r) * 4);
-      const float f = st.x == -__builtin_inff() ? (st.y == st.y ? 0.0f : st.y) : __builtin_amdgcn_exp2f((st.x - most) * c);
+      const float4 st = *reinterpret_cast<const float4*>(factors + (w * 16 + r) * 4);
       const float4 u = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + w * Tile::kWave) + r * D + 4 * (ch ^ r));
-      sum += f * st.y;
+      sum += st.y;
       seen += st.z;
-      v.x += f * u.x, v.y += f * u.y, v.z += f * u.z, v.w += f * u.w;
+      most = st.w;
+      v.x += st.x * u.x, v.y += st.x * u.y, v.z += st.x * u.z, v.w += st.x * u.w;
     }
+    if (kVBf16 && !(__builtin_fabsf(v.x) + __builtin_fabsf(v.y) + __builtin_fabsf(v.z) + __builtin_fabsf(v.w) <= 0x1p100f)) *flag = 1;
     if (whole) {
       const float inv = seen > 0.0f ? 1.0f / sum : 0.0f;
       *reinterpret_cast<uint2*>(a.o + (static_cast<int64_t>(b) * a.Hq + hq0 + r) * D + 4 * ch) = pack4(a.out_type, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
     } else {
       float* const p = a.ws + static_cast<int64_t>(blockIdx.x) * Tile::kSlot;
       *reinterpret_cast<float4*>(p + r * D + 4 * ch) = v;
-      if (ch == 0) *reinterpret_cast<float4*>(p + 16 * D + 4 * r) = make_float4(most, sum, seen, 0.0f);
+      if (ch == 0) *reinterpret_cast<float4*>(p + 16 * D + 4 * r) = make_float4(most, sum, seen, shift);
     }
   }
+  if constexpr (kVBf16) {
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(*flag);
+  } else {
+    return false;   // f16 values are too small for it
+  }
+}
+
+template <int D, bool kBf16, bool kQuant, bool kWide>
+__global__ __launch_bounds__((DecodeTile<D, kQuant, kWide>::kThreads), (std::max(1, DecodeTile<D, kQuant, kWide>::kPerCu * DecodeTile<D, kQuant, kWide>::kWaves / 4)))
+void attn_decode_kernel(DecodeArgs a) {
+  using Tile = DecodeTile<D, kQuant, kWide>;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[Tile::kLds];
+  // this workgroup's piece: tiles t0 .. t1 - 1 of the nt of sequence b and virtual head hv
+  int b, hv, len, t0 = 0, t1, nt;
+  if (a.pieces) {
+    const Cut cut(a);
+    int before = 0, f = 0, np = 0;
+    uint64_t here = 0;
+    for (int b0 = 0; b0 < a.B && !here; b0 += 64) {
+      const int ln = cut.len(a, b0 + (threadIdx.x & 63)), n = cut.pieces(ln), sum = lanes_scan(n * a.hv);
+      here = __ballot(before + sum > static_cast<int>(blockIdx.x));
+      if (here) {
+        f = __builtin_ctzll(here);
+        b = b0 + f;
+        len = __builtin_amdgcn_readlane(ln, f);
+        np = __builtin_amdgcn_readlane(n, f);
+        before += __builtin_amdgcn_readlane(sum, f) - np * a.hv;
+      } else {
+        before += __builtin_amdgcn_readlane(sum, 63);
+      }
+    }
+    if (!here) return;   // fewer pieces than the host allowed for
+    const int in = blockIdx.x - before, i = in % np;
+    hv = in / np;
+    nt = tiles_of(len);
+    t0 = static_cast<int>(static_cast<int64_t>(nt) * i / np);
+    t1 = static_cast<int>(static_cast<int64_t>(nt) * (i + 1) / np);
+  } else {
+    b = blockIdx.x / a.hv;
+    hv = blockIdx.x % a.hv;
+    len = __builtin_amdgcn_readfirstlane(seq_len(a, b));
+    t1 = nt = tiles_of(len);
+  }
+
+  const DecodePiece piece{b, hv, len, t0, t1, nt};
+  if (decode_walk<D, kBf16, kQuant, kWide>(a, piece, smem, 0.0f)) decode_walk<D, kBf16, kQuant, kWide>(a, piece, smem, kFar);
 }
 
 // The pieces of one sequence and query head, in the order of the line: their weights first, then D / 4 threads each take 4
@@ -430,7 +475,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(DecodeArgs a) {
   constexpr int kLanes = D / 4, kParts = 256 / kLanes, kSlot = 16 * D + 64;
   __shared__ __attribute__((aligned(16))) float part[kParts][D];
   __shared__ float weight[kMostPieces + 1];
-  __shared__ float sums[3][4];
+  __shared__ float sums[4][4];
   const int b = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq;
   const int h = hq / a.G, hv = h * a.tiles_of_heads + hq % a.G / 16, r = hq % a.G % 16;
   const int tid = threadIdx.x, lane = tid % kLanes, p = tid / kLanes;
@@ -457,17 +502,23 @@ __global__ __launch_bounds__(256) void attn_join_kernel(DecodeArgs a) {
   for (int j = 0; j < kAhead; ++j) u[j] = *reinterpret_cast<const float4*>(piece(std::min(p + j * kParts, pieces - 1)) + r * D + 4 * lane);
   auto state = [&](int i) { return *reinterpret_cast<const float4*>(piece(i) + 16 * D + 4 * r); };
   const float4 mine = state(std::min(tid, pieces - 1));
-  float most = mine.x;
-  for (int i = tid + 256; i < pieces; i += 256) most = __builtin_fmaxf(most, state(i).x);
+  float most = mine.x, least = mine.w;
+  for (int i = tid + 256; i < pieces; i += 256) {
+    const float4 st = state(i);
+    most = __builtin_fmaxf(most, st.x);
+    least = __builtin_fminf(least, st.w);
+  }
 #pragma unroll
   for (int m = 1; m < 64; m *= 2) most = __builtin_fmaxf(most, __shfl_xor(most, m));
-  if ((tid & 63) == 0) sums[0][tid >> 6] = most;
+  least = __any(least != 0.0f) ? kFar : 0.0f;
+  if ((tid & 63) == 0) sums[0][tid >> 6] = most, sums[3][tid >> 6] = least;
   __syncthreads();
   most = __builtin_fmaxf(__builtin_fmaxf(sums[0][0], sums[0][1]), __builtin_fmaxf(sums[0][2], sums[0][3]));
+  least = __builtin_fminf(__builtin_fminf(sums[3][0], sums[3][1]), __builtin_fminf(sums[3][2], sums[3][3]));
   float sum = 0.0f, seen = 0.0f;
   for (int i = tid; i < pieces; i += 256) {
     const float4 st = i == tid ? mine : state(i);
-    const float f = st.x == -__builtin_inff() ? (st.y == st.y ? 0.0f : st.y) : __builtin_amdgcn_exp2f((st.x - most) * c);
+    const float f = state_factor(st, most, c, least);
     weight[i] = f;
     sum += f * st.y;
     seen += st.z;

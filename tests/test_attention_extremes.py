@@ -114,3 +114,56 @@ def test_decode_scales_that_leave_one_weight(n, cache, kind, scale):
     tol = ta.E[o.dtype] * want.abs() + 1.01 * 2.0 ** -16 * (A + want.abs()) + (4 * n + 8) * U * A + 2.0 ** -25
     err = (o[0].double() - want).abs()
     assert bool((err <= tol).all()), f"{float((err / tol).max()):.3g} of the tolerance"
+
+
+# ------------------------------------------------------------------------------------------
+def _ends(g, n, D):
+    """Values up to the largest that bf16 holds, both signs, and ordinary ones."""
+    x = (2 * torch.rand((n, 1, D), generator=g) - 1) * 3.38e38
+    x[:, :, 1] = 3.3895313892515355e38
+    x[:, :, 2::4] = torch.randn((n, 1, len(range(2, D, 4))), generator=g)
+    x[:, :, 3::4] *= 1e-20
+    return x
+
+
+@pytest.mark.parametrize("scale", [1e-6, 0.125, 3.0])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("lens", [[300, 40, 1], [700, 20], [5000, 300]])
+def test_decode_largest_values(lens, D, cache, scale):
+    """A mean of finite values is finite, whatever their sum is: equal weights, and a maximum that keeps rising along the keys."""
+    g = torch.Generator().manual_seed(sum(lens) + D)
+    page = 16
+    need = [-(-n // page) for n in lens]
+    pages = sum(need) + 1
+    order = torch.randperm(pages, generator=g).to(I32)
+    table = torch.full((len(lens), max(need)), -1, dtype=I32)
+    kc = torch.full((pages, 1, page, D), math.nan, dtype=BF16)
+    vc, vs = kc.clone(), torch.full((pages, 1, page), math.nan)
+    ks, code = vs.clone(), [torch.full((pages, 1, page, D), 0x7F, dtype=U8) for _ in range(2)]
+    rows, at = [[], []], 0
+    for b, n in enumerate(lens):
+        table[b, :need[b]] = order[at:at + need[b]]
+        at += need[b]
+        k = torch.randn((n, 1, D), generator=g)
+        k[:, 0, 0] = torch.linspace(-40, 40, n)
+        v = _ends(g, n, D) if b < 2 else torch.randn((n, 1, D), generator=g)
+        p, r = table[b].long()[torch.arange(n) // page], torch.arange(n) % page
+        for w, x in enumerate((k, v)):
+            if cache == "e4m3":
+                s = x.abs().amax(-1) / 448
+                c = (x / s[..., None]).to(E4M3)
+                code[w][p, :, r], (ks, vs)[w][p, :, r] = c.view(U8), s
+                rows[w].append(c.double() * s.double()[..., None])
+            else:
+                x = x.to(BF16)
+                (kc, vc)[w][p, :, r] = x
+                rows[w].append(x.double())
+    q = torch.randn((len(lens), 4, D), generator=g)
+    q[:, :, 0] = 30
+    q = q.to(BF16).cuda()
+    dev = [c.cuda() for c in (code if cache == "e4m3" else (kc, vc))]
+    sc = [ks.cuda(), vs.cuda()] if cache == "e4m3" else [None, None]
+    o = pq.attn_decode(q, *dev, table.cuda(), _i32(*lens), *sc, scale=scale)
+    assert bool(torch.isfinite(o).all())
+    ta._check_decode(o, q, rows, lens, float(torch.tensor(scale, dtype=torch.float32)), "largest values")
