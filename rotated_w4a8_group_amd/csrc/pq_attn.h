@@ -146,7 +146,8 @@ __device__ __forceinline__ void lane_values(const uint8_t* row, float s, float (
   for (int i = 0; i < D / 64; ++i) v[i] = s * __builtin_amdgcn_cvt_f32_fp8(row[lane * (D / 64) + i], 0);
 }
 
-// Running softmax of one query row: the largest score so far, the sum of exp2(c (score - largest)) and the weighted values.
+// Running softmax of one query row: the largest score so far, the sum of exp2(c (score - largest)) and the mean of the values so
+// far under these weights - a mean, as the weighted sum of finite values may pass binary32 where their mean does not.
 template <int D>
 struct RowState {
   float m = -__builtin_inff(), l = 0.0f, o[D / 64] = {};
@@ -156,18 +157,20 @@ struct RowState {
     const float p = s == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(c * (s - n));
     m = n;
     l = l * f + p;
+    if (l == 0.0f) return;           // scores of -inf alone so far
+    const float w = p / l, rest = 1.0f - w;
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) o[i] = o[i] * f + p * v[i];
+    for (int i = 0; i < D / 64; ++i) o[i] = o[i] * rest + v[i] * w;
   }
 };
 
 template <int D>
 __device__ __forceinline__ void store_row(uint16_t* out, const RowState<D>& r, bool any, int out_type) {
   const int lane = threadIdx.x & 63;
-  const float inv = any ? 1.0f / r.l : 0.0f;
+  const float none = r.l > 0.0f ? 0.0f : __builtin_nanf("");   // no weight at all, or NaN
 #pragma unroll
   for (int i = 0; i < D / 64; ++i) {
-    const float v = any ? r.o[i] * inv : 0.0f;
+    const float v = any ? r.o[i] + none : 0.0f;
     out[lane * (D / 64) + i] = static_cast<uint16_t>(out_type == PQ_BF16 ? pack2<true>(v, v) : pack2<false>(v, v));
   }
 }

@@ -167,3 +167,18 @@ def test_decode_largest_values(lens, D, cache, scale):
     o = pq.attn_decode(q, *dev, table.cuda(), _i32(*lens), *sc, scale=scale)
     assert bool(torch.isfinite(o).all())
     ta._check_decode(o, q, rows, lens, float(torch.tensor(scale, dtype=torch.float32)), "largest values")
+
+
+@pytest.mark.parametrize("scale", [1e-6, 0.125, 3.0])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("nq,nk", [(70, 70), (20, 3000)])
+def test_prefill_largest_values(nq, nk, D, scale):
+    g = torch.Generator().manual_seed(nk + D)
+    k = torch.randn((nk, 1, D), generator=g)
+    k[:, 0, 0] = torch.linspace(-40, 40, nk)
+    q = torch.randn((nq, 2, D), generator=g)
+    q[:, :, 0] = 30
+    q, k, v = q.to(BF16).cuda(), k.to(BF16).cuda(), _ends(g, nk, D).to(BF16).cuda()
+    o = pq.attn_prefill(q, k, v, _i32(0, nq), _i32(0, nk), scale=scale)
+    assert bool(torch.isfinite(o).all())
+    ta._check_prompts(o, q, k, v, [(nq, nk)], 0, True, float(torch.tensor(scale, dtype=torch.float32)), "largest values")
