@@ -9,7 +9,7 @@
 //                 the contraction is free, a lane's own 8 are taken as they lie - P never leaves its registers - and V^T
 //                 follows that order: two transposing LDS reads of 4 keys each per 16 keys and 32 channels.
 // Scores, sums and O are binary32. P is rounded to v's type for the second product (half a step of it, 2^-8 or 2^-11 of each
-// weight), which is what the output's own rounding costs. Only where o is f16 and v bf16 would it be the larger by far (6.6e-4 of the norm
+// weight, and 2^-32 of the largest for f16: kF16Lift), which is what the output's own rounding costs. Only where o is f16 and v bf16 would it be the larger by far (6.6e-4 of the norm
 // against 1.9e-4): there P is held in two bf16 pieces (2^-16), each with a product of its own, for 27 to 42 % more time (9 packed
 // prompts 92 -> 117 us, 8192 rows 780 -> 1087, 512 of 256 channels behind 8191 128 -> 167, 4096 rows of 24 heads of 64 69 -> 99).
 //
@@ -17,7 +17,7 @@
 // that the 16 lanes of an operand read, and the 4 keys of a transposing one, lie in different banks.
 //
 // The score m that p = exp2(c (s - m)) is taken against is the largest of the first tile and is raised only where the weights of a
-// tile pass what their type holds with room to spare (their sum 2^60, f16 2^15: a wave-wide vote): the softmax does not depend
+// tile pass what their type holds (their sum 2^60, or an f16 one its type: a wave-wide vote): the softmax does not depend
 // on m, sums and O are binary32, and neither the maximum nor a rescaling of O is part of an ordinary tile. The sum takes the rounded p, so
 // a rounding moves weight between values and leaves their sum at 1. Keys that a query does not see get the score -inf, in the tiles
 // that need it only. Their values still enter the product, with weight 0: a row whose result is not finite is
@@ -60,6 +60,12 @@ __device__ __forceinline__ f32x16 mfma_32(const attn_u32x4& a, const attn_u32x4&
   if constexpr (kBf16) return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
   else return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
+
+// log2 of what f16 weights are taken times, which divides out: f16 reaches down to 2^-24 and up to 2^16, and the largest score of the first
+// tile would be 1. What rounding takes from a small weight is then 2^-32 of the largest at most, less than the output's rounding beside 1e6 such
+// keys. (0, 7, 10, 13: 8192 rows of 48 heads of 128 810, 821, 830, 859 us; 9 packed prompts 95, 97, 99, 103; later maxima pass what
+// is left above sooner, and a tile's weights are taken twice.)
+constexpr float kF16Lift = 7.0f;
 
 // a b, rounded to binary32 and not fused with what follows.
 __device__ __forceinline__ float rounded_product(float a, float b) {
@@ -227,6 +233,7 @@ template <int D, bool kBf16, bool kSplit>
 __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(PrefillArgs a) {
   using Tile = PrefillTile<D>;
   constexpr int kDB = D / 32, kKB = Tile::kKeys / 32, kSteps = D / 16;
+  constexpr float kLift = kBf16 ? 0.0f : kF16Lift;
   constexpr bool kOpaque = D == 256;   // registers: at 128 channels the 1 % that it costs buys nothing
   __shared__ __attribute__((aligned(1024))) uint8_t smem[Tile::kLds];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -340,7 +347,7 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(PrefillArgs a) {
       mt = both_halves_max(mt);
       // The weights so far were taken against mc as it was rounded, so the factor is the difference of the rounded ones (fused with
       // a product it would be that of others, off by 2^(half a step of mc)).
-      const float to = mt == -__builtin_inff() ? 0.0f : rounded_product(mt, c), f = m == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(mc - to);
+      const float to = mt == -__builtin_inff() ? 0.0f : rounded_product(mt, c) - kLift, f = m == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(mc - to);
       m = mt;
       mc = to;
       l *= f;
@@ -387,7 +394,7 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(PrefillArgs a) {
     for (int e = 0; e < kReadV; ++e) vf[e] = read_v(e);
     if (fresh) raise();
     weights();
-    if (__any(!(sum <= (kBf16 ? 0x1p60f : 0x1p15f)))) {
+    if (__any(!(sum <= 0x1p60f))) {   // an f16 weight past its type is an infinity, and so is the sum
       raise();
       weights();
     }

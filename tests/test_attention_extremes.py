@@ -182,3 +182,44 @@ def test_prefill_largest_values(nq, nk, D, scale):
     o = pq.attn_prefill(q, k, v, _i32(0, nq), _i32(0, nk), scale=scale)
     assert bool(torch.isfinite(o).all())
     ta._check_prompts(o, q, k, v, [(nq, nk)], 0, True, float(torch.tensor(scale, dtype=torch.float32)), "largest values")
+
+
+# ------------------------------------------------------------------------------------------
+LN2 = float(torch.tensor(math.log(2), dtype=torch.float32))   # as a scale: its product with log2(e) rounds to 1 in binary32
+GAPS = [0.0, 8.0, 14.5, 17.5, 20.5, 23.5, 25.0, 27.0]          # powers of two between one key's weight and every other's
+
+
+def _one_large(g, n, D, at):
+    """q [1, heads, D], k, v [n, 1, D]: with scale LN2 head h's weights are 1 at the keys `at` and 2^-GAPS[h] at all others; the first kind's values are 0,
+    the others' have a mean of about 1.5: the output is what the small weights sum to."""
+    k, v = torch.zeros((n, 1, D)), torch.randint(0, 4, (n, 1, D), generator=g).float()
+    k[at, 0, 0], v[at] = 1, 0
+    q = torch.zeros((1, len(GAPS), D))
+    q[0, :, 0] = torch.tensor(GAPS)
+    return q.to(F16).cuda(), k, v
+
+
+def _check_small_weights(o, q, k, v, e_p, floor, what):
+    """test_attention's tolerance but for two terms. `floor`: what rounding takes from a weight at most, relative to the largest (there 2^-25).
+    (4 n + 8) u is for sums of n terms in any order; here n is 1e5, and no chain of additions is longer than a lane's keys, a quarter of its wave's,
+    which has half of them at most, and one for each wave and piece: (n / 8 + 1200) u between both sums."""
+    n, D = k.shape
+    want, Q, A, S = ta._reference(q.double(), k.double(), v.double(), LN2, torch.ones((q.shape[0], n), dtype=torch.bool, device="cuda"))
+    tol = ta.E[o.dtype] * want.abs() + 1.01 * (2 * (2 * (2 * D + 4) * U * Q + 4 * U) + (n / 8 + 1200) * U) * A + 1.01 * e_p * (A + want.abs()) + 2.0 ** -25
+    tol = tol + 1.01 * floor * (S + n * want.abs())
+    worst = ((o.double() - want).abs() / tol).amax(-1)
+    assert bool((worst <= 1).all()), f"{what}: {[f'{float(w):.2f}' for w in worst]} of the tolerance"
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("at", [0, 70000, 131070])
+@pytest.mark.parametrize("beside", [0, 520])
+def test_prefill_weights_far_below_the_largest(D, at, beside):
+    """f16 weights, taken 2^7 times as large, so that 2^-25 is 2^-32 of the largest: cut along the keys, and whole beside many other sequences."""
+    g, n = torch.Generator().manual_seed(D), 131071
+    q, k, v = _one_large(g, n, D, at)
+    more = torch.ones((beside, 1, D))
+    o = pq.attn_prefill(torch.cat([q] + [q] * beside), torch.cat([k, more]).to(F16).cuda(), torch.cat([v, more]).to(F16).cuda(),
+                        torch.arange(beside + 2, dtype=I32, device="cuda"), _i32(0, *range(n, n + beside + 1)), scale=LN2)
+    _check_small_weights(o[0], q[0], k[:, 0].cuda(), v[:, 0].cuda(), 2.0 ** -11, 2.0 ** -32, "prefill")
+    assert bool((o[1:] == 1).all())
