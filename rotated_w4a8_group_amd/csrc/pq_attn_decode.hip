@@ -10,7 +10,8 @@
 //                 transposing LDS reads of that order.
 // Codes become 16-bit values, exactly, on their way from LDS to the matrix core (of q's type for K, bf16 for V); a key's
 // scale multiplies its score, a value's its weight. p is held in two 16-bit pieces, hi + lo, each with a product of its
-// own: the matrix core has the time, and no rounding of p shows in an f16 output (2^-16 of it is left).
+// own: the matrix core has the time, and no rounding of p shows in an f16 output (2^-16 of it is left; of f16 pieces 2^-32 of the
+// largest weight, where that is more: kF16Lift).
 //
 // Work is split over the cache's length: each head's tiles of a sequence are cut into pieces of at most a share of all of them
 // (Cut), a workgroup each, whatever the lengths. A piece that is not the whole head leaves its maximum, sum and O in the
@@ -124,6 +125,10 @@ __device__ __forceinline__ float four_groups(float v, F f) {
 // log2 of the factor of a second walk: 2^31 weights of up to 2^8 times values of up to 2^128 stay below 2^120, and the weights
 // are bf16 with 2^-78 of the largest one still normal.
 constexpr float kFar = -48.0f;
+
+// log2 of what the weights of f16 values are taken times, which divides out: m is raised before one passes 2^8, so 2^15 of f16's 2^16 are used, and its
+// 2^-25 is 2^-32 of the largest weight.
+constexpr float kF16Lift = 7.0f;
 
 // What a state (maximum, sum, seen, log2 of its weights' factor) counts beside others: with the largest maximum and the least factor.
 __device__ __forceinline__ float state_factor(const float4& st, float most, float c, float least) {
@@ -334,7 +339,7 @@ __device__ __forceinline__ bool decode_walk(const DecodeArgs& a, const DecodePie
         float p[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          p[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i + k] - ref, c, shift));   // the difference first: 0 at the largest score, whatever the scale
+          p[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i + k] - ref, c, kVBf16 ? shift : kF16Lift));   // the difference first: 0 at the largest score, whatever the scale
           l += p[k];
           if constexpr (kQuant) p[k] *= vs[kb][i + k];
         }

@@ -223,3 +223,17 @@ def test_prefill_weights_far_below_the_largest(D, at, beside):
                         torch.arange(beside + 2, dtype=I32, device="cuda"), _i32(0, *range(n, n + beside + 1)), scale=LN2)
     _check_small_weights(o[0], q[0], k[:, 0].cuda(), v[:, 0].cuda(), 2.0 ** -11, 2.0 ** -32, "prefill")
     assert bool((o[1:] == 1).all())
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("at", [(0,), (0, 32768, 65536, 98304), (131070,)])
+@pytest.mark.parametrize("B", [1, 2048])
+def test_decode_weights_far_below_the_largest(D, at, B):
+    """An f16 cache: both pieces of a weight are f16, taken 2^7 times as large as the weight, so 2^-25 is 2^-32 of the largest. One sequence,
+    cut into pieces that most hold small weights only, and so many on the same pages that each is whole, with a large one in each wave's part."""
+    g, n = torch.Generator().manual_seed(D), 131071
+    q, k, v = _one_large(g, n, D, list(at))
+    c, table, _ = _cache(g, n, D, "f16", k, v)
+    o = pq.attn_decode(q.expand(B, -1, -1).contiguous(), *c, table.expand(B, -1).contiguous(), torch.full((B,), n, dtype=I32, device="cuda"), scale=LN2)
+    _check_small_weights(o[0], q[0], k[:, 0].cuda(), v[:, 0].cuda(), 2.0 ** -16, 2.0 ** -32, "decode")
+    assert torch.equal(o, o[:1].expand(B, -1, -1))
