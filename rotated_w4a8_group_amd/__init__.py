@@ -927,6 +927,11 @@ def _attn_out(out, dtype, q, what="out"):
     return dtype, _type_code(dtype, what), [] if out is None else [(out, what, dtype, tuple(q.shape))]
 
 
+def _score_scale(scale, D):
+    """The scale of the scores, D ** -0.5 by default; a head of no channels is the library's to refuse."""
+    return (D ** -0.5 if D else 1.0) if scale is None else float(scale)
+
+
 def attn_decode_workspace_bytes(B, Hq, Hkv, D):
     """Bytes of the workspace of ``attn_decode``."""
     if B > INT_MAX or Hq > INT_MAX or Hkv > INT_MAX or D > INT_MAX:
@@ -971,7 +976,7 @@ def attn_decode(q, k_cache, v_cache, block_table, lengths, k_scale=None, v_scale
         workspace = _new((need,), torch.uint8, q.device, stream)
     _launch("pq_attn_decode", q.device, stream, q.data_ptr(), ldq, hsq, _type_code(q.dtype, "q"), k_cache.data_ptr(), v_cache.data_ptr(),
             _addr(k_scale), _addr(v_scale), pages, page, block_table.data_ptr(), width, lengths.data_ptr(), B, Hq, Hkv, D,
-            D ** -0.5 if scale is None else float(scale), out.data_ptr(), code, _addr(workspace), workspace.numel() if workspace is not None else 0)
+            _score_scale(scale, D), out.data_ptr(), code, _addr(workspace), workspace.numel() if workspace is not None else 0)
     return out
 
 
@@ -1022,7 +1027,7 @@ def attn_prefill(q, k, v, cu_q, cu_k=None, scale=None, causal=True, out=None, dt
     if workspace is None and need:
         workspace = _new((need,), torch.uint8, q.device, stream)
     _launch("pq_attn_prefill", q.device, stream, q.data_ptr(), ldq, hsq, k.data_ptr(), ldk, hsk, v.data_ptr(), ldv, hsv, _type_code(q.dtype, "q"),
-            cu_q.data_ptr(), cu_k.data_ptr(), B, Tq, Tk, Hq, Hkv, D, D ** -0.5 if scale is None else float(scale), 1 if causal else 0,
+            cu_q.data_ptr(), cu_k.data_ptr(), B, Tq, Tk, Hq, Hkv, D, _score_scale(scale, D), 1 if causal else 0,
             out.data_ptr(), code, _addr(workspace), workspace.numel() if workspace is not None else 0)
     return out
 

@@ -237,3 +237,13 @@ def test_decode_weights_far_below_the_largest(D, at, B):
     o = pq.attn_decode(q.expand(B, -1, -1).contiguous(), *c, table.expand(B, -1).contiguous(), torch.full((B,), n, dtype=I32, device="cuda"), scale=LN2)
     _check_small_weights(o[0], q[0], k[:, 0].cuda(), v[:, 0].cuda(), 2.0 ** -16, 2.0 ** -32, "decode")
     assert torch.equal(o, o[:1].expand(B, -1, -1))
+
+
+def test_head_size_zero_is_refused_on_a_stream_too():
+    z, s = torch.zeros((2, 4, 0), dtype=F16, device="cuda"), torch.cuda.current_stream()
+    c, t = torch.zeros((3, 4, 16, 0), dtype=F16, device="cuda"), torch.zeros((2, 1), dtype=I32, device="cuda")
+    for stream in (None, s):
+        with pytest.raises(pq.PQError):
+            pq.attn_decode(z, c, c.clone(), t, _i32(1, 1), stream=stream)
+        with pytest.raises(pq.PQError):
+            pq.attn_prefill(z, z, z.clone(), _i32(0, 2), stream=stream)
