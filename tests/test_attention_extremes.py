@@ -247,3 +247,35 @@ def test_head_size_zero_is_refused_on_a_stream_too():
             pq.attn_decode(z, c, c.clone(), t, _i32(1, 1), stream=stream)
         with pytest.raises(pq.PQError):
             pq.attn_prefill(z, z, z.clone(), _i32(0, 2), stream=stream)
+
+
+# ------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("nq,nk", [(50, 50), (40, 3000)])
+def test_prefill_infinite_values_keep_their_sign(kind, D, bad, nq, nk):
+    """An infinite value that a row sees, at scores whose weights are far from binary32's ends: that infinity in its channel, whole and cut."""
+    g = torch.Generator().manual_seed(D)
+    q, k, v, cu_q, cu_k = ta._prompts(g, [(nq, nk)], 4, 2, D, ta.TYPES[kind])
+    at = nk - 15                                             # seen from row nq - 15 on, by the heads of key head 0
+    v[at, 0, 5] = bad
+    o = pq.attn_prefill(q, k, v, cu_q, cu_k, scale=0.02)
+    rest = [c for c in range(D) if c != 5]
+    seen = o[nq - 15:, :2]
+    assert bool(torch.isnan(seen[:, :, 5]).all()) if math.isnan(bad) else bool((seen[:, :, 5] == bad).all())
+    assert bool(torch.isfinite(seen[:, :, rest]).all()) and bool(torch.isfinite(o[:nq - 15]).all()) and bool(torch.isfinite(o[:, 2:]).all())
+
+
+@pytest.mark.parametrize("nq,nk", [(50, 50), (40, 3000)])
+def test_prefill_infinite_values_of_no_weight(nq, nk):
+    """An infinite value whose weight is below what binary32 holds: NaN in its channel, as 0 times an infinity is, and nothing in others."""
+    g = torch.Generator().manual_seed(3)
+    q, k, v, cu_q, cu_k = ta._prompts(g, [(nq, nk)], 2, 1, 64, BF16)
+    k[:, 0], q[:, :, 0], v[0, 0, 5] = 0, 8, math.inf
+    k[1:, 0, 0] = 8                                          # key 0 is 64 scale below all others
+    o = pq.attn_prefill(q, k, v, cu_q, cu_k, scale=4.0)
+    seen = o[1 if nq == nk else 0:]                          # row 0 of the first sees key 0 alone
+    assert bool(torch.isnan(seen[:, :, 5]).all()) and bool(torch.isfinite(o[:, :, :5]).all()) and bool(torch.isfinite(o[:, :, 6:]).all())
+    if nq == nk:
+        assert bool((o[0, :, 5] == math.inf).all())
