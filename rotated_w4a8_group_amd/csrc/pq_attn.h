@@ -139,12 +139,6 @@ __device__ __forceinline__ void lane_values(const uint16_t* row, float (&v)[D / 
     v[i] = kBf16 ? bf16_to_f32(w) : f16_to_f32(w);
   }
 }
-template <int D>
-__device__ __forceinline__ void lane_values(const uint8_t* row, float s, float (&v)[D / 64]) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int i = 0; i < D / 64; ++i) v[i] = s * __builtin_amdgcn_cvt_f32_fp8(row[lane * (D / 64) + i], 0);
-}
 
 // Running softmax of one query row: the largest score so far, the sum of exp2(c (score - largest)) and the mean of the values so
 // far under these weights - a mean, as the weighted sum of finite values may pass binary32 where their mean does not.
@@ -188,7 +182,7 @@ inline int overlap(const char* what) { return set_error(PQ_ERR_SHAPE, "%s: an ou
 int check_cache(const char* what, const void* kc, const void* vc, const float* ks, const float* vs, int64_t pages, int page, int Hkv, int D);
 int64_t cache_bytes(const float* scales, int64_t pages, int page, int Hkv, int D);
 int64_t scale_bytes(const float* scales, int64_t pages, int page, int Hkv);
-int check_heads(const char* what, const char* name, const void* p, int64_t ld, int64_t hs, int T, int H, int D);
+int check_heads(const char* what, const char* name, const void* p, int64_t ld, int64_t hs, int T);
 inline int check_attention(const char* what, int type, int out_type, int Hq, int Hkv, int D, float scale) {
   if ((type != PQ_F16 && type != PQ_BF16) || (out_type != PQ_F16 && out_type != PQ_BF16))
     return set_error(PQ_ERR_SHAPE, "%s: types (%d, out %d): f16 or bf16", what, type, out_type);

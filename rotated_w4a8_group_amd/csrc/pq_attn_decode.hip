@@ -626,7 +626,7 @@ int pq_attn_decode(const uint16_t* q_d, int64_t ldq, int64_t hsq, int type, cons
   if (B < 0 || width < 0) return set_error(PQ_ERR_SHAPE, "%s: B=%d, width=%d: negative", what, B, width);
   int rc = check_attention(what, type, out_type, Hq, Hkv, D, scale);
   if (rc == PQ_OK) rc = check_cache(what, kc_d, vc_d, ks_d, vs_d, pages, page, Hkv, D);
-  if (rc == PQ_OK) rc = check_heads(what, "q", q_d, ldq, hsq, B, Hq, D);
+  if (rc == PQ_OK) rc = check_heads(what, "q", q_d, ldq, hsq, B);
   if (rc != PQ_OK) return rc;
   if (static_cast<int64_t>(B) * Hq * 512 > 0xFFFFFFFFll)   // the runtime counts a launch's threads in 32 bits
     return set_error(PQ_ERR_SHAPE, "%s: B=%d sequences of %d heads too many for one call", what, B, Hq);

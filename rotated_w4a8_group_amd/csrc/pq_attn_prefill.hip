@@ -570,9 +570,9 @@ int pq_attn_prefill(const uint16_t* q_d, int64_t ldq, int64_t hsq, const uint16_
   const char* what = "pq_attn_prefill";
   if (B < 0 || Tq < 0 || Tk < 0) return set_error(PQ_ERR_SHAPE, "%s: B=%d, Tq=%d, Tk=%d: negative", what, B, Tq, Tk);
   int rc = check_attention(what, type, out_type, Hq, Hkv, D, scale);
-  if (rc == PQ_OK) rc = check_heads(what, "q", q_d, ldq, hsq, Tq, Hq, D);
-  if (rc == PQ_OK) rc = check_heads(what, "k", k_d, ldk, hsk, Tk, Hkv, D);
-  if (rc == PQ_OK) rc = check_heads(what, "v", v_d, ldv, hsv, Tk, Hkv, D);
+  if (rc == PQ_OK) rc = check_heads(what, "q", q_d, ldq, hsq, Tq);
+  if (rc == PQ_OK) rc = check_heads(what, "k", k_d, ldk, hsk, Tk);
+  if (rc == PQ_OK) rc = check_heads(what, "v", v_d, ldv, hsv, Tk);
   if (rc != PQ_OK) return rc;
   if (Tq > kMostRows || Tk > kMostRows) return set_error(PQ_ERR_SHAPE, "%s: Tq=%d, Tk=%d: at most 2^30 rows", what, Tq, Tk);
   if ((Tq / 128 + static_cast<int64_t>(B)) * Hq * 256 > 0xFFFFFFFFll)   // the runtime counts a launch's threads in 32 bits

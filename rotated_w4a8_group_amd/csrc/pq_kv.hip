@@ -196,7 +196,7 @@ int check_cache(const char* what, const void* kc, const void* vc, const float* k
   return PQ_OK;
 }
 
-int check_heads(const char* what, const char* name, const void* p, int64_t ld, int64_t hs, int T, int H, int D) {
+int check_heads(const char* what, const char* name, const void* p, int64_t ld, int64_t hs, int T) {
   if (ld % 8 || hs % 8 || ld < 0 || hs < 0 || ld > kAttnMaxStride || hs > kAttnMaxStride)
     return set_error(PQ_ERR_SHAPE, "%s: strides of %s (%lld, %lld) must be multiples of 8 in 0..2^24", what, name,
                      static_cast<long long>(ld), static_cast<long long>(hs));
@@ -217,8 +217,8 @@ int pq_kv_write(const uint16_t* k_d, int64_t ldk, int64_t hsk, const uint16_t* v
   if (T < 0) return set_error(PQ_ERR_SHAPE, "%s: T=%d < 0", what, T);
   if (type != PQ_F16 && type != PQ_BF16) return set_error(PQ_ERR_SHAPE, "%s: type %d, expected f16 or bf16", what, type);
   int rc = check_cache(what, kc_d, vc_d, ks_d, vs_d, pages, page, Hkv, D);
-  if (rc == PQ_OK) rc = check_heads(what, "k", k_d, ldk, hsk, T, Hkv, D);
-  if (rc == PQ_OK) rc = check_heads(what, "v", v_d, ldv, hsv, T, Hkv, D);
+  if (rc == PQ_OK) rc = check_heads(what, "k", k_d, ldk, hsk, T);
+  if (rc == PQ_OK) rc = check_heads(what, "v", v_d, ldv, hsv, T);
   if (rc != PQ_OK) return rc;
   const int64_t rows = static_cast<int64_t>(T) * Hkv, per = 256 / (D / 8), grid = (rows + per - 1) / per;
   if (grid * 256 > 0xFFFFFFFFll) return set_error(PQ_ERR_SHAPE, "%s: T=%d rows too many for one call (split the rows)", what, T);
