@@ -440,17 +440,22 @@ int pq_kv_read(const void* kc_d, const void* vc_d, const float* ks_d, const floa
  * on key head h / (Hq / Hkv). Scores, maxima, sums and outputs are held in binary32; one rounding where o is stored. What a
  * query does not see has no influence, infinities and NaN included; a query that sees no key gives zeros. An infinite value that is
  * seen gives an infinity of its sign (NaN where its weight is below what binary32 holds), from attn_decode that or NaN, in its channel alone. The weights p enter their
- * product in v's type: attn_prefill's rounded once, but in two bf16 pieces where o is f16 and v bf16; attn_decode's in two pieces.
+ * product in v's type: attn_prefill's rounded once, but in two bf16 pieces where o is f16 and v bf16; attn_decode's in two pieces. What is left of
+ * an f16 weight by that is 2^-32 of the largest at best.
  *
  * pq_attn_decode: one query for each sequence over the paged cache, positions 0 .. lens[b] - 1 through table[b] (as in
  *   pq_kv_read; a position whose page is not one of the cache's is left out, and no length passes width * page).
  *   q_d       f16 or bf16 (type) [B rows], strides as pq_kv_write's k; a cache without scales holds this type.
  *   lens_d    int32 [B].
  *   o_d       out f16 or bf16 (out_type) [B, Hq, D], 16-byte aligned.
+ *   The lengths are not known on the host, so width * page decides how the work is laid out: a table that could hold more than 256 to 1024
+ *   positions, by the size of a row (2048 of many sequences), takes a second launch that joins pieces of heads, 2 to 12 us more where the sequences
+ *   are short.
  * pq_attn_prefill: packed prompts. Sequence b has the queries cu_q[b] .. cu_q[b + 1] - 1 and the keys cu_k[b] .. cu_k[b + 1] - 1
  *   of the Tq and Tk rows (at most 2^30 of each); query i of nq sees the keys j <= i + nk - nq (causal != 0) or all nk of them.
  *   cu_q_d, cu_k_d  int32 [B + 1], ascending; values past Tq and Tk count as those. Rows of o of no sequence are left as they were.
  *   o_d       out f16 or bf16 (out_type) [Tq, Hq, D], 16-byte aligned.
+ *   A row whose sums are not finite, or whose scores times scale pass 7e8, is computed again key by key, some hundred times slower.
  *
  * 0 < scale <= 2^64. Outputs and the workspace overlap no input and each other (PQ_ERR_SHAPE). ws_d: at least pq_attn_*_workspace_bytes() of the device in use,
  * 16-byte aligned (may be NULL where that is 0); its contents need no initialisation and are not kept, so calls that may run at the same

@@ -885,7 +885,8 @@ def kv_read(k_cache, v_cache, block_table, cu, T, k_scale=None, v_scale=None, ou
     """The rows of sequences back from a paged cache (``kv_write``'s): block_table int32 [B, width], the pages of each
     sequence in order; cu int32 [B + 1], where its rows begin in the packed output -> (k, v) [T, Hkv, D] of ``dtype`` (f16 or
     bf16; the cache's own type where it holds 16-bit values, f16 by default otherwise), or into ``out``, a pair of those.
-    Rows of no sequence are left as they were; a position whose page is not one of the cache's reads as zeros."""
+    Rows of no sequence are left as they were - in tensors made here, uninitialised: give ``out`` where what follows reads them; a
+    position whose page is not one of the cache's reads as zeros."""
     f = _native() if _fast is None else _fast
     if f and stream is None:
         done = f.kv_read(k_cache, v_cache, block_table, cu, T, k_scale, v_scale, out, dtype)
@@ -948,7 +949,8 @@ def attn_decode(q, k_cache, v_cache, block_table, lengths, k_scale=None, v_scale
     type by default), or into ``out``. scale: of the scores, D ** -0.5 by default.
 
     A sequence of length 0 gives zeros; positions whose page is not one of the cache's are left out, and no length passes the
-    table's width. What the cache holds behind a sequence's end - infinities and NaN too - does not count."""
+    table's width. What the cache holds behind a sequence's end - infinities and NaN too - does not count. A table much wider than the
+    sequences costs a second launch (1 x 509 positions 9.4 us instead of 7.6): narrow it where they are known to be short."""
     f = _native() if _fast is None else _fast
     if f and stream is None:
         done = f.attn_decode(q, k_cache, v_cache, block_table, lengths, k_scale, v_scale, scale, out, dtype, workspace)
@@ -995,7 +997,8 @@ def attn_prefill(q, k, v, cu_q, cu_k=None, scale=None, causal=True, out=None, dt
     (all with causal=False): the chunk of a prompt whose earlier keys came back through ``kv_read`` is the last nq of nk.
 
     A query that sees no key gives zeros, whatever it does not see does not count (infinities and NaN too), and rows of no
-    sequence are left as they were. scale: of the scores, D ** -0.5 by default."""
+    sequence are left as they were - in a tensor made here, uninitialised: give ``out`` where what follows reads them. scale: of the
+    scores, D ** -0.5 by default. Strides are 2^24 at most."""
     f = _native() if _fast is None else _fast
     if f and stream is None:
         done = f.attn_prefill(q, k, v, cu_q, cu_k, scale, causal, out, dtype, workspace)

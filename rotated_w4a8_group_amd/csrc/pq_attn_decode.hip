@@ -18,9 +18,10 @@
 // workspace, and attn_join_kernel puts the pieces together in their order. Which pieces exist follows from the lengths on
 // the device; the host only bounds them.
 //
-// Measured: 64 sequences of up to 8191 positions (8 heads of 128, 16-bit, 1.04 GB of rows) 178 us, 5.84 TB/s; one of 131071, e4m3
+// Measured: 64 sequences of up to 8192 positions (8 heads of 128, 16-bit, 1.04 GB of rows) 178 us, 5.84 TB/s; one of 131071, e4m3
 // (277 MB) 53 us, 5.2 TB/s; a read of as much memory and nothing else reaches 6.3. Small calls are the waits of one chain: length,
-// page, row, score, and the join's launch (17 sequences of up to 4000, 4 heads of 256, e4m3, 36 MB: 17.5 us).
+// page, row, score, and the join's launch (17 sequences of up to 4000, 4 heads of 256, e4m3, 36 MB: 17.7 us).
+// "n x <= L" below is n sequences, one of length L and the others spread below it as L r^1.5, r uniform: 0.4 L on average.
 #include <algorithm>
 #include <utility>
 
@@ -45,17 +46,17 @@ struct DecodeArgs {
 
 constexpr int kTileKeys = 32;
 // While a piece for every place of the device is at most this many tiles, there are no more pieces than places, each a whole number of
-// tiles for every wave: what a second round costs is the wait of its first loads (8 x 3000 of 4 heads of 256, 16-bit: 2 tiles a piece, 750
-// pieces for 512 places 23 us, 4 tiles 17.2; 4 x 500, 2 tiles 9.9, 4 12, 8 16; 17 x up to 4000 of 4 of 256, e4m3, 5 tiles for 4 waves
-// 17.9, 8 17.5). Longer ones are cut into wanted_pieces() of two tiles a wave at least (16 x 8000 of 4 of 256, 16-bit, 12 tiles in one
-// round 61, 6 in two 51; 12 x 4000 of 8 of 128, 16-bit, 5 tiles 30.5, 8 27.9).
+// tiles for every wave: what a second round costs is the wait of its first loads (8 x <= 3000 of 4 heads of 256, 16-bit: 2 tiles a piece, 750
+// pieces for 512 places 23 us, 4 tiles 17.2; 4 x <= 500, 2 tiles 9.9, 4 12, 8 16; 17 x <= 4000 of 4 of 256, e4m3, 5 tiles for 4 waves
+// 17.9, 8 17.5). Longer ones are cut into wanted_pieces() of two tiles a wave at least (16 x <= 8000 of 4 of 256, 16-bit, 12 tiles in one
+// round 61, 6 in two 51; 12 x <= 4000 of 8 of 128, 16-bit, 5 tiles 30.5, 8 27.9).
 constexpr int kOneRound = 8;
 constexpr int kTableHalves = 128;   // 16-key halves whose pages a wave holds at a time
 constexpr int kMostPieces = 4096;   // of one head
 
 // kWide: as many waves as the LDS holds, for whole heads that are no more than the CUs (1 x 509 of 8 heads of 128, e4m3: 7.5 us, else 9.6; 32 x
-// 1000 11.7, 18.5; 60 x 250 of 4 of 256, 16-bit 12.2, 15.5); else several workgroups a CU (60 x 500 of 8 of 128, 16-bit 15.6, wide 17.4;
-// 128 x 2000, e4m3 53.9, 58.4; but 40 x 1000 18.6, 16.9).
+// <= 1000 11.7, 18.5; 60 x <= 250 of 4 of 256, 16-bit 12.2, 15.5); else several workgroups a CU (60 x <= 500 of 8 of 128, 16-bit 15.6, wide 17.4;
+// 128 x <= 2000, e4m3 53.9, 58.4; but 40 x <= 1000 18.6, 16.9).
 template <int D, bool kQuant, bool kWide>
 struct DecodeTile {
   static constexpr int kRow = D * (kQuant ? 1 : 2);        // bytes of a row
@@ -565,7 +566,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(DecodeArgs a) {
 }
 
 // Pieces that the line is cut into: so many that those workgroups that get their data later than others get fewer, and few enough
-// for the join. (64 ragged sequences of up to 8192, 16-bit, two workgroups a CU: 2, 4, 6, 8 pieces a CU 191, 178, 184, 184 us; one
+// for the join. (64 x <= 8192, 16-bit, two workgroups a CU: 2, 4, 6, 8 pieces a CU 191, 178, 184, 184 us; one
 // of 131071, e4m3, four a CU: 4, 8, 12, 16 pieces 53.7, 58.9, 64, 67.)
 static int wanted_pieces() { return std::min(kMostPieces, 4 * cu_count()); }
 
@@ -583,11 +584,13 @@ template <int D, bool kBf16, bool kQuant>
 static hipError_t decode_launch(DecodeArgs a, hipStream_t s) {
   const int64_t length = static_cast<int64_t>(a.c.width) << a.c.page_shift;
   const int64_t heads = static_cast<int64_t>(a.B) * a.hv;
-  // A head stays in one workgroup, and no join follows, while a wide one's waves have two tiles each (60 x 1000 of 8 heads of 128,
-  // e4m3: 20.6 us, cut 25.9; 20 x 1000 11.1, 13.6; 2 x 500, 16-bit 8.8, 9.5) - one tile where sixteen waves would be few heads' only
-  // ones (1 x 1000, e4m3: 10.4, cut 9.0; 8 x 1000 10.7, 10.5; 1 x 509 7.5, 9.0) - or where there are heads enough to fill half of the
-  // places wanted and none takes so long that the others' end leaves it alone (128 x 2000 of 8 heads of 128, e4m3: 56, cut 63; 100 x 2000,
-  // 16-bit 77, 84; 60 x 2000 50, 55; 40 x 2000, e4m3 33, 29; 100 x 2000 of 4 of 256, 16-bit 91, 86).
+  // By the longest sequence that the table's width allows, as the lengths are on the device (1 x 509 of 8 heads of 128, e4m3 7.6 us, with a table
+  // for 2048 positions or more 9.4; 64 x <= 500, 16-bit 16, for more than 2048 26.6; 128 x <= 2000, e4m3 54.7, 66.9):
+  // a head stays in one workgroup, and no join follows, while a wide one's waves have two tiles each (60 x <= 1000 of 8 heads of 128,
+  // e4m3: 20.6 us, cut 25.9; 20 x <= 1000 11.1, 13.6; 2 x <= 500, 16-bit 8.8, 9.5) - one tile where sixteen waves would be few heads' only
+  // ones (1 x 1000, e4m3: 10.4, cut 9.0; 8 x <= 1000 10.7, 10.5; 1 x 509 7.5, 9.0) - or where there are heads enough to fill half of the
+  // places wanted and none takes so long that the others' end leaves it alone (128 x <= 2000 of 8 heads of 128, e4m3: 56, cut 63; 100 x <= 2000,
+  // 16-bit 77, 84; 60 x <= 2000 50, 55; 40 x <= 2000, e4m3 33, 29; 100 x <= 2000 of 4 of 256, 16-bit 91, 86).
   using Wide = DecodeTile<D, kQuant, true>;
   const int waves = Wide::kWaves, tiles = waves < 16 || heads > cu_count() / 8 ? 2 : 1;
   if (length <= (heads >= wanted_pieces() / 2 ? 2048 : tiles * kTileKeys * waves))

@@ -10,8 +10,9 @@
 //                 follows that order: two transposing LDS reads of 4 keys each per 16 keys and 32 channels.
 // Scores, sums and O are binary32. P is rounded to v's type for the second product (half a step of it, 2^-8 or 2^-11 of each
 // weight, and 2^-32 of the largest for f16: kF16Lift), which is what the output's own rounding costs. Only where o is f16 and v bf16 would it be the larger by far (6.6e-4 of the norm
-// against 1.9e-4): there P is held in two bf16 pieces (2^-16), each with a product of its own, for 27 to 42 % more time (9 packed
-// prompts 92 -> 117 us, 8192 rows 780 -> 1087, 512 of 256 channels behind 8191 128 -> 167, 4096 rows of 24 heads of 64 69 -> 99).
+// against 1.9e-4): there P is held in two bf16 pieces (2^-16), each with a product of its own, for 28 to 38 % more time (9 packed
+// prompts 93 -> 119 us, 8192 rows 762 -> 1053, 512 of 256 channels behind 8191 126 -> 165, 4096 rows of 24 heads of 64 71 -> 97; f16 inputs
+// 96, 811, 133.5, 73.5). Figures beside each other here and below are of one run; runs on other boards differ by up to 8 %.
 //
 // K and V tiles go global -> LDS by direct loads, row-major with the 16-byte chunks of a row permuted (kswizzle, vswizzle) so
 // that the 16 lanes of an operand read, and the 4 keys of a transposing one, lie in different banks.
@@ -102,7 +103,8 @@ struct PrefillTile {
 };
 
 // One row key by key, exactly as the formula reads: keys j < keys, four of them loaded together. A query that is not finite has no
-// finite weight: its result is NaN.
+// finite weight: its result is NaN. This is for the rare row, a wave each, and slow: a NaN in the first value of 8192 rows, which all rows of its 6
+// query heads see, makes 306 ms of 0.8, in the first of 2048 23 ms of 0.08; an infinity in the last of 8192, which the rows of its tile load, 97.
 template <int D, bool kBf16>
 __device__ __forceinline__ void attend_row(const PrefillArgs& a, int64_t t, int hq, int k0, int keys) {
   const int h = hq / (a.Hq / a.Hkv);
