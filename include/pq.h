@@ -439,9 +439,9 @@ int pq_kv_read(const void* kc_d, const void* vc_d, const float* ks_d, const floa
  * Attention (device): o[h] = sum_j p_j v_j, p = softmax over the keys that the query sees of scale * q[h] . k_j, with query head h
  * on key head h / (Hq / Hkv). Scores, maxima, sums and outputs are held in binary32; one rounding where o is stored. What a
  * query does not see has no influence, infinities and NaN included; a query that sees no key gives zeros. An infinite value that is
- * seen gives an infinity of its sign (NaN where its weight is below what binary32 holds), from attn_decode that or NaN, in its channel alone. The weights p enter their
- * product in v's type: attn_prefill's rounded once, but in two bf16 pieces where o is f16 and v bf16; attn_decode's in two pieces. What is left of
- * an f16 weight by that is 2^-32 of the largest at best.
+ * seen gives an infinity of its sign (NaN where its weight is below what binary32 holds), from attn_decode that or NaN, in its channel
+ * alone. The weights p enter their product in v's type: attn_prefill's rounded once, but in two bf16 pieces where o is f16 and v bf16;
+ * attn_decode's in two pieces. An f16 weight, or its last piece, is off by up to 2^-32 of the largest weight besides, however small it is.
  *
  * pq_attn_decode: one query for each sequence over the paged cache, positions 0 .. lens[b] - 1 through table[b] (as in
  *   pq_kv_read; a position whose page is not one of the cache's is left out, and no length passes width * page).

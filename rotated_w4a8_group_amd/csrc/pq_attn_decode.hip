@@ -123,18 +123,18 @@ __device__ __forceinline__ float four_groups(float v, F f) {
   return f(x.lo, x.hi);
 }
 
-// log2 of the factor of a second walk: 2^31 weights of up to 2^8 times values of up to 2^128 stay below 2^120, and the weights
-// are bf16 with 2^-78 of the largest one still normal.
-constexpr float kFar = -48.0f;
+// What values are taken times in a second walk: 2^31 weights of up to 2^8 times values of up to 2^128 stay below 2^120. (Smaller weights instead would
+// lose those of large values; of values this takes 2^-69 a key at most, beside sums past 2^100.)
+constexpr float kSmaller = 0x1p-48f;
 
 // log2 of what the weights of f16 values are taken times, which divides out: m is raised before one passes 2^8, so 2^15 of f16's 2^16 are used, and its
 // 2^-25 is 2^-32 of the largest weight.
 constexpr float kF16Lift = 7.0f;
 
-// What a state (maximum, sum, seen, log2 of its weights' factor) counts beside others: with the largest maximum and the least factor.
-__device__ __forceinline__ float state_factor(const float4& st, float most, float c, float least) {
+// What a state (maximum, sum, seen, the factor of its O) counts beside others, with the largest maximum.
+__device__ __forceinline__ float state_factor(const float4& st, float most, float c) {
   if (st.x == -__builtin_inff()) return st.y == st.y ? 0.0f : st.y;
-  return __builtin_amdgcn_exp2f(__builtin_fmaf(st.x - most, c, least - st.w));
+  return __builtin_amdgcn_exp2f((st.x - most) * c);
 }
 
 // Positions and tiles of a sequence.
@@ -164,12 +164,12 @@ struct DecodePiece {
   int b, hv, len, t0, t1, nt;
 };
 
-// Walks the piece's tiles and stores what they give, with all weights (and so sums and O) 2^shift times as large. Whether a sum passed 2^100, or a
-// NaN came: it may have passed binary32 on the way, or will beside other pieces', though the mean does not. Such a piece is walked a second
-// time with kFar. (The second call is code of its own: as a loop around one, its registers cost the first walk 5 %. What a thread's
-// number gives is computed in each, not kept for the second.)
-template <int D, bool kBf16, bool kQuant, bool kWide>
-__device__ __forceinline__ bool decode_walk(const DecodeArgs& a, const DecodePiece& piece, uint8_t* smem, float shift) {
+// Walks the piece's tiles and stores what they give. Whether a sum passed 2^100, or a NaN came: it may have passed binary32 on the way, or will
+// beside other pieces', though the mean does not. Such a piece is walked a second time (kAgain) with values kSmaller times as large. (That is
+// code of its own: as a loop around one walk, its registers cost the first 5 %. What a thread's number gives is computed in each, not
+// kept for the second.)
+template <int D, bool kBf16, bool kQuant, bool kWide, bool kAgain>
+__device__ __forceinline__ bool decode_walk(const DecodeArgs& a, const DecodePiece& piece, uint8_t* smem) {
   using Tile = DecodeTile<D, kQuant, kWide>;
   constexpr int kDB = D / 16, kSteps = D / 32;
   constexpr bool kVBf16 = kQuant || kBf16;
@@ -191,7 +191,7 @@ __device__ __forceinline__ bool decode_walk(const DecodeArgs& a, const DecodePie
   float* const state = reinterpret_cast<float*>(smem + Tile::kWaves * Tile::kWave);
   float* const factors = state + Tile::kState / 4;
   int* const flag = reinterpret_cast<int*>(factors + Tile::kState / 4);
-  if (shift == 0.0f && tid == 0) *flag = 0;   // not by the second walk: waves may still be reading it
+  if (!kAgain && tid == 0) *flag = 0;   // not by the second walk: waves may still be reading it
 
   // this wave's tiles
   const int count = t1 - t0, ta = t0 + static_cast<int>(static_cast<int64_t>(count) * wave / Tile::kWaves),
@@ -299,6 +299,9 @@ __device__ __forceinline__ bool decode_walk(const DecodeArgs& a, const DecodePie
         const float4 ks4 = *reinterpret_cast<const float4*>(sc + 16 * kb + 4 * g), vs4 = *reinterpret_cast<const float4*>(sc + 32 + 16 * kb + 4 * g);
         s[kb] = v4f{s[kb][0] * ks4.x, s[kb][1] * ks4.y, s[kb][2] * ks4.z, s[kb][3] * ks4.w};
         vs[kb][0] = vs4.x, vs[kb][1] = vs4.y, vs[kb][2] = vs4.z, vs[kb][3] = vs4.w;
+        if constexpr (kAgain)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) vs[kb][i] *= kSmaller;
       }
     }
     wait_lds_reads();                 // K's slot is free
@@ -340,7 +343,7 @@ __device__ __forceinline__ bool decode_walk(const DecodeArgs& a, const DecodePie
         float p[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          p[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i + k] - ref, c, kVBf16 ? shift : kF16Lift));   // the difference first: 0 at the largest score, whatever the scale
+          p[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i + k] - ref, c, kVBf16 ? 0.0f : kF16Lift));   // the difference first: 0 at the largest score, whatever the scale
           l += p[k];
           if constexpr (kQuant) p[k] *= vs[kb][i + k];
         }
@@ -374,6 +377,13 @@ __device__ __forceinline__ bool decode_walk(const DecodeArgs& a, const DecodePie
         const uint2 v0 = lds_read_transposed(vslot + r * Tile::kRow + 16 * (ch ^ Tile::vswizzle(r)) + 8 * (lane & 1));
         const uint2 v1 = lds_read_transposed(vslot + (r + 16) * Tile::kRow + 16 * (ch ^ Tile::vswizzle(r + 16)) + 8 * (lane & 1));
         w = attn_u32x4{v0.x, v0.y, v1.x, v1.y};
+        if constexpr (kAgain) {
+          float v[8];
+          unpack16x8<kVBf16>(w, v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] *= kSmaller;
+          w = pack16x8<kVBf16>(v);
+        }
       }
       o[db] = mfma_16<kVBf16>(w, ph, o[db]);
       o[db] = mfma_16<kVBf16>(w, pl, o[db]);
@@ -397,7 +407,7 @@ __device__ __forceinline__ bool decode_walk(const DecodeArgs& a, const DecodePie
 #pragma unroll
     for (int w = 0; w < Tile::kWaves; ++w) most = __builtin_fmaxf(most, state[(w * 16 + (tid & 15)) * 4]);
     const float4 st = *reinterpret_cast<const float4*>(state + tid * 4);
-    const float f = state_factor(st, most, c, 0.0f);
+    const float f = state_factor(st, most, c);
     *reinterpret_cast<float4*>(factors + tid * 4) = make_float4(f, f * st.y, st.z, most);
   }
   __syncthreads();
@@ -417,19 +427,19 @@ __device__ __forceinline__ bool decode_walk(const DecodeArgs& a, const DecodePie
     }
     if (kVBf16 && !(__builtin_fabsf(v.x) + __builtin_fabsf(v.y) + __builtin_fabsf(v.z) + __builtin_fabsf(v.w) <= 0x1p100f)) *flag = 1;
     if (whole) {
-      const float inv = seen > 0.0f ? 1.0f / sum : 0.0f;
+      const float inv = seen > 0.0f ? 1.0f / (sum * (kAgain ? kSmaller : 1.0f)) : 0.0f;
       *reinterpret_cast<uint2*>(a.o + (static_cast<int64_t>(b) * a.Hq + hq0 + r) * D + 4 * ch) = pack4(a.out_type, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
     } else {
       float* const p = a.ws + static_cast<int64_t>(blockIdx.x) * Tile::kSlot;
       *reinterpret_cast<float4*>(p + r * D + 4 * ch) = v;
-      if (ch == 0) *reinterpret_cast<float4*>(p + 16 * D + 4 * r) = make_float4(most, sum, seen, shift);
+      if (ch == 0) *reinterpret_cast<float4*>(p + 16 * D + 4 * r) = make_float4(most, sum, seen, kAgain ? kSmaller : 1.0f);
     }
   }
-  if constexpr (kVBf16) {
+  if constexpr (kVBf16 && !kAgain) {
     __syncthreads();
     return __builtin_amdgcn_readfirstlane(*flag);
   } else {
-    return false;   // f16 values are too small for it
+    return false;   // (f16 values are too small for it)
   }
 }
 
@@ -471,7 +481,7 @@ void attn_decode_kernel(DecodeArgs a) {
   }
 
   const DecodePiece piece{b, hv, len, t0, t1, nt};
-  if (decode_walk<D, kBf16, kQuant, kWide>(a, piece, smem, 0.0f)) decode_walk<D, kBf16, kQuant, kWide>(a, piece, smem, kFar);
+  if (decode_walk<D, kBf16, kQuant, kWide, false>(a, piece, smem)) decode_walk<D, kBf16, kQuant, kWide, true>(a, piece, smem);
 }
 
 // The pieces of one sequence and query head, in the order of the line: their weights first, then D / 4 threads each take 4
@@ -516,7 +526,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(DecodeArgs a) {
   }
 #pragma unroll
   for (int m = 1; m < 64; m *= 2) most = __builtin_fmaxf(most, __shfl_xor(most, m));
-  least = __any(least != 0.0f) ? kFar : 0.0f;
+  least = __any(least != 1.0f) ? kSmaller : 1.0f;
   if ((tid & 63) == 0) sums[0][tid >> 6] = most, sums[3][tid >> 6] = least;
   __syncthreads();
   most = __builtin_fmaxf(__builtin_fmaxf(sums[0][0], sums[0][1]), __builtin_fmaxf(sums[0][2], sums[0][3]));
@@ -524,8 +534,8 @@ __global__ __launch_bounds__(256) void attn_join_kernel(DecodeArgs a) {
   float sum = 0.0f, seen = 0.0f;
   for (int i = tid; i < pieces; i += 256) {
     const float4 st = i == tid ? mine : state(i);
-    const float f = state_factor(st, most, c, least);
-    weight[i] = f;
+    const float f = state_factor(st, most, c);
+    weight[i] = st.w == least ? f : f * kSmaller;
     sum += f * st.y;
     seen += st.z;
   }
@@ -561,7 +571,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(DecodeArgs a) {
     const float4 u = *reinterpret_cast<const float4*>(&part[i][4 * lane]);
     v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
   }
-  const float inv = seen > 0.0f ? 1.0f / sum : 0.0f;
+  const float inv = seen > 0.0f ? 1.0f / (sum * least) : 0.0f;
   *reinterpret_cast<uint2*>(out + 4 * lane) = pack4(a.out_type, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
 }
 

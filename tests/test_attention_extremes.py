@@ -279,3 +279,24 @@ def test_prefill_infinite_values_of_no_weight(nq, nk):
     assert bool(torch.isnan(seen[:, :, 5]).all()) and bool(torch.isfinite(o[:, :, :5]).all()) and bool(torch.isfinite(o[:, :, 6:]).all())
     if nq == nk:
         assert bool((o[0, :, 5] == math.inf).all())
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n", [300, 5000])
+def test_decode_a_large_value_of_every_weight(n, D, cache):
+    """One key's values of 1e35 under weights of 1 down to 2^-120 of the others', which have ordinary ones, in heads of one product: those whose sums
+    are large leave the others' small weights as they are."""
+    g = torch.Generator().manual_seed(n)
+    gaps = [0.0, 20.0, 40.0, 60.0, 70.0, 80.0, 90.0, 100.0, 110.0, 120.0]
+    k, v = torch.zeros((n, 1, D)), torch.randint(-4, 5, (n, 1, D), generator=g).float()
+    k[n // 3, 0, 0], v[n // 3] = -1, torch.where(torch.rand((1, D), generator=g) < 0.5, 1.0, 0.5) * 2.0 ** 116
+    q = torch.zeros((1, len(gaps), D))
+    q[0, :, 0] = torch.tensor(gaps)
+    c, table, s = _cache(g, n, D, "bf16", k, v)
+    if cache == "e4m3":
+        c, table, s = _cache(g, n, D, cache, k, torch.where(v.abs() > 4, v * 2.0 ** -116, v))
+        at = (n // 3) // 16
+        s[1][table[0, at], 0, n // 3 % 16] *= 2.0 ** 116
+    o = pq.attn_decode(q.to(BF16).cuda(), *c, table, _i32(n), *s, scale=LN2)
+    ta._check_decode(o, q.to(BF16).cuda(), [[k.double()], [v.double()]], [n], LN2, "a large value")
